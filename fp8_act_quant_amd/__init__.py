@@ -18,13 +18,16 @@ import torch
 from . import _lib
 from ._lib import (FP8Q_GEMM_EXACT_SLICES, FP8Q_GEMM_FP8_PRODUCTS, FP8Q_OUT_BF16, FP8Q_OUT_F32, FP8Q_SA_KMAJOR,
                    Fp8qError, check, lib)
+from .int8 import int8_gemm, int8_grouped_gemm, int8_linear, int8_quant
+from .moe import moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward
 
 BLOCK = 128
 
 __all__ = [
     "BLOCK", "Fp8qError", "act_quant", "weight_quant", "weight_dequant", "fp8_gemm", "fp8_grouped_gemm",
     "linear", "gemm_workspace_bytes", "lib", "act_quant_t", "weight_transpose", "fp8_gemm_rowwise",
-    "linear_backward", "bf16_gemm",
+    "linear_backward", "bf16_gemm", "moe_route", "moe_route_backward", "moe_place", "moe_combine",
+    "moe_combine_backward", "int8_quant", "int8_gemm", "int8_linear", "int8_grouped_gemm",
 ]
 
 

@@ -28,9 +28,15 @@ FP8Q_GEMM_FP8_PRODUCTS = 0x100
 FP8Q_GEMM_EXACT_SLICES = 0x200
 FP8Q_SA_KMAJOR = 0x1000
 
+FP8Q_MOE_SOFTMAX = 1
+FP8Q_MOE_GROUP_MAX = 2
+FP8Q_MOE_KEEP_SCORES = 4
+
 # name -> (restype, argtypes); the exports of include/fp8q.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_INT = ctypes.c_int
+_F32 = ctypes.c_float
 SIGNATURES = {
     "fp8_act_quant": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
     "fp8_act_quant_kmajor": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
@@ -48,6 +54,15 @@ SIGNATURES = {
     "fp8_weight_transpose": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _P]),
     "fp8_rowwise_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "fp8_rowwise_gemm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, ctypes.c_int]),
+    "moe_route": (_INT, [_P, _INT, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _INT, _P]),
+    "moe_route_backward": (_INT, [_P, _P, _INT, _P, _P, _I64, _I64, _I64, _F32, _INT, _P]),
+    "moe_place": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "moe_place_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "moe_combine": (_INT, [_P, _INT, _P, _P, _P, _I64, _I64, _I64, _I64, _P]),
+    "moe_combine_backward": (_INT, [_P, _P, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]),
+    "int8_quant": (_INT, [_P, _P, _P, _I64, _I64, _P]),
+    "int8_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P]),
+    "int8_grouped_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P]),
     "fp8q_gemm_force_config": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "fp8q_gemm_config_name": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8q_gemm_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, _P, _P]),

@@ -62,6 +62,37 @@ int shape_ok(int64_t rows, int64_t K) {
     return FP8Q_OK;
 }
 
+// Routed-expert layer: a row (of logits, of assignments) is a wave's or a workgroup's, so its
+// count is bounded by the grid (256 threads each); assignments and rows are 32-bit.
+constexpr int64_t kMaxTokens = kMaxBlocks256;
+constexpr int64_t kMaxTopK = 32, kMaxGroups = 64;
+// 8-bit products: the sum of K products of at most 2^14 fits 32 bits while K < 2^17
+constexpr int64_t kInt8Step = 16, kMaxInt8K = ((int64_t)1 << 17) - kInt8Step;
+constexpr int64_t kMaxGatherBytes = 0xFFFFFFF0ll;   // gathered rows have 32-bit byte offsets
+
+bool is_type(int dtype) { return dtype == FP8Q_OUT_F32 || dtype == FP8Q_OUT_BF16; }
+
+// T rows of top_k of `experts` experts
+bool routing_ok(int64_t T, int64_t experts, int64_t top_k) {
+    return T >= 0 && T <= kMaxTokens && experts >= 1 && experts <= fp8q::kMaxGroupedExperts && top_k >= 1 &&
+           top_k <= kMaxTopK && T <= (INT32_MAX - 1) / top_k;
+}
+
+int combine_ok(int dtype, int64_t T, int64_t rows, int64_t H, int64_t top_k) {
+    if (!is_type(dtype)) return FP8Q_ERR_DTYPE;
+    if (T < 0 || rows < 0 || H < 0 || top_k < 1 || top_k > kMaxTopK || rows > INT32_MAX) return FP8Q_ERR_SHAPE;
+    // one workgroup of 256 threads per token (and, forward, per 256 elements at the least)
+    if (T > kMaxTokens || T > INT32_MAX / top_k || (H + 255) / 256 > kMaxGridY) return FP8Q_ERR_SHAPE;
+    return FP8Q_OK;
+}
+
+int int8_ok(int dtype, int64_t M, int64_t N, int64_t K) {
+    if (!is_type(dtype)) return FP8Q_ERR_DTYPE;
+    if (M < 0 || N < 0 || K < 0 || K % kInt8Step || K > kMaxInt8K) return FP8Q_ERR_SHAPE;
+    if (M > kMaxGemmRows || N > kMaxGemmRows || (M > 0 && N > kMaxElems / M)) return FP8Q_ERR_SHAPE;
+    return FP8Q_OK;
+}
+
 int finish(hipError_t e) { return e == hipSuccess ? FP8Q_OK : FP8Q_ERR_LAUNCH; }
 
 }  // namespace
@@ -274,6 +305,127 @@ size_t fp8_block_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int y_dty
     return fp8q::gemm_workspace_bytes(M, N, K, dtype == FP8Q_OUT_BF16, exact);
 }
 
+int moe_route(const void *logits, int dtype, const float *bias, float *weights, int32_t *experts, int64_t T, int64_t E,
+              int64_t top_k, int64_t groups, int64_t topk_groups, float scale, int flags, void *stream) {
+    if (!is_type(dtype) || (flags & ~(FP8Q_MOE_SOFTMAX | FP8Q_MOE_GROUP_MAX | FP8Q_MOE_KEEP_SCORES)))
+        return FP8Q_ERR_DTYPE;
+    if (!routing_ok(T, E, top_k) || groups < 1 || groups > kMaxGroups || E % groups || topk_groups < 1 ||
+        topk_groups > groups || top_k > topk_groups * (E / groups))
+        return FP8Q_ERR_SHAPE;
+    if (T == 0) return FP8Q_OK;
+    if (!logits || !weights || !experts) return FP8Q_ERR_NULL;
+    if (misaligned(logits, dtype == FP8Q_OUT_BF16 ? 2 : 4) || misaligned(bias, 4) || misaligned(weights, 4) ||
+        misaligned(experts, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_moe_route(logits, dtype == FP8Q_OUT_BF16, bias, weights, experts, T, (int)E, (int)top_k,
+                                         (int)groups, (int)topk_groups, flags & FP8Q_MOE_SOFTMAX,
+                                         !(flags & FP8Q_MOE_GROUP_MAX), !(flags & FP8Q_MOE_KEEP_SCORES), scale,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const float *dweights, const void *logits, int dtype, const int32_t *experts, void *dlogits,
+                       int64_t T, int64_t E, int64_t top_k, float scale, int flags, void *stream) {
+    if (!is_type(dtype) || (flags & ~(FP8Q_MOE_SOFTMAX | FP8Q_MOE_KEEP_SCORES))) return FP8Q_ERR_DTYPE;
+    if (!routing_ok(T, E, top_k)) return FP8Q_ERR_SHAPE;
+    if (T == 0) return FP8Q_OK;
+    if (!dweights || !logits || !experts || !dlogits) return FP8Q_ERR_NULL;
+    const uintptr_t size = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+    if (misaligned(logits, size) || misaligned(dlogits, size) || misaligned(dweights, 4) || misaligned(experts, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_moe_route_backward(dweights, logits, dtype == FP8Q_OUT_BF16, experts, dlogits, T, (int)E,
+                                                  (int)top_k, flags & FP8Q_MOE_SOFTMAX,
+                                                  !(flags & FP8Q_MOE_KEEP_SCORES), scale,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_place_workspace_bytes(int64_t T, int64_t top_k, int64_t experts) {
+    if (!routing_ok(T, experts, top_k) || T == 0) return 0;
+    return fp8q::moe_place_workspace_bytes(T * top_k, experts);
+}
+
+int moe_place(const int32_t *assigned, int64_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int64_t top_k,
+              int64_t experts, int64_t first, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!routing_ok(T, experts, top_k) || first < 0 || first > INT32_MAX - experts) return FP8Q_ERR_SHAPE;
+    if (!offsets || (T > 0 && (!assigned || !rows || !slots))) return FP8Q_ERR_NULL;
+    if (misaligned(assigned, 4) || misaligned(offsets, 8) || misaligned(rows, 4) || misaligned(slots, 4) ||
+        misaligned(workspace, 4))
+        return FP8Q_ERR_ALIGN;
+    if (fp8q::moe_place_workspace_bytes(T * top_k, experts) > (workspace ? workspace_bytes : 0))
+        return FP8Q_ERR_WORKSPACE;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_moe_place(assigned, offsets, rows, slots, T, (int)top_k, (int)experts, (int)first,
+                                         workspace, static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine(const void *h, int dtype, const int32_t *slots, const float *weights, void *y, int64_t T,
+                int64_t top_k, int64_t rows, int64_t H, void *stream) {
+    if (int e = combine_ok(dtype, T, rows, H, top_k)) return e;
+    if (T == 0 || H == 0) return FP8Q_OK;
+    if (!slots || !y || (rows > 0 && !h)) return FP8Q_ERR_NULL;
+    const uintptr_t size = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+    if (misaligned(h, size) || misaligned(y, size) || misaligned(slots, 4) || misaligned(weights, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_moe_combine(h, dtype == FP8Q_OUT_BF16, slots, weights, y, T, rows, H, (int)top_k,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_backward(const void *dy, const void *h, int dtype, const int32_t *slots, const float *weights, void *dh,
+                         float *dweights, int64_t T, int64_t top_k, int64_t rows, int64_t H, void *stream) {
+    if (int e = combine_ok(dtype, T, rows, H, top_k)) return e;
+    if (T == 0) return FP8Q_OK;
+    if (!slots || !weights || !dweights || (H > 0 && (!dy || (rows > 0 && (!h || !dh))))) return FP8Q_ERR_NULL;
+    const uintptr_t size = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+    if (misaligned(dy, size) || misaligned(h, size) || misaligned(dh, size) || misaligned(slots, 4) ||
+        misaligned(weights, 4) || misaligned(dweights, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_moe_combine_backward(dy, h, dtype == FP8Q_OUT_BF16, slots, weights, dh, dweights, T,
+                                                    rows, H, (int)top_k, static_cast<hipStream_t>(stream)));
+}
+
+int int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, int64_t K, void *stream) {
+    if (M < 0 || K < 0 || K % kInt8Step || (K > 0 && M > kMaxElems / K) || M > kMaxTokens) return FP8Q_ERR_SHAPE;
+    if (M == 0 || K == 0) return FP8Q_OK;
+    if (!x || !q || !s) return FP8Q_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(q, 16) || misaligned(s, 4)) return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_int8_quant(x, q, s, M, K, static_cast<hipStream_t>(stream)));
+}
+
+int int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias, void *y,
+              int y_dtype, int64_t M, int64_t N, int64_t K, void *stream) {
+    if (int e = int8_ok(y_dtype, M, N, K)) return e;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (!y || (K > 0 && (!a || !sa || !w || !sw))) return FP8Q_ERR_NULL;
+    if (misaligned(a, 16) || misaligned(w, 16) || misaligned(y, 4) || misaligned(sa, 4) || misaligned(sw, 4) ||
+        misaligned(bias, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_int8_gemm(a, sa, w, sw, bias, y, y_dtype == FP8Q_OUT_BF16, M, N, K,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const int64_t *offsets,
+                      const int32_t *rows, void *y, int y_dtype, int64_t experts, int64_t M, int64_t tokens, int64_t N,
+                      int64_t K, void *stream) {
+    if (int e = int8_ok(y_dtype, M, N, K)) return e;
+    if (experts < 1 || experts > fp8q::kMaxGroupedExperts || M > INT32_MAX / 2) return FP8Q_ERR_SHAPE;
+    if (N > 0 && K > 0 && experts > kMaxElems / N / K) return FP8Q_ERR_SHAPE;
+    if (tokens < 0 || tokens > INT32_MAX || (!rows && M > 0 && tokens != M)) return FP8Q_ERR_SHAPE;
+    if (rows && K > 0 && tokens > kMaxGatherBytes / K) return FP8Q_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (!y || !offsets || (K > 0 && (!w || !sw || (tokens > 0 && (!a || !sa))))) return FP8Q_ERR_NULL;
+    if (misaligned(a, 16) || misaligned(w, 16) || misaligned(y, 4) || misaligned(sa, 4) || misaligned(sw, 4) ||
+        misaligned(offsets, 8) || misaligned(rows, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_int8_grouped_gemm(a, sa, w, sw, offsets, rows, y, y_dtype == FP8Q_OUT_BF16, experts, M,
+                                                 tokens, N, K, static_cast<hipStream_t>(stream)));
+}
+
 int fp8q_gemm_force_config(int config, int splits) {
     return fp8q::gemm_force_config(config, splits) ? FP8Q_OK : FP8Q_ERR_SHAPE;
 }
@@ -305,11 +457,12 @@ const char *fp8q_strerror(int status) {
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_WORKSPACE:
         return "the shape's split-K schedule needs more scratch than the static scratch holds "
-               "(FP8Q_NOALLOC_SCRATCH_BYTES); call fp8_block_gemm with a workspace instead";
+               "(FP8Q_NOALLOC_SCRATCH_BYTES); call fp8_block_gemm with a workspace instead (moe_place: the workspace "
+               "is smaller than moe_place_workspace_bytes)";
     default: return "unknown status";
     }
 }
 
-int fp8q_version(void) { return (1 << 16) | 5; }
+int fp8q_version(void) { return (1 << 16) | 6; }
 
 }  // extern "C"

@@ -70,4 +70,36 @@ const char *gemm_config_name(int tile);
 // workspace of at least gemm_workspace_bytes
 void gemm_plan(int64_t M, int64_t N, int64_t K, bool out_bf16, bool exact, int *tile, int *splits);
 
+
+// Routing of tokens to experts (route.hip). logits [T, E] bf16 or fp32, bias [E] or null;
+// weights, experts [T, k]. E <= kMaxGroupedExperts, k <= 32, groups <= 64 dividing E.
+hipError_t launch_moe_route(const void *logits, bool bf16, const float *bias, float *weights, int32_t *experts,
+                            int64_t T, int E, int k, int groups, int topk_groups, bool softmax, bool group_top2,
+                            bool renormalize, float scale, hipStream_t stream);
+hipError_t launch_moe_route_backward(const float *dweights, const void *logits, bool bf16, const int32_t *experts,
+                                     void *dlogits, int64_t T, int E, int k, bool softmax, bool renormalize,
+                                     float scale, hipStream_t stream);
+
+// Rows into expert order and back (place.hip): T * k < 2^31 pairs, E <= kMaxGroupedExperts
+// experts from `first`; the workspace holds moe_place_workspace_bytes (any contents).
+size_t moe_place_workspace_bytes(int64_t pairs, int64_t E);
+hipError_t launch_moe_place(const int32_t *experts, int64_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int k,
+                            int E, int first, void *workspace, hipStream_t stream);
+hipError_t launch_moe_combine(const void *h, bool bf16, const int32_t *slots, const float *weights, void *y, int64_t T,
+                              int64_t rows, int64_t H, int k, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const void *dy, const void *h, bool bf16, const int32_t *slots,
+                                       const float *weights, void *dh, float *dweights, int64_t T, int64_t rows,
+                                       int64_t H, int k, hipStream_t stream);
+
+// 8-bit integers with one scale per row of each operand (int8.hip): K a multiple of 16 below
+// 2^17. grouped: offsets [experts + 1] and rows [M] (or null) on the device; with rows,
+// tokens * K stays below 2^32 - 16.
+hipError_t launch_int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, int64_t K, hipStream_t stream);
+hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias,
+                            void *y, bool out_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw,
+                                    const int64_t *offsets, const int32_t *rows, void *y, bool out_bf16,
+                                    int64_t experts, int64_t M, int64_t tokens, int64_t N, int64_t K,
+                                    hipStream_t stream);
+
 }  // namespace fp8q

@@ -1,0 +1,380 @@
+// place.hip -- rows of a routed-expert layer into expert order, and back, for gfx950.
+//
+// moe_place: the T * k (token, choice) pairs, stably sorted by expert: offsets[e] .. offsets[e
+// + 1] are expert e's rows, rows[r] the token of row r, slots[t, j] the row of token t's j-th
+// choice. A counting sort: every workgroup owns a contiguous chunk of the pairs and each of
+// its waves a contiguous segment of the chunk; counts per (wave, expert) are turned into first
+// rows, and each wave then walks its segment 64 pairs at a time, a pair's row being its
+// expert's next row plus the number of earlier lanes with the same expert. Nothing depends on
+// the order in which waves or workgroups run. Integer work on a few hundred KB: what bounds it
+// is the latency of its dependent steps, not bandwidth.
+//
+// moe_combine: y[t] = sum_j w[t, j] h[slots[t, j]], and its gradient. One pass over h, 16 bytes
+// a lane; memory bound.
+#include <fp8q.h>
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8q {
+namespace {
+
+constexpr int kMaxExperts = (int)kMaxGroupedExperts;
+constexpr int PW = 8;               // waves of a placement workgroup
+constexpr int PT = 64 * PW;
+constexpr int64_t kOneChunk = 4096; // pairs that one workgroup places by itself
+constexpr int64_t kChunk = 2048;    // pairs of a chunk where there are several
+constexpr int64_t kMaxChunks = 256;
+
+struct PlaceArgs {
+    const int32_t *experts;
+    int64_t *offsets;
+    int32_t *rows;
+    int32_t *slots;
+    uint32_t *counts;   // [chunks][E]: each chunk's pairs of each expert
+    int64_t pairs;
+    int64_t seg;        // pairs of a wave, a multiple of 64
+    int E, first, k, chunks;
+};
+
+// this wave's pairs, and its counts by expert into hist[wave]
+__device__ __forceinline__ void count_segment(const PlaceArgs &a, int64_t p0, int64_t p1, uint32_t *hist, int lane) {
+    for (int64_t p = p0 + lane; p < p1; p += 64) {
+        const int e = a.experts[p] - a.first;
+        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&hist[e], 1u);
+    }
+}
+
+__global__ __launch_bounds__(PT) void place_count_kernel(PlaceArgs a) {
+    __shared__ uint32_t hist[kMaxExperts];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int e = threadIdx.x; e < a.E; e += PT) hist[e] = 0;
+    __syncthreads();
+    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg;
+    count_segment(a, p0, min(p0 + a.seg, a.pairs), hist, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += PT) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+}
+
+// exclusive prefix over the workgroup's threads; *all: the total
+__device__ __forceinline__ uint32_t prefix(uint32_t v, uint32_t *scratch, uint32_t *all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(s, d, 64);
+        s += lane >= d ? o : 0u;
+    }
+    if (lane == 63) scratch[wave] = s;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < PW; ++w) {
+        before += w < wave ? scratch[w] : 0u;
+        total += scratch[w];
+    }
+    *all = total;
+    return before + s - v;
+}
+
+__global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
+    __shared__ uint32_t hist[PW][kMaxExperts];
+    __shared__ uint32_t scratch[PW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int e = threadIdx.x; e < a.E; e += PT)
+#pragma unroll
+        for (int w = 0; w < PW; ++w) hist[w][e] = 0;
+    __syncthreads();
+    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg, p1 = min(p0 + a.seg, a.pairs);
+    count_segment(a, p0, p1, hist[wave], lane);
+    __syncthreads();
+
+    // each thread owns the experts 2 i and 2 i + 1
+    constexpr int PER = kMaxExperts / PT;
+    uint32_t total[PER], before[PER], sum = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int e = threadIdx.x * PER + u;
+        total[u] = before[u] = 0;
+        if (e < a.E) {
+            uint32_t own = 0;
+#pragma unroll
+            for (int w = 0; w < PW; ++w) {
+                const uint32_t c = hist[w][e];
+                hist[w][e] = own;
+                own += c;
+            }
+            if (a.chunks == 1) {
+                total[u] = own;
+            } else {
+                for (int c = 0; c < a.chunks; ++c) {
+                    const uint32_t n = a.counts[(int64_t)c * a.E + e];
+                    before[u] += c < (int)blockIdx.x ? n : 0u;
+                    total[u] += n;
+                }
+            }
+        }
+        sum += total[u];
+    }
+    uint32_t all;
+    uint32_t at = prefix(sum, scratch, &all);
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int e = threadIdx.x * PER + u;
+        if (e < a.E) {
+#pragma unroll
+            for (int w = 0; w < PW; ++w) hist[w][e] += at + before[u];
+            if (blockIdx.x == 0) a.offsets[e] = at;
+        }
+        at += total[u];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
+    // rows that no pair fills
+    for (int64_t r = all + (int64_t)blockIdx.x * PT + threadIdx.x; r < a.pairs; r += (int64_t)a.chunks * PT)
+        a.rows[r] = -1;
+    __syncthreads();
+
+    uint32_t *next = hist[wave];
+    const int bits = 32 - __builtin_clz(a.E);
+    for (int64_t p = p0; p < p1; p += 64) {
+        const int64_t i = p + lane;
+        const bool in = i < p1;
+        const int e = in ? a.experts[i] - a.first : -1;
+        const bool there = (uint32_t)e < (uint32_t)a.E;
+        uint64_t same = __ballot(there);   // the lanes with this lane's expert
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? set : ~set;
+        }
+        if (there) {
+            const int earlier = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
+                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
+            const uint32_t r = next[e] + earlier;
+            a.slots[i] = (int32_t)r;
+            a.rows[r] = (int32_t)((uint32_t)i / (uint32_t)a.k);
+            // (LDS accesses of a wave run in order; the fence keeps the compiler's order)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if ((same >> lane) == 1ull) next[e] = r + 1;   // the last of these lanes
+        } else if (in) {
+            a.slots[i] = -1;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+int64_t chunks_of(int64_t pairs) {
+    if (pairs <= kOneChunk) return 1;
+    const int64_t c = (pairs + kChunk - 1) / kChunk;
+    return c < kMaxChunks ? c : kMaxChunks;
+}
+
+// ---------------------------------------------------------------------------------------
+
+struct CombineArgs {
+    const void *h;
+    const int32_t *slots;
+    const float *weights;   // or null: every weight 1
+    void *y;
+    const void *dy;
+    void *dh;
+    float *dweights;
+    int64_t T, H, rows;
+    int k;
+};
+
+// VEC consecutive elements, BF16 or fp32
+template <int BF16, int VEC>
+struct Piece {
+    float v[VEC];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        if constexpr (BF16) {
+            const uint16_t *q = reinterpret_cast<const uint16_t *>(p) + i;
+            if constexpr (VEC == 8) {
+                const u32x4 u = *reinterpret_cast<const u32x4 *>(q);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    v[2 * d] = bf16lo_to_f32(u[d]);
+                    v[2 * d + 1] = bf16hi_to_f32(u[d]);
+                }
+            } else {
+                v[0] = __uint_as_float((uint32_t)q[0] << 16);
+            }
+        } else {
+            const float *q = reinterpret_cast<const float *>(p) + i;
+            if constexpr (VEC == 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(q);
+                v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            } else {
+                v[0] = q[0];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *p, int64_t i) const {
+        if constexpr (BF16) {
+            uint16_t *q = reinterpret_cast<uint16_t *>(p) + i;
+            if constexpr (VEC == 8) {
+                u32x4 u;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) u[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
+                *reinterpret_cast<u32x4 *>(q) = u;
+            } else {
+                q[0] = (uint16_t)pack_bf16x2(v[0], 0.0f);
+            }
+        } else {
+            float *q = reinterpret_cast<float *>(p) + i;
+            if constexpr (VEC == 4) *reinterpret_cast<float4 *>(q) = float4{v[0], v[1], v[2], v[3]};
+            else q[0] = v[0];
+        }
+    }
+};
+
+constexpr int CT = 256;   // threads of a combine workgroup
+constexpr int KB = 8;     // choices whose rows are in flight together
+
+// A workgroup sums a piece of one token's row.
+template <int BF16, int VEC>
+__global__ __launch_bounds__(CT) void combine_kernel(CombineArgs a) {
+    const int64_t t = blockIdx.x;
+    const int64_t col = ((int64_t)blockIdx.y * CT + threadIdx.x) * VEC;
+    if (col >= a.H) return;
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+        Piece<BF16, VEC> p[KB];
+        float w[KB];
+#pragma unroll
+        for (int u = 0; u < KB; ++u) {
+            const int j = j0 + u;
+            const int s = j < a.k ? a.slots[t * a.k + j] : -1;
+            w[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) p[u].v[i] = 0.0f;
+            if (s >= 0 && s < a.rows) {
+                w[u] = a.weights ? a.weights[t * a.k + j] : 1.0f;
+                p[u].load(a.h, (int64_t)s * a.H + col);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < KB; ++u)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(w[u], p[u].v[i], acc[i]);
+    }
+    Piece<BF16, VEC> out;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out.v[i] = acc[i];
+    out.store(a.y, t * a.H + col);
+}
+
+// dh[slot] = w dy and dw = <dy, h[slot]>, a workgroup per token: each row of h is read and
+// each row of dh written once. The dot products are summed in fp32 in a fixed order.
+template <int BF16, int VEC>
+__global__ __launch_bounds__(CT) void combine_grad_kernel(CombineArgs a) {
+    __shared__ float part[CT / 64][KB];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+        int slot[KB];
+        float w[KB], dot[KB];
+#pragma unroll
+        for (int u = 0; u < KB; ++u) {
+            const int j = j0 + u;
+            const int s = j < a.k ? a.slots[t * a.k + j] : -1;
+            slot[u] = s < a.rows ? s : -1;
+            w[u] = slot[u] >= 0 ? a.weights[t * a.k + j] : 0.0f;
+            dot[u] = 0.0f;
+        }
+        for (int64_t col = (int64_t)threadIdx.x * VEC; col < a.H; col += CT * VEC) {
+            Piece<BF16, VEC> g, p[KB], out;
+            g.load(a.dy, t * a.H + col);
+#pragma unroll
+            for (int u = 0; u < KB; ++u)
+                if (slot[u] >= 0) p[u].load(a.h, (int64_t)slot[u] * a.H + col);
+#pragma unroll
+            for (int u = 0; u < KB; ++u) {
+                if (slot[u] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        dot[u] = __builtin_fmaf(g.v[i], p[u].v[i], dot[u]);
+                        out.v[i] = w[u] * g.v[i];
+                    }
+                    out.store(a.dh, (int64_t)slot[u] * a.H + col);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < KB; ++u) {
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) dot[u] += __shfl_xor(dot[u], m, 64);
+            if (lane == 0) part[wave][u] = dot[u];
+        }
+        __syncthreads();
+        if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < CT / 64; ++v) sum += part[v][threadIdx.x];
+            a.dweights[t * a.k + j0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+bool vec_ok(int64_t H, int size, const void *p, const void *q, const void *r) {
+    return H * size % 16 == 0 &&
+           ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(r)) & 15) == 0;
+}
+
+}  // namespace
+
+size_t moe_place_workspace_bytes(int64_t pairs, int64_t E) {
+    const int64_t c = chunks_of(pairs);
+    return c == 1 ? 0 : (size_t)(c * E * 4);
+}
+
+hipError_t launch_moe_place(const int32_t *experts, int64_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int k,
+                            int E, int first, void *workspace, hipStream_t stream) {
+    PlaceArgs a{experts, offsets, rows, slots, static_cast<uint32_t *>(workspace), T * k, 0, E, first, k, 0};
+    a.chunks = (int)chunks_of(a.pairs);
+    const int64_t waves = (int64_t)a.chunks * PW;
+    a.seg = ((a.pairs + waves - 1) / waves + 63) / 64 * 64;
+    if (a.chunks > 1) {
+        place_count_kernel<<<dim3(a.chunks), dim3(PT), 0, stream>>>(a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    place_kernel<<<dim3(a.chunks), dim3(PT), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void *h, bool bf16, const int32_t *slots, const float *weights, void *y, int64_t T,
+                              int64_t rows, int64_t H, int k, hipStream_t stream) {
+    const CombineArgs a{h, slots, weights, y, nullptr, nullptr, nullptr, T, H, rows, k};
+    const bool vec = vec_ok(H, bf16 ? 2 : 4, h, y, nullptr);
+    const int per = vec ? (bf16 ? 8 : 4) : 1;
+    const dim3 grid((unsigned)T, (unsigned)((H + (int64_t)CT * per - 1) / ((int64_t)CT * per))), block(CT);
+    if (bf16) {
+        if (vec) combine_kernel<1, 8><<<grid, block, 0, stream>>>(a);
+        else combine_kernel<1, 1><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (vec) combine_kernel<0, 4><<<grid, block, 0, stream>>>(a);
+        else combine_kernel<0, 1><<<grid, block, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const void *dy, const void *h, bool bf16, const int32_t *slots,
+                                       const float *weights, void *dh, float *dweights, int64_t T, int64_t rows,
+                                       int64_t H, int k, hipStream_t stream) {
+    const CombineArgs a{h, slots, weights, nullptr, dy, dh, dweights, T, H, rows, k};
+    const bool vec = vec_ok(H, bf16 ? 2 : 4, h, dy, dh);
+    const dim3 grid((unsigned)T), block(CT);
+    if (bf16) {
+        if (vec) combine_grad_kernel<1, 8><<<grid, block, 0, stream>>>(a);
+        else combine_grad_kernel<1, 1><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (vec) combine_grad_kernel<0, 4><<<grid, block, 0, stream>>>(a);
+        else combine_grad_kernel<0, 1><<<grid, block, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace fp8q

@@ -59,7 +59,8 @@ extern "C" {
 #define FP8Q_ERR_DTYPE 4       /* unknown output dtype                                      */
 #define FP8Q_ERR_UNSUPPORTED 5 /* no gfx950 device is current                               */
 #define FP8Q_ERR_LAUNCH 6      /* the kernel launch failed                                  */
-#define FP8Q_ERR_WORKSPACE 7   /* more scratch needed than fp8_block_gemm_noalloc holds     */
+#define FP8Q_ERR_WORKSPACE 7   /* more scratch needed than fp8_block_gemm_noalloc holds, or
+                                  a workspace smaller than moe_place needs                  */
 
 /* Output dtypes of fp8_block_gemm (low 8 bits of its y_dtype argument). */
 #define FP8Q_OUT_F32 0
@@ -256,6 +257,106 @@ int fp8_weight_transpose(const uint8_t *wq, const float *sw, uint8_t *wqt, float
 int fp8_rowwise_gemm(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb, void *y, int y_dtype,
                      int64_t M, int64_t N, int64_t K, void *workspace, size_t workspace_bytes, void *stream);
 size_t fp8_rowwise_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int y_dtype);
+
+/* ---- Routed experts ------------------------------------------------------------------
+ * What a mixture-of-experts layer does around its grouped products: moe_route gives each
+ * token its experts and their weights, moe_place the offsets that fp8_grouped_gemm and
+ * int8_grouped_gemm take (and which token each row is), moe_combine the weighted sum of a
+ * token's rows. Element types (dtype) are FP8Q_OUT_F32 or FP8Q_OUT_BF16. T tokens of top_k
+ * experts each: T < 2^24, T * top_k < 2^31, 1 <= top_k <= 32, 1 <= experts <= 1024. */
+
+/* Flags of moe_route and moe_route_backward. */
+#define FP8Q_MOE_SOFTMAX 1     /* scores by softmax over the experts (default: sigmoid of each)  */
+#define FP8Q_MOE_GROUP_MAX 2   /* a group's value is its largest choice (default: sum of its two) */
+#define FP8Q_MOE_KEEP_SCORES 4 /* weights are the scores (default: divided by their sum)          */
+
+/* moe_route -- each token's experts and their weights.
+ * (pomoai.com "DeepSeek-V3", MoE section: sigmoid scores, 8 of 256 experts out of 4 of 8
+ * groups, a routing bias that balances the load and enters the selection only; softmax
+ * scores and a group's largest score are the predecessor's.)
+ *   logits [T, E] fp32 or bf16 (dtype); bias [E] fp32, or NULL for none.
+ *   s_i = 1 / (1 + exp(-x_i)), or exp(x_i - max) / sum; choice c_i = s_i + bias_i.
+ *   groups > 1 (at most 64, dividing E): the experts are `groups` runs of E / groups; the
+ *   topk_groups runs with the largest value take part. Of their experts the top_k with the
+ *   largest c are the token's, largest first; equal values rank by the lower index.
+ *   weights [T, top_k] fp32: scale * s_j / (sum of the selected s), or scale * s_j
+ *   (FP8Q_MOE_KEEP_SCORES); experts [T, top_k] int32.
+ *   top_k <= topk_groups * (E / groups). Logits of -inf (experts switched off for a token)
+ *   have score 0 and, without a bias, come after every other; a token whose selected scores
+ *   are all 0 has weights 0. NaN and +inf are outside the contract (the experts are still in
+ *   range). Every fp32 step of s and c is rounded to nearest; the softmax's sum is taken in
+ *   fp64 and rounded once. Any alignment of the element type. */
+int moe_route(const void *logits, int dtype, const float *bias, float *weights, int32_t *experts, int64_t T, int64_t E,
+              int64_t top_k, int64_t groups, int64_t topk_groups, float scale, int flags, void *stream);
+
+/* moe_route_backward -- the gradient of moe_route's weights with respect to the logits (the
+ * selection has none; the bias has none).
+ *   dweights [T, top_k] fp32; logits [T, E] and dlogits [T, E] of type dtype; experts as
+ *   moe_route gave them (distinct within a token; entries outside [0, E) take no part).
+ *   flags: FP8Q_MOE_SOFTMAX, FP8Q_MOE_KEEP_SCORES and scale as in the forward call. */
+int moe_route_backward(const float *dweights, const void *logits, int dtype, const int32_t *experts, void *dlogits,
+                       int64_t T, int64_t E, int64_t top_k, float scale, int flags, void *stream);
+
+/* moe_place -- rows in expert order.
+ *   assigned [T, top_k] int32: each token's experts. Those in [first, first + experts) are
+ *      placed (one GPU's share of an expert-parallel layer); others have no row.
+ *   offsets [experts + 1] int64: expert first + e owns rows offsets[e] .. offsets[e + 1] - 1;
+ *      offsets[experts] is the number of rows. 8-byte aligned.
+ *   rows [T * top_k] int32: the token of each row, ascending within an expert; -1 past the
+ *      last row.
+ *   slots [T, top_k] int32: the row of each (token, choice), or -1.
+ *   workspace: moe_place_workspace_bytes bytes of any contents, 4-byte aligned (NULL where
+ *      that is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at
+ *      the same time must not share it. T = 0 still writes offsets (all zero). */
+int moe_place(const int32_t *assigned, int64_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int64_t top_k,
+              int64_t experts, int64_t first, void *workspace, size_t workspace_bytes, void *stream);
+size_t moe_place_workspace_bytes(int64_t T, int64_t top_k, int64_t experts);
+
+/* moe_combine -- y[t] = sum over j of weights[t, j] * h[slots[t, j]].
+ *   h [rows, H] and y [T, H] of type dtype; slots [T, top_k] int32, entries outside
+ *   [0, rows) adding nothing; weights [T, top_k] fp32, or NULL for all 1 (the gradient of
+ *   the gather by moe_place's rows). Summed in fp32 in the order of j, rounded once. Any
+ *   alignment of the element type (16-byte rows are faster). */
+int moe_combine(const void *h, int dtype, const int32_t *slots, const float *weights, void *y, int64_t T,
+                int64_t top_k, int64_t rows, int64_t H, void *stream);
+
+/* moe_combine_backward -- dh[slots[t, j]] = weights[t, j] * dy[t] and
+ * dweights[t, j] = <dy[t], h[slots[t, j]]> (fp32; 0 where the slot is outside [0, rows)).
+ *   dh [rows, H] of type dtype: each row that a slot names is written, others are not (slots
+ *   name a row once, as moe_place gives them). */
+int moe_combine_backward(const void *dy, const void *h, int dtype, const int32_t *slots, const float *weights, void *dh,
+                         float *dweights, int64_t T, int64_t top_k, int64_t rows, int64_t H, void *stream);
+
+/* ---- 8-bit integers with one scale per token and one per channel -----------------------
+ * For weights kept as signed bytes with a scale per output channel, and tokens quantised as
+ * they come: Y = RN_out(float(sum_k a[m, k] w[n, k]) * sa[m] * sw[n] + bias[n]). The sum is
+ * exact in 32 bits; its conversion, the two scalings and the bias each round once in fp32.
+ * K is a multiple of 16 below 2^17. */
+
+/* int8_quant -- rows of bf16 to signed bytes: tokens of an activation, or channels of a weight.
+ *   x [M, K] bf16 (16-byte aligned), q [M, K] int8 (16), s [M] fp32 (4):
+ *   s[m] = RN_fp32(max |x[m]| * RN_fp32(1/127)) (a division by a constant as torch takes it
+ *   on GPU tensors), q = RNE(RN_fp32(x / s)) within [-127, 127]; a row of zeros has s = 0 and
+ *   q = 0. Any K that is a multiple of 16; M < 2^24. */
+int int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, int64_t K, void *stream);
+
+/* int8_gemm -- Y [M, N] = (a . w^T) * sa * sw (+ bias).
+ *   a [M, K] int8 with sa [M] fp32, w [N, K] int8 with sw [N] fp32 (a, w 16-byte aligned);
+ *   bias [N] fp32 or NULL; y fp32 or bf16 (y_dtype), 4-byte aligned. With K = 0 the output is
+ *   the bias (or zeros; sa and sw are then not read). */
+int int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias, void *y,
+              int y_dtype, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* int8_grouped_gemm -- int8_gemm for every expert's rows in one launch.
+ *   offsets [experts + 1] int64 on the device, as for fp8_grouped_gemm (clamped the same way);
+ *   w [experts, N, K] int8 with sw [experts, N].
+ *   rows [M] int32 on the device: row r of Y is token rows[r] of a [tokens, K], sa [tokens]
+ *      (moe_place's rows; entries outside [0, tokens) count as a token of zeros); needs
+ *      tokens * K < 2^32 - 16. Or NULL: row r is row r of a, and tokens must be M.
+ *   y [M, N]; rows that no expert owns are not written. */
+int int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const int64_t *offsets,
+                      const int32_t *rows, void *y, int y_dtype, int64_t experts, int64_t M, int64_t tokens, int64_t N,
+                      int64_t K, void *stream);
 
 /* Workspace size in bytes that lets fp8_block_gemm use its split-K schedule for this
  * shape and y_dtype (including the mode bits); 0 if that call does not use one or the

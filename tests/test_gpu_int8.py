@@ -1,0 +1,325 @@
+"""GPU parity of the 8-bit integer products against plain implementations in 64 bits.
+
+The integer sums are exact in float64 (below 2^53), so the reference knows them; the outputs'
+only errors are the rounding of the sum to fp32, two products and, with a bias, one sum, each
+within u = 2^-24: |y - ref| <= 4 u (|v| + |bias|), v the scaled sum; bf16 outputs lie between
+the bf16 roundings of those bounds. Those steps are stated, so fp32 outputs are also compared bit for bit with the same
+steps taken by numpy on the exact sum, and bf16 outputs with their rounding: whatever kernel
+variant a shape takes, it gives the same bits.
+"""
+import numpy as np
+import pytest
+import torch
+
+import fp8_act_quant_amd as fq
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def rng(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def codes(g, *shape):
+    return torch.randint(-128, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def scales(g, *shape):
+    return torch.rand(shape, generator=g, device="cuda") * 0.1 + 1e-3
+
+
+def check(y, a, sa, w, sw, bias, out):
+    exact = a.double() @ w.double().t()
+    v = exact * sa.double()[:, None] * sw.double()
+    ref = v if bias is None else v + bias.double()
+    mag = v.abs() if bias is None else v.abs() + bias.double().abs()
+    lo, hi = ref - 4 * U * mag - 1e-37, ref + 4 * U * mag + 1e-37
+    if out == "bf16":
+        lo, hi = lo.bfloat16().double(), hi.bfloat16().double()
+    assert ((y.double() >= lo) & (y.double() <= hi)).all(), float(((y.double() - ref).abs() / (mag + 1e-37)).max())
+    e32 = exact.cpu().numpy().astype(np.float32)
+    s = e32 * sa.cpu().numpy()[:, None] * sw.cpu().numpy()
+    if bias is not None:
+        s = s + bias.cpu().numpy()
+    assert torch.equal(y.cpu(), torch.from_numpy(s).to(DT[out]))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,biased", [
+    (1, 1, 16, True), (1, 16, 64, False), (1, 7168, 7168, False), (2, 100, 48, True), (15, 17, 144, False),
+    (16, 130, 1040, True), (17, 33, 128, False), (31, 1000, 656, True), (33, 15, 64, True), (64, 300, 2064, False),
+    (65, 129, 176, True), (128, 128, 128, False), (129, 257, 16, True), (200, 100, 1040, False),
+    (300, 1001, 304, True), (1000, 576, 1536, False), (4096, 4100, 272, True), (4097, 4096, 144, False),
+])
+def test_gemm(M, N, K, biased, out):
+    g = rng(M + N + K)
+    a, w, sa, sw = codes(g, M, K), codes(g, N, K), scales(g, M), scales(g, N)
+    bias = torch.randn(N, generator=g, device="cuda") if biased else None
+    y = fq.int8_gemm(a, sa, w, sw, bias, out_dtype=DT[out])
+    assert y.dtype == DT[out] and y.shape == (M, N)
+    check(y, a, sa, w, sw, bias, out)
+
+
+@pytest.mark.parametrize("M", [3, 100, 300])
+def test_gemm_largest_sums(M):
+    """Every code at the end of its range over the longest K: the sum nearly fills 32 bits."""
+    K, N = (1 << 17) - 16, 20
+    a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    w[1::2] = 127
+    g = rng(M)
+    sa, sw = scales(g, M), scales(g, N)
+    check(fq.int8_gemm(a, sa, w, sw, out_dtype=torch.float32), a, sa, w, sw, None, "f32")
+
+
+@pytest.mark.parametrize("M,N", [(5, 33), (40, 70), (200, 130)])
+def test_gemm_writes_only_its_output(M, N):
+    """The output a view into a larger buffer, 4 bytes past a 16-byte boundary; operands that
+    end where their allocation does are read no further (their neighbours hold other codes)."""
+    g = rng(M)
+    K = 208
+    a, w, sa, sw = codes(g, M, K), codes(g, N, K), scales(g, M), scales(g, N)
+    for out, per in (("f32", 1), ("bf16", 2)):
+        buf = torch.full((M * N + 64,), 7.0, dtype=DT[out], device="cuda")
+        y = buf[per:per + M * N].view(M, N)
+        fq.int8_gemm(a, sa, w, sw, out_dtype=DT[out], out=y)
+        check(y, a, sa, w, sw, None, out)
+        assert (buf[:per] == 7).all() and (buf[per + M * N:] == 7).all()
+
+
+def test_gemm_empty():
+    a = torch.empty((3, 0), dtype=torch.int8, device="cuda")
+    w = torch.empty((5, 0), dtype=torch.int8, device="cuda")
+    bias = torch.randn(5, device="cuda")
+    y = fq.int8_gemm(a, torch.ones(3, device="cuda"), w, torch.ones(5, device="cuda"), bias, out_dtype=torch.float32)
+    assert torch.equal(y, bias.expand(3, 5))
+    big = fq.int8_gemm(torch.empty((300, 0), dtype=torch.int8, device="cuda"), torch.ones(300, device="cuda"), w,
+                       torch.ones(5, device="cuda"), out_dtype=torch.float32)
+    assert (big == 0).all() and big.shape == (300, 5)
+    assert fq.int8_gemm(torch.empty((0, 16), dtype=torch.int8, device="cuda"), torch.ones(0, device="cuda"),
+                        torch.ones((5, 16), dtype=torch.int8, device="cuda"), torch.ones(5, device="cuda")).shape == (0, 5)
+
+
+def quant_ref(x):
+    x = x.float().cpu().numpy()
+    top = np.abs(x).max(-1, initial=0)
+    s = top * (np.float32(1) / np.float32(127))
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.where(s[..., None] > 0, np.rint(x / s[..., None]), 0)
+    return np.clip(q, -127, 127).astype(np.int8), s
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (5, 48), (3, 512), (7, 528), (4, 2048), (9, 2064), (2, 7168), (3, 8192),
+                                 (2, 8208), (3, 32768), (2, 32784), (2, 70000)])
+def test_quant(M, K):
+    g = rng(M + K)
+    x = (torch.randn((M, K), generator=g, device="cuda") * torch.logspace(-3, 3, M, device="cuda")[:, None]).bfloat16()
+    x[0, : K // 2] = 0
+    q, s = fq.int8_quant(x)
+    rq, rs = quant_ref(x)
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
+def test_quant_every_pair():
+    """Every (x, amax) pair of bf16 significands at every distance of exponents that can give a
+    code other than 0 (x down to amax / 512), with both signs, and amax from the smallest
+    subnormal to the largest number: the scale and the quotient round as the format says."""
+    frac = torch.arange(128, dtype=torch.int32)
+    rows = []
+    for top_exp in (0, 1, 2, 3, 7, 8, 9, 64, 120, 127, 128, 134, 200, 254):
+        for f in range(128):
+            top = (top_exp << 7) | f
+            if top == 0:
+                continue
+            body = [(max(top_exp - d, 0) << 7) | frac for d in range(10)]
+            body = torch.cat(body)
+            body = torch.where(body <= top, body, 0)
+            rows.append(torch.cat([torch.tensor([top], dtype=torch.int32), body, body | 0x8000,
+                                   torch.zeros(15, dtype=torch.int32)]))
+    bits = torch.stack(rows)
+    bits = torch.where(bits >= 0x8000, bits - 0x10000, bits).to(torch.int16)
+    x = bits.view(torch.bfloat16).cuda()
+    q, s = fq.int8_quant(x)
+    rq, rs = quant_ref(x)
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
+def test_quant_zero_rows_and_empty():
+    x = torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda")
+    x[1, 5] = -2.0
+    q, s = fq.int8_quant(x)
+    assert (s[[0, 2]] == 0).all() and (q[[0, 2]] == 0).all() and q[1, 5] == -127 and int(q[1].abs().sum()) == 127
+    q, s = fq.int8_quant(torch.empty((4, 0), dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (4, 0) and (s == 0).all()
+    q, s = fq.int8_quant(torch.empty((0, 32), dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (0, 32) and s.shape == (0,)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,N", [((1, 256), 96), ((2, 3, 1536), 200), ((300, 512), 576)])
+def test_linear(shape, N, out):
+    """Quantisation and product against the 64-bit product of what the codes stand for."""
+    g = rng(N)
+    x = torch.randn(shape, generator=g, device="cuda").bfloat16()
+    wq, ws = fq.int8_quant((torch.randn((N, shape[-1]), generator=g, device="cuda") * 0.02).bfloat16())
+    bias = torch.randn(N, generator=g, device="cuda")
+    y = fq.int8_linear(x, wq, ws, bias, out_dtype=DT[out])
+    assert y.shape == (*shape[:-1], N)
+    rq, rs = quant_ref(x.view(-1, shape[-1]))
+    check(y.view(-1, N), torch.from_numpy(rq).cuda(), torch.from_numpy(rs).cuda(), wq, ws, bias, out)
+
+
+def grouped_check(y, a, sa, w, sw, offsets, rows, out):
+    bounds = offsets.tolist()
+    for e in range(w.shape[0]):
+        lo, hi = bounds[e], bounds[e + 1]
+        if hi > lo:
+            t = torch.arange(lo, hi, device="cuda") if rows is None else rows[lo:hi].long()
+            there = (t >= 0) & (t < a.shape[0])
+            aa = torch.where(there[:, None], a[t.clamp(0, a.shape[0] - 1)], 0)
+            ss = torch.where(there, sa[t.clamp(0, a.shape[0] - 1)], 0.0)
+            check(y[lo:hi], aa, ss, w[e], sw[e], None, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([0, 1, 127, 128, 129, 0, 300, 5], 256, 256), ([37, 0, 0, 200], 200, 400), ([3, 250, 1], 1100, 144),
+    ([0, 0, 64], 64, 1024), ([1, 0, 2, 0, 0, 3, 16, 17, 0, 4], 100, 1040), ([0] * 63 + [1] + [0] * 10 + [2], 33, 48),
+    ([1], 7, 16), ([0, 0], 16, 64), ([20] * 70, 48, 128), ([40, 0, 33, 64, 65], 500, 656),
+])
+def test_grouped(sizes, N, K, gather, out):
+    E, R = len(sizes), sum(sizes)
+    g = rng(E + R + N)
+    tokens = max(1, R // 3) if gather else R
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int64, device="cuda")
+    rows = torch.randint(0, tokens, (R,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    a, sa = codes(g, tokens, K), scales(g, tokens)
+    w, sw = codes(g, E, N, K), scales(g, E, N)
+    y = fq.int8_grouped_gemm(a, sa, w, sw, offsets, rows=rows, out_dtype=DT[out])
+    assert y.shape == (R, N) and y.dtype == DT[out]
+    grouped_check(y, a, sa, w, sw, offsets, rows, out)
+
+
+@pytest.mark.parametrize("sizes", [[2, 0, 3], [150, 30, 0, 90]])
+def test_grouped_rows_no_expert_owns(sizes):
+    """Rows past the last offset are not written; rows of no token (-1, past the end) are rows
+    of zeros; offsets that point outside are clamped."""
+    E, R, N, K = len(sizes), sum(sizes) + 9, 64, 160
+    g = rng(R)
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int64, device="cuda")
+    a, sa, w, sw = codes(g, 11, K), scales(g, 11), codes(g, E, N, K), scales(g, E, N)
+    rows = torch.randint(0, 11, (R,), generator=g, device="cuda", dtype=torch.int32)
+    rows[1], rows[3] = -1, 11
+    out = torch.full((R, N), 7.0, device="cuda")
+    fq.int8_grouped_gemm(a, sa, w, sw, offsets, rows=rows, out_dtype=torch.float32, out=out)
+    grouped_check(out, a, sa, w, sw, offsets, rows, "f32")
+    assert (out[1] == 0).all() and (out[3] == 0).all() and (out[-9:] == 7).all()
+    wild = offsets.clone()
+    wild[-1] = 1 << 40
+    wild[0] = -5
+    out2 = fq.int8_grouped_gemm(a, sa, w, sw, wild, rows=rows, out_dtype=torch.float32)
+    assert torch.equal(out2[:-9], out[:-9])
+
+
+def test_grouped_with_placement():
+    """moe_place's offsets and rows as the product takes them, against each token's own product."""
+    T, k, E, N, K = 70, 4, 16, 96, 256
+    g = rng(2)
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    wq, ws = fq.int8_quant(torch.randn((E, N, K), generator=g, device="cuda").bfloat16())
+    _, experts = fq.moe_route(torch.randn((T, E), generator=g, device="cuda"), k)
+    offsets, rows, slots = fq.moe_place(experts, E)
+    q, s = fq.int8_quant(x)
+    y = fq.int8_grouped_gemm(q, s, wq, ws, offsets, rows=rows, out_dtype=torch.float32)
+    for t in (0, 33, T - 1):
+        for j in range(k):
+            e = int(experts[t, j])
+            check(y[slots[t, j]][None], q[t:t + 1], s[t:t + 1], wq[e], ws[e], None, "f32")
+
+
+def test_other_stream_and_repeats():
+    g = rng(3)
+    a, w, sa, sw = codes(g, 200, 512), codes(g, 300, 512), scales(g, 200), scales(g, 300)
+    y = fq.int8_gemm(a, sa, w, sw)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        z = [fq.int8_gemm(a, sa, w, sw) for _ in range(3)]
+    st.synchronize()
+    assert all(torch.equal(y, v) for v in z)
+
+
+def test_captured_in_a_graph():
+    """A whole routed layer's calls captured once and replayed on new inputs, with eager work
+    between the replays: every replay gives the eager result."""
+    T, k, E, N, K = 24, 3, 8, 80, 128
+    g = rng(4)
+    wq, ws = fq.int8_quant(torch.randn((E, N, K), generator=g, device="cuda").bfloat16())
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    logits = torch.randn((T, E), generator=g, device="cuda")
+
+    def layer():
+        weights, experts = fq.moe_route(logits, k)
+        offsets, rows, slots = fq.moe_place(experts, E)
+        q, s = fq.int8_quant(x)
+        return fq.moe_combine(fq.int8_grouped_gemm(q, s, wq, ws, offsets, rows=rows), slots, weights)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer()
+    for _ in range(4):
+        x.copy_(torch.randn((T, K), generator=g, device="cuda"))
+        logits.copy_(torch.randn((T, E), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, layer())
+
+
+def test_refusals():
+    a = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
+    w = torch.zeros((8, 32), dtype=torch.int8, device="cuda")
+    sa, sw = torch.ones(4, device="cuda"), torch.ones(8, device="cuda")
+    with pytest.raises(TypeError):
+        fq.int8_gemm(a.float(), sa, w, sw)
+    with pytest.raises(TypeError):
+        fq.int8_gemm(a, sa, w, sw, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a[:, :16].contiguous(), sa, w, sw)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a[:, :24].contiguous(), sa, w[:, :24].contiguous(), sw)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a, sa[:3], w, sw)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a, sa, w.t().contiguous().t(), sw)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a, sa, w, sw, bias=torch.ones(7, device="cuda"))
+    with pytest.raises(ValueError):
+        fq.int8_gemm(a, sa, w.cpu(), sw)
+    with pytest.raises(ValueError):
+        fq.int8_gemm(torch.zeros(4 * 32 + 1, dtype=torch.int8, device="cuda")[1:].view(4, 32), sa, w, sw)
+    with pytest.raises(TypeError):
+        fq.int8_quant(torch.zeros((2, 16), device="cuda"))
+    with pytest.raises(ValueError):
+        fq.int8_quant(torch.zeros((2, 24), dtype=torch.bfloat16, device="cuda"))
+    off = torch.tensor([0, 4], device="cuda")
+    w3 = w[None]
+    with pytest.raises(TypeError):
+        fq.int8_grouped_gemm(a, sa, w3, sw[None], off.int())
+    with pytest.raises(ValueError):
+        fq.int8_grouped_gemm(a, sa, w3, sw[None], off[:1])
+    with pytest.raises(ValueError):
+        fq.int8_grouped_gemm(a, sa, w, sw, off)
+    with pytest.raises(TypeError):
+        fq.int8_grouped_gemm(a, sa, w3, sw[None], off, rows=torch.zeros(4, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        fq.int8_grouped_gemm(a, sa, w3, sw[None], off, rows=torch.zeros((2, 2), dtype=torch.int32, device="cuda"))
