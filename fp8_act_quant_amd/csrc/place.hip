@@ -79,42 +79,56 @@ __device__ __forceinline__ uint32_t prefix(uint32_t v, uint32_t *scratch, uint32
 
 __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
     __shared__ uint32_t hist[PW][kMaxExperts];
+    __shared__ uint32_t total[kMaxExperts], before[kMaxExperts];   // several chunks: of all, of the earlier ones
     __shared__ uint32_t scratch[PW];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.E; e += PT)
+    for (int e = threadIdx.x; e < a.E; e += PT) {
 #pragma unroll
         for (int w = 0; w < PW; ++w) hist[w][e] = 0;
+        total[e] = before[e] = 0;
+    }
     __syncthreads();
     const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg, p1 = min(p0 + a.seg, a.pairs);
     count_segment(a, p0, p1, hist[wave], lane);
+    if (a.chunks > 1) {
+        // the whole table [chunks][E], 8 loads in flight; sums of integers, whose order does
+        // not matter
+        const int n = a.chunks * a.E, own = blockIdx.x * a.E;
+        for (int i0 = threadIdx.x; i0 < n; i0 += 8 * PT) {
+            uint32_t c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) c[u] = i0 + u * PT < n ? a.counts[i0 + u * PT] : 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = i0 + u * PT;
+                if (c[u]) {
+                    const int e = (int)((uint32_t)i % (uint32_t)a.E);
+                    atomicAdd(&total[e], c[u]);
+                    if (i < own) atomicAdd(&before[e], c[u]);
+                }
+            }
+        }
+    }
     __syncthreads();
 
     // each thread owns the experts 2 i and 2 i + 1
     constexpr int PER = kMaxExperts / PT;
-    uint32_t total[PER], before[PER], sum = 0;
+    uint32_t mine[PER], sum = 0;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
         const int e = threadIdx.x * PER + u;
-        total[u] = before[u] = 0;
+        mine[u] = 0;
         if (e < a.E) {
-            uint32_t own = 0;
+            uint32_t here = 0;
 #pragma unroll
             for (int w = 0; w < PW; ++w) {
                 const uint32_t c = hist[w][e];
-                hist[w][e] = own;
-                own += c;
+                hist[w][e] = here;
+                here += c;
             }
-            if (a.chunks == 1) {
-                total[u] = own;
-            } else {
-                for (int c = 0; c < a.chunks; ++c) {
-                    const uint32_t n = a.counts[(int64_t)c * a.E + e];
-                    before[u] += c < (int)blockIdx.x ? n : 0u;
-                    total[u] += n;
-                }
-            }
+            mine[u] = a.chunks == 1 ? here : total[e];
         }
-        sum += total[u];
+        sum += mine[u];
     }
     uint32_t all;
     uint32_t at = prefix(sum, scratch, &all);
@@ -122,11 +136,12 @@ __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
     for (int u = 0; u < PER; ++u) {
         const int e = threadIdx.x * PER + u;
         if (e < a.E) {
+            const uint32_t first = at + before[e];
 #pragma unroll
-            for (int w = 0; w < PW; ++w) hist[w][e] += at + before[u];
+            for (int w = 0; w < PW; ++w) hist[w][e] += first;
             if (blockIdx.x == 0) a.offsets[e] = at;
         }
-        at += total[u];
+        at += mine[u];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
     // rows that no pair fills
@@ -141,19 +156,21 @@ __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
         const bool in = i < p1;
         const int e = in ? a.experts[i] - a.first : -1;
         const bool there = (uint32_t)e < (uint32_t)a.E;
-        uint64_t same = __ballot(there);   // the lanes with this lane's expert
+        const uint64_t placed = __ballot(there);
+        uint32_t lo = (uint32_t)placed, hi = (uint32_t)(placed >> 32);   // the lanes with this lane's expert
         for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((e >> b) & 1);
-            same &= (e >> b) & 1 ? set : ~set;
+            const uint32_t bit = (uint32_t)__builtin_amdgcn_sbfe(e, b, 1);   // 0 or all ones
+            const uint64_t set = __ballot(bit != 0);
+            lo &= ~((uint32_t)set ^ bit);
+            hi &= ~((uint32_t)(set >> 32) ^ bit);
         }
         if (there) {
-            const int earlier = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
-                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
-            const uint32_t r = next[e] + earlier;
+            const uint32_t r = next[e] + __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
             a.slots[i] = (int32_t)r;
             a.rows[r] = (int32_t)((uint32_t)i / (uint32_t)a.k);
             // (LDS accesses of a wave run in order; the fence keeps the compiler's order)
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const uint64_t same = ((uint64_t)hi << 32) | lo;
             if ((same >> lane) == 1ull) next[e] = r + 1;   // the last of these lanes
         } else if (in) {
             a.slots[i] = -1;

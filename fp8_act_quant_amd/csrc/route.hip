@@ -46,33 +46,57 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xF, false);
-}
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
-// maximum over the wave's 64 lanes, the same in every lane
+// v of another lane of the same 16 (all of whose lanes are active)
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+
+// maximum over the wave's 64 lanes
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = umax(v, dpp<0xB1>(v));            // quad_perm [1,0,3,2]
-    v = umax(v, dpp<0x4E>(v));            // quad_perm [2,3,0,1]
-    v = umax(v, dpp<0x141>(v));           // row_half_mirror
-    v = umax(v, dpp<0x140>(v));           // row_mirror: every lane has its row's maximum
-    v = umax(v, dpp<0x142, 0xA>(v));      // row_bcast15 into rows 1 and 3
-    v = umax(v, dpp<0x143, 0xC>(v));      // row_bcast31 into rows 2 and 3
+    v = umax(v, dpp<kXor1>(v));
+    v = umax(v, dpp<kXor2>(v));
+    v = umax(v, dpp<kMirror8>(v));
+    v = umax(v, dpp<kMirror16>(v));   // every lane has its 16 lanes' maximum
+    v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast15
+    v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // row_bcast31
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// sum over the wave's 64 lanes, the same in every lane and of a fixed order
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-    return v;
+// sums over the wave's 64 lanes, in a fixed order and the same in every lane
+__device__ __forceinline__ float read_f(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-    return v;
+    v += dpp_f<kXor1>(v);
+    v += dpp_f<kXor2>(v);
+    v += dpp_f<kMirror8>(v);
+    v += dpp_f<kMirror16>(v);
+    return (read_f(v, 0) + read_f(v, 16)) + (read_f(v, 32) + read_f(v, 48));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)u) | (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32);
+}
+__device__ __forceinline__ double read_d(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v += dpp_d<kXor1>(v);
+    v += dpp_d<kXor2>(v);
+    v += dpp_d<kMirror8>(v);
+    v += dpp_d<kMirror16>(v);
+    return (read_d(v, 0) + read_d(v, 16)) + (read_d(v, 32) + read_d(v, 48));
 }
 
 template <int BF16>
@@ -81,65 +105,140 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
     else return reinterpret_cast<const float *>(p)[i];
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// V consecutive logits from row + first, n of which belong to this lane; -inf for the others.
+// FULL: n is V or at most 0 and rows are aligned to V elements, so they come in one load.
+// Every lane loads (from a place within the row if it has nothing to load), without a branch.
+template <int V, int BF16, int FULL>
+__device__ __forceinline__ void load_logits(const void *p, int64_t row, int first, int n, int E, float (&x)[V]) {
+    if constexpr (FULL) {
+        const int64_t i = row + (n > 0 ? first : 0);
+        if constexpr (BF16) {
+            typedef uint16_t piece __attribute__((ext_vector_type(V)));
+            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const uint16_t *>(p) + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = __uint_as_float((uint32_t)u[j] << 16);
+        } else {
+            typedef float piece __attribute__((ext_vector_type(V)));
+            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const float *>(p) + i);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = u[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = load_logit<BF16>(p, row + min(first + j, E - 1));
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j < n ? x[j] : -__builtin_inff();
+}
+
+// 1 / (1 + exp(-x)) with every step rounded to nearest. The quotient is v_rcp_f32 and one
+// Newton step, which gives the correctly rounded reciprocal of every float in [1, 2^126)
+// (checked for all of them), in 3 operations instead of a division's 10; past that (x < -87)
+// the division itself is taken.
+template <int V>
+__device__ __forceinline__ void sigmoid(const float (&x)[V], float (&s)[V]) {
+    float d[V];
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        d[i] = 1.0f + expf(-x[i]);
+        const float y = __builtin_amdgcn_rcpf(d[i]);
+        s[i] = __builtin_fmaf(__builtin_fmaf(-d[i], y, 1.0f), y, y);
+        far |= !(d[i] < 0x1p126f);
+    }
+    if (__any(far)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = d[i] < 0x1p126f ? s[i] : 1.0f / d[i];
+    }
+}
 
 // softmax's maximum and denominator from each lane's values (-inf where there is none);
-// total = 0 when no value is above -inf, and every score is then 0
+// total = 0 when no value is above -inf, and every score is then 0. e: the numerators.
 template <int V>
-__device__ __forceinline__ void softmax_of(const float (&x)[V], float &top, float &total) {
+__device__ __forceinline__ void softmax_of(const float (&x)[V], float (&e)[V], float &top, float &total) {
     uint32_t m = key_of(x[0]);
 #pragma unroll
     for (int i = 1; i < V; ++i) m = umax(m, key_of(x[i]));
     top = of_key(wave_max(m));
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += (double)expf(x[i] - top);
+    for (int i = 0; i < V; ++i) {
+        e[i] = expf(x[i] - top);
+        sum += (double)e[i];
+    }
     total = top == -__builtin_inff() ? 0.0f : (float)wave_sum(sum);
+}
+
+// The scores of a lane's logits; top and total are softmax's.
+template <int V, int SOFTMAX>
+__device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], float &top, float &total) {
+    if constexpr (SOFTMAX) {
+        softmax_of<V>(x, s, top, total);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = total > 0.0f ? s[i] / total : 0.0f;
+    } else {
+        sigmoid<V>(x, s);
+    }
+}
+
+// One logit's score, given them
+template <int SOFTMAX>
+__device__ __forceinline__ float score_of(float x, float top, float total) {
+    if constexpr (SOFTMAX) {
+        return total > 0.0f ? expf(x - top) / total : 0.0f;
+    } else {
+        const float in[1] = {x};
+        float out[1];
+        sigmoid<1>(in, out);
+        return out[0];
+    }
+}
+
+// The two largest keys of the group's lanes, from each lane's two
+__device__ __forceinline__ void merge2(uint32_t &m1, uint32_t &m2, uint32_t o1, uint32_t o2) {
+    m2 = umax(umax(m2, o2), umin(m1, o1));
+    m1 = umax(m1, o1);
 }
 
 // One wave per token. Lane l belongs to group l >> lane_shift and holds V consecutive experts
 // of it, so lane order is expert order, and a reduction over a group is one over a power of
-// two of adjacent lanes.
-template <int V, int BF16, int SOFTMAX>
+// two of adjacent lanes. Each lane sorts its keys (V <= 8; equal ones keep their order), so a
+// selected expert is always some lane's first: a maximum over the first ones, then that lane
+// moves up. About 20 operations per selected expert; with more experts a lane the sorting
+// would cost more than it saves, and each step looks at all of them. Bound by these operations
+// (some 400 a token), not by the 4 E bytes it reads.
+template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
     if (t >= a.T) return;
     const int lanes = 1 << a.lane_shift;
     const int group = lane >> a.lane_shift;
-    const int at = (lane & (lanes - 1)) * V;                     // first expert within the group
-    const int n = group < a.groups ? min(a.per - at, V) : 0;     // (may be negative: none)
+    const int at = (lane & (lanes - 1)) * V;                          // first expert within the group
+    const int n = group < a.groups ? max(min(a.per - at, V), 0) : 0;  // experts of this lane
     const int e0 = group * a.per + at;
     const int64_t row = t * a.E;
 
-    float x[V];
+    float x[V], s[V], top = 0.0f, total = 1.0f;
+    load_logits<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
+    float bias[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = i < n ? load_logit<BF16>(a.logits, row + e0 + i) : -__builtin_inff();
-    float top = 0.0f, total = 1.0f;
-    if constexpr (SOFTMAX) softmax_of<V>(x, top, total);
-    auto score = [&](float v) {
-        if constexpr (SOFTMAX) return total > 0.0f ? expf(v - top) / total : 0.0f;
-        else return sigmoid(v);
-    };
+    for (int i = 0; i < V; ++i) bias[i] = 0.0f;
+    if (a.bias) load_logits<V, 0, 0>(a.bias, 0, e0, n, a.E, bias);
+    scores<V, SOFTMAX>(x, s, top, total);
     uint32_t key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        key[i] = 0;
-        if (i < n) key[i] = key_of(score(x[i]) + (a.bias ? a.bias[e0 + i] : 0.0f));
-    }
+    for (int i = 0; i < V; ++i) key[i] = i < n ? key_of(s[i] + bias[i]) : 0u;
 
     if (a.groups > 1) {
-        uint32_t m1 = 0, m2 = 0;   // the two largest keys of the group
+        uint32_t m1 = key[0], m2 = 0;   // the two largest keys of the group
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            m2 = umax(m2, m1 < key[i] ? m1 : key[i]);
-            m1 = umax(m1, key[i]);
-        }
-        for (int d = 1; d < lanes; d <<= 1) {
-            const uint32_t o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
-            m2 = umax(umax(m2, o2), m1 < o1 ? m1 : o1);
-            m1 = umax(m1, o1);
-        }
+        for (int i = 1; i < V; ++i) merge2(m1, m2, key[i], 0);
+        if (lanes > 1) merge2(m1, m2, dpp<kXor1>(m1), dpp<kXor1>(m2));
+        if (lanes > 2) merge2(m1, m2, dpp<kXor2>(m1), dpp<kXor2>(m2));
+        if (lanes > 4) merge2(m1, m2, dpp<kMirror8>(m1), dpp<kMirror8>(m2));
+        if (lanes > 8) merge2(m1, m2, dpp<kMirror16>(m1), dpp<kMirror16>(m2));
+        if (lanes > 16) merge2(m1, m2, __shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));
         uint32_t value = m1;
         if (a.group_top2 && m2) value = key_of(of_key(m1) + of_key(m2));
         bool kept = false;
@@ -152,32 +251,66 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0;
+        for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
     }
 
     int mine = 0;   // lane j: the token's j-th expert
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t m = key[0];
+    if constexpr (V <= 8) {
+        uint64_t pos = 0;   // the sorted keys' places, 8 bits each
+        int p[V];
 #pragma unroll
-        for (int i = 1; i < V; ++i) m = umax(m, key[i]);
-        const uint32_t best = wave_max(m);
-        const int owner = __builtin_ctzll(__ballot(m == best));
-        int pos = 0;
+        for (int i = 0; i < V; ++i) p[i] = i;
+        // exchanges of neighbours only, and only of unequal ones: equal keys keep their order
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i) pos = key[i] == best ? i : pos;
-        const bool own = lane == owner;
+        for (int r = 0; r < V; ++r) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = own && i == pos ? 0u : key[i];
-        const int e = __builtin_amdgcn_readlane(e0 + pos, owner);
-        mine = lane == j ? e : mine;
+            for (int i = r & 1; i + 1 < V; i += 2) {
+                const uint32_t ki = key[i], kj = key[i + 1];
+                const int pi = p[i], pj = p[i + 1];
+                const bool up = ki < kj;
+                key[i] = umax(ki, kj), key[i + 1] = umin(ki, kj);
+                p[i] = up ? pj : pi, p[i + 1] = up ? pi : pj;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) pos |= (uint64_t)p[i] << (8 * i);
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t best = wave_max(key[0]);
+            const int owner = __builtin_ctzll(__ballot(key[0] == best));
+            const int e = __builtin_amdgcn_readlane(e0 + (int)(pos & 0xFF), owner);
+            mine = lane == j ? e : mine;
+            const bool own = lane == owner;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t here = key[i], next = i + 1 < V ? key[i + 1] : 0u;
+                key[i] = own ? next : here;
+            }
+            if constexpr (V <= 4) pos = own ? (uint32_t)pos >> 8 : (uint32_t)pos;
+            else pos = own ? pos >> 8 : pos;
+        }
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t m = key[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) m = umax(m, key[i]);
+            const uint32_t best = wave_max(m);
+            const int owner = __builtin_ctzll(__ballot(m == best));
+            int pos = 0;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i) pos = key[i] == best ? i : pos;
+            const bool own = lane == owner;
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = own && i == pos ? 0u : key[i];
+            const int e = __builtin_amdgcn_readlane(e0 + pos, owner);
+            mine = lane == j ? e : mine;
+        }
     }
 
-    float s = 0.0f;
-    if (lane < a.k) s = score(load_logit<BF16>(a.logits, row + mine));
-    float w = s;
+    const float xe = load_logit<BF16>(a.logits, row + mine);
+    float w = lane < a.k ? score_of<SOFTMAX>(xe, top, total) : 0.0f;
     if (a.renormalize) {
-        const float sum = wave_sum(s);
-        w = sum != 0.0f ? s / sum : 0.0f;   // (a token none of whose experts has a score has weights 0)
+        const float sum = wave_sum(w);
+        w = sum != 0.0f ? w / sum : 0.0f;   // (a token none of whose experts has a score has weights 0)
     }
     if (lane < a.k) {
         a.weights[t * a.k + lane] = w * a.scale;
@@ -202,76 +335,125 @@ struct RouteGradArgs {
 //     sigmoid: dx_j = ds_j s_j (1 - s_j), 0 for the experts that were not selected
 //     softmax: dx_i = s_i (ds_i - sum_j ds_j s_j), ds_i = 0 for those
 // The row of ds goes through LDS, from the k selected experts' lanes to the experts' lanes.
-template <int V, int BF16, int SOFTMAX>
+template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a) {
-    __shared__ float rows[kWaves][64 * V];
+    typedef float piece __attribute__((ext_vector_type(V)));
+    __shared__ piece rows[kWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= a.T) return;
-    float *ds_row = rows[wave];
-    const int e0 = lane * V, n = min(a.E - e0, V);
+    const int e0 = lane * V, n = max(min(a.E - e0, V), 0);
     const int64_t row = t * a.E;
-
-    float x[V], top = 0.0f, total = 1.0f;
-    if constexpr (SOFTMAX) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = i < n ? load_logit<BF16>(a.logits, row + e0 + i) : -__builtin_inff();
-        softmax_of<V>(x, top, total);
-    }
-    auto score = [&](float v) {
-        if constexpr (SOFTMAX) return total > 0.0f ? expf(v - top) / total : 0.0f;
-        else return sigmoid(v);
-    };
-#pragma unroll
-    for (int i = 0; i < V; ++i) ds_row[i * 64 + lane] = 0.0f;
 
     const int e = lane < a.k ? a.experts[t * a.k + lane] : -1;
     const bool there = e >= 0 && e < a.E;
-    const float xe = there ? load_logit<BF16>(a.logits, row + e) : 0.0f;
-    const float s = there ? score(xe) : 0.0f;
-    float d = there ? a.dweights[t * a.k + lane] * a.scale : 0.0f;
+    const float dw = there ? a.dweights[t * a.k + lane] : 0.0f;
+    const float xe = load_logit<BF16>(a.logits, row + (there ? e : 0));
+    float x[V], p[V], top = 0.0f, total = 1.0f;
+    if constexpr (SOFTMAX) {
+        load_logits<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
+        scores<V, 1>(x, p, top, total);
+    }
+    piece zero;
+#pragma unroll
+    for (int i = 0; i < V; ++i) zero[i] = 0.0f;
+    rows[wave][lane] = zero;
+
+    const float s = there ? score_of<SOFTMAX>(xe, top, total) : 0.0f;
+    float d = dw * a.scale;
     if (a.renormalize) {
         const float sum = wave_sum(s), dot = wave_sum(d * s);
         d = there && sum != 0.0f ? (d - dot / sum) / sum : 0.0f;
     }
     const float all = SOFTMAX ? wave_sum(d * s) : 0.0f;
     if constexpr (!SOFTMAX) d *= s * (1.0f - s);
+    // (LDS accesses of a wave run in order; the fences keep the compiler's order)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (there) ds_row[e] = d;
+    if (there) reinterpret_cast<float *>(rows[wave])[e] = d;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
+    piece g = rows[wave][lane];
+    if constexpr (SOFTMAX) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i < n) {
-            float v = ds_row[e0 + i];
-            if constexpr (SOFTMAX) v = score(x[i]) * (v - all);
-            if constexpr (BF16) reinterpret_cast<uint16_t *>(a.dlogits)[row + e0 + i] = (uint16_t)pack_bf16x2(v, 0.0f);
-            else reinterpret_cast<float *>(a.dlogits)[row + e0 + i] = v;
+        for (int i = 0; i < V; ++i) g[i] = p[i] * (g[i] - all);
+    }
+    if constexpr (BF16) {
+        typedef uint16_t half_piece __attribute__((ext_vector_type(V)));
+        half_piece h;
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = (uint16_t)pack_bf16x2(g[i], 0.0f);
+        uint16_t *dst = reinterpret_cast<uint16_t *>(a.dlogits) + row + e0;
+        if constexpr (FULL) {
+            if (n > 0) *reinterpret_cast<half_piece *>(dst) = h;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) dst[i] = h[i];
+        }
+    } else {
+        float *dst = reinterpret_cast<float *>(a.dlogits) + row + e0;
+        if constexpr (FULL) {
+            if (n > 0) *reinterpret_cast<piece *>(dst) = g;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) dst[i] = g[i];
         }
     }
 }
 
+template <int V, int BF16, int SOFTMAX>
+void route_f(const RouteArgs &a, bool full, dim3 grid, hipStream_t st) {
+    const dim3 block(64 * kWaves);
+    if constexpr (V > 1) {
+        if (full) {
+            route_kernel<V, BF16, SOFTMAX, 1><<<grid, block, 0, st>>>(a);
+            return;
+        }
+    }
+    route_kernel<V, BF16, SOFTMAX, 0><<<grid, block, 0, st>>>(a);
+}
+
+template <int V, int BF16, int SOFTMAX>
+void route_grad_f(const RouteGradArgs &a, bool full, dim3 grid, hipStream_t st) {
+    const dim3 block(64 * kWaves);
+    if constexpr (V > 1) {
+        if (full) {
+            route_grad_kernel<V, BF16, SOFTMAX, 1><<<grid, block, 0, st>>>(a);
+            return;
+        }
+    }
+    route_grad_kernel<V, BF16, SOFTMAX, 0><<<grid, block, 0, st>>>(a);
+}
+
+// Whether every lane's V elements of a row come in one access: rows and groups are whole
+// numbers of V elements, and the buffers aligned to them (16 bytes at most are needed).
+bool whole(int V, int per, bool bf16, const void *p, const void *q) {
+    const uintptr_t bytes = (uintptr_t)V * (bf16 ? 2 : 4), mask = (bytes < 16 ? bytes : 16) - 1;
+    return per % V == 0 && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & mask) == 0;
+}
+
 template <int V>
 void route_v(const RouteArgs &a, bool bf16, bool softmax, dim3 grid, hipStream_t st) {
-    const dim3 block(64 * kWaves);
+    const bool full = whole(V, a.per, bf16, a.logits, nullptr);
     if (bf16) {
-        if (softmax) route_kernel<V, 1, 1><<<grid, block, 0, st>>>(a);
-        else route_kernel<V, 1, 0><<<grid, block, 0, st>>>(a);
+        if (softmax) route_f<V, 1, 1>(a, full, grid, st);
+        else route_f<V, 1, 0>(a, full, grid, st);
     } else {
-        if (softmax) route_kernel<V, 0, 1><<<grid, block, 0, st>>>(a);
-        else route_kernel<V, 0, 0><<<grid, block, 0, st>>>(a);
+        if (softmax) route_f<V, 0, 1>(a, full, grid, st);
+        else route_f<V, 0, 0>(a, full, grid, st);
     }
 }
 
 template <int V>
 void route_grad_v(const RouteGradArgs &a, bool bf16, bool softmax, dim3 grid, hipStream_t st) {
-    const dim3 block(64 * kWaves);
+    const bool full = whole(V, a.E, bf16, a.logits, a.dlogits);
     if (bf16) {
-        if (softmax) route_grad_kernel<V, 1, 1><<<grid, block, 0, st>>>(a);
-        else route_grad_kernel<V, 1, 0><<<grid, block, 0, st>>>(a);
+        if (softmax) route_grad_f<V, 1, 1>(a, full, grid, st);
+        else route_grad_f<V, 1, 0>(a, full, grid, st);
     } else {
-        if (softmax) route_grad_kernel<V, 0, 1><<<grid, block, 0, st>>>(a);
-        else route_grad_kernel<V, 0, 0><<<grid, block, 0, st>>>(a);
+        if (softmax) route_grad_f<V, 0, 1>(a, full, grid, st);
+        else route_grad_f<V, 0, 0>(a, full, grid, st);
     }
 }
 

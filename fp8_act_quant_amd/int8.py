@@ -23,12 +23,12 @@ def _depth(K: int) -> None:
         raise ValueError(f"the last dimension must be a multiple of {STEP} below {MAX_K}")
 
 
-def _out(out, shape, out_dtype, device) -> torch.Tensor:
+def _out(out, shape, out_dtype, a) -> torch.Tensor:
     if out_dtype not in CODE:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     if out is None:
-        return torch.empty(shape, dtype=out_dtype, device=device)
-    need(out, "out", out_dtype, shape, device=device)
+        return a.new_empty(shape, dtype=out_dtype)
+    need(out, "out", out_dtype, shape, device=a.device)
     return out
 
 
@@ -40,10 +40,10 @@ def int8_quant(x: torch.Tensor):
     need(x, "x", torch.bfloat16, align=16)
     if x.dim() < 1 or x.shape[-1] % STEP:
         raise ValueError(f"the last dimension must be a multiple of {STEP}")
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    q = torch.empty_like(x, dtype=torch.int8)
     K = x.shape[-1]
     # (rows of no elements have the scale of a zero row)
-    s = (torch.empty if K else torch.zeros)(x.shape[:-1], dtype=torch.float32, device=x.device)
+    s = (x.new_empty if K else x.new_zeros)(x.shape[:-1], dtype=torch.float32)
     launch("int8_quant", lib.int8_quant, x, x.data_ptr(), q.data_ptr(), s.data_ptr(), math.prod(x.shape[:-1]), K)
     return q, s
 
@@ -66,7 +66,7 @@ def int8_gemm(a: torch.Tensor, a_s: torch.Tensor, w: torch.Tensor, w_s: torch.Te
     if bias is not None:
         need(bias, "bias", torch.float32, (N,), device=a.device)
         b_ptr = bias.data_ptr()
-    out = _out(out, (*a.shape[:-1], N), out_dtype, a.device)
+    out = _out(out, (*a.shape[:-1], N), out_dtype, a)
     launch("int8_gemm", lib.int8_gemm, a, a.data_ptr(), a_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), b_ptr,
            out.data_ptr(), CODE[out_dtype], math.prod(a.shape[:-1]), N, K)
     return out
@@ -106,7 +106,7 @@ def int8_grouped_gemm(a: torch.Tensor, a_s: torch.Tensor, w: torch.Tensor, w_s: 
         if rows.dim() != 1:
             raise ValueError("rows must be [R]")
         R, r_ptr = rows.shape[0], rows.data_ptr()
-    out = _out(out, (R, N), out_dtype, a.device)
+    out = _out(out, (R, N), out_dtype, a)
     launch("int8_grouped_gemm", lib.int8_grouped_gemm, a, a.data_ptr(), a_s.data_ptr(), w.data_ptr(), w_s.data_ptr(),
            offsets.data_ptr(), r_ptr, out.data_ptr(), CODE[out_dtype], E, R, tokens, N, K)
     return out

@@ -11,9 +11,8 @@ from __future__ import annotations
 import torch
 
 from ._lib import FP8Q_MOE_GROUP_MAX, FP8Q_MOE_KEEP_SCORES, FP8Q_MOE_SOFTMAX, lib
-from ._tensor import CODE, launch, need
+from ._tensor import CODE, launch, need, need_float
 
-_FLOATS = (torch.float32, torch.bfloat16)
 _SCORES = {"sigmoid": 0, "softmax": FP8Q_MOE_SOFTMAX}
 _GROUPS = {"top2": 0, "max": FP8Q_MOE_GROUP_MAX}
 MAX_EXPERTS, MAX_TOP_K, MAX_GROUPS = 1024, 32, 64
@@ -36,7 +35,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "sigmoid", bias:
     largest) take part. Returns ``(weights, experts)``, both [..., top_k]: float32 weights
     (the scores, divided by their sum if renormalize, times scale) and int32 experts, the
     largest choice first, equal ones by index."""
-    need(logits, "logits", _FLOATS, align=logits.element_size() if isinstance(logits, torch.Tensor) else 4)
+    need_float(logits, "logits")
     if logits.dim() < 1:
         raise ValueError("logits must be [..., E]")
     E = logits.shape[-1]
@@ -54,8 +53,8 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "sigmoid", bias:
         need(bias, "bias", torch.float32, (E,), device=logits.device)
         b_ptr = bias.data_ptr()
     shape = (*logits.shape[:-1], top_k)
-    weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    experts = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    weights = logits.new_empty(shape, dtype=torch.float32)
+    experts = torch.empty_like(weights, dtype=torch.int32)
     launch("moe_route", lib.moe_route, logits, logits.data_ptr(), CODE[logits.dtype], b_ptr, weights.data_ptr(),
            experts.data_ptr(), logits.numel() // E, E, top_k, groups, topk_groups, scale,
            flags | _GROUPS[group_score])
@@ -67,7 +66,7 @@ def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: to
     """Gradient of moe_route's weights with respect to the logits (which it has the shape and
     dtype of). dweights [..., k] float32 and experts [..., k] int32 as moe_route returned
     them; score, renormalize and scale as in that call. The selection has no gradient."""
-    need(logits, "logits", _FLOATS, align=logits.element_size() if isinstance(logits, torch.Tensor) else 4)
+    need_float(logits, "logits")
     if logits.dim() < 1 or not 1 <= logits.shape[-1] <= MAX_EXPERTS:
         raise ValueError(f"logits must be [..., E] with 1 to {MAX_EXPERTS} experts")
     need(experts, "experts", torch.int32, device=logits.device)
@@ -96,19 +95,19 @@ def moe_place(experts: torch.Tensor, n_experts: int, *, first: int = 0):
     if not 1 <= n_experts <= MAX_EXPERTS or first < 0:
         raise ValueError(f"n_experts must be 1 to {MAX_EXPERTS} and first not negative")
     T, k = experts.shape
-    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=experts.device)
-    rows = torch.empty(T * k, dtype=torch.int32, device=experts.device)
+    offsets = experts.new_empty(n_experts + 1, dtype=torch.int64)
+    rows = experts.new_empty(T * k)
     slots = torch.empty_like(experts)
     need_bytes = lib.moe_place_workspace_bytes(T, k, n_experts)
     # from torch's allocator, which keeps it from calls on other streams until this one is done
-    ws = torch.empty(need_bytes, dtype=torch.uint8, device=experts.device) if need_bytes else None
+    ws = experts.new_empty(need_bytes, dtype=torch.uint8) if need_bytes else None
     launch("moe_place", lib.moe_place, experts, experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
            slots.data_ptr(), T, k, n_experts, first, ws.data_ptr() if need_bytes else None, need_bytes)
     return offsets, rows, slots
 
 
 def _rows_of(h: torch.Tensor, slots: torch.Tensor) -> None:
-    need(h, "h", _FLOATS, align=h.element_size() if isinstance(h, torch.Tensor) else 4)
+    need_float(h, "h")
     if h.dim() != 2:
         raise ValueError("h must be [rows, H]")
     need(slots, "slots", torch.int32, device=h.device)
@@ -129,9 +128,9 @@ def moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | No
     T, k = slots.shape
     shape = (T, h.shape[1])
     if out is None:
-        out = torch.empty(shape, dtype=h.dtype, device=h.device)
+        out = h.new_empty(shape)
     else:
-        need(out, "out", h.dtype, shape, align=out.element_size(), device=h.device)
+        need_float(out, "out", h.dtype, shape, h.device)
     launch("moe_combine", lib.moe_combine, h, h.data_ptr(), CODE[h.dtype], slots.data_ptr(), w_ptr, out.data_ptr(),
            T, k, h.shape[0], h.shape[1])
     return out
@@ -144,7 +143,7 @@ def moe_combine_backward(dy: torch.Tensor, h: torch.Tensor, slots: torch.Tensor,
     _rows_of(h, slots)
     need(weights, "weights", torch.float32, slots.shape, device=h.device)
     T, k = slots.shape
-    need(dy, "dy", h.dtype, (T, h.shape[1]), align=h.element_size(), device=h.device)
+    need_float(dy, "dy", h.dtype, (T, h.shape[1]), h.device)
     dh, dweights = torch.empty_like(h), torch.empty_like(weights)
     launch("moe_combine_backward", lib.moe_combine_backward, h, dy.data_ptr(), h.data_ptr(), CODE[h.dtype],
            slots.data_ptr(), weights.data_ptr(), dh.data_ptr(), dweights.data_ptr(), T, k, h.shape[0], h.shape[1])
