@@ -165,32 +165,46 @@ __device__ __forceinline__ void expert_rows(const Int8Args &g, int e, int64_t &r
     r1 = r1 < r0 ? r0 : (r1 > g.M ? g.M : r1);
 }
 
-// The expert and the block of `bm` of its rows that row block `unit` (of all experts' blocks,
-// in order) is. Each wave finds it by itself, 64 experts at a time. False: there is no such block.
-// Also gives the number of blocks of that expert before it.
-__device__ __forceinline__ bool find_block(const Int8Args &g, int bm, int unit, int &expert, int64_t &row0,
-                                           int64_t &row1) {
+// Grouped work order. Expert e has n_e = ceil(rows_e / bm) row blocks; its n_e * cols tiles are
+// numbered consecutively, experts in order, the row block varying fastest, so that tiles which
+// read the same weight panel are neighbours and an expert's rows stay in the L2 of the XCD
+// that walks it. count_blocks gives the number of row blocks of all experts, find_block the
+// expert, rows and column of tile `unit`. Each wave works them out by itself, 64 experts at a time.
+__device__ __forceinline__ int blocks_of(const Int8Args &g, int e, int bm) {
+    int64_t r0 = 0, r1 = 0;
+    if (e < g.experts) expert_rows(g, e, r0, r1);
+    return (int)((r1 - r0 + bm - 1) / bm);
+}
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d, 64);
+        v += lane >= d ? o : 0;
+    }
+    return v;
+}
+__device__ __forceinline__ int count_blocks(const Int8Args &g, int bm) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 64) n += blocks_of(g, e0 + lane, bm);
+    return __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
+}
+__device__ __forceinline__ bool find_block(const Int8Args &g, int bm, int cols, int unit, int &expert, int64_t &row0,
+                                           int64_t &row1, int &col) {
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
-        const int e = e0 + lane;
-        int64_t r0 = 0, r1 = 0;
-        if (e < g.experts) expert_rows(g, e, r0, r1);
-        const int n = (int)((r1 - r0 + bm - 1) / bm);
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d, 64);
-            sum += lane >= d ? o : 0;
-        }
-        const int first = before + sum - n;
-        const uint64_t hit = __ballot(unit >= first && unit < first + n);
+        const int n = blocks_of(g, e0 + lane, bm);
+        const int sum = wave_scan(n, lane);
+        const int first = (before + sum - n) * cols;
+        const uint64_t hit = __ballot(unit >= first && unit < first + n * cols);
         if (hit) {
             const int at = __builtin_ctzll(hit);
+            const int within = unit - __builtin_amdgcn_readlane(first, at), blocks = __builtin_amdgcn_readlane(n, at);
             expert = e0 + at;
-            expert_rows(g, expert, r0, r1);
-            row0 = r0 + (int64_t)(unit - __builtin_amdgcn_readlane(first, at)) * bm;
-            row1 = r1;
+            col = within / blocks;
+            expert_rows(g, expert, row0, row1);
+            row0 += (int64_t)(within - col * blocks) * bm;
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -233,17 +247,18 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args g) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
-    const int block = blockIdx.x / g.tiles_n;
-    const int64_t n0 = (int64_t)(blockIdx.x - block * g.tiles_n) * 16;
     const int8_t *w = g.w;
     const float *sw = g.sw;
-    int64_t m0, m1;
+    int64_t m0, m1, n0;
     if constexpr (GROUPED) {
-        int expert;
-        if (!find_block(g, 16 * MT, block, expert, m0, m1)) return;
+        int expert, col;
+        if (!find_block(g, 16 * MT, g.tiles_n, blockIdx.x, expert, m0, m1, col)) return;
         w += (int64_t)expert * g.N * g.K;
         sw += (int64_t)expert * g.N;
+        n0 = (int64_t)col * 16;
     } else {
+        const int block = blockIdx.x / g.tiles_n;
+        n0 = (int64_t)(blockIdx.x - block * g.tiles_n) * 16;
         m0 = (int64_t)block * 16 * MT;
         m1 = g.M;
     }
@@ -335,22 +350,64 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args g) {
     }
 }
 
-// Many rows: tiles of BM x BN in LDS, 8 or 4 waves of (BM / WAVES_M) x 64.
-template <int BM_, int BN_, int NW_, int WAVES_M_>
+// Many rows: tiles of BM x BN in LDS, NW waves of (BM / WAVES_M) x 64 each. Tile rows go to the
+// waves in runs of 64, so that the first 128 rows are every wave's first 64 and the next 128 its
+// next: row group i (16 rows) of a wave in row wm of the wave grid starts at tile row
+// wave_row(wm, i).
+__device__ __forceinline__ constexpr int wave_row(int wm, int i) { return i / 4 * 128 + wm * 64 + i % 4 * 16; }
+
+template <int BM_, int BN_, int NW_, int WAVES_M_, int NSTAGE_>
 struct Int8Tile {
     static constexpr int BM = BM_, BN = BN_, NW = NW_, WAVES_M = WAVES_M_, WAVES_N = NW_ / WAVES_M_;
-    static constexpr int NSTAGE = 2;
+    static constexpr int NSTAGE = NSTAGE_;
     static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int SUB_M = WM / 16, SUB_N = WN / 16;
     static constexpr int A_BYTES = BM * KB, W_BYTES = BN * KB, STAGE = A_BYTES + W_BYTES;
     static constexpr int A_INSTR = BM / (8 * NW), W_INSTR = BN / (8 * NW), IPW = A_INSTR + W_INSTR;
-    static_assert(WAVES_M * WAVES_N == NW && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile shape");
+    static_assert(WAVES_M * WAVES_N == NW && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && WN == 64, "tile shape");
     static_assert(STAGE * NSTAGE <= 160 * 1024 && IPW < 64, "LDS budget");
 };
 
-// This wave's copies global -> LDS. Instruction t moves tile rows 8 (NW t + wave) .. + 7 of A
-// (t < A_INSTR), then of W; lane L fills LDS row L / 8 of those, physical chunk L % 8. VARIANT
-// makes the type unique to each kernel instantiation (see Bf16Dma for why).
+// A workgroup's tile
+struct TileAt {
+    int64_t m0, m1, n0;   // first row, end of the rows (not of the tile), first channel
+    const int8_t *w;      // the tile's weight and its scales
+    const float *sw;
+};
+
+// Tile of a workgroup: b runs on XCD b % 8, and each XCD takes a contiguous run of tile numbers;
+// one weight's tiles are numbered down `group` tile rows per tile column, so that the tiles
+// that an XCD holds at once share A and W panels in its L2. False: no tile (grouped: the grid
+// is an upper bound; the numbers are dealt over the real tiles, so every XCD has its share).
+template <class T, int GROUPED>
+__device__ __forceinline__ bool find_tile(const Int8Args &g, TileAt &t) {
+    const int tiles = (GROUPED ? count_blocks(g, T::BM) : g.tiles_m) * g.tiles_n;
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int q = tiles >> 3, rem = tiles & 7;
+    const int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
+    t.w = g.w;
+    t.sw = g.sw;
+    if constexpr (GROUPED) {
+        int expert, col;
+        if (slot >= q + (xcd < rem) || !find_block(g, T::BM, g.tiles_n, tl, expert, t.m0, t.m1, col)) return false;
+        t.n0 = (int64_t)col * T::BN;
+        t.w += (int64_t)expert * g.N * g.K;
+        t.sw += (int64_t)expert * g.N;
+    } else {
+        const int band = tl / (g.group * g.tiles_n);
+        const int in_band = tl - band * g.group * g.tiles_n;
+        const int band_rows = min(g.group, g.tiles_m - band * g.group);
+        t.m0 = (int64_t)(band * g.group + in_band % band_rows) * T::BM;
+        t.n0 = (int64_t)(in_band / band_rows) * T::BN;
+        t.m1 = g.M;
+    }
+    return true;
+}
+
+// This wave's copies global -> LDS. Instruction t moves 8 rows of A (t < A_INSTR), then of W;
+// lane L fills LDS row L / 8 of those, physical chunk L % 8. VARIANT makes the type unique to
+// each kernel instantiation: the host pass emits a launch stub for only one kernel among those
+// that share such a type.
 template <class T, int VARIANT>
 struct Int8Dma {
     rsrc_t ra, rw;
@@ -358,20 +415,24 @@ struct Int8Dma {
     int wave, chunk_byte, K;
     uint8_t *smem;
 
-    __device__ __forceinline__ Int8Dma(const Int8Args &g, const int8_t *w, int64_t m0, int64_t m1, int64_t n0,
-                                       int wave_, int lane, uint8_t *smem_)
+    // the first tile row of instruction t
+    __device__ __forceinline__ int row_of(int t) const {
+        return 8 * (T::NW * (t < T::A_INSTR ? t : t - T::A_INSTR) + wave);
+    }
+
+    __device__ __forceinline__ Int8Dma(const Int8Args &g, const TileAt &at, int wave_, int lane, uint8_t *smem_)
         : wave(wave_), K((int)g.K), smem(smem_) {
         const int sub = lane >> 3;
-        const int64_t mrows = m1 - m0 < T::BM ? m1 - m0 : T::BM, nrows = g.N - n0 < T::BN ? g.N - n0 : T::BN;
-        rw = make_rsrc(w + n0 * K, nrows * K);
-        ra = g.rows ? make_rsrc(g.a, g.tokens * K) : make_rsrc(g.a + m0 * K, mrows * K);
-        chunk_byte = swz_chunk(sub, lane & 7) << 4;   // (tile rows 8 i + sub: their swizzle is sub's)
+        const int64_t mrows = at.m1 - at.m0 < T::BM ? at.m1 - at.m0 : T::BM;
+        const int64_t nrows = g.N - at.n0 < T::BN ? g.N - at.n0 : T::BN;
+        rw = make_rsrc(at.w + at.n0 * K, nrows * K);
+        ra = g.rows ? make_rsrc(g.a, g.tokens * K) : make_rsrc(g.a + at.m0 * K, mrows * K);
+        chunk_byte = swz_chunk(sub, lane & 7) << 4;   // (rows 8 i + sub: their swizzle is sub's)
 #pragma unroll
         for (int t = 0; t < T::IPW; ++t) {
-            const int tt = t < T::A_INSTR ? t : t - T::A_INSTR;
-            const int row = 8 * (T::NW * tt + wave) + sub;
+            const int row = row_of(t) + sub;
             if (t < T::A_INSTR && g.rows) {
-                const int token = row < mrows ? g.rows[m0 + row] : -1;
+                const int token = row < mrows ? g.rows[at.m0 + row] : -1;
                 off[t] = token >= 0 && token < g.tokens ? (uint32_t)token * (uint32_t)K + chunk_byte : kNowhere;
             } else {
                 off[t] = (uint32_t)(row * K) + chunk_byte;
@@ -379,21 +440,19 @@ struct Int8Dma {
         }
     }
 
-    // the copies of K step ks into its stage buffer. Bytes of W past K read as zero, which
-    // makes what A holds there (the next row's bytes) count for nothing.
-    __device__ __forceinline__ void issue(int ks) const {
+    // copies first .. first + count - 1 (constants where this is inlined) of K step ks into its
+    // stage buffer. Bytes past K (and steps past the last) read as zero, so that what the other
+    // operand holds there counts for nothing.
+    __device__ __forceinline__ void issue(int ks, int first = 0, int count = T::IPW) const {
         uint8_t *base = smem + (ks % T::NSTAGE) * T::STAGE;
         const int koff = __builtin_amdgcn_readfirstlane(ks * KB);
         const bool past = koff + chunk_byte >= K;
 #pragma unroll
         for (int t = 0; t < T::IPW; ++t) {
-            if (t < T::A_INSTR)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(base + 8 * (T::NW * t + wave) * KB), 16,
-                                                         past ? kNowhere : off[t], koff, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rw, (lds_void *)(base + T::A_BYTES + 8 * (T::NW * (t - T::A_INSTR) + wave) * KB), 16,
-                    past ? kNowhere : off[t], koff, 0, 0);
+            if (t < first || t >= first + count) continue;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                t < T::A_INSTR ? ra : rw, (lds_void *)(base + (t < T::A_INSTR ? 0 : T::A_BYTES) + row_of(t) * KB), 16,
+                past ? kNowhere : off[t], koff, 0, 0);
         }
     }
 };
@@ -409,40 +468,233 @@ struct Int8Epilogue {
     static_assert(IPR >= 1, "epilogue staging does not fit");
 };
 
+// The accumulators' scaled rows go through LDS and leave in whole 128-byte pieces, masked to
+// the tile's rows and to N. (Stored straight from the fragments each line would be written in
+// 8-byte pieces by several instructions.) Begins with a workgroup barrier.
+template <class T, int OUT_BF16>
+__device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, uint8_t *smem, int lane, int wm, int wn,
+                                           const i32x4 (&acc)[T::SUB_M][T::SUB_N]) {
+    using E = Int8Epilogue<T, OUT_BF16>;
+    constexpr int OB = E::OB, EPC = E::EPC, LDS_ROW = E::LDS_ROW, RG = E::RG, IPR = E::IPR, CPR = E::CPR;
+    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, WN = T::WN;
+    const int frow = lane & 15, kg = lane >> 4;
+    const bool vec = ((g.N * OB) & 15) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
+    f32x4 scale_n[SUB_N], bias[SUB_N];
+#pragma unroll
+    for (int j = 0; j < SUB_N; ++j) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t n = at.n0 + wn * WN + 16 * j + 4 * kg + r;
+            scale_n[j][r] = n < g.N ? at.sw[n] : 0.0f;
+            bias[j][r] = g.bias && n < g.N ? g.bias[n] : 0.0f;
+        }
+    }
+    float scale_m[SUB_M];
+#pragma unroll
+    for (int i = 0; i < SUB_M; ++i) {
+        int64_t m = at.m0 + wave_row(wm, i) + frow;
+        scale_m[i] = 0.0f;
+        if (m < at.m1) {
+            if (g.rows) m = g.rows[m];
+            if (m >= 0 && m < g.tokens) scale_m[i] = g.sa[m];
+        }
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < SUB_M; i0 += IPR) {
+        __syncthreads();
+#pragma unroll
+        for (int ii = 0; ii < IPR; ++ii) {
+            if (i0 + ii < SUB_M) {
+                uint8_t *rowp = smem + (ii * RG + wm * 16 + frow) * LDS_ROW;
+#pragma unroll
+                for (int j = 0; j < SUB_N; ++j) {
+                    const int col = wn * WN + 16 * j + 4 * kg;
+                    f32x4 v;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = (float)acc[i0 + ii][j][r] * scale_m[i0 + ii] * scale_n[j][r] + bias[j][r];
+                    if constexpr (OUT_BF16)
+                        *reinterpret_cast<u32x2 *>(rowp + col * 2) =
+                            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    else
+                        *reinterpret_cast<f32x4 *>(rowp + col * 4) = v;
+                }
+            }
+        }
+        __syncthreads();
+        const int groups = (SUB_M - i0) < IPR ? (SUB_M - i0) : IPR;
+        const int chunks = groups * RG * CPR;
+        for (int c = threadIdx.x; c < chunks; c += T::NW * 64) {
+            const int r = c / CPR, cb = c - r * CPR;
+            const int ii = r / RG, within = r - ii * RG;
+            const int64_t m = at.m0 + wave_row(within >> 4, i0 + ii) + (within & 15);
+            const int64_t n = at.n0 + cb * EPC;
+            if (m >= at.m1 || n >= g.N) continue;
+            const uint8_t *src = smem + r * LDS_ROW + cb * 16;
+            uint8_t *yp = reinterpret_cast<uint8_t *>(g.y) + (m * g.N + n) * OB;
+            if (vec && n + EPC <= g.N) {
+                *reinterpret_cast<u32x4 *>(yp) = *reinterpret_cast<const u32x4 *>(src);
+            } else {
+                for (int e = 0; e < EPC && n + e < g.N; ++e) {
+                    if constexpr (OUT_BF16)
+                        reinterpret_cast<uint16_t *>(yp)[e] = reinterpret_cast<const uint16_t *>(src)[e];
+                    else
+                        reinterpret_cast<float *>(yp)[e] = reinterpret_cast<const float *>(src)[e];
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14)); }
+
+// Tiles of 8 waves, two to a SIMD, that take turns: waves 0-3 and 4-7 are one barrier apart, so
+// that in each interval between two barriers ("slot") one wave of a SIMD multiplies from
+// registers while the other fills its own from LDS and queues copies. A wave's K step of 128
+// bytes is PH phases (2 for BM = 256, 1 for 128), each a load slot and a multiply slot of 32
+// MFMAs (512 cycles): phase 0 loads the step's W fragments and the wave's first 64 rows of A,
+// phase 1 the other 64 rows, over the same registers. In a tile that is not FULL of rows, groups of
+// 16 rows past the last are not multiplied (the branches cost a full tile 5%).
+//
+// Copies. A region of a stage buffer is free once both groups have loaded it, which each load
+// slot ends by waiting for (lgkmcnt). With two phases and two stages, the copies of step ks + 2
+// for W and the tile's first 128 rows are queued in load slot 1 of step ks, those of its other
+// rows in load slot 0 of step ks + 1; with one phase and three stages, those of step ks + 2 in
+// the load slot of step ks. Copies retire in order, and the count left open at the end of each
+// load slot (IPW) covers exactly what the load slots before the data's use have queued since;
+// the barrier then makes it visible. Steps past the last copy zeros, which keeps the counts
+// the same.
+//
+// What bounds it: 16384 x 7168 x 7168 takes 500 us on zeros (3.4 POP/s: the matrix unit busy 0.78 of
+// the cycles) and 640 us on normal data, at a lower clock (about 1.6 GHz): the power limit. The
+// 32x32x32 instruction, at half the K and so twice the accumulator traffic, has fewer cycles
+// and yet takes 685 us.
+template <class T, int FULL, int VARIANT, int OUT_BF16>
+__device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8_t *smem) {
+    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, PH = SUB_M / 4;
+    static_assert(PH == 1 || PH == 2, "phases");
+    constexpr int I0 = T::A_INSTR / 2;   // two phases: copies of the first 128 rows
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int nks = (int)((g.K + KB - 1) / KB);
+    const Int8Dma<T, VARIANT> dma(g, at, wave, lane, smem);
+    const int rows = (int)(at.m1 - at.m0 < T::BM ? at.m1 - at.m0 : T::BM);
+
+    i32x4 acc[SUB_M][SUB_N];
+#pragma unroll
+    for (int i = 0; i < SUB_M; ++i)
+#pragma unroll
+        for (int j = 0; j < SUB_N; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int frow = lane & 15, kg = lane >> 4;
+    const int lo = frow * KB + (swz_chunk(frow, kg) << 4);
+    const int hi = frow * KB + (swz_chunk(frow, 4 + kg) << 4);
+    const int w_base = T::A_BYTES + wn * T::WN * KB;
+
+    if constexpr (PH == 2) {
+        dma.issue(0, T::A_INSTR, T::W_INSTR);
+        dma.issue(0, 0, I0);
+        dma.issue(0, I0, I0);
+        dma.issue(1, T::A_INSTR, T::W_INSTR);
+        dma.issue(1, 0, I0);
+    } else {
+        dma.issue(0);
+        dma.issue(1);
+    }
+    wait_vmcnt<T::IPW>();
+    lds_barrier();
+    if (wave >= 4) lds_barrier();   // one slot behind
+
+    for (int ks = 0; ks < nks; ++ks) {
+        const uint8_t *stage = smem + (ks % T::NSTAGE) * T::STAGE;
+        u32x4 wf[SUB_N][2];
+#pragma unroll
+        for (int ph = 0; ph < PH; ++ph) {
+            u32x4 xf[4][2];
+            if (ph == 0) {
+#pragma unroll
+                for (int j = 0; j < SUB_N; ++j) {
+                    wf[j][0] = *reinterpret_cast<const u32x4 *>(stage + w_base + 16 * j * KB + lo);
+                    wf[j][1] = *reinterpret_cast<const u32x4 *>(stage + w_base + 16 * j * KB + hi);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xf[i][0] = *reinterpret_cast<const u32x4 *>(stage + wave_row(wm, 4 * ph + i) * KB + lo);
+                xf[i][1] = *reinterpret_cast<const u32x4 *>(stage + wave_row(wm, 4 * ph + i) * KB + hi);
+            }
+            if constexpr (PH == 1) {
+                dma.issue(ks + 2);
+            } else if (ph == 0) {
+                dma.issue(ks + 1, I0, I0);
+            } else {
+                dma.issue(ks + 2, T::A_INSTR, T::W_INSTR);
+                dma.issue(ks + 2, 0, I0);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // the waits stay behind the loads and copies
+            wait_lgkm0();
+            wait_vmcnt<T::IPW>();
+            lds_barrier();
+            __builtin_amdgcn_s_setprio(1);
+            if constexpr (FULL) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < SUB_N; ++j)
+                            acc[4 * ph + i][j] = mfma_i8(wf[j][h], xf[i][h], acc[4 * ph + i][j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (wave_row(wm, 4 * ph + i) < rows) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < SUB_N; ++j)
+                                acc[4 * ph + i][j] = mfma_i8(wf[j][h], xf[i][h], acc[4 * ph + i][j]);
+                    }
+                }
+            }
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+        }
+    }
+    if (wave < 4) lds_barrier();
+    wait_vmcnt<0>();   // the copies past the last step, before LDS takes the output
+    store_tile<T, OUT_BF16>(g, at, smem, lane, wm, wn, acc);
+}
+
+// A tile with at most 128 rows (an expert's last, or only one) takes half the phases.
+template <int OUT_BF16, int GROUPED>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_turns_kernel(Int8Args g) {
+    using T2 = Int8Tile<256, 256, 8, 2, 2>;
+    using T1 = Int8Tile<128, 256, 8, 2, 3>;
+    constexpr int A = T2::STAGE * T2::NSTAGE, B = T1::STAGE * T1::NSTAGE;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[A > B ? A : B];
+    TileAt at;
+    if (!find_tile<T2, GROUPED>(g, at)) return;
+    constexpr int VARIANT = OUT_BF16 * 2 + GROUPED;
+    if (at.m1 - at.m0 >= 256) turns<T2, 1, VARIANT, OUT_BF16>(g, at, smem);
+    else if (at.m1 - at.m0 > 128) turns<T2, 0, VARIANT, OUT_BF16>(g, at, smem);
+    else turns<T1, 0, VARIANT, OUT_BF16>(g, at, smem);
+}
+
+// 128 x 128 tiles of 4 waves, two workgroups per CU, each step's A fragments read one row group
+// ahead of their MFMAs: for shapes with too few of the larger tiles.
 template <int BM_, int BN_, int NW_, int WAVES_M_, int OUT_BF16, int GROUPED>
 __global__ __launch_bounds__(NW_ * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_tile_kernel(Int8Args g) {
-    using T = Int8Tile<BM_, BN_, NW_, WAVES_M_>;
-    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, WM = T::WM, WN = T::WN;
+    using T = Int8Tile<BM_, BN_, NW_, WAVES_M_, 2>;
+    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N;
     __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * T::NSTAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % T::WAVES_M, wn = wave / T::WAVES_M;
-
-    // XCD-contiguous tile index (workgroup b runs on XCD b % 8), then down `group` tile rows
-    // per tile column
-    const int tiles = g.tiles_m * g.tiles_n;
-    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-    const int q = tiles >> 3, rem = tiles & 7;
-    const int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
-    const int band = tl / (g.group * g.tiles_n);
-    const int in_band = tl - band * g.group * g.tiles_n;
-    const int band_rows = min(g.group, g.tiles_m - band * g.group);
-    const int tile_m = band * g.group + in_band % band_rows;
-    const int64_t n0 = (int64_t)(in_band / band_rows) * T::BN;
-    int64_t m0, m1;
-    const int8_t *w = g.w;
-    const float *sw = g.sw;
-    if constexpr (GROUPED) {
-        int expert;
-        if (!find_block(g, T::BM, tile_m, expert, m0, m1)) return;
-        w += (int64_t)expert * g.N * g.K;
-        sw += (int64_t)expert * g.N;
-    } else {
-        m0 = (int64_t)tile_m * T::BM;
-        m1 = g.M;
-    }
+    TileAt at;
+    if (!find_tile<T, GROUPED>(g, at)) return;
     const int nks = (int)((g.K + KB - 1) / KB);
-    const Int8Dma<T, OUT_BF16 * 2 + GROUPED> dma(g, w, m0, m1, n0, wave, lane, smem);
+    const Int8Dma<T, 4 + OUT_BF16 * 2 + GROUPED> dma(g, at, wave, lane, smem);
 
     i32x4 acc[SUB_M][SUB_N];
 #pragma unroll
@@ -453,7 +705,7 @@ __global__ __launch_bounds__(NW_ * 64) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int frow = lane & 15, kg = lane >> 4;
     const int lo = frow * KB + (swz_chunk(frow, kg) << 4);
     const int hi = frow * KB + (swz_chunk(frow, 4 + kg) << 4);
-    const int a_base = wm * WM * KB, w_base = T::A_BYTES + wn * WN * KB;
+    const int a_base = wave_row(wm, 0) * KB, w_base = T::A_BYTES + wn * T::WN * KB;
 
     if (nks > 0) dma.issue(0);
     if (nks > 1) {
@@ -487,83 +739,13 @@ __global__ __launch_bounds__(NW_ * 64) __attribute__((amdgpu_waves_per_eu(2, 2))
             xa[0] = xn[0];
             xa[1] = xn[1];
         }
-        __builtin_amdgcn_sched_barrier(0);                                  // the waits stay behind this step's MFMAs
-        __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
-        if (ks + 1 < nks) wait_vmcnt<0>();                                  // step ks + 1 has landed
+        __builtin_amdgcn_sched_barrier(0);   // the waits stay behind this step's MFMAs
+        wait_lgkm0();
+        if (ks + 1 < nks) wait_vmcnt<0>();   // step ks + 1 has landed
         lds_barrier();
         if (ks + 2 < nks) dma.issue(ks + 2);
     }
-
-    // Epilogue: scaled rows go through LDS and leave in whole 128-byte pieces (as in
-    // bf16_gemm.hip), masked to the tile's rows and to N.
-    using E = Int8Epilogue<T, OUT_BF16>;
-    constexpr int OB = E::OB, EPC = E::EPC, LDS_ROW = E::LDS_ROW, RG = E::RG, IPR = E::IPR, CPR = E::CPR;
-    const bool vec = ((g.N * OB) & 15) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
-    f32x4 scale_n[SUB_N], bias[SUB_N];
-#pragma unroll
-    for (int j = 0; j < SUB_N; ++j) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t n = n0 + wn * WN + 16 * j + 4 * kg + r;
-            scale_n[j][r] = n < g.N ? sw[n] : 0.0f;
-            bias[j][r] = g.bias && n < g.N ? g.bias[n] : 0.0f;
-        }
-    }
-    float scale_m[SUB_M];
-#pragma unroll
-    for (int i = 0; i < SUB_M; ++i) {
-        int64_t m = m0 + wm * WM + 16 * i + frow;
-        scale_m[i] = 0.0f;
-        if (m < m1) {
-            if (g.rows) m = g.rows[m];
-            if (m >= 0 && m < g.tokens) scale_m[i] = g.sa[m];
-        }
-    }
-#pragma unroll
-    for (int i0 = 0; i0 < SUB_M; i0 += IPR) {
-        __syncthreads();
-#pragma unroll
-        for (int ii = 0; ii < IPR; ++ii) {
-            if (i0 + ii < SUB_M) {
-                uint8_t *rowp = smem + (ii * RG + wm * 16 + frow) * LDS_ROW;
-#pragma unroll
-                for (int j = 0; j < SUB_N; ++j) {
-                    const int col = wn * WN + 16 * j + 4 * kg;
-                    f32x4 v;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = (float)acc[i0 + ii][j][r] * scale_m[i0 + ii] * scale_n[j][r] + bias[j][r];
-                    if constexpr (OUT_BF16)
-                        *reinterpret_cast<u32x2 *>(rowp + col * 2) =
-                            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                    else
-                        *reinterpret_cast<f32x4 *>(rowp + col * 4) = v;
-                }
-            }
-        }
-        __syncthreads();
-        const int groups = (SUB_M - i0) < IPR ? (SUB_M - i0) : IPR;
-        const int chunks = groups * RG * CPR;
-        for (int c = threadIdx.x; c < chunks; c += T::NW * 64) {
-            const int r = c / CPR, cb = c - r * CPR;
-            const int ii = r / RG, within = r - ii * RG;
-            const int64_t m = m0 + (within >> 4) * WM + 16 * (i0 + ii) + (within & 15);
-            const int64_t n = n0 + cb * EPC;
-            if (m >= m1 || n >= g.N) continue;
-            const uint8_t *src = smem + r * LDS_ROW + cb * 16;
-            uint8_t *yp = reinterpret_cast<uint8_t *>(g.y) + (m * g.N + n) * OB;
-            if (vec && n + EPC <= g.N) {
-                *reinterpret_cast<u32x4 *>(yp) = *reinterpret_cast<const u32x4 *>(src);
-            } else {
-                for (int e = 0; e < EPC && n + e < g.N; ++e) {
-                    if constexpr (OUT_BF16)
-                        reinterpret_cast<uint16_t *>(yp)[e] = reinterpret_cast<const uint16_t *>(src)[e];
-                    else
-                        reinterpret_cast<float *>(yp)[e] = reinterpret_cast<const float *>(src)[e];
-                }
-            }
-        }
-    }
+    store_tile<T, OUT_BF16>(g, at, smem, lane, wm, wn, acc);
 }
 
 template <int MT, int U>
@@ -585,11 +767,11 @@ hipError_t launch_few(Int8Args a, bool out_bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int NW, int WAVES_M>
-hipError_t launch_tile(Int8Args a, bool out_bf16, hipStream_t stream) {
+// tile counts and the tile rows walked per tile column (an XCD's ~32 resident tiles form a
+// compact block); false if the grid would be too large
+bool lay_out(Int8Args &a, int BM, int BN, int threads) {
     a.tiles_m = (int)((a.M + BM - 1) / BM + (a.offsets ? (a.experts < a.M ? a.experts : a.M) : 0));
     a.tiles_n = (int)((a.N + BN - 1) / BN);
-    // tile rows walked per tile column: an XCD's ~32 resident tiles form a compact block
     int64_t best = -1;
     for (int gsz = 1; gsz <= 32; gsz *= 2) {
         const int64_t gg = gsz < a.tiles_m ? gsz : a.tiles_m, cols = (32 + gg - 1) / gg;
@@ -599,9 +781,26 @@ hipError_t launch_tile(Int8Args a, bool out_bf16, hipStream_t stream) {
             a.group = gsz;
         }
     }
-    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-    if (tiles * NW * 64 > 0xFFFFFFFFll) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)tiles), block(NW * 64);
+    return (int64_t)a.tiles_m * a.tiles_n * threads <= 0xFFFFFFFFll;
+}
+
+hipError_t launch_turns(Int8Args a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a, 256, 256, 512)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(512);
+    if (a.offsets) {
+        if (out_bf16) int8_turns_kernel<1, 1><<<grid, block, 0, stream>>>(a);
+        else int8_turns_kernel<0, 1><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (out_bf16) int8_turns_kernel<1, 0><<<grid, block, 0, stream>>>(a);
+        else int8_turns_kernel<0, 0><<<grid, block, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int NW, int WAVES_M>
+hipError_t launch_tile(Int8Args a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a, BM, BN, NW * 64)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(NW * 64);
     if (a.offsets) {
         if (out_bf16) int8_tile_kernel<BM, BN, NW, WAVES_M, 1, 1><<<grid, block, 0, stream>>>(a);
         else int8_tile_kernel<BM, BN, NW, WAVES_M, 0, 1><<<grid, block, 0, stream>>>(a);
@@ -631,7 +830,7 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     if (M <= 32) return launch_few<2, 4>(g, out_bf16, stream);
     if (M <= 64) return launch_few<4, 4>(g, out_bf16, stream);
     const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
-    if (large >= 256) return launch_tile<256, 256, 8, 2>(g, out_bf16, stream);
+    if (large >= 256) return launch_turns(g, out_bf16, stream);
     return launch_tile<128, 128, 4, 2>(g, out_bf16, stream);
 }
 
@@ -641,7 +840,7 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
                                     hipStream_t stream) {
     const Int8Args g{a, sa, w, sw, nullptr, y, offsets, rows, M, N, K, tokens, (int)experts, 0, 0, 1};
     if (M <= 16 * experts) return launch_few<1, 8>(g, out_bf16, stream);
-    return launch_tile<128, 128, 4, 2>(g, out_bf16, stream);
+    return launch_turns(g, out_bf16, stream);
 }
 
 }  // namespace fp8q
