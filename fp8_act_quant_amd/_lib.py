@@ -62,6 +62,8 @@ SIGNATURES = {
     "moe_combine_backward": (_INT, [_P, _P, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]),
     "int8_quant": (_INT, [_P, _P, _P, _I64, _I64, _P]),
     "int8_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P]),
+    "int8_linear": (_INT, [_P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "int8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "int8_grouped_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P]),
     "fp8q_gemm_force_config": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "fp8q_gemm_config_name": (ctypes.c_char_p, [ctypes.c_int]),

@@ -408,6 +408,26 @@ int int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw
                                          static_cast<hipStream_t>(stream)));
 }
 
+size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (int8_ok(FP8Q_OUT_F32, M, N, K) || M == 0 || N == 0 || M > kMaxTokens) return 0;
+    return fp8q::int8_linear_workspace_bytes(M, K);
+}
+
+int int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y, int y_dtype, int64_t M,
+                int64_t N, int64_t K, void *workspace, size_t workspace_bytes, void *stream) {
+    if (int e = int8_ok(y_dtype, M, N, K)) return e;
+    if (M > kMaxTokens) return FP8Q_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (!y || (K > 0 && (!x || !w || !sw))) return FP8Q_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(y, 4) || misaligned(sw, 4) || misaligned(bias, 4) ||
+        misaligned(workspace, 16))
+        return FP8Q_ERR_ALIGN;
+    if (fp8q::int8_linear_workspace_bytes(M, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_int8_linear(x, w, sw, bias, y, y_dtype == FP8Q_OUT_BF16, M, N, K, workspace,
+                                           static_cast<hipStream_t>(stream)));
+}
+
 int int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const int64_t *offsets,
                       const int32_t *rows, void *y, int y_dtype, int64_t experts, int64_t M, int64_t tokens, int64_t N,
                       int64_t K, void *stream) {
@@ -457,8 +477,8 @@ const char *fp8q_strerror(int status) {
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_WORKSPACE:
         return "the shape's split-K schedule needs more scratch than the static scratch holds "
-               "(FP8Q_NOALLOC_SCRATCH_BYTES); call fp8_block_gemm with a workspace instead (moe_place: the workspace "
-               "is smaller than moe_place_workspace_bytes)";
+               "(FP8Q_NOALLOC_SCRATCH_BYTES); call fp8_block_gemm with a workspace instead (moe_place, int8_linear: "
+               "the workspace is smaller than their _workspace_bytes)";
     default: return "unknown status";
     }
 }

@@ -30,20 +30,43 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // ---- row quantisation ------------------------------------------------------------------
 
-// 8 codes of 8 bf16 values over the row's scale
-__device__ __forceinline__ u32x2 codes8(u32x4 v, float d) {
+// A row's scale and what its codes are formed with. RN(x / s) comes from the rounded reciprocal
+// and two corrections (fast_quotient's steps, of which only the sign of a zero is left out); that
+// it gives the same code as the division for every bf16 x and maximum is checked exhaustively.
+// It needs s >= 2^-92; smaller scales take the division, and a clamp, since a scale below the
+// normal range may be off by more than the half step that separates 127 from 127.5.
+struct RowScale {
+    float s, d, y;
+    bool fast;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top_bits) {
+    RowScale r;
+    r.s = __uint_as_float(top_bits << 16) * (1.0f / 127.0f);
+    r.d = top_bits ? r.s : 1.0f;
+    r.y = 1.0f / r.d;
+    r.fast = r.d >= kFastDivMin;
+    return r;
+}
+
+// 8 codes of 8 bf16 values. Adding 1.5 * 2^23 rounds to the nearest whole number, ties to even, and
+// leaves it in the low bits.
+__device__ __forceinline__ u32x2 codes8(u32x4 v, const RowScale &r) {
     u32x2 out;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t word = 0;
+        uint32_t c[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const uint32_t u = v[2 * h + b / 2];
             const float x = b & 1 ? bf16hi_to_f32(u) : bf16lo_to_f32(u);
-            const float q = __builtin_amdgcn_fmed3f(__builtin_rintf(x / d), -127.0f, 127.0f);
-            word |= ((uint32_t)(int)q & 0xFFu) << (8 * b);
+            const float q0 = x * r.y;
+            float q = __builtin_fmaf(__builtin_fmaf(-q0, r.d, x), r.y, q0);
+            if (!r.fast) q = __builtin_amdgcn_fmed3f(x / r.d, -127.0f, 127.0f);
+            c[b] = __float_as_uint(q + 0x1.8p23f);
         }
-        out[h] = word;
+        const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400);   // bytes 0 of c[0], c[1]
+        const uint32_t hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000C0C);   // of c[2], c[3], above
+        out[h] = lo | hi;
     }
     return out;
 }
@@ -95,17 +118,16 @@ __global__ __launch_bounds__(256) void row_quant_kernel(const uint16_t *x, int8_
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) top = top > part[w] ? top : part[w];
     }
-    const float scale = __uint_as_float(top << 16) * (1.0f / 127.0f);
-    const float d = top ? scale : 1.0f;
+    const RowScale r = row_scale(top);
     u32x2 *dst = reinterpret_cast<u32x2 *>(q + (in ? m : 0) * K);
     if constexpr (NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (tid + i * NT < n) dst[tid + i * NT] = codes8(v[i], d);
+            if (tid + i * NT < n) dst[tid + i * NT] = codes8(v[i], r);
     } else {
-        for (int64_t i = tid; i < n; i += NT) dst[i] = codes8(src[i], d);
+        for (int64_t i = tid; i < n; i += NT) dst[i] = codes8(src[i], r);
     }
-    if (in && tid == 0) s[m] = scale;
+    if (in && tid == 0) s[m] = r.s;
 }
 
 // ---- products --------------------------------------------------------------------------
@@ -236,136 +258,162 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
     }
 }
 
-// Few rows (a decode step): every byte of W is read once and met by at most 16 * MT tokens, so
-// the read of W is what counts. A workgroup takes 16 channels; its 4 waves take a quarter of K
-// each, straight from memory into MFMA operands (no LDS: nothing is read twice), U steps of 64
-// bytes a batch, the next batch in flight while this one is multiplied. The quarters are added
-// in LDS, exactly.
-template <int MT, int U, int OUT_BF16, int GROUPED>
-__global__ __launch_bounds__(256) void int8_few_kernel(Int8Args g) {
-    __shared__ i32x4 part[4][MT][64];
+// At most 16 rows (a decode step): every byte of W meets all of them once, so the read of W is
+// what counts. A workgroup takes 16 channels; its 4 waves take a quarter of K each, W straight
+// from memory into MFMA operands (nothing of it is used twice), 2 U steps of 64 bytes in flight.
+// The quarters are added in LDS, exactly.
+//
+// QUANT: the rows come as bf16 and are quantised here (at most kFewQuantRows of at most
+// kFewQuantK elements): every workgroup does it for itself, in LDS, while its first reads of W are
+// on their way, which costs less than a launch of its own. 1 x 7168 x 7168: 10 us in all, of which
+// the 51 MB of W are 9 at 5.7 TB/s.
+constexpr int kFewRows = 16, kFewQuantRows = 4, kFewQuantK = 8192;
+
+struct Int8FewArgs {
+    const int8_t *a;       // QUANT: null
+    const float *sa;
+    const uint16_t *x;     // QUANT: [M, K] bf16
+    const int8_t *w;
+    const float *sw;
+    const float *bias;
+    void *y;
+    int64_t N;
+    int M, K;
+};
+
+template <int U, int QUANT, int OUT_BF16>
+__global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
+    constexpr int PITCH = kFewQuantK + 16;
+    __shared__ i32x4 part[4][64];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[QUANT ? kFewQuantRows * PITCH : 16];
+    __shared__ uint32_t tops[4][QUANT ? kFewQuantRows : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
-    const int8_t *w = g.w;
-    const float *sw = g.sw;
-    int64_t m0, m1, n0;
-    if constexpr (GROUPED) {
-        int expert, col;
-        if (!find_block(g, 16 * MT, g.tiles_n, blockIdx.x, expert, m0, m1, col)) return;
-        w += (int64_t)expert * g.N * g.K;
-        sw += (int64_t)expert * g.N;
-        n0 = (int64_t)col * 16;
-    } else {
-        const int block = blockIdx.x / g.tiles_n;
-        n0 = (int64_t)(blockIdx.x - block * g.tiles_n) * 16;
-        m0 = (int64_t)block * 16 * MT;
-        m1 = g.M;
-    }
-    const int K = (int)g.K;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int K = g.K, M = g.M;
     const int nw = (int)(g.N - n0 < 16 ? g.N - n0 : 16);
-    const rsrc_t rw = make_rsrc(w + n0 * K, (int64_t)nw * K);
-    // (grouped: one buffer over all tokens; else over this block's)
-    const int8_t *a0 = g.rows ? g.a : g.a + m0 * K;
-    const rsrc_t ra = make_rsrc(a0, g.rows ? g.tokens * K : (m1 - m0 < 16 * MT ? m1 - m0 : 16 * MT) * K);
-    uint32_t aoff[MT];
-    int64_t token[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + row;
-        token[i] = -1;
-        aoff[i] = kNowhere;
-        if (m < m1) {
-            token[i] = m;
-            if (g.rows) {
-                const int t = g.rows[m];
-                token[i] = t >= 0 && t < g.tokens ? t : -1;
-                if (token[i] >= 0) aoff[i] = (uint32_t)t * (uint32_t)K;
-            } else {
-                aoff[i] = (uint32_t)(16 * i + row) * (uint32_t)K;
-            }
-        }
-    }
+    const rsrc_t rw = make_rsrc(g.w + n0 * K, (int64_t)nw * K);
+    const rsrc_t ra = make_rsrc(QUANT ? (const void *)g.x : g.a, QUANT ? (int64_t)M * K * 2 : (int64_t)M * K);
     const int steps = (K + 63) / 64;
     const int s0 = wave * steps / 4, s1 = (wave + 1) * steps / 4;
 
-    i32x4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
-    u32x4 wv[2][U], av[2][MT][U];
+    i32x4 acc = {0, 0, 0, 0};
+    u32x4 wv[2][U], av[2][QUANT ? 1 : U];
+    // Bytes of W past K or past the last channel read as zero, which makes what the rows hold
+    // there count for nothing.
     auto load = [&](int b, int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s + u) * 64 + kg * 16;
             const bool in = s + u < s1 && k < K;
-            const u32x4 z = {0, 0, 0, 0};
-            wv[b][u] = z;
-            if (s + u < s1)
-                wv[b][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                         rw, in ? (uint32_t)(row * K + k) : kNowhere, 0, 0));
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                av[b][i][u] = z;
-                if (s + u < s1)
-                    av[b][i][u] = __builtin_bit_cast(
-                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                   ra, in && aoff[i] != kNowhere ? aoff[i] + (uint32_t)k : kNowhere, 0, 0));
-            }
+            wv[b][u] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (uint32_t)(row * K + k) : kNowhere, 0, 0));
+            if constexpr (!QUANT)
+                av[b][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                         ra, in && row < M ? (uint32_t)(row * K + k) : kNowhere, 0, 0));
         }
     };
-    auto multiply = [&](int b) {
+    auto multiply = [&](int b, int s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) acc[i] = mfma_i8(wv[b][u], av[b][i][u], acc[i]);
+        for (int u = 0; u < U; ++u) {
+            u32x4 x = {0, 0, 0, 0};
+            if constexpr (QUANT) {
+                // (past K: whatever lies there, against zeros of W; always inside `codes`)
+                const int k = min((s + u) * 64 + kg * 16, kFewQuantK);
+                if (row < M) x = *reinterpret_cast<const u32x4 *>(codes + row * PITCH + k);
+            } else {
+                x = av[b][u];
+            }
+            acc = mfma_i8(wv[b][u], x, acc);
+        }
     };
     load(0, s0);
+    float scale = 0.0f;   // of this lane's row
+    if constexpr (QUANT) {
+        load(1, s0 + U);
+        constexpr int NV = kFewQuantK / 8 / 256;   // pieces of 8 elements a thread keeps of a row
+        u32x4 v[kFewQuantRows][NV];
+#pragma unroll
+        for (int m = 0; m < kFewQuantRows; ++m) {
+            if (m < M) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int p = threadIdx.x + 256 * i;
+                    v[m][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                            ra, 8 * p < K ? (uint32_t)(2 * (m * K + 8 * p)) : kNowhere, 0, 0));
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const uint32_t b = absmax_bits8(v[m][i]);
+                    top = top > b ? top : b;
+                }
+                top = wave_umax(top);
+                if (lane == 0) tops[wave][m] = top;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < kFewQuantRows; ++m) {
+            if (m < M) {
+                uint32_t top = tops[0][m];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) top = top > tops[w][m] ? top : tops[w][m];
+                const RowScale r = row_scale(top);
+                scale = row == m ? r.s : scale;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int p = threadIdx.x + 256 * i;
+                    if (8 * p < K) *reinterpret_cast<u32x2 *>(codes + m * PITCH + 8 * p) = codes8(v[m][i], r);
+                }
+            }
+        }
+        __syncthreads();
+    } else {
+        if (row < M && K > 0) scale = g.sa[row];
+    }
     for (int s = s0; s < s1; s += 2 * U) {
-        load(1, s + U);
-        multiply(0);
+        if (!QUANT || s != s0) load(1, s + U);
+        multiply(0, s);
         load(0, s + 2 * U);
-        multiply(1);
+        multiply(1, s + U);
     }
 
-#pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    part[wave][lane] = acc;
     __syncthreads();
-    const bool vec = (g.N & 3) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
+    const int64_t n = n0 + 4 * kg;
+    if (wave != 0 || row >= M || n >= g.N) return;
+    i32x4 sum = part[0][lane];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        if ((i & 3) != wave) continue;
-        i32x4 sum = part[0][i][lane];
+    for (int v = 1; v < 4; ++v) sum += part[v][lane];
+    f32x4 out;
 #pragma unroll
-        for (int v = 1; v < 4; ++v) sum += part[v][i][lane];
-        const int64_t m = m0 + 16 * i + row, n = n0 + 4 * kg;
-        if (m >= m1 || n >= g.N) continue;
-        const float sm = token[i] >= 0 ? g.sa[token[i]] : 0.0f;
-        f32x4 v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t nr = n + r < g.N ? n + r : g.N - 1;
-            v[r] = (float)sum[r] * sm * sw[nr] + (g.bias ? g.bias[nr] : 0.0f);
-        }
-        store4<OUT_BF16>(g.y, m * g.N + n, v, g.N - n, vec);
+    for (int r = 0; r < 4; ++r) {
+        const int64_t nr = n + r < g.N ? n + r : g.N - 1;
+        out[r] = (float)sum[r] * scale * (K > 0 ? g.sw[nr] : 0.0f) + (g.bias ? g.bias[nr] : 0.0f);
     }
+    const bool vec = (g.N & 3) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
+    store4<OUT_BF16>(g.y, row * g.N + n, out, g.N - n, vec);
 }
 
-// Many rows: tiles of BM x BN in LDS, NW waves of (BM / WAVES_M) x 64 each. Tile rows go to the
-// waves in runs of 64, so that the first 128 rows are every wave's first 64 and the next 128 its
-// next: row group i (16 rows) of a wave in row wm of the wave grid starts at tile row
-// wave_row(wm, i).
-__device__ __forceinline__ constexpr int wave_row(int wm, int i) { return i / 4 * 128 + wm * 64 + i % 4 * 16; }
-
+// Many rows: tiles of BM x BN in LDS, NW waves in a WAVES_M x (NW / WAVES_M) grid. Tile rows go to
+// the waves in runs of RUN, so that with 256 rows the first 128 are every wave's first 64 and the
+// next 128 its next: row group i (16 rows) of the waves in row wm of the grid starts at tile row
+// row(wm, i).
 template <int BM_, int BN_, int NW_, int WAVES_M_, int NSTAGE_>
 struct Int8Tile {
     static constexpr int BM = BM_, BN = BN_, NW = NW_, WAVES_M = WAVES_M_, WAVES_N = NW_ / WAVES_M_;
     static constexpr int NSTAGE = NSTAGE_;
-    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, RUN = WM < 64 ? WM : 64;
     static constexpr int SUB_M = WM / 16, SUB_N = WN / 16;
     static constexpr int A_BYTES = BM * KB, W_BYTES = BN * KB, STAGE = A_BYTES + W_BYTES;
     static constexpr int A_INSTR = BM / (8 * NW), W_INSTR = BN / (8 * NW), IPW = A_INSTR + W_INSTR;
-    static_assert(WAVES_M * WAVES_N == NW && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && WN == 64, "tile shape");
-    static_assert(STAGE * NSTAGE <= 160 * 1024 && IPW < 64, "LDS budget");
+    static_assert(WAVES_M * WAVES_N == NW && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile shape");
+    static_assert(STAGE * NSTAGE <= 160 * 1024 && IPW * (NSTAGE - 1) < 64, "LDS budget, vmcnt range");
+    __device__ static __forceinline__ constexpr int row(int wm, int i) {
+        return i / (RUN / 16) * (RUN * WAVES_M) + wm * RUN + i % (RUN / 16) * 16;
+    }
 };
 
 // A workgroup's tile
@@ -413,15 +461,14 @@ struct Int8Dma {
     rsrc_t ra, rw;
     uint32_t off[T::IPW];
     int wave, chunk_byte, K;
-    uint8_t *smem;
 
     // the first tile row of instruction t
     __device__ __forceinline__ int row_of(int t) const {
         return 8 * (T::NW * (t < T::A_INSTR ? t : t - T::A_INSTR) + wave);
     }
 
-    __device__ __forceinline__ Int8Dma(const Int8Args &g, const TileAt &at, int wave_, int lane, uint8_t *smem_)
-        : wave(wave_), K((int)g.K), smem(smem_) {
+    __device__ __forceinline__ Int8Dma(const Int8Args &g, const TileAt &at, int wave_, int lane)
+        : wave(wave_), K((int)g.K) {
         const int sub = lane >> 3;
         const int64_t mrows = at.m1 - at.m0 < T::BM ? at.m1 - at.m0 : T::BM;
         const int64_t nrows = g.N - at.n0 < T::BN ? g.N - at.n0 : T::BN;
@@ -440,11 +487,10 @@ struct Int8Dma {
         }
     }
 
-    // copies first .. first + count - 1 (constants where this is inlined) of K step ks into its
-    // stage buffer. Bytes past K (and steps past the last) read as zero, so that what the other
+    // copies first .. first + count - 1 (constants where this is inlined) of K step ks into the
+    // stage buffer at `base`. Bytes past K (and steps past the last) read as zero, so that what the other
     // operand holds there counts for nothing.
-    __device__ __forceinline__ void issue(int ks, int first = 0, int count = T::IPW) const {
-        uint8_t *base = smem + (ks % T::NSTAGE) * T::STAGE;
+    __device__ __forceinline__ void issue(uint8_t *base, int ks, int first = 0, int count = T::IPW) const {
         const int koff = __builtin_amdgcn_readfirstlane(ks * KB);
         const bool past = koff + chunk_byte >= K;
 #pragma unroll
@@ -485,16 +531,16 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t n = at.n0 + wn * WN + 16 * j + 4 * kg + r;
-            scale_n[j][r] = n < g.N ? at.sw[n] : 0.0f;
+            scale_n[j][r] = n < g.N && g.K > 0 ? at.sw[n] : 0.0f;
             bias[j][r] = g.bias && n < g.N ? g.bias[n] : 0.0f;
         }
     }
     float scale_m[SUB_M];
 #pragma unroll
     for (int i = 0; i < SUB_M; ++i) {
-        int64_t m = at.m0 + wave_row(wm, i) + frow;
+        int64_t m = at.m0 + T::row(wm, i) + frow;
         scale_m[i] = 0.0f;
-        if (m < at.m1) {
+        if (m < at.m1 && g.K > 0) {   // (with K = 0 there may be no scales)
             if (g.rows) m = g.rows[m];
             if (m >= 0 && m < g.tokens) scale_m[i] = g.sa[m];
         }
@@ -527,7 +573,7 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
         for (int c = threadIdx.x; c < chunks; c += T::NW * 64) {
             const int r = c / CPR, cb = c - r * CPR;
             const int ii = r / RG, within = r - ii * RG;
-            const int64_t m = at.m0 + wave_row(within >> 4, i0 + ii) + (within & 15);
+            const int64_t m = at.m0 + T::row(within >> 4, i0 + ii) + (within & 15);
             const int64_t n = at.n0 + cb * EPC;
             if (m >= at.m1 || n >= g.N) continue;
             const uint8_t *src = smem + r * LDS_ROW + cb * 16;
@@ -578,7 +624,7 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int nks = (int)((g.K + KB - 1) / KB);
-    const Int8Dma<T, VARIANT> dma(g, at, wave, lane, smem);
+    const Int8Dma<T, VARIANT> dma(g, at, wave, lane);
     const int rows = (int)(at.m1 - at.m0 < T::BM ? at.m1 - at.m0 : T::BM);
 
     i32x4 acc[SUB_M][SUB_N];
@@ -592,21 +638,22 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
     const int w_base = T::A_BYTES + wn * T::WN * KB;
 
     if constexpr (PH == 2) {
-        dma.issue(0, T::A_INSTR, T::W_INSTR);
-        dma.issue(0, 0, I0);
-        dma.issue(0, I0, I0);
-        dma.issue(1, T::A_INSTR, T::W_INSTR);
-        dma.issue(1, 0, I0);
+        dma.issue(smem, 0, T::A_INSTR, T::W_INSTR);
+        dma.issue(smem, 0, 0, I0);
+        dma.issue(smem, 0, I0, I0);
+        dma.issue(smem + T::STAGE, 1, T::A_INSTR, T::W_INSTR);
+        dma.issue(smem + T::STAGE, 1, 0, I0);
     } else {
-        dma.issue(0);
-        dma.issue(1);
+        dma.issue(smem, 0);
+        dma.issue(smem + T::STAGE, 1);
     }
     wait_vmcnt<T::IPW>();
     lds_barrier();
     if (wave >= 4) lds_barrier();   // one slot behind
 
+    uint8_t *stage = smem, *stage1 = smem + T::STAGE;   // of steps ks and ks + 1
     for (int ks = 0; ks < nks; ++ks) {
-        const uint8_t *stage = smem + (ks % T::NSTAGE) * T::STAGE;
+        uint8_t *stage2 = stage1 + T::STAGE == smem + T::STAGE * T::NSTAGE ? smem : stage1 + T::STAGE;
         u32x4 wf[SUB_N][2];
 #pragma unroll
         for (int ph = 0; ph < PH; ++ph) {
@@ -620,16 +667,16 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                xf[i][0] = *reinterpret_cast<const u32x4 *>(stage + wave_row(wm, 4 * ph + i) * KB + lo);
-                xf[i][1] = *reinterpret_cast<const u32x4 *>(stage + wave_row(wm, 4 * ph + i) * KB + hi);
+                xf[i][0] = *reinterpret_cast<const u32x4 *>(stage + T::row(wm, 4 * ph + i) * KB + lo);
+                xf[i][1] = *reinterpret_cast<const u32x4 *>(stage + T::row(wm, 4 * ph + i) * KB + hi);
             }
             if constexpr (PH == 1) {
-                dma.issue(ks + 2);
+                dma.issue(stage2, ks + 2);
             } else if (ph == 0) {
-                dma.issue(ks + 1, I0, I0);
+                dma.issue(stage1, ks + 1, I0, I0);
             } else {
-                dma.issue(ks + 2, T::A_INSTR, T::W_INSTR);
-                dma.issue(ks + 2, 0, I0);
+                dma.issue(stage2, ks + 2, T::A_INSTR, T::W_INSTR);
+                dma.issue(stage2, ks + 2, 0, I0);
             }
             __builtin_amdgcn_sched_barrier(0);   // the waits stay behind the loads and copies
             wait_lgkm0();
@@ -647,7 +694,7 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (wave_row(wm, 4 * ph + i) < rows) {
+                    if (T::row(wm, 4 * ph + i) < rows) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -660,110 +707,134 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
             __builtin_amdgcn_sched_barrier(0);
             lds_barrier();
         }
+        stage = stage1;
+        stage1 = stage2;
     }
     if (wave < 4) lds_barrier();
     wait_vmcnt<0>();   // the copies past the last step, before LDS takes the output
     store_tile<T, OUT_BF16>(g, at, smem, lane, wm, wn, acc);
 }
 
-// A tile with at most 128 rows (an expert's last, or only one) takes half the phases.
-template <int OUT_BF16, int GROUPED>
+// Tiles of BM x 256. With BM = 256 a tile with at most 128 rows (an expert's last, or only one)
+// takes half the phases.
+template <int BM, int OUT_BF16, int GROUPED>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_turns_kernel(Int8Args g) {
     using T2 = Int8Tile<256, 256, 8, 2, 2>;
     using T1 = Int8Tile<128, 256, 8, 2, 3>;
-    constexpr int A = T2::STAGE * T2::NSTAGE, B = T1::STAGE * T1::NSTAGE;
+    constexpr int A = T2::STAGE * T2::NSTAGE, B = T1::STAGE * T1::NSTAGE, VARIANT = OUT_BF16 * 2 + GROUPED;
     __shared__ __attribute__((aligned(16))) uint8_t smem[A > B ? A : B];
     TileAt at;
-    if (!find_tile<T2, GROUPED>(g, at)) return;
-    constexpr int VARIANT = OUT_BF16 * 2 + GROUPED;
-    if (at.m1 - at.m0 >= 256) turns<T2, 1, VARIANT, OUT_BF16>(g, at, smem);
-    else if (at.m1 - at.m0 > 128) turns<T2, 0, VARIANT, OUT_BF16>(g, at, smem);
-    else turns<T1, 0, VARIANT, OUT_BF16>(g, at, smem);
+    if constexpr (BM == 256) {
+        if (!find_tile<T2, GROUPED>(g, at)) return;
+        if (at.m1 - at.m0 >= 256) turns<T2, 1, VARIANT, OUT_BF16>(g, at, smem);
+        else if (at.m1 - at.m0 > 128) turns<T2, 0, VARIANT, OUT_BF16>(g, at, smem);
+        else turns<T1, 0, VARIANT, OUT_BF16>(g, at, smem);
+    } else {
+        if (!find_tile<T1, GROUPED>(g, at)) return;
+        if (at.m1 - at.m0 >= 128) turns<T1, 1, 8 + VARIANT, OUT_BF16>(g, at, smem);
+        else turns<T1, 0, 8 + VARIANT, OUT_BF16>(g, at, smem);
+    }
 }
 
-// 128 x 128 tiles of 4 waves, two workgroups per CU, each step's A fragments read one row group
-// ahead of their MFMAs: for shapes with too few of the larger tiles.
-template <int BM_, int BN_, int NW_, int WAVES_M_, int OUT_BF16, int GROUPED>
-__global__ __launch_bounds__(NW_ * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_tile_kernel(Int8Args g) {
-    using T = Int8Tile<BM_, BN_, NW_, WAVES_M_, 2>;
-    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * T::NSTAGE];
+// Smaller tiles of 4 waves, for shapes with too few of the large ones. Their time is K's steps one
+// after another, each waiting for memory, so as many stages as fit are in flight (128 KB a CU).
+// Two register sets hold the fragments of two steps: the MFMAs of step ks take one while the
+// other is filled with step ks + 1. A stage buffer is free once its step is in registers
+// everywhere (lgkmcnt, then the barrier), and takes the copies of step ks + NSTAGE; steps past
+// the last copy zeros, so that the count left open always covers NSTAGE - 1 steps.
+template <class T>
+__device__ __forceinline__ u32x4 read_piece(const uint8_t *stage, int f, int wm, int w_base, int at) {
+    return *reinterpret_cast<const u32x4 *>(
+        stage + (f < T::SUB_N ? w_base + 16 * f * KB : T::row(wm, f - T::SUB_N) * KB) + at);
+}
+
+// A wave issues in order, and a copy waits for the CU's one address unit (16 cycles a copy): queued
+// in a row ahead of the MFMAs, the copies and LDS reads add to their time instead of hiding
+// behind it. So each row group's MFMAs are preceded by their share of both.
+template <class T, class Dma>
+__device__ __forceinline__ void deep_step(int ks, const Dma &dma, uint8_t *stage, const uint8_t *stage1, int wm,
+                                          int w_base, int lo, int hi,
+                                          const u32x4 (&wf)[T::SUB_N][2], const u32x4 (&xf)[T::SUB_M][2],
+                                          u32x4 (&wf_next)[T::SUB_N][2], u32x4 (&xf_next)[T::SUB_M][2],
+                                          i32x4 (&acc)[T::SUB_M][T::SUB_N]) {
+    constexpr int GROUPS = 2 * T::SUB_M, READS = 2 * (T::SUB_M + T::SUB_N);
+    __builtin_amdgcn_sched_barrier(0);          // the waits stay behind the previous step's MFMAs
+    wait_lgkm0();                               // step ks is in registers
+    wait_vmcnt<T::IPW * (T::NSTAGE - 2)>();     // step ks + 1 has landed
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+#pragma unroll
+        for (int r = q * READS / GROUPS; r < (q + 1) * READS / GROUPS; ++r) {
+            const u32x4 v = read_piece<T>(stage1, r / 2, wm, w_base, r & 1 ? hi : lo);
+            if (r / 2 < T::SUB_N) wf_next[r / 2][r & 1] = v;
+            else xf_next[r / 2 - T::SUB_N][r & 1] = v;
+        }
+        dma.issue(stage, ks + T::NSTAGE, q * T::IPW / GROUPS, (q + 1) * T::IPW / GROUPS - q * T::IPW / GROUPS);
+        const int h = q / T::SUB_M, i = q % T::SUB_M;
+#pragma unroll
+        for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = mfma_i8(wf[j][h], xf[i][h], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <int BM_, int BN_, int NSTAGE_, int OUT_BF16, int GROUPED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void int8_deep_kernel(Int8Args g) {
+    using T = Int8Tile<BM_, BN_, 4, 2, NSTAGE_>;
+    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, NSTAGE = T::NSTAGE;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % T::WAVES_M, wn = wave / T::WAVES_M;
+    const int wm = wave & 1, wn = wave >> 1;
     TileAt at;
     if (!find_tile<T, GROUPED>(g, at)) return;
     const int nks = (int)((g.K + KB - 1) / KB);
-    const Int8Dma<T, 4 + OUT_BF16 * 2 + GROUPED> dma(g, at, wave, lane, smem);
+    const Int8Dma<T, 4 + OUT_BF16 * 2 + GROUPED> dma(g, at, wave, lane);
 
     i32x4 acc[SUB_M][SUB_N];
 #pragma unroll
     for (int i = 0; i < SUB_M; ++i)
 #pragma unroll
         for (int j = 0; j < SUB_N; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
     const int frow = lane & 15, kg = lane >> 4;
     const int lo = frow * KB + (swz_chunk(frow, kg) << 4);
     const int hi = frow * KB + (swz_chunk(frow, 4 + kg) << 4);
-    const int a_base = wave_row(wm, 0) * KB, w_base = T::A_BYTES + wn * T::WN * KB;
+    const int w_base = T::A_BYTES + wn * T::WN * KB;
 
-    if (nks > 0) dma.issue(0);
-    if (nks > 1) {
-        dma.issue(1);
-        wait_vmcnt<T::IPW>();
-    } else {
-        wait_vmcnt<0>();
-    }
+#pragma unroll
+    for (int s = 0; s < NSTAGE; ++s) dma.issue(smem + s * T::STAGE, s);
+    wait_vmcnt<T::IPW *(NSTAGE - 1)>();
     lds_barrier();
-    for (int ks = 0; ks < nks; ++ks) {
-        const uint8_t *stage = smem + (ks & 1) * T::STAGE;
-        u32x4 wf[SUB_N][2];
+    u32x4 wf0[SUB_N][2], xf0[SUB_M][2], wf1[SUB_N][2], xf1[SUB_M][2];
 #pragma unroll
-        for (int j = 0; j < SUB_N; ++j) {
-            wf[j][0] = *reinterpret_cast<const u32x4 *>(stage + w_base + 16 * j * KB + lo);
-            wf[j][1] = *reinterpret_cast<const u32x4 *>(stage + w_base + 16 * j * KB + hi);
-        }
-        u32x4 xa[2] = {*reinterpret_cast<const u32x4 *>(stage + a_base + lo),
-                       *reinterpret_cast<const u32x4 *>(stage + a_base + hi)};
-#pragma unroll
-        for (int i = 0; i < SUB_M; ++i) {
-            u32x4 xn[2] = {xa[0], xa[1]};
-            if (i + 1 < SUB_M) {
-                xn[0] = *reinterpret_cast<const u32x4 *>(stage + a_base + 16 * (i + 1) * KB + lo);
-                xn[1] = *reinterpret_cast<const u32x4 *>(stage + a_base + 16 * (i + 1) * KB + hi);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < SUB_N; ++j) acc[i][j] = mfma_i8(wf[j][h], xa[h], acc[i][j]);
-            xa[0] = xn[0];
-            xa[1] = xn[1];
-        }
-        __builtin_amdgcn_sched_barrier(0);   // the waits stay behind this step's MFMAs
-        wait_lgkm0();
-        if (ks + 1 < nks) wait_vmcnt<0>();   // step ks + 1 has landed
-        lds_barrier();
-        if (ks + 2 < nks) dma.issue(ks + 2);
+    for (int r = 0; r < 2 * (SUB_M + SUB_N); ++r) {
+        const u32x4 v = read_piece<T>(smem, r / 2, wm, w_base, r & 1 ? hi : lo);
+        if (r / 2 < SUB_N) wf0[r / 2][r & 1] = v;
+        else xf0[r / 2 - SUB_N][r & 1] = v;
     }
+    uint8_t *const end = smem + NSTAGE * T::STAGE;
+    uint8_t *stage = smem;
+    for (int ks = 0; ks < nks; ks += 2) {
+        // (with an odd number of steps the last one here multiplies zeros)
+        uint8_t *stage1 = stage + T::STAGE == end ? smem : stage + T::STAGE;
+        uint8_t *stage2 = stage1 + T::STAGE == end ? smem : stage1 + T::STAGE;
+        deep_step<T>(ks, dma, stage, stage1, wm, w_base, lo, hi, wf0, xf0, wf1, xf1, acc);
+        deep_step<T>(ks + 1, dma, stage1, stage2, wm, w_base, lo, hi, wf1, xf1, wf0, xf0, acc);
+        stage = stage2;
+    }
+    wait_lgkm0();
+    wait_vmcnt<0>();   // the copies past the last step, before LDS takes the output
     store_tile<T, OUT_BF16>(g, at, smem, lane, wm, wn, acc);
 }
 
-template <int MT, int U>
-hipError_t launch_few(Int8Args a, bool out_bf16, hipStream_t stream) {
-    a.tiles_n = (int)((a.N + 15) / 16);
-    // grouped: an upper bound on the experts' row blocks (an expert without rows has none)
-    int64_t blocks = (a.M + 16 * MT - 1) / (16 * MT);
-    if (a.offsets) blocks += a.experts < a.M ? a.experts : a.M;
-    const int64_t units = blocks * a.tiles_n;
+template <int QUANT>
+hipError_t launch_few(const Int8FewArgs &a, bool out_bf16, hipStream_t stream) {
+    const int64_t units = (a.N + 15) / 16;
     if (units * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    constexpr int U = QUANT ? 14 : 8;   // (28 steps, K = 7168's quarter, all in flight)
     const dim3 grid((unsigned)units), block(256);
-    if (a.offsets) {
-        if (out_bf16) int8_few_kernel<MT, U, 1, 1><<<grid, block, 0, stream>>>(a);
-        else int8_few_kernel<MT, U, 0, 1><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (out_bf16) int8_few_kernel<MT, U, 1, 0><<<grid, block, 0, stream>>>(a);
-        else int8_few_kernel<MT, U, 0, 0><<<grid, block, 0, stream>>>(a);
-    }
+    if (out_bf16) int8_few_kernel<U, QUANT, 1><<<grid, block, 0, stream>>>(a);
+    else int8_few_kernel<U, QUANT, 0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -784,30 +855,21 @@ bool lay_out(Int8Args &a, int BM, int BN, int threads) {
     return (int64_t)a.tiles_m * a.tiles_n * threads <= 0xFFFFFFFFll;
 }
 
+template <int BM, int GROUPED>
 hipError_t launch_turns(Int8Args a, bool out_bf16, hipStream_t stream) {
-    if (!lay_out(a, 256, 256, 512)) return hipErrorInvalidValue;
+    if (!lay_out(a, BM, 256, 512)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(512);
-    if (a.offsets) {
-        if (out_bf16) int8_turns_kernel<1, 1><<<grid, block, 0, stream>>>(a);
-        else int8_turns_kernel<0, 1><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (out_bf16) int8_turns_kernel<1, 0><<<grid, block, 0, stream>>>(a);
-        else int8_turns_kernel<0, 0><<<grid, block, 0, stream>>>(a);
-    }
+    if (out_bf16) int8_turns_kernel<BM, 1, GROUPED><<<grid, block, 0, stream>>>(a);
+    else int8_turns_kernel<BM, 0, GROUPED><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <int BM, int BN, int NW, int WAVES_M>
-hipError_t launch_tile(Int8Args a, bool out_bf16, hipStream_t stream) {
-    if (!lay_out(a, BM, BN, NW * 64)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(NW * 64);
-    if (a.offsets) {
-        if (out_bf16) int8_tile_kernel<BM, BN, NW, WAVES_M, 1, 1><<<grid, block, 0, stream>>>(a);
-        else int8_tile_kernel<BM, BN, NW, WAVES_M, 0, 1><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (out_bf16) int8_tile_kernel<BM, BN, NW, WAVES_M, 1, 0><<<grid, block, 0, stream>>>(a);
-        else int8_tile_kernel<BM, BN, NW, WAVES_M, 0, 0><<<grid, block, 0, stream>>>(a);
-    }
+template <int BM, int BN, int NSTAGE, int GROUPED>
+hipError_t launch_deep(Int8Args a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a, BM, BN, 256)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(256);
+    if (out_bf16) int8_deep_kernel<BM, BN, NSTAGE, 1, GROUPED><<<grid, block, 0, stream>>>(a);
+    else int8_deep_kernel<BM, BN, NSTAGE, 0, GROUPED><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -825,13 +887,51 @@ hipError_t launch_int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, 
 
 hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias,
                             void *y, bool out_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+    // Few tiles of 32 x 64 and few rows: 16 channels a workgroup use more of the CUs (16 x 1536 x 7168:
+    // 9.3 us against 10.1; 16 x 7168 x 7168, 112 tiles: 15.9 against 10.6).
+    const int64_t tiles32 = (M + 31) / 32 * ((N + 63) / 64);
+    if (M <= kFewRows && tiles32 <= 64)
+        return launch_few<0>({a, sa, nullptr, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
     const Int8Args g{a, sa, w, sw, bias, y, nullptr, nullptr, M, N, K, M, 0, 0, 0, 1};
-    if (M <= 16) return launch_few<1, 8>(g, out_bf16, stream);
-    if (M <= 32) return launch_few<2, 4>(g, out_bf16, stream);
-    if (M <= 64) return launch_few<4, 4>(g, out_bf16, stream);
-    const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
-    if (large >= 256) return launch_turns(g, out_bf16, stream);
-    return launch_tile<128, 128, 4, 2>(g, out_bf16, stream);
+    // The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps. The
+    // constants are fitted to times at K = 512 and 7168, N = 1536 and 7168, M = 16 to 4096 (us): the
+    // first round's step, a later round's (less where two workgroups share a CU's waits), the epilogue.
+    const double steps = (double)((K + KB - 1) / KB);
+    auto time = [&](int bm, int bn, double first, double more, double end) {
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        const double rounds = (double)((tiles + 255) / 256);
+        return steps * (first + more * (rounds - 1.0)) + end * rounds;
+    };
+    const double t[6] = {time(32, 64, 0.155, 0.125, 1.1), time(64, 64, 0.21, 0.18, 1.4),
+                         time(64, 128, 0.34, 0.27, 1.5),  time(128, 128, 0.45, 0.53, 5.0),
+                         time(128, 256, 0.75, 0.83, 5.7), time(256, 256, 1.3, 1.5, 8.0)};
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (t[i] < t[best]) best = i;
+    switch (best) {
+    case 0: return launch_deep<32, 64, 6, 0>(g, out_bf16, stream);
+    case 1: return launch_deep<64, 64, 5, 0>(g, out_bf16, stream);
+    case 2: return launch_deep<64, 128, 3, 0>(g, out_bf16, stream);
+    case 3: return launch_deep<128, 128, 4, 0>(g, out_bf16, stream);
+    case 4: return launch_turns<128, 0>(g, out_bf16, stream);
+    default: return launch_turns<256, 0>(g, out_bf16, stream);
+    }
+}
+
+// Quantised rows of a linear layer between the two launches: the codes, then the scales
+size_t int8_linear_workspace_bytes(int64_t M, int64_t K) {
+    if (M <= kFewQuantRows && K <= kFewQuantK) return 0;
+    return (size_t)(M * K + 4 * M);
+}
+
+hipError_t launch_int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y,
+                              bool out_bf16, int64_t M, int64_t N, int64_t K, void *workspace, hipStream_t stream) {
+    if (M <= kFewQuantRows && K <= kFewQuantK)
+        return launch_few<1>({nullptr, nullptr, x, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
+    int8_t *q = static_cast<int8_t *>(workspace);
+    float *s = reinterpret_cast<float *>(q + M * K);
+    if (hipError_t e = launch_int8_quant(x, q, s, M, K, stream)) return e;
+    return launch_int8_gemm(q, s, w, sw, bias, y, out_bf16, M, N, K, stream);
 }
 
 hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw,
@@ -839,8 +939,18 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
                                     int64_t experts, int64_t M, int64_t tokens, int64_t N, int64_t K,
                                     hipStream_t stream) {
     const Int8Args g{a, sa, w, sw, nullptr, y, offsets, rows, M, N, K, tokens, (int)experts, 0, 0, 1};
-    if (M <= 16 * experts) return launch_few<1, 8>(g, out_bf16, stream);
-    return launch_turns(g, out_bf16, stream);
+    // By the average rows of an expert (its true count is on the device). Measured in us, 64 experts'
+    // 4096 x 7168, at 1.5 / 6 / 24 / 96 / 192 rows: 32 x 64 204 / 277 / 355 / 638 / 1072, 64 x 128
+    // 216 / 290 / 332 / 477 / 681, 128 x 256 218 / 292 / 317 / 407 / 538, 256 x 256
+    // 218 / 292 / 333 / 408 / 488. With a short K the smallest tile's many epilogues count: 256 experts'
+    // 2048 x 1024 at 2 rows, 103 / 84 / 96 / 96.
+    const int64_t mean = M / experts;
+    if (mean < 24) {
+        if (K >= 4096) return launch_deep<32, 64, 6, 1>(g, out_bf16, stream);
+        return launch_deep<64, 128, 3, 1>(g, out_bf16, stream);
+    }
+    if (mean < 96) return launch_turns<128, 1>(g, out_bf16, stream);
+    return launch_turns<256, 1>(g, out_bf16, stream);
 }
 
 }  // namespace fp8q

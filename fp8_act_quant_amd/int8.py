@@ -75,10 +75,27 @@ def int8_gemm(a: torch.Tensor, a_s: torch.Tensor, w: torch.Tensor, w_s: torch.Te
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
                 bias: torch.Tensor | None = None, out_dtype=torch.bfloat16) -> torch.Tensor:
     """y = x . weight^T (+ bias) for bf16 activations x [..., K] and an 8-bit weight [N, K] with
-    one scale per channel [N] (as int8_quant gives them): x is quantised per token, then
-    multiplied by int8_gemm."""
-    q, s = int8_quant(x)
-    return int8_gemm(q, s, weight, weight_scale, bias, out_dtype=out_dtype)
+    one scale per channel [N] (as int8_quant gives them): int8_gemm of int8_quant(x), bit for
+    bit, in one call (at most 4 tokens: in one launch)."""
+    need(x, "x", torch.bfloat16, align=16)
+    need(weight, "weight", torch.int8, align=16, device=x.device)
+    if x.dim() < 1 or weight.dim() != 2 or weight.shape[1] != x.shape[-1]:
+        raise ValueError("weight must be [N, K] with the activation's K")
+    N, K = weight.shape
+    _depth(K)
+    need(weight_scale, "weight_scale", torch.float32, (N,), device=x.device)
+    b_ptr = None
+    if bias is not None:
+        need(bias, "bias", torch.float32, (N,), device=x.device)
+        b_ptr = bias.data_ptr()
+    M = math.prod(x.shape[:-1])
+    out = _out(None, (*x.shape[:-1], N), out_dtype, x)
+    ws_bytes = lib.int8_linear_workspace_bytes(M, N, K)
+    # from torch's allocator, which keeps it from calls on other streams until this one is done
+    ws = x.new_empty(ws_bytes, dtype=torch.int8) if ws_bytes else None
+    launch("int8_linear", lib.int8_linear, x, x.data_ptr(), weight.data_ptr(), weight_scale.data_ptr(), b_ptr,
+           out.data_ptr(), CODE[out_dtype], M, N, K, ws.data_ptr() if ws_bytes else None, ws_bytes)
+    return out
 
 
 def int8_grouped_gemm(a: torch.Tensor, a_s: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor,

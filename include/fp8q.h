@@ -60,7 +60,7 @@ extern "C" {
 #define FP8Q_ERR_UNSUPPORTED 5 /* no gfx950 device is current                               */
 #define FP8Q_ERR_LAUNCH 6      /* the kernel launch failed                                  */
 #define FP8Q_ERR_WORKSPACE 7   /* more scratch needed than fp8_block_gemm_noalloc holds, or
-                                  a workspace smaller than moe_place needs                  */
+                                  a workspace smaller than moe_place or int8_linear need    */
 
 /* Output dtypes of fp8_block_gemm (low 8 bits of its y_dtype argument). */
 #define FP8Q_OUT_F32 0
@@ -346,6 +346,16 @@ int int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, int64_t K, voi
  *   the bias (or zeros; sa and sw are then not read). */
 int int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias, void *y,
               int y_dtype, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* int8_linear -- int8_quant of x [M, K] bf16 (16-byte aligned) and int8_gemm of its codes: a
+ * linear layer with 8-bit weights in one call (few rows: in one launch). Bit for bit what the two
+ * calls give; arguments as theirs, M < 2^24.
+ *   workspace: int8_linear_workspace_bytes bytes of any contents, 16-byte aligned (NULL where
+ *   that is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at the same
+ *   time must not share it. */
+int int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y, int y_dtype, int64_t M,
+                int64_t N, int64_t K, void *workspace, size_t workspace_bytes, void *stream);
+size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* int8_grouped_gemm -- int8_gemm for every expert's rows in one launch.
  *   offsets [experts + 1] int64 on the device, as for fp8_grouped_gemm (clamped the same way);

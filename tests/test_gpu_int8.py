@@ -53,6 +53,8 @@ def check(y, a, sa, w, sw, bias, out):
     (16, 130, 1040, True), (17, 33, 128, False), (31, 1000, 656, True), (33, 15, 64, True), (64, 300, 2064, False),
     (65, 129, 176, True), (128, 128, 128, False), (129, 257, 16, True), (200, 100, 1040, False),
     (300, 1001, 304, True), (1000, 576, 1536, False), (4096, 4100, 272, True), (4097, 4096, 144, False),
+    (9, 7168, 1536, True), (100, 5000, 2048, False), (700, 1536, 3088, True), (513, 7168, 1024, False),
+    (1030, 7168, 528, True), (2050, 7100, 1040, False),
 ])
 def test_gemm(M, N, K, biased, out):
     g = rng(M + N + K)
@@ -96,6 +98,9 @@ def test_gemm_empty():
     bias = torch.randn(5, device="cuda")
     y = fq.int8_gemm(a, torch.ones(3, device="cuda"), w, torch.ones(5, device="cuda"), bias, out_dtype=torch.float32)
     assert torch.equal(y, bias.expand(3, 5))
+    z = fq.int8_linear(torch.empty((3, 0), dtype=torch.bfloat16, device="cuda"), w, torch.ones(5, device="cuda"), bias,
+                       out_dtype=torch.float32)
+    assert torch.equal(z, y)
     big = fq.int8_gemm(torch.empty((300, 0), dtype=torch.int8, device="cuda"), torch.ones(300, device="cuda"), w,
                        torch.ones(5, device="cuda"), out_dtype=torch.float32)
     assert (big == 0).all() and big.shape == (300, 5)
@@ -161,7 +166,9 @@ def test_quant_zero_rows_and_empty():
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-@pytest.mark.parametrize("shape,N", [((1, 256), 96), ((2, 3, 1536), 200), ((300, 512), 576)])
+@pytest.mark.parametrize("shape,N", [((1, 256), 96), ((2, 3, 1536), 200), ((300, 512), 576), ((1, 16), 1),
+                                     ((2, 1040), 33), ((3, 7168), 130), ((4, 8192), 100), ((4, 8208), 100),
+                                     ((5, 7168), 64), ((2, 2, 64), 7168), ((0, 64), 16)])
 def test_linear(shape, N, out):
     """Quantisation and product against the 64-bit product of what the codes stand for."""
     g = rng(N)
@@ -307,6 +314,12 @@ def test_refusals():
         fq.int8_gemm(a, sa, w.cpu(), sw)
     with pytest.raises(ValueError):
         fq.int8_gemm(torch.zeros(4 * 32 + 1, dtype=torch.int8, device="cuda")[1:].view(4, 32), sa, w, sw)
+    with pytest.raises(TypeError):
+        fq.int8_linear(a, w, sw)
+    with pytest.raises(ValueError):
+        fq.int8_linear(a.bfloat16(), w[:, :16].contiguous(), sw)
+    with pytest.raises(ValueError):
+        fq.int8_linear(a.bfloat16(), w, sw[:7])
     with pytest.raises(TypeError):
         fq.int8_quant(torch.zeros((2, 16), device="cuda"))
     with pytest.raises(ValueError):

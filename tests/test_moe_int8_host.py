@@ -102,6 +102,18 @@ def test_int8_validation(L):
         assert gemm(**bad) == L.FP8Q_ERR_ALIGN
     assert gemm(M=0, a=None, y=None) == gemm(N=0, w=None) == L.FP8Q_OK
 
+    def linear(x=FAKE, w=FAKE, sw=FAKE, bias=None, y=FAKE, dtype=1, M=100, N=8, K=32, ws=FAKE, size=1 << 20):
+        return lib.int8_linear(x, w, sw, bias, y, dtype, M, N, K, ws, size, None)
+    for bad in (dict(M=-1), dict(K=24), dict(M=1 << 24)):
+        assert linear(**bad) == L.FP8Q_ERR_SHAPE
+    assert linear(x=None) == linear(sw=None) == linear(y=None) == L.FP8Q_ERR_NULL
+    assert linear(x=FAKE + 8) == linear(ws=FAKE + 8) == L.FP8Q_ERR_ALIGN
+    need = lib.int8_linear_workspace_bytes(100, 8, 32)
+    assert need >= 100 * 36 and lib.int8_linear_workspace_bytes(1, 8, 32) == 0
+    assert lib.int8_linear_workspace_bytes(0, 8, 32) == lib.int8_linear_workspace_bytes(100, 8, 31) == 0
+    assert linear(ws=None) == linear(size=need - 1) == L.FP8Q_ERR_WORKSPACE
+    assert linear(M=0, x=None, ws=None) == L.FP8Q_OK
+
     def grouped(a=FAKE, sa=FAKE, w=FAKE, sw=FAKE, off=FAKE, rows=None, y=FAKE, dtype=0, E=2, M=4, tokens=4, N=8, K=32):
         return lib.int8_grouped_gemm(a, sa, w, sw, off, rows, y, dtype, E, M, tokens, N, K, None)
     for bad in (dict(E=0), dict(E=1025), dict(tokens=3), dict(tokens=-1, rows=FAKE), dict(K=8), dict(M=1 << 31),
