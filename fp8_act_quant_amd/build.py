@@ -1,16 +1,19 @@
-"""Build libfp8q.so (the HIP kernels and the C ABI) in-tree for gfx950 with hipcc."""
+"""Build libfp8q.so (the HIP kernels and the C ABI) in-tree for gfx950 with hipcc, and _native.so,
+the Python binding of the routed-expert and 8-bit operators, against it and torch."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8q.so")
+BINDING = os.path.join(PKG, "_native.so")
 
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "transpose.hip", "bf16_gemm.hip", "route.hip", "place.hip",
            "int8.hip"]
@@ -50,7 +53,35 @@ def build(verbose: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("hipcc failed building libfp8q.so")
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_native.so: host code only. It finds libfp8q.so beside itself; torch's libraries are loaded
+    by the `import torch` before it."""
+    import torch
+    top = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    cxx = shutil.which("g++")
+    if cxx is None:
+        raise RuntimeError("g++ not found; it is required to build _native.so")
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for d in (os.path.join(top, "include"), os.path.join(rocm, "include"),
+                         sysconfig.get_paths()["include"]) for f in ("-isystem", d)),
+           "-I", INCLUDE, os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(top, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _native.so")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

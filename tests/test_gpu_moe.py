@@ -419,6 +419,14 @@ def test_refusals():
         fq.moe_place(i, 0)
     with pytest.raises(ValueError):
         fq.moe_place(i, 8, first=-1)
+    with pytest.raises(fq.Fp8qError):   # refused by the library itself
+        fq.moe_place(i, 8, first=2 ** 31)
+    with pytest.raises(ValueError):
+        fq.moe_place(i, 8, first=2 ** 70)
+    with pytest.raises(TypeError):
+        fq.moe_route(x, 2.5)
+    with pytest.raises(TypeError):
+        fq.moe_combine([1.0], i, w)
     h = torch.zeros((8, 32), device="cuda")
     with pytest.raises(ValueError):
         fq.moe_combine(h, i, w[:3])
