@@ -187,46 +187,53 @@ __device__ __forceinline__ void expert_rows(const Int8Args &g, int e, int64_t &r
     r1 = r1 < r0 ? r0 : (r1 > g.M ? g.M : r1);
 }
 
-// Grouped work order. Expert e has n_e = ceil(rows_e / bm) row blocks; its n_e * cols tiles are
-// numbered consecutively, experts in order, the row block varying fastest, so that tiles which
-// read the same weight panel are neighbours and an expert's rows stay in the L2 of the XCD
-// that walks it. count_blocks gives the number of row blocks of all experts, find_block the
-// expert, rows and column of tile `unit`. Each wave works them out by itself, 64 experts at a time.
-__device__ __forceinline__ int blocks_of(const Int8Args &g, int e, int bm) {
-    int64_t r0 = 0, r1 = 0;
-    if (e < g.experts) expert_rows(g, e, r0, r1);
-    return (int)((r1 - r0 + bm - 1) / bm);
-}
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d, 64);
-        v += lane >= d ? o : 0;
-    }
+// Grouped work order. An expert's rows are cut into blocks of BM, the last of them short. Its tiles
+// are numbered with the row block varying fastest, experts one after another: neighbours then
+// read the same weight panel, and an expert's rows stay in the L2 of the XCD that walks it. The
+// numbers are dealt to the XCDs in contiguous, equal runs. (64 experts' 4096 x 7168, 12288 rows:
+// 508 us; numbered by size, long tiles first, 542, an expert's blocks then being read through
+// several XCDs; runs of equal cost instead of equal counts 536, the grid's larger bound costing
+// more than the balance gains.)
+//
+// Each wave works this out by itself, 64 experts at a time.
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive prefix sum over the lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast31 into rows 2 and 3
     return v;
 }
-__device__ __forceinline__ int count_blocks(const Int8Args &g, int bm) {
+template <int BM>
+__device__ __forceinline__ int blocks_of(const Int8Args &g, int e) {   // of expert e's rows
+    int64_t r0 = 0, r1 = 0;
+    if (e < g.experts) expert_rows(g, e, r0, r1);
+    return ((int)(r1 - r0) + BM - 1) / BM;
+}
+template <int BM>
+__device__ __forceinline__ int count_blocks(const Int8Args &g) {
     const int lane = threadIdx.x & 63;
     int n = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 64) n += blocks_of(g, e0 + lane, bm);
-    return __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
+    for (int e0 = 0; e0 < g.experts; e0 += 64) n += blocks_of<BM>(g, e0 + lane);
+    return __builtin_amdgcn_readlane(wave_scan(n), 63);
 }
-__device__ __forceinline__ bool find_block(const Int8Args &g, int bm, int cols, int unit, int &expert, int64_t &row0,
+// the expert, rows and column of tile `index`; false: there is none
+template <int BM>
+__device__ __forceinline__ bool find_block(const Int8Args &g, int cols, int index, int &expert, int64_t &row0,
                                            int64_t &row1, int &col) {
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
-        const int n = blocks_of(g, e0 + lane, bm);
-        const int sum = wave_scan(n, lane);
-        const int first = (before + sum - n) * cols;
-        const uint64_t hit = __ballot(unit >= first && unit < first + n * cols);
+        const int n = blocks_of<BM>(g, e0 + lane), sum = wave_scan(n), first = (before + sum - n) * cols;
+        const uint64_t hit = __ballot(index >= first && index < first + n * cols);
         if (hit) {
-            const int at = __builtin_ctzll(hit);
-            const int within = unit - __builtin_amdgcn_readlane(first, at), blocks = __builtin_amdgcn_readlane(n, at);
-            expert = e0 + at;
-            col = within / blocks;
+            const int l = __builtin_ctzll(hit);
+            const int within = index - __builtin_amdgcn_readlane(first, l), per = __builtin_amdgcn_readlane(n, l);
+            expert = e0 + l;
+            col = within / per;
             expert_rows(g, expert, row0, row1);
-            row0 += (int64_t)(within - col * blocks) * bm;
+            row0 += (int64_t)(within - col * per) * BM;
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
@@ -423,13 +430,13 @@ struct TileAt {
     const float *sw;
 };
 
-// Tile of a workgroup: b runs on XCD b % 8, and each XCD takes a contiguous run of tile numbers;
-// one weight's tiles are numbered down `group` tile rows per tile column, so that the tiles
-// that an XCD holds at once share A and W panels in its L2. False: no tile (grouped: the grid
-// is an upper bound; the numbers are dealt over the real tiles, so every XCD has its share).
+// Tile of a workgroup. Workgroup b runs on XCD b % 8, and each XCD takes a contiguous run of the
+// tile numbers. One weight's tiles are numbered down `group` tile rows per tile column, so that
+// the tiles that an XCD holds at once share A and W panels in its L2. False: no tile (grouped: the
+// grid is an upper bound).
 template <class T, int GROUPED>
 __device__ __forceinline__ bool find_tile(const Int8Args &g, TileAt &t) {
-    const int tiles = (GROUPED ? count_blocks(g, T::BM) : g.tiles_m) * g.tiles_n;
+    const int tiles = (GROUPED ? count_blocks<T::BM>(g) : g.tiles_m) * g.tiles_n;
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
     const int q = tiles >> 3, rem = tiles & 7;
     const int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
@@ -437,7 +444,7 @@ __device__ __forceinline__ bool find_tile(const Int8Args &g, TileAt &t) {
     t.sw = g.sw;
     if constexpr (GROUPED) {
         int expert, col;
-        if (slot >= q + (xcd < rem) || !find_block(g, T::BM, g.tiles_n, tl, expert, t.m0, t.m1, col)) return false;
+        if (slot >= q + (xcd < rem) || !find_block<T::BM>(g, g.tiles_n, tl, expert, t.m0, t.m1, col)) return false;
         t.n0 = (int64_t)col * T::BN;
         t.w += (int64_t)expert * g.N * g.K;
         t.sw += (int64_t)expert * g.N;
@@ -838,10 +845,11 @@ hipError_t launch_few(const Int8FewArgs &a, bool out_bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// tile counts and the tile rows walked per tile column (an XCD's ~32 resident tiles form a
-// compact block); false if the grid would be too large
+// The launch's tiles: their counts (grouped: an upper bound, full row blocks and a last one for each
+// expert that has rows), and the tile rows walked per tile column (an XCD's ~32 resident tiles
+// form a compact block). False if the grid would be too large.
 bool lay_out(Int8Args &a, int BM, int BN, int threads) {
-    a.tiles_m = (int)((a.M + BM - 1) / BM + (a.offsets ? (a.experts < a.M ? a.experts : a.M) : 0));
+    a.tiles_m = (int)(a.offsets ? a.M / BM + (a.experts < a.M ? a.experts : a.M) : (a.M + BM - 1) / BM);
     a.tiles_n = (int)((a.N + BN - 1) / BN);
     int64_t best = -1;
     for (int gsz = 1; gsz <= 32; gsz *= 2) {
