@@ -335,22 +335,30 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
             acc = mfma_i8(wv[b][u], x, acc);
         }
     };
-    load(0, s0);
     float scale = 0.0f;   // of this lane's row
     if constexpr (QUANT) {
-        load(1, s0 + U);
         constexpr int NV = kFewQuantK / 8 / 256;   // pieces of 8 elements a thread keeps of a row
         u32x4 v[kFewQuantRows][NV];
+        // the rows first: loads return in order, and these are needed before W
 #pragma unroll
         for (int m = 0; m < kFewQuantRows; ++m) {
             if (m < M) {
-                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int p = threadIdx.x + 256 * i;
                     v[m][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                             ra, 8 * p < K ? (uint32_t)(2 * (m * K + 8 * p)) : kNowhere, 0, 0));
                 }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(0, s0);
+        load(1, s0 + U);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < kFewQuantRows; ++m) {
+            if (m < M) {
+                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const uint32_t b = absmax_bits8(v[m][i]);
@@ -378,6 +386,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
         }
         __syncthreads();
     } else {
+        load(0, s0);
         if (row < M && K > 0) scale = g.sa[row];
     }
     for (int s = s0; s < s1; s += 2 * U) {
