@@ -35,10 +35,10 @@ struct RouteArgs {
     float scale;
 };
 
-// Order-preserving integer key of a float: a > b as floats is key(a) > key(b) as unsigned.
-// Every key of a number is above 0; 0 stands for "no candidate". NaN ranks as -inf.
+// Order-preserving integer key of a number: a > b as floats is key(a) > key(b) as unsigned. Every
+// number's key is above 0; 0 stands for "no candidate". (A choice is never -0: scores are +0 at the
+// least, and +0 + -0 = +0.)
 __device__ __forceinline__ uint32_t key_of(float c) {
-    c = c != c ? -__builtin_inff() : c + 0.0f;   // (-0 ranks as +0)
     const uint32_t u = __float_as_uint(c);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
@@ -67,12 +67,20 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// sums over the wave's 64 lanes, in a fixed order and the same in every lane
 __device__ __forceinline__ float read_f(float v, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp_f<kXor1>(v));
+    v = fmaxf(v, dpp_f<kXor2>(v));
+    v = fmaxf(v, dpp_f<kMirror8>(v));
+    v = fmaxf(v, dpp_f<kMirror16>(v));
+    return fmaxf(fmaxf(read_f(v, 0), read_f(v, 16)), fmaxf(read_f(v, 32), read_f(v, 48)));
+}
+
+// sums over the wave's 64 lanes, in a fixed order and the same in every lane
 __device__ __forceinline__ float wave_sum(float v) {
     v += dpp_f<kXor1>(v);
     v += dpp_f<kXor2>(v);
@@ -156,10 +164,10 @@ __device__ __forceinline__ void sigmoid(const float (&x)[V], float (&s)[V]) {
 // total = 0 when no value is above -inf, and every score is then 0. e: the numerators.
 template <int V>
 __device__ __forceinline__ void softmax_of(const float (&x)[V], float (&e)[V], float &top, float &total) {
-    uint32_t m = key_of(x[0]);
+    float m = x[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = umax(m, key_of(x[i]));
-    top = of_key(wave_max(m));
+    for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+    top = wave_max(m);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -169,13 +177,26 @@ __device__ __forceinline__ void softmax_of(const float (&x)[V], float (&e)[V], f
     total = top == -__builtin_inff() ? 0.0f : (float)wave_sum(sum);
 }
 
-// The scores of a lane's logits; top and total are softmax's.
+// The scores of a lane's logits; top and total are softmax's. e / total is rounded to nearest:
+// Markstein's two corrections on the rounded reciprocal, which are exact while their residual
+// does not underflow (e >= 2^-90, or 0); smaller ones take the division.
 template <int V, int SOFTMAX>
 __device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], float &top, float &total) {
     if constexpr (SOFTMAX) {
-        softmax_of<V>(x, s, top, total);
+        float e[V];
+        softmax_of<V>(x, e, top, total);
+        const float y = 1.0f / total;
+        bool far = false;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = total > 0.0f ? s[i] / total : 0.0f;
+        for (int i = 0; i < V; ++i) {
+            const float q = e[i] * y;
+            s[i] = __builtin_fmaf(__builtin_fmaf(-q, total, e[i]), y, q);
+            far |= e[i] != 0.0f && !(e[i] >= 0x1p-90f);
+        }
+        if (__any(far) || !(total > 0.0f)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = total > 0.0f ? e[i] / total : 0.0f;
+        }
     } else {
         sigmoid<V>(x, s);
     }
@@ -277,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
         for (int j = 0; j < a.k; ++j) {
             const uint32_t best = wave_max(key[0]);
             const int owner = __builtin_ctzll(__ballot(key[0] == best));
-            const int e = __builtin_amdgcn_readlane(e0 + (int)(pos & 0xFF), owner);
+            const int e = __builtin_amdgcn_readlane(e0, owner) + (__builtin_amdgcn_readlane((int)(uint32_t)pos, owner) & 0xFF);
             mine = lane == j ? e : mine;
             const bool own = lane == owner;
 #pragma unroll
