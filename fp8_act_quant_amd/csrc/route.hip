@@ -113,21 +113,21 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
     else return reinterpret_cast<const float *>(p)[i];
 }
 
-// V consecutive logits from row + first, n of which belong to this lane; -inf for the others.
-// FULL: n is V or at most 0 and rows are aligned to V elements, so they come in one load.
-// Every lane loads (from a place within the row if it has nothing to load), without a branch.
+// V consecutive elements from row + first, n of which belong to this lane (what the others hold is
+// some element of the row). FULL: n is V or at most 0 and rows are aligned to V elements, so they
+// come in one load. Every lane loads, without a branch.
 template <int V, int BF16, int FULL>
-__device__ __forceinline__ void load_logits(const void *p, int64_t row, int first, int n, int E, float (&x)[V]) {
+__device__ __forceinline__ void load_row(const void *p, int64_t row, int first, int n, int E, float (&x)[V]) {
     if constexpr (FULL) {
-        const int64_t i = row + (n > 0 ? first : 0);
+        const int i = n > 0 ? first : 0;
         if constexpr (BF16) {
             typedef uint16_t piece __attribute__((ext_vector_type(V)));
-            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const uint16_t *>(p) + i);
+            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const uint16_t *>(p) + row + i);
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = __uint_as_float((uint32_t)u[j] << 16);
         } else {
             typedef float piece __attribute__((ext_vector_type(V)));
-            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const float *>(p) + i);
+            const piece u = *reinterpret_cast<const piece *>(reinterpret_cast<const float *>(p) + row + i);
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = u[j];
         }
@@ -135,8 +135,11 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t row, int firs
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = load_logit<BF16>(p, row + min(first + j, E - 1));
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = j < n ? x[j] : -__builtin_inff();
+}
+// whether element j of a lane's V is one of its n
+template <int FULL>
+__device__ __forceinline__ bool has(int j, int n) {
+    return FULL ? n > 0 : j < n;
 }
 
 // 1 / (1 + exp(-x)) with every step rounded to nearest. The quotient is v_rcp_f32 and one
@@ -230,8 +233,10 @@ __device__ __forceinline__ void merge2(uint32_t &m1, uint32_t &m2, uint32_t o1, 
 // (some 400 a token), not by the 4 E bytes it reads.
 template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    typedef float piece __attribute__((ext_vector_type(V)));
+    __shared__ piece rows[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= a.T) return;
     const int lanes = 1 << a.lane_shift;
     const int group = lane >> a.lane_shift;
@@ -240,16 +245,25 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
     const int e0 = group * a.per + at;
     const int64_t row = t * a.E;
 
-    float x[V], s[V], top = 0.0f, total = 1.0f;
-    load_logits<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
-    float bias[V];
+    float x[V], s[V], bias[V], top = 0.0f, total = 1.0f;
+    load_row<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = 0.0f;
-    if (a.bias) load_logits<V, 0, 0>(a.bias, 0, e0, n, a.E, bias);
+    if (a.bias) load_row<V, 0, FULL>(a.bias, 0, e0, n, a.E, bias);
+    if constexpr (SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = has<FULL>(i, n) ? x[i] : -__builtin_inff();
+    }
     scores<V, SOFTMAX>(x, s, top, total);
     uint32_t key[V];
+    piece kept_scores;
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = i < n ? key_of(s[i] + bias[i]) : 0u;
+    for (int i = 0; i < V; ++i) {
+        const uint32_t k = key_of(s[i] + bias[i]);
+        key[i] = has<FULL>(i, n) ? k : 0u;
+        kept_scores[i] = s[i];
+    }
+    rows[wave][lane] = kept_scores;   // lane l's i-th expert is place l * V + i
 
     if (a.groups > 1) {
         uint32_t m1 = key[0], m2 = 0;   // the two largest keys of the group
@@ -275,7 +289,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
         for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
     }
 
-    int mine = 0;   // lane j: the token's j-th expert
+    int mine = 0;   // lane j: the place of the token's j-th expert
     if constexpr (V <= 8) {
         uint64_t pos = 0;   // the sorted keys' places, 8 bits each
         int p[V];
@@ -298,8 +312,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
         for (int j = 0; j < a.k; ++j) {
             const uint32_t best = wave_max(key[0]);
             const int owner = __builtin_ctzll(__ballot(key[0] == best));
-            const int e = __builtin_amdgcn_readlane(e0, owner) + (__builtin_amdgcn_readlane((int)(uint32_t)pos, owner) & 0xFF);
-            mine = lane == j ? e : mine;
+            const int place = owner * V + (__builtin_amdgcn_readlane((int)(uint32_t)pos, owner) & 0xFF);
+            mine = lane == j ? place : mine;
             const bool own = lane == owner;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -322,20 +336,23 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
             const bool own = lane == owner;
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = own && i == pos ? 0u : key[i];
-            const int e = __builtin_amdgcn_readlane(e0 + pos, owner);
-            mine = lane == j ? e : mine;
+            const int place = owner * V + __builtin_amdgcn_readlane(pos, owner);
+            mine = lane == j ? place : mine;
         }
     }
 
-    const float xe = load_logit<BF16>(a.logits, row + mine);
-    float w = lane < a.k ? score_of<SOFTMAX>(xe, top, total) : 0.0f;
+    // (LDS accesses of a wave run in order; the fence keeps the compiler's order)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float w = lane < a.k ? reinterpret_cast<const float *>(rows[wave])[mine] : 0.0f;
+    const int from = mine / V;   // the lane that holds it
+    const int expert = (from >> a.lane_shift) * a.per + (from & (lanes - 1)) * V + mine % V;
     if (a.renormalize) {
         const float sum = wave_sum(w);
         w = sum != 0.0f ? w / sum : 0.0f;   // (a token none of whose experts has a score has weights 0)
     }
     if (lane < a.k) {
         a.weights[t * a.k + lane] = w * a.scale;
-        a.experts[t * a.k + lane] = mine;
+        a.experts[t * a.k + lane] = expert;
     }
 }
 
@@ -360,7 +377,7 @@ template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a) {
     typedef float piece __attribute__((ext_vector_type(V)));
     __shared__ piece rows[kWaves][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= a.T) return;
     const int e0 = lane * V, n = max(min(a.E - e0, V), 0);
@@ -372,7 +389,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a
     const float xe = load_logit<BF16>(a.logits, row + (there ? e : 0));
     float x[V], p[V], top = 0.0f, total = 1.0f;
     if constexpr (SOFTMAX) {
-        load_logits<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
+        load_row<V, BF16, FULL>(a.logits, row, e0, n, a.E, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = has<FULL>(i, n) ? x[i] : -__builtin_inff();
         scores<V, 1>(x, p, top, total);
     }
     piece zero;
@@ -456,7 +475,7 @@ bool whole(int V, int per, bool bf16, const void *p, const void *q) {
 
 template <int V>
 void route_v(const RouteArgs &a, bool bf16, bool softmax, dim3 grid, hipStream_t st) {
-    const bool full = whole(V, a.per, bf16, a.logits, nullptr);
+    const bool full = whole(V, a.per, bf16, a.logits, nullptr) && whole(V, a.per, false, a.bias, nullptr);
     if (bf16) {
         if (softmax) route_f<V, 1, 1>(a, full, grid, st);
         else route_f<V, 1, 0>(a, full, grid, st);
