@@ -81,8 +81,8 @@ bool routing_ok(int64_t T, int64_t experts, int64_t top_k) {
 int combine_ok(int dtype, int64_t T, int64_t rows, int64_t H, int64_t top_k) {
     if (!is_type(dtype)) return FP8Q_ERR_DTYPE;
     if (T < 0 || rows < 0 || H < 0 || top_k < 1 || top_k > kMaxTopK || rows > INT32_MAX) return FP8Q_ERR_SHAPE;
-    // one workgroup of 256 threads per token (and, forward, of 128 per 128 elements at the least)
-    if (T > kMaxTokens || T > INT32_MAX / top_k || (H + 127) / 128 > kMaxGridY) return FP8Q_ERR_SHAPE;
+    // one workgroup of 256 threads per token (and, forward, of 128 per 512 elements at the least)
+    if (T > kMaxTokens || T > INT32_MAX / top_k || (H + 511) / 512 > kMaxGridY) return FP8Q_ERR_SHAPE;
     return FP8Q_OK;
 }
 

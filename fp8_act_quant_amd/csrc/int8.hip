@@ -241,13 +241,18 @@ __device__ __forceinline__ bool find_block(const Int8Args &g, int cols, int inde
     return false;
 }
 
+// Output rows start anywhere that 4 bytes (or with an odd N 2) allow; the vector stores take that
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+
+// four consecutive outputs of a row with `left` elements from here on
 template <int OUT_BF16>
-__device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int64_t left, bool vec) {
+__device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int64_t left) {
     if constexpr (OUT_BF16) {
         uint16_t *p = reinterpret_cast<uint16_t *>(y) + at;
         const u32x2 u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        if (vec && left >= 4) {
-            *reinterpret_cast<u32x2 *>(p) = u;
+        if (left >= 4) {
+            *reinterpret_cast<u32x2_any *>(p) = u;
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -255,8 +260,8 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
         }
     } else {
         float *p = reinterpret_cast<float *>(y) + at;
-        if (vec && left >= 4) {
-            *reinterpret_cast<f32x4 *>(p) = v;
+        if (left >= 4) {
+            *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4, v);
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -409,8 +414,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
         const int64_t nr = n + r < g.N ? n + r : g.N - 1;
         out[r] = (float)sum[r] * scale * (K > 0 ? g.sw[nr] : 0.0f) + (g.bias ? g.bias[nr] : 0.0f);
     }
-    const bool vec = (g.N & 3) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
-    store4<OUT_BF16>(g.y, row * g.N + n, out, g.N - n, vec);
+    store4<OUT_BF16>(g.y, row * g.N + n, out, g.N - n);
 }
 
 // Many rows: tiles of BM x BN in LDS, NW waves in a WAVES_M x (NW / WAVES_M) grid. Tile rows go to
@@ -540,7 +544,6 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
     constexpr int OB = E::OB, EPC = E::EPC, LDS_ROW = E::LDS_ROW, RG = E::RG, IPR = E::IPR, CPR = E::CPR;
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, WN = T::WN;
     const int frow = lane & 15, kg = lane >> 4;
-    const bool vec = ((g.N * OB) & 15) == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15) == 0;
     f32x4 scale_n[SUB_N], bias[SUB_N];
 #pragma unroll
     for (int j = 0; j < SUB_N; ++j) {
@@ -594,8 +597,8 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
             if (m >= at.m1 || n >= g.N) continue;
             const uint8_t *src = smem + r * LDS_ROW + cb * 16;
             uint8_t *yp = reinterpret_cast<uint8_t *>(g.y) + (m * g.N + n) * OB;
-            if (vec && n + EPC <= g.N) {
-                *reinterpret_cast<u32x4 *>(yp) = *reinterpret_cast<const u32x4 *>(src);
+            if (n + EPC <= g.N) {
+                *reinterpret_cast<u32x4_any *>(yp) = *reinterpret_cast<const u32x4 *>(src);
             } else {
                 for (int e = 0; e < EPC && n + e < g.N; ++e) {
                     if constexpr (OUT_BF16)

@@ -20,9 +20,9 @@ namespace fp8q {
 namespace {
 
 constexpr int kMaxExperts = (int)kMaxGroupedExperts;
-constexpr int PW = 8;               // waves of a placement workgroup
+constexpr int PW = 16;               // waves of a placement workgroup
 constexpr int PT = 64 * PW;
-constexpr int64_t kOneChunk = 4096; // pairs that one workgroup places by itself
+constexpr int64_t kOneChunk = 16384; // pairs that one workgroup places by itself
 constexpr int64_t kChunk = 2048;    // pairs of a chunk where there are several
 constexpr int64_t kMaxChunks = 256;
 
@@ -111,8 +111,7 @@ __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
     }
     __syncthreads();
 
-    // each thread owns the experts 2 i and 2 i + 1
-    constexpr int PER = kMaxExperts / PT;
+    constexpr int PER = kMaxExperts / PT;   // experts of a thread
     uint32_t mine[PER], sum = 0;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
@@ -199,63 +198,91 @@ struct CombineArgs {
     int k;
 };
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
+// 16 bytes at any element's address: rows of any length and alignment are read and written so
+// (6958 x 3 x 1447 bf16 17 us, element by element 43)
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-template <int STREAM, class V>
-__device__ __forceinline__ V load16(const void *p) {
-    if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
-    else return *reinterpret_cast<const V *>(p);
+template <int STREAM>
+__device__ __forceinline__ u32x4 load16(const void *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+    else return *reinterpret_cast<const u32x4_any *>(p);
 }
 
-// VEC consecutive elements, BF16 or fp32. Whole vectors are stored past the caches: nothing here
-// reads them again, and what the caches hold of the inputs stays (the gradient of 2047 x 6 x 7168
-// 80 -> 60 us). STREAM loads them past the caches too.
-template <int BF16, int VEC>
+// VEC = 16 bytes of consecutive elements, BF16 or fp32. Whole pieces are stored past the caches:
+// nothing here reads them again, and what the caches hold of the inputs stays (the gradient of
+// 2047 x 6 x 7168 80 -> 60 us). STREAM loads them past the caches too. Of a piece of fewer than VEC
+// elements (a row shorter than that) the first n count.
+template <int BF16>
 struct Piece {
+    static constexpr int VEC = BF16 ? 8 : 4;
     float v[VEC];
     template <int STREAM = 0>
     __device__ __forceinline__ void load(const void *p, int64_t i) {
-        if constexpr (BF16) {
-            const uint16_t *q = reinterpret_cast<const uint16_t *>(p) + i;
-            if constexpr (VEC == 8) {
-                const u32x4 u = load16<STREAM, u32x4>(q);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    v[2 * d] = bf16lo_to_f32(u[d]);
-                    v[2 * d + 1] = bf16hi_to_f32(u[d]);
-                }
-            } else {
-                v[0] = __uint_as_float((uint32_t)q[0] << 16);
-            }
-        } else {
-            const float *q = reinterpret_cast<const float *>(p) + i;
-            if constexpr (VEC == 4) {
-                const f32x4_t u = load16<STREAM, f32x4_t>(q);
-                v[0] = u[0], v[1] = u[1], v[2] = u[2], v[3] = u[3];
-            } else {
-                v[0] = q[0];
-            }
-        }
+        set(load16<STREAM>(reinterpret_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4)));
     }
     __device__ __forceinline__ void store(void *p, int64_t i) const {
-        if constexpr (BF16) {
-            uint16_t *q = reinterpret_cast<uint16_t *>(p) + i;
-            if constexpr (VEC == 8) {
-                u32x4 u;
+        __builtin_nontemporal_store(get(), reinterpret_cast<u32x4_any *>(reinterpret_cast<uint8_t *>(p) + i * (BF16 ? 2 : 4)));
+    }
+    __device__ __forceinline__ void load_some(const void *p, int64_t i, int n) {
+        u32x4 u = {0, 0, 0, 0};
 #pragma unroll
-                for (int d = 0; d < 4; ++d) u[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
-                __builtin_nontemporal_store(u, reinterpret_cast<u32x4 *>(q));
-            } else {
-                q[0] = (uint16_t)pack_bf16x2(v[0], 0.0f);
+        for (int j = 0; j < VEC; ++j) {
+            if (j >= n) continue;
+            if constexpr (BF16) u[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(p)[i + j] << (16 * (j & 1));
+            else u[j] = reinterpret_cast<const uint32_t *>(p)[i + j];
+        }
+        set(u);
+    }
+    __device__ __forceinline__ void store_some(void *p, int64_t i, int n) const {
+        const u32x4 u = get();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            if (j >= n) continue;
+            if constexpr (BF16) reinterpret_cast<uint16_t *>(p)[i + j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
+            else reinterpret_cast<uint32_t *>(p)[i + j] = u[j];
+        }
+    }
+    __device__ __forceinline__ void set(const u32x4 &u) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            if constexpr (BF16) v[j] = j & 1 ? bf16hi_to_f32(u[j / 2]) : bf16lo_to_f32(u[j / 2]);
+            else v[j] = __uint_as_float(u[j]);
+        }
+    }
+    __device__ __forceinline__ u32x4 get() const {
+        u32x4 u;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if constexpr (BF16) u[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
+            else u[d] = __float_as_uint(v[d]);
+        }
+        return u;
+    }
+};
+
+// Where a row's pieces lie. WHOLE: its length is a multiple of VEC. Otherwise the last piece is the
+// row's last VEC elements, the first `again` of which belong to the piece before as well (both
+// write the same values there); and a row of fewer than VEC elements is one piece of n.
+template <int VEC, int WHOLE>
+struct Place {
+    int64_t col;
+    int again, n;
+    __device__ __forceinline__ Place(int64_t piece, int64_t H) : col(piece * VEC), again(0), n(VEC) {
+        if constexpr (!WHOLE) {
+            if (H < VEC) {
+                n = (int)H;
+            } else if (col + VEC > H) {
+                again = (int)(col + VEC - H);
+                col -= again;
             }
-        } else {
-            float *q = reinterpret_cast<float *>(p) + i;
-            if constexpr (VEC == 4)
-                __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t *>(q));
-            else q[0] = v[0];
         }
     }
 };
+// all but rows shorter than a piece
+template <int VEC, int WHOLE>
+__device__ __forceinline__ bool long_row(int64_t H) {
+    return WHOLE || H >= VEC;
+}
 
 constexpr int KB = 8;     // choices whose rows are in flight together
 constexpr int CT = 128;   // threads of a combine workgroup
@@ -265,21 +292,24 @@ constexpr int CT = 128;   // threads of a combine workgroup
 // 14 KB rows at a time from memory): 8192 x 8 x 7168 bf16 213 -> 174 us, 6.1 TB/s. Rows that an
 // expert's product has just left there are read with ordinary loads, a token's pieces far apart:
 // 2047 x 6 x 7168 30 us, against 36 the other way.
-template <int BF16, int VEC, int STREAM>
+template <int BF16, int STREAM, int WHOLE>
 __global__ __launch_bounds__(CT) void combine_kernel(CombineArgs a) {
+    constexpr int VEC = Piece<BF16>::VEC;
     int64_t t = blockIdx.x, piece = blockIdx.y;
     if constexpr (STREAM) {
         const int64_t n = (a.H + CT * VEC - 1) / (CT * VEC);
         piece = blockIdx.x % n;
         t = blockIdx.x / n;
     }
-    const int64_t col = (piece * CT + threadIdx.x) * VEC;
-    if (col >= a.H) return;
+    piece = piece * CT + threadIdx.x;
+    if (piece * VEC >= a.H) return;
+    const Place<VEC, WHOLE> at(piece, a.H);
+    const bool whole = long_row<VEC, WHOLE>(a.H);
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < a.k; j0 += KB) {
-        Piece<BF16, VEC> p[KB];
+        Piece<BF16> p[KB];
         float w[KB];
 #pragma unroll
         for (int u = 0; u < KB; ++u) {
@@ -290,7 +320,8 @@ __global__ __launch_bounds__(CT) void combine_kernel(CombineArgs a) {
             for (int i = 0; i < VEC; ++i) p[u].v[i] = 0.0f;
             if (s >= 0 && s < a.rows) {
                 w[u] = a.weights ? a.weights[t * a.k + j] : 1.0f;
-                p[u].template load<STREAM>(a.h, (int64_t)s * a.H + col);
+                if (whole) p[u].template load<STREAM>(a.h, (int64_t)s * a.H + at.col);
+                else p[u].load_some(a.h, (int64_t)s * a.H, at.n);
             }
         }
 #pragma unroll
@@ -298,10 +329,11 @@ __global__ __launch_bounds__(CT) void combine_kernel(CombineArgs a) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) acc[i] = __builtin_fmaf(w[u], p[u].v[i], acc[i]);
     }
-    Piece<BF16, VEC> out;
+    Piece<BF16> out;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) out.v[i] = acc[i];
-    out.store(a.y, t * a.H + col);
+    if (whole) out.store(a.y, t * a.H + at.col);
+    else out.store_some(a.y, t * a.H, at.n);
 }
 
 // dh[slot] = w dy and dw = <dy, h[slot]>, a workgroup per token: each row of h is read and
@@ -309,11 +341,13 @@ __global__ __launch_bounds__(CT) void combine_kernel(CombineArgs a) {
 // THREADS: as many as keep all tokens on the GPU at once (its registers allow 1024 threads a CU): 512
 // up to 256 tokens (64 x 8 x 7168 11 -> 9 us), 256 up to 1024, else 128 (2047 x 6 x 7168 84 -> 73 us with
 // STREAM, 5.2 TB/s).
-template <int BF16, int VEC, int THREADS, int STREAM>
+template <int BF16, int THREADS, int STREAM, int WHOLE>
 __global__ __launch_bounds__(THREADS) void combine_grad_kernel(CombineArgs a) {
+    constexpr int VEC = Piece<BF16>::VEC;
     __shared__ float part[THREADS / 64][KB];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool whole = long_row<VEC, WHOLE>(a.H);
     for (int j0 = 0; j0 < a.k; j0 += KB) {
         int slot[KB];
         float w[KB], dot[KB];
@@ -325,21 +359,29 @@ __global__ __launch_bounds__(THREADS) void combine_grad_kernel(CombineArgs a) {
             w[u] = slot[u] >= 0 ? a.weights[t * a.k + j] : 0.0f;
             dot[u] = 0.0f;
         }
-        for (int64_t col = (int64_t)threadIdx.x * VEC; col < a.H; col += THREADS * VEC) {
-            Piece<BF16, VEC> g, p[KB], out;
-            g.load(a.dy, t * a.H + col);
+        for (int64_t piece = threadIdx.x; piece * VEC < a.H; piece += THREADS) {
+            const Place<VEC, WHOLE> at(piece, a.H);
+            Piece<BF16> g, p[KB], out;
+            if (whole) g.load(a.dy, t * a.H + at.col);
+            else g.load_some(a.dy, t * a.H, at.n);
 #pragma unroll
-            for (int u = 0; u < KB; ++u)
-                if (slot[u] >= 0) p[u].template load<STREAM>(a.h, (int64_t)slot[u] * a.H + col);
+            for (int u = 0; u < KB; ++u) {
+                if (slot[u] >= 0) {
+                    if (whole) p[u].template load<STREAM>(a.h, (int64_t)slot[u] * a.H + at.col);
+                    else p[u].load_some(a.h, (int64_t)slot[u] * a.H, at.n);
+                }
+            }
 #pragma unroll
             for (int u = 0; u < KB; ++u) {
                 if (slot[u] >= 0) {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        dot[u] = __builtin_fmaf(g.v[i], p[u].v[i], dot[u]);
+                        const float gi = WHOLE || i >= at.again ? g.v[i] : 0.0f;   // (counted once)
+                        dot[u] = __builtin_fmaf(gi, p[u].v[i], dot[u]);
                         out.v[i] = w[u] * g.v[i];
                     }
-                    out.store(a.dh, (int64_t)slot[u] * a.H + col);
+                    if (whole) out.store(a.dh, (int64_t)slot[u] * a.H + at.col);
+                    else out.store_some(a.dh, (int64_t)slot[u] * a.H, at.n);
                 }
             }
         }
@@ -358,11 +400,6 @@ __global__ __launch_bounds__(THREADS) void combine_grad_kernel(CombineArgs a) {
         }
         __syncthreads();
     }
-}
-
-bool vec_ok(int64_t H, int size, const void *p, const void *q, const void *r) {
-    return H * size % 16 == 0 &&
-           ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(r)) & 15) == 0;
 }
 
 }  // namespace
@@ -386,49 +423,42 @@ hipError_t launch_moe_place(const int32_t *experts, int64_t *offsets, int32_t *r
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const void *h, bool bf16, const int32_t *slots, const float *weights, void *y, int64_t T,
-                              int64_t rows, int64_t H, int k, hipStream_t stream) {
-    const CombineArgs a{h, slots, weights, y, nullptr, nullptr, nullptr, T, H, rows, k};
-    const int size = bf16 ? 2 : 4;
-    const bool vec = vec_ok(H, size, h, y, nullptr);
-    const int64_t per = CT * (vec ? 16 / size : 1), pieces = (H + per - 1) / per;
-    const bool stream_rows = vec && T * k * H * size > ((int64_t)256 << 20) && T * pieces * CT <= 0xFFFFFFFFll;
-    const dim3 block(CT), grid = stream_rows ? dim3((unsigned)(T * pieces)) : dim3((unsigned)T, (unsigned)pieces);
-    if (bf16) {
-        if (stream_rows) combine_kernel<1, 8, 1><<<grid, block, 0, stream>>>(a);
-        else if (vec) combine_kernel<1, 8, 0><<<grid, block, 0, stream>>>(a);
-        else combine_kernel<1, 1, 0><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (stream_rows) combine_kernel<0, 4, 1><<<grid, block, 0, stream>>>(a);
-        else if (vec) combine_kernel<0, 4, 0><<<grid, block, 0, stream>>>(a);
-        else combine_kernel<0, 1, 0><<<grid, block, 0, stream>>>(a);
-    }
-    return hipGetLastError();
+template <int BF16, int WHOLE>
+void combine(const CombineArgs &a, hipStream_t stream) {
+    constexpr int VEC = Piece<BF16>::VEC;
+    const int64_t per = CT * VEC, pieces = (a.H + per - 1) / per;
+    const bool stream_rows = a.T * a.k * a.H * (16 / VEC) > ((int64_t)256 << 20) && a.T * pieces * CT <= 0xFFFFFFFFll;
+    if (stream_rows)
+        combine_kernel<BF16, 1, WHOLE><<<dim3((unsigned)(a.T * pieces)), dim3(CT), 0, stream>>>(a);
+    else
+        combine_kernel<BF16, 0, WHOLE><<<dim3((unsigned)a.T, (unsigned)pieces), dim3(CT), 0, stream>>>(a);
 }
 
-template <int BF16, int VEC>
+template <int BF16, int WHOLE>
 void combine_grad(const CombineArgs &a, hipStream_t stream) {
     const dim3 grid((unsigned)a.T);
     // (h and dh past what the caches hold: the forward pass's h is no longer there)
-    const bool stream_rows = VEC > 1 && a.T > 1024 && a.T * a.k * a.H * (BF16 ? 2 : 4) > ((int64_t)128 << 20);
-    if (stream_rows) combine_grad_kernel<BF16, VEC, 128, VEC != 1><<<grid, dim3(128), 0, stream>>>(a);
-    else if (a.T <= 256) combine_grad_kernel<BF16, VEC, 512, 0><<<grid, dim3(512), 0, stream>>>(a);
-    else if (a.T <= 1024) combine_grad_kernel<BF16, VEC, 256, 0><<<grid, dim3(256), 0, stream>>>(a);
-    else combine_grad_kernel<BF16, VEC, 128, 0><<<grid, dim3(128), 0, stream>>>(a);
+    const bool stream_rows = a.T > 1024 && a.T * a.k * a.H * (16 / Piece<BF16>::VEC) > ((int64_t)128 << 20);
+    if (stream_rows) combine_grad_kernel<BF16, 128, 1, WHOLE><<<grid, dim3(128), 0, stream>>>(a);
+    else if (a.T <= 256) combine_grad_kernel<BF16, 512, 0, WHOLE><<<grid, dim3(512), 0, stream>>>(a);
+    else if (a.T <= 1024) combine_grad_kernel<BF16, 256, 0, WHOLE><<<grid, dim3(256), 0, stream>>>(a);
+    else combine_grad_kernel<BF16, 128, 0, WHOLE><<<grid, dim3(128), 0, stream>>>(a);
+}
+
+hipError_t launch_moe_combine(const void *h, bool bf16, const int32_t *slots, const float *weights, void *y, int64_t T,
+                              int64_t rows, int64_t H, int k, hipStream_t stream) {
+    const CombineArgs a{h, slots, weights, y, nullptr, nullptr, nullptr, T, H, rows, k};
+    if (bf16) H % 8 ? combine<1, 0>(a, stream) : combine<1, 1>(a, stream);
+    else H % 4 ? combine<0, 0>(a, stream) : combine<0, 1>(a, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const void *dy, const void *h, bool bf16, const int32_t *slots,
                                        const float *weights, void *dh, float *dweights, int64_t T, int64_t rows,
                                        int64_t H, int k, hipStream_t stream) {
     const CombineArgs a{h, slots, weights, nullptr, dy, dh, dweights, T, H, rows, k};
-    const bool vec = vec_ok(H, bf16 ? 2 : 4, h, dy, dh);
-    if (bf16) {
-        if (vec) combine_grad<1, 8>(a, stream);
-        else combine_grad<1, 1>(a, stream);
-    } else {
-        if (vec) combine_grad<0, 4>(a, stream);
-        else combine_grad<0, 1>(a, stream);
-    }
+    if (bf16) H % 8 ? combine_grad<1, 0>(a, stream) : combine_grad<1, 1>(a, stream);
+    else H % 4 ? combine_grad<0, 0>(a, stream) : combine_grad<0, 1>(a, stream);
     return hipGetLastError();
 }
 

@@ -292,7 +292,8 @@ def placed(g, T, k, E, n=None, first=0):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,k,H,E,n", [(1, 1, 8, 4, 4), (1, 8, 7168, 256, 256), (37, 6, 100, 64, 64), (5, 3, 1, 8, 8),
-                                       (19, 9, 2056, 32, 10), (3, 32, 300, 40, 40), (130, 2, 4097, 8, 3)])
+                                       (19, 9, 2056, 32, 10), (3, 32, 300, 40, 40), (130, 2, 4097, 8, 3), (7, 3, 7, 8, 8), (20, 4, 3, 8, 5),
+                                       (300, 3, 1001, 16, 16), (1100, 2, 515, 8, 8)])
 def test_combine(T, k, H, E, n, dtype):
     g = rng(T + H)
     _, _, slots = placed(g, T, k, E, n)
@@ -312,7 +313,8 @@ def test_combine(T, k, H, E, n, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,k,H,E,n", [(1, 1, 8, 4, 4), (37, 6, 7168, 64, 64), (5, 3, 1, 8, 8), (19, 9, 2056, 32, 10),
-                                       (3, 32, 300, 40, 40), (130, 2, 4097, 8, 8)])
+                                       (3, 32, 300, 40, 40), (130, 2, 4097, 8, 8), (7, 3, 7, 8, 8), (20, 4, 3, 8, 5),
+                                       (300, 3, 1001, 16, 16), (1100, 2, 515, 8, 8)])
 def test_combine_backward(T, k, H, E, n, dtype):
     g = rng(T + H + 1)
     _, _, slots = placed(g, T, k, E, n)
