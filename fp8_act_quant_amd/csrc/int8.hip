@@ -147,7 +147,11 @@ struct Int8Args {
     int64_t tokens;           // rows of a
     int experts;
     int tiles_m, tiles_n, group;
+    bool stream;              // grouped: W is larger than the last-level cache
 };
+
+constexpr int kNonTemporal = 2;   // cache policy of buffer loads
+constexpr int64_t kLastLevelCache = 256 << 20;
 
 // A past-the-end offset: loads there return zero (every buffer here is shorter)
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
@@ -218,10 +222,10 @@ __device__ __forceinline__ int count_blocks(const Int8Args &g) {
     for (int e0 = 0; e0 < g.experts; e0 += 64) n += blocks_of<BM>(g, e0 + lane);
     return __builtin_amdgcn_readlane(wave_scan(n), 63);
 }
-// the expert, rows and column of tile `index`; false: there is none
+// the expert, rows and column of tile `index`, and the expert's row blocks; false: there is none
 template <int BM>
 __device__ __forceinline__ bool find_block(const Int8Args &g, int cols, int index, int &expert, int64_t &row0,
-                                           int64_t &row1, int &col) {
+                                           int64_t &row1, int &col, int &per) {
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
@@ -229,7 +233,8 @@ __device__ __forceinline__ bool find_block(const Int8Args &g, int cols, int inde
         const uint64_t hit = __ballot(index >= first && index < first + n * cols);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int within = index - __builtin_amdgcn_readlane(first, l), per = __builtin_amdgcn_readlane(n, l);
+            const int within = index - __builtin_amdgcn_readlane(first, l);
+            per = __builtin_amdgcn_readlane(n, l);
             expert = e0 + l;
             col = within / per;
             expert_rows(g, expert, row0, row1);
@@ -441,6 +446,7 @@ struct TileAt {
     int64_t m0, m1, n0;   // first row, end of the rows (not of the tile), first channel
     const int8_t *w;      // the tile's weight and its scales
     const float *sw;
+    bool stream;          // its W panel is read once in this call and by no next one: non-temporally
 };
 
 // Tile of a workgroup. Workgroup b runs on XCD b % 8, and each XCD takes a contiguous run of the
@@ -455,9 +461,11 @@ __device__ __forceinline__ bool find_tile(const Int8Args &g, TileAt &t) {
     const int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
     t.w = g.w;
     t.sw = g.sw;
+    t.stream = false;
     if constexpr (GROUPED) {
-        int expert, col;
-        if (slot >= q + (xcd < rem) || !find_block<T::BM>(g, g.tiles_n, tl, expert, t.m0, t.m1, col)) return false;
+        int expert, col, per;
+        if (slot >= q + (xcd < rem) || !find_block<T::BM>(g, g.tiles_n, tl, expert, t.m0, t.m1, col, per)) return false;
+        t.stream = g.stream && per == 1;
         t.n0 = (int64_t)col * T::BN;
         t.w += (int64_t)expert * g.N * g.K;
         t.sw += (int64_t)expert * g.N;
@@ -476,7 +484,7 @@ __device__ __forceinline__ bool find_tile(const Int8Args &g, TileAt &t) {
 // lane L fills LDS row L / 8 of those, physical chunk L % 8. VARIANT makes the type unique to
 // each kernel instantiation: the host pass emits a launch stub for only one kernel among those
 // that share such a type.
-template <class T, int VARIANT>
+template <class T, int VARIANT, int STREAM>
 struct Int8Dma {
     rsrc_t ra, rw;
     uint32_t off[T::IPW];
@@ -516,9 +524,12 @@ struct Int8Dma {
 #pragma unroll
         for (int t = 0; t < T::IPW; ++t) {
             if (t < first || t >= first + count) continue;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                t < T::A_INSTR ? ra : rw, (lds_void *)(base + (t < T::A_INSTR ? 0 : T::A_BYTES) + row_of(t) * KB), 16,
-                past ? kNowhere : off[t], koff, 0, 0);
+            const uint32_t at = past ? kNowhere : off[t];
+            if (t < T::A_INSTR)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(base + row_of(t) * KB), 16, at, koff, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(base + T::A_BYTES + row_of(t) * KB), 16, at,
+                                                         koff, 0, STREAM ? kNonTemporal : 0);
         }
     }
 };
@@ -634,7 +645,7 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 // the cycles) and 640 us on normal data, at a lower clock (about 1.6 GHz): the power limit. The
 // 32x32x32 instruction, at half the K and so twice the accumulator traffic, has fewer cycles
 // and yet takes 685 us.
-template <class T, int FULL, int VARIANT, int OUT_BF16>
+template <class T, int FULL, int VARIANT, int STREAM, int OUT_BF16>
 __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8_t *smem) {
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, PH = SUB_M / 4;
     static_assert(PH == 1 || PH == 2, "phases");
@@ -643,7 +654,7 @@ __device__ __forceinline__ void turns(const Int8Args &g, const TileAt &at, uint8
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int nks = (int)((g.K + KB - 1) / KB);
-    const Int8Dma<T, VARIANT> dma(g, at, wave, lane);
+    const Int8Dma<T, VARIANT, STREAM> dma(g, at, wave, lane);
     const int rows = (int)(at.m1 - at.m0 < T::BM ? at.m1 - at.m0 : T::BM);
 
     i32x4 acc[SUB_M][SUB_N];
@@ -745,13 +756,21 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     TileAt at;
     if constexpr (BM == 256) {
         if (!find_tile<T2, GROUPED>(g, at)) return;
-        if (at.m1 - at.m0 >= 256) turns<T2, 1, VARIANT, OUT_BF16>(g, at, smem);
-        else if (at.m1 - at.m0 > 128) turns<T2, 0, VARIANT, OUT_BF16>(g, at, smem);
-        else turns<T1, 0, VARIANT, OUT_BF16>(g, at, smem);
+        const int64_t rows = at.m1 - at.m0;
+        if (rows >= 256) {
+            turns<T2, 1, VARIANT, 0, OUT_BF16>(g, at, smem);
+        } else if (GROUPED && at.stream) {
+            if (rows > 128) turns<T2, 0, VARIANT, GROUPED, OUT_BF16>(g, at, smem);
+            else turns<T1, 0, VARIANT, GROUPED, OUT_BF16>(g, at, smem);
+        } else {
+            if (rows > 128) turns<T2, 0, VARIANT, 0, OUT_BF16>(g, at, smem);
+            else turns<T1, 0, VARIANT, 0, OUT_BF16>(g, at, smem);
+        }
     } else {
         if (!find_tile<T1, GROUPED>(g, at)) return;
-        if (at.m1 - at.m0 >= 128) turns<T1, 1, 8 + VARIANT, OUT_BF16>(g, at, smem);
-        else turns<T1, 0, 8 + VARIANT, OUT_BF16>(g, at, smem);
+        if (at.m1 - at.m0 >= 128) turns<T1, 1, 8 + VARIANT, 0, OUT_BF16>(g, at, smem);
+        else if (GROUPED && at.stream) turns<T1, 0, 8 + VARIANT, GROUPED, OUT_BF16>(g, at, smem);
+        else turns<T1, 0, 8 + VARIANT, 0, OUT_BF16>(g, at, smem);
     }
 }
 
@@ -797,18 +816,14 @@ __device__ __forceinline__ void deep_step(int ks, const Dma &dma, uint8_t *stage
     }
 }
 
-template <int BM_, int BN_, int NSTAGE_, int OUT_BF16, int GROUPED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void int8_deep_kernel(Int8Args g) {
-    using T = Int8Tile<BM_, BN_, 4, 2, NSTAGE_>;
+template <class T, int VARIANT, int STREAM, int OUT_BF16>
+__device__ __forceinline__ void deep(const Int8Args &g, const TileAt &at, uint8_t *smem) {
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, NSTAGE = T::NSTAGE;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
-    TileAt at;
-    if (!find_tile<T, GROUPED>(g, at)) return;
     const int nks = (int)((g.K + KB - 1) / KB);
-    const Int8Dma<T, 4 + OUT_BF16 * 2 + GROUPED> dma(g, at, wave, lane);
+    const Int8Dma<T, VARIANT, STREAM> dma(g, at, wave, lane);
 
     i32x4 acc[SUB_M][SUB_N];
 #pragma unroll
@@ -844,6 +859,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     wait_lgkm0();
     wait_vmcnt<0>();   // the copies past the last step, before LDS takes the output
     store_tile<T, OUT_BF16>(g, at, smem, lane, wm, wn, acc);
+}
+
+template <int BM, int BN, int NSTAGE, int OUT_BF16, int GROUPED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void int8_deep_kernel(Int8Args g) {
+    using T = Int8Tile<BM, BN, 4, 2, NSTAGE>;
+    constexpr int VARIANT = 4 + OUT_BF16 * 2 + GROUPED;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    TileAt at;
+    if (!find_tile<T, GROUPED>(g, at)) return;
+    if (GROUPED && at.stream) deep<T, VARIANT, GROUPED, OUT_BF16>(g, at, smem);
+    else deep<T, VARIANT, 0, OUT_BF16>(g, at, smem);
 }
 
 template <int QUANT>
@@ -912,7 +938,7 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     const int64_t tiles32 = (M + 31) / 32 * ((N + 63) / 64);
     if (M <= kFewRows && tiles32 <= 64)
         return launch_few<0>({a, sa, nullptr, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
-    const Int8Args g{a, sa, w, sw, bias, y, nullptr, nullptr, M, N, K, M, 0, 0, 0, 1};
+    const Int8Args g{a, sa, w, sw, bias, y, nullptr, nullptr, M, N, K, M, 0, 0, 0, 1, false};
     // The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps. The
     // constants are fitted to times at K = 512 and 7168, N = 1536 and 7168, M = 16 to 4096 (us): the
     // first round's step, a later round's (less where two workgroups share a CU's waits), the epilogue.
@@ -958,7 +984,8 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
                                     const int64_t *offsets, const int32_t *rows, void *y, bool out_bf16,
                                     int64_t experts, int64_t M, int64_t tokens, int64_t N, int64_t K,
                                     hipStream_t stream) {
-    const Int8Args g{a, sa, w, sw, nullptr, y, offsets, rows, M, N, K, tokens, (int)experts, 0, 0, 1};
+    const Int8Args g{a, sa, w, sw, nullptr, y, offsets, rows, M, N, K, tokens, (int)experts, 0, 0, 1,
+                     experts * N * K > kLastLevelCache};
     // By the average rows of an expert (its true count is on the device). Measured in us, 64 experts'
     // 4096 x 7168, at 1.5 / 6 / 24 / 96 / 192 rows: 32 x 64 204 / 277 / 355 / 638 / 1072, 64 x 128
     // 216 / 290 / 332 / 477 / 681, 128 x 256 218 / 292 / 317 / 407 / 538, 256 x 256
