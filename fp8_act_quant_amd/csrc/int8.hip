@@ -986,17 +986,26 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
                                     hipStream_t stream) {
     const Int8Args g{a, sa, w, sw, nullptr, y, offsets, rows, M, N, K, tokens, (int)experts, 0, 0, 1,
                      experts * N * K > kLastLevelCache};
-    // By the average rows of an expert (its true count is on the device). Measured in us, 64 experts'
-    // 4096 x 7168, at 1.5 / 6 / 24 / 96 / 192 rows: 32 x 64 204 / 277 / 355 / 638 / 1072, 64 x 128
-    // 216 / 290 / 332 / 477 / 681, 128 x 256 218 / 292 / 317 / 407 / 538, 256 x 256
-    // 218 / 292 / 333 / 408 / 488. With a short K the smallest tile's many epilogues count: 256 experts'
-    // 2048 x 1024 at 2 rows, 103 / 84 / 96 / 96.
+    // By the average rows of an expert (its true count is on the device). Measured in us at 1.5 / 15 /
+    // 24 / 48 / 96 / 192 rows of each of 64 experts:
+    //     4096 x 7168   32 x 128 158 / 280 / 326 / 432 / 606 / 976    64 x 128 165 / 287 / 296 / 365 / 482 / 689
+    //                  128 x 256 189 / 286 / 303 / 357 / 407 / 562   256 x 256 190 / 286 / 304 / 336 / 389 / 500
+    //      512 x 1024 at 30 / 96 / 192  10 / 17 / 28,  11 / 17 / 22,  13 / 15 / 27,  13 / 22 / 25
+    // With few tiles the smallest that still all run at once: 29 experts' 169 x 4912 at 38 rows 32 x 64
+    // 12, 64 x 64 15, 64 x 128 21; 53 experts' 106 x 3328 at 72 rows 11, 10, 13; 48 experts' 300 x 4000 at
+    // 52 rows 64 x 128 19, 128 x 256 34. Between the last two by rounds of 256 tiles, blocks of 256
+    // rows taking 1.5 times as long (few are full) but reading W less often: 32 experts' 1408 x 2048 at
+    // 250 rows 42 against 59; 8 experts' 4096 x 7168 at 128 rows 48 / 79, at 256 92 / 81.
     const int64_t mean = M / experts;
-    if (mean < 24) {
-        if (K >= 4096) return launch_deep<32, 64, 6, 1>(g, out_bf16, stream);
-        return launch_deep<64, 128, 3, 1>(g, out_bf16, stream);
-    }
-    if (mean < 96) return launch_turns<128, 1>(g, out_bf16, stream);
+    auto tiles = [&](int bm, int bn) {   // an expert's last row block counted as half
+        return (M / bm + (experts < M ? experts : M) / 2) * ((N + bn - 1) / bn);
+    };
+    if (tiles(32, 64) <= 256) return launch_deep<32, 64, 6, 1>(g, out_bf16, stream);
+    if (mean < 16) return launch_deep<32, 128, 4, 1>(g, out_bf16, stream);
+    if (tiles(64, 64) <= 256) return launch_deep<64, 64, 5, 1>(g, out_bf16, stream);
+    if (mean < 32 || tiles(64, 128) <= 512) return launch_deep<64, 128, 3, 1>(g, out_bf16, stream);
+    if (2 * ((tiles(128, 256) + 255) / 256) <= 3 * ((tiles(256, 256) + 255) / 256))
+        return launch_turns<128, 1>(g, out_bf16, stream);
     return launch_turns<256, 1>(g, out_bf16, stream);
 }
 
