@@ -410,7 +410,7 @@ int int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw
 
 size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (int8_ok(FP8Q_OUT_F32, M, N, K) || M == 0 || N == 0 || M > kMaxTokens) return 0;
-    return fp8q::int8_linear_workspace_bytes(M, K);
+    return fp8q::int8_linear_workspace_bytes(M, N, K);
 }
 
 int int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y, int y_dtype, int64_t M,
@@ -422,7 +422,7 @@ int int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float
     if (misaligned(x, 16) || misaligned(w, 16) || misaligned(y, 4) || misaligned(sw, 4) || misaligned(bias, 4) ||
         misaligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
-    if (fp8q::int8_linear_workspace_bytes(M, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    if (fp8q::int8_linear_workspace_bytes(M, N, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
     if (int e = check_device()) return e;
     return finish(fp8q::launch_int8_linear(x, w, sw, bias, y, y_dtype == FP8Q_OUT_BF16, M, N, K, workspace,
                                            static_cast<hipStream_t>(stream)));

@@ -280,11 +280,13 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
 // from memory into MFMA operands (nothing of it is used twice), 2 U steps of 64 bytes in flight.
 // The quarters are added in LDS, exactly.
 //
-// QUANT: the rows come as bf16 and are quantised here (at most kFewQuantRows of at most
-// kFewQuantK elements): every workgroup does it for itself, in LDS, while its first reads of W are
-// on their way, which costs less than a launch of its own. 1 x 7168 x 7168: 10 us in all, of which
-// the 51 MB of W are 9 at 5.7 TB/s.
-constexpr int kFewRows = 16, kFewQuantRows = 4, kFewQuantK = 8192;
+// QUANT: the rows come as bf16 and are quantised here: every workgroup does it for itself, in LDS,
+// while its first reads of W are on their way, which costs less than a launch of its own. 1: at
+// most 4 rows of at most 8192 elements, each shared by the waves. 2: at most 8 rows of at most
+// 2048, each a wave's own. 1 x 7168 x 7168: 10 us in all, of which the 51 MB of W are 9 at 5.7 TB/s.
+constexpr int kFewRows = 16;
+constexpr int few_quant_rows(int quant) { return quant == 1 ? 2 : 8; }
+constexpr int few_quant_k(int quant) { return quant == 1 ? 8192 : 2048; }
 
 struct Int8FewArgs {
     const int8_t *a;       // QUANT: null
@@ -300,10 +302,10 @@ struct Int8FewArgs {
 
 template <int U, int QUANT, int OUT_BF16>
 __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
-    constexpr int PITCH = kFewQuantK + 16;
+    constexpr int QROWS = few_quant_rows(QUANT), QK = few_quant_k(QUANT), PITCH = QK + 16;
     __shared__ i32x4 part[4][64];
-    __shared__ __attribute__((aligned(16))) uint8_t codes[QUANT ? kFewQuantRows * PITCH : 16];
-    __shared__ uint32_t tops[4][QUANT ? kFewQuantRows : 1];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[QUANT ? QROWS * PITCH : 16];
+    __shared__ uint32_t tops[QUANT == 1 ? 4 : 1][QUANT ? QROWS : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
@@ -337,7 +339,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
             u32x4 x = {0, 0, 0, 0};
             if constexpr (QUANT) {
                 // (past K: whatever lies there, against zeros of W; always inside `codes`)
-                const int k = min((s + u) * 64 + kg * 16, kFewQuantK);
+                const int k = min((s + u) * 64 + kg * 16, QK);
                 if (row < M) x = *reinterpret_cast<const u32x4 *>(codes + row * PITCH + k);
             } else {
                 x = av[b][u];
@@ -347,16 +349,19 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
     };
     float scale = 0.0f;   // of this lane's row
     if constexpr (QUANT) {
-        constexpr int NV = kFewQuantK / 8 / 256;   // pieces of 8 elements a thread keeps of a row
-        u32x4 v[kFewQuantRows][NV];
+        // piece i of row j of this thread's: of all rows (1) or every fourth (2)
+        constexpr int ROWS = 2, STRIDE = QUANT == 1 ? 256 : 64, NV = QK / 8 / STRIDE;
+        const int first = QUANT == 1 ? 0 : wave, next = QUANT == 1 ? 1 : 4, at = QUANT == 1 ? threadIdx.x : lane;
+        u32x4 v[ROWS][NV];
         // the rows first: loads return in order, and these are needed before W
 #pragma unroll
-        for (int m = 0; m < kFewQuantRows; ++m) {
+        for (int j = 0; j < ROWS; ++j) {
+            const int m = first + next * j;
             if (m < M) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int p = threadIdx.x + 256 * i;
-                    v[m][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                    const int p = at + STRIDE * i;
+                    v[j][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                             ra, 8 * p < K ? (uint32_t)(2 * (m * K + 8 * p)) : kNowhere, 0, 0));
                 }
             }
@@ -365,36 +370,48 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
         load(0, s0);
         load(1, s0 + U);
         __builtin_amdgcn_sched_barrier(0);
+        uint32_t top[ROWS];
 #pragma unroll
-        for (int m = 0; m < kFewQuantRows; ++m) {
+        for (int j = 0; j < ROWS; ++j) {
+            const int m = first + next * j;
             if (m < M) {
-                uint32_t top = 0;
+                top[j] = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const uint32_t b = absmax_bits8(v[m][i]);
-                    top = top > b ? top : b;
+                    const uint32_t b = absmax_bits8(v[j][i]);
+                    top[j] = top[j] > b ? top[j] : b;
                 }
-                top = wave_umax(top);
-                if (lane == 0) tops[wave][m] = top;
+                top[j] = wave_umax(top[j]);
+                if (lane == 0) tops[QUANT == 1 ? wave : 0][m] = top[j];
             }
         }
-        __syncthreads();
+        if constexpr (QUANT == 1) {
+            __syncthreads();
 #pragma unroll
-        for (int m = 0; m < kFewQuantRows; ++m) {
-            if (m < M) {
-                uint32_t top = tops[0][m];
+            for (int j = 0; j < ROWS; ++j) {
+                if (j < M) {
+                    top[j] = tops[0][j];
 #pragma unroll
-                for (int w = 1; w < 4; ++w) top = top > tops[w][m] ? top : tops[w][m];
-                const RowScale r = row_scale(top);
-                scale = row == m ? r.s : scale;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int p = threadIdx.x + 256 * i;
-                    if (8 * p < K) *reinterpret_cast<u32x2 *>(codes + m * PITCH + 8 * p) = codes8(v[m][i], r);
+                    for (int w = 1; w < 4; ++w) top[j] = top[j] > tops[w][j] ? top[j] : tops[w][j];
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const int m = first + next * j;
+            if (m < M) {
+                const RowScale r = row_scale(top[j]);
+                if constexpr (QUANT == 1) scale = row == m ? r.s : scale;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int p = at + STRIDE * i;
+                    if (8 * p < K) *reinterpret_cast<u32x2 *>(codes + m * PITCH + 8 * p) = codes8(v[j][i], r);
+                }
+            }
+        }
         __syncthreads();
+        if constexpr (QUANT == 2)
+            if (row < M) scale = row_scale(tops[0][row]).s;
     } else {
         load(0, s0);
         if (row < M && K > 0) scale = g.sa[row];
@@ -872,11 +889,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     else deep<T, VARIANT, 0, OUT_BF16>(g, at, smem);
 }
 
-template <int QUANT>
+template <int U, int QUANT>
 hipError_t launch_few(const Int8FewArgs &a, bool out_bf16, hipStream_t stream) {
     const int64_t units = (a.N + 15) / 16;
     if (units * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
-    constexpr int U = QUANT ? 14 : 8;   // (28 steps, K = 7168's quarter, all in flight)
     const dim3 grid((unsigned)units), block(256);
     if (out_bf16) int8_few_kernel<U, QUANT, 1><<<grid, block, 0, stream>>>(a);
     else int8_few_kernel<U, QUANT, 0><<<grid, block, 0, stream>>>(a);
@@ -937,7 +953,7 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     // 9.3 us against 10.1; 16 x 7168 x 7168, 112 tiles: 15.9 against 10.6).
     const int64_t tiles32 = (M + 31) / 32 * ((N + 63) / 64);
     if (M <= kFewRows && tiles32 <= 64)
-        return launch_few<0>({a, sa, nullptr, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
+        return launch_few<8, 0>({a, sa, nullptr, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
     const Int8Args g{a, sa, w, sw, bias, y, nullptr, nullptr, M, N, K, M, 0, 0, 0, 1, false};
     // The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps. The
     // constants are fitted to times at K = 512 and 7168, N = 1536 and 7168, M = 16 to 4096 (us): the
@@ -964,16 +980,28 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     }
 }
 
+// Whether a linear layer is one launch, and as which of int8_few_kernel's forms
+static int one_launch(int64_t M, int64_t N, int64_t K) {
+    const int64_t units = (N + 15) / 16;
+    if (M <= few_quant_rows(2) && K <= few_quant_k(2) && units <= 1024) return 2;
+    if (M <= few_quant_rows(1) && K <= few_quant_k(1) && units <= 512) return 1;
+    return 0;
+}
+
 // Quantised rows of a linear layer between the two launches: the codes, then the scales
-size_t int8_linear_workspace_bytes(int64_t M, int64_t K) {
-    if (M <= kFewQuantRows && K <= kFewQuantK) return 0;
-    return (size_t)(M * K + 4 * M);
+size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return one_launch(M, N, K) ? 0 : (size_t)(M * K + 4 * M);
 }
 
 hipError_t launch_int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y,
                               bool out_bf16, int64_t M, int64_t N, int64_t K, void *workspace, hipStream_t stream) {
-    if (M <= kFewQuantRows && K <= kFewQuantK)
-        return launch_few<1>({nullptr, nullptr, x, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
+    const Int8FewArgs few{nullptr, nullptr, x, w, sw, bias, y, N, (int)M, (int)K};
+    switch (one_launch(M, N, K)) {
+    case 1:   // (2 U steps cover a wave's quarter of K, all in flight at once)
+        if (K <= 4096) return launch_few<8, 1>(few, out_bf16, stream);
+        return launch_few<14, 1>(few, out_bf16, stream);
+    case 2: return launch_few<4, 2>(few, out_bf16, stream);
+    }
     int8_t *q = static_cast<int8_t *>(workspace);
     float *s = reinterpret_cast<float *>(q + M * K);
     if (hipError_t e = launch_int8_quant(x, q, s, M, K, stream)) return e;

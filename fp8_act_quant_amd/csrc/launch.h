@@ -99,7 +99,7 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
                             void *y, bool out_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
 // int8_quant and int8_gemm of x [M, K] bf16; the workspace (16-byte aligned, any contents) holds
 // int8_linear_workspace_bytes.
-size_t int8_linear_workspace_bytes(int64_t M, int64_t K);
+size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_linear(const uint16_t *x, const int8_t *w, const float *sw, const float *bias, void *y,
                               bool out_bf16, int64_t M, int64_t N, int64_t K, void *workspace, hipStream_t stream);
 hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw,

@@ -181,6 +181,23 @@ def test_linear(shape, N, out):
     check(y.view(-1, N), torch.from_numpy(rq).cuda(), torch.from_numpy(rs).cuda(), wq, ws, bias, out)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 9])
+@pytest.mark.parametrize("K,N", [(16, 40), (1040, 130), (2048, 16400), (2064, 100), (4096, 8200), (4112, 77),
+                                 (8192, 50), (8208, 50)])
+def test_linear_is_quant_and_gemm(M, K, N):
+    """However many launches the layer takes, the outputs are those of its two halves, bit for bit;
+    a row of zeros and one of subnormal numbers among them."""
+    g = rng(M + K + N)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    if M > 2:
+        x[0], x[1] = 0.0, 1e-40
+    wq, ws = codes(g, N, K), scales(g, N)
+    q, s = fq.int8_quant(x)
+    for out in DT.values():
+        y = fq.int8_linear(x, wq, ws, out_dtype=out)
+        assert torch.equal(y, fq.int8_gemm(q, s, wq, ws, out_dtype=out))
+
+
 def grouped_check(y, a, sa, w, sw, offsets, rows, out):
     bounds = offsets.tolist()
     for e in range(w.shape[0]):
