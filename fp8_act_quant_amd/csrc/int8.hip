@@ -15,6 +15,8 @@
 // Grouped products. Expert e owns the rows offsets[e] .. offsets[e + 1] - 1 of Y; row r's
 // token is rows[r] (the gather is part of the loads, a token is quantised once however many
 // experts take it), or r itself.
+#include <type_traits>
+
 #include <fp8q.h>
 
 #include "device_common.h"
@@ -565,6 +567,11 @@ struct Int8Epilogue {
 // The accumulators' scaled rows go through LDS and leave in whole 128-byte pieces, masked to
 // the tile's rows and to N. (Stored straight from the fragments each line would be written in
 // 8-byte pieces by several instructions.) Begins with a workgroup barrier.
+//
+// The large tiles' outputs bypass the caches, which hold what the other tiles read, where the rows
+// are whole 64-byte blocks: 16384 x 7168 x 7168 619 -> 601 us, x 128 86 -> 77. (With rows of other
+// lengths the blocks that two stores share cost more: 8903 x 4080 x 256 37 -> 43. Small outputs
+// are read again soon: 64 x 7168 x 2048 and a reader of it 9.6 -> 10.1.)
 template <class T, int OUT_BF16>
 __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, uint8_t *smem, int lane, int wm, int wn,
                                            const i32x4 (&acc)[T::SUB_M][T::SUB_N]) {
@@ -572,6 +579,7 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
     constexpr int OB = E::OB, EPC = E::EPC, LDS_ROW = E::LDS_ROW, RG = E::RG, IPR = E::IPR, CPR = E::CPR;
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, WN = T::WN;
     const int frow = lane & 15, kg = lane >> 4;
+    const bool whole = T::NW == 8 && g.N * OB % 64 == 0 && reinterpret_cast<uintptr_t>(g.y) % 64 == 0;
     f32x4 scale_n[SUB_N], bias[SUB_N];
 #pragma unroll
     for (int j = 0; j < SUB_N; ++j) {
@@ -617,25 +625,32 @@ __device__ __forceinline__ void store_tile(const Int8Args &g, const TileAt &at, 
         __syncthreads();
         const int groups = (SUB_M - i0) < IPR ? (SUB_M - i0) : IPR;
         const int chunks = groups * RG * CPR;
-        for (int c = threadIdx.x; c < chunks; c += T::NW * 64) {
-            const int r = c / CPR, cb = c - r * CPR;
-            const int ii = r / RG, within = r - ii * RG;
-            const int64_t m = at.m0 + T::row(within >> 4, i0 + ii) + (within & 15);
-            const int64_t n = at.n0 + cb * EPC;
-            if (m >= at.m1 || n >= g.N) continue;
-            const uint8_t *src = smem + r * LDS_ROW + cb * 16;
-            uint8_t *yp = reinterpret_cast<uint8_t *>(g.y) + (m * g.N + n) * OB;
-            if (n + EPC <= g.N) {
-                *reinterpret_cast<u32x4_any *>(yp) = *reinterpret_cast<const u32x4 *>(src);
-            } else {
-                for (int e = 0; e < EPC && n + e < g.N; ++e) {
-                    if constexpr (OUT_BF16)
-                        reinterpret_cast<uint16_t *>(yp)[e] = reinterpret_cast<const uint16_t *>(src)[e];
-                    else
-                        reinterpret_cast<float *>(yp)[e] = reinterpret_cast<const float *>(src)[e];
+        // (a loop for either policy: two stores in one loop's branches would be merged into a plain one)
+        auto copy_out = [&](auto stream) {
+            for (int c = threadIdx.x; c < chunks; c += T::NW * 64) {
+                const int r = c / CPR, cb = c - r * CPR;
+                const int ii = r / RG, within = r - ii * RG;
+                const int64_t m = at.m0 + T::row(within >> 4, i0 + ii) + (within & 15);
+                const int64_t n = at.n0 + cb * EPC;
+                if (m >= at.m1 || n >= g.N) continue;
+                const uint8_t *src = smem + r * LDS_ROW + cb * 16;
+                uint8_t *yp = reinterpret_cast<uint8_t *>(g.y) + (m * g.N + n) * OB;
+                if constexpr (decltype(stream)::value) {   // (N is a multiple of EPC)
+                    __builtin_nontemporal_store(*reinterpret_cast<const u32x4 *>(src), reinterpret_cast<u32x4 *>(yp));
+                } else if (n + EPC <= g.N) {
+                    *reinterpret_cast<u32x4_any *>(yp) = *reinterpret_cast<const u32x4 *>(src);
+                } else {
+                    for (int e = 0; e < EPC && n + e < g.N; ++e) {
+                        if constexpr (OUT_BF16)
+                            reinterpret_cast<uint16_t *>(yp)[e] = reinterpret_cast<const uint16_t *>(src)[e];
+                        else
+                            reinterpret_cast<float *>(yp)[e] = reinterpret_cast<const float *>(src)[e];
+                    }
                 }
             }
-        }
+        };
+        if (whole) copy_out(std::true_type{});
+        else copy_out(std::false_type{});
     }
 }
 
