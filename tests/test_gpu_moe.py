@@ -125,6 +125,52 @@ def test_route(T, E, k, groups, topk_groups, group_score, biased, score, dtype):
         check_route(logits, bias, w, e, k, score, groups, topk_groups, group_score, renormalize, scale)
 
 
+MANY = [
+    # T, E, k, groups, topk_groups, group_score, biased: many tokens, no whole number of waves
+    (8193, 256, 8, 8, 4, "top2", True), (8205, 256, 16, 1, 1, "max", False), (4098, 72, 6, 1, 1, "max", False),
+    (6147, 160, 6, 8, 3, "max", False), (6150, 130, 7, 2, 1, "top2", True), (2049, 64, 8, 16, 5, "top2", True),
+    (2050, 16, 16, 16, 16, "max", False), (2051, 3, 2, 1, 1, "max", True), (6145, 100, 7, 5, 2, "top2", True),
+    (8192, 241, 9, 1, 1, "max", True), (2048, 33, 3, 11, 4, "max", False), (4099, 36, 6, 9, 3, "top2", True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k,groups,topk_groups,group_score,biased", MANY)
+def test_route_many(T, E, k, groups, topk_groups, group_score, biased, score, dtype):
+    """Also bit for bit what a few of the tokens alone give (bf16 logits tie often)."""
+    g = rng(T * E + k)
+    logits = randn(g, T, E).to(DT[dtype])
+    bias = 0.2 * randn(g, E).clamp(-4, 4) if biased else None
+    kw = dict(score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_score=group_score)
+    for renormalize, scale in ((True, 2.5), (False, 1.0)):
+        w, e = fq.moe_route(logits, k, renormalize=renormalize, scale=scale, **kw)
+        check_route(logits, bias, w, e, k, score, groups, topk_groups, group_score, renormalize, scale)
+        for part in (slice(0, 100), slice(T - 37, T)):
+            wp, ep = fq.moe_route(logits[part].contiguous(), k, renormalize=renormalize, scale=scale, **kw)
+            assert torch.equal(e[part], ep)
+            assert torch.equal(w[part], wp)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_many_masked_and_tied(score):
+    """Experts at -inf, rows of one value, large logits and rows with many ties beside ordinary rows."""
+    T, E, k = 8195, 256, 8
+    logits = randn(rng(5), T, E)
+    logits[::7, 40:] = float("-inf")
+    logits[1::7] = 0.25
+    logits[2::7, 200] = float("inf") if score == "sigmoid" else 50.0
+    logits[3::7] = torch.round(logits[3::7])
+    logits[4::7] = -100.0
+    for groups, topk_groups in ((1, 1), (8, 4)):
+        w, e = fq.moe_route(logits, k, score=score, groups=groups, topk_groups=topk_groups)
+        for part in (slice(0, 200), slice(T - 300, T)):
+            wp, ep = fq.moe_route(logits[part].contiguous(), k, score=score, groups=groups, topk_groups=topk_groups)
+            assert torch.equal(e[part], ep) and torch.equal(w[part], wp)
+        assert bool((e[1::7] == torch.arange(k, device="cuda", dtype=torch.int32)).all())
+        assert bool(torch.isfinite(w).all())
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 2)])
 def test_route_ties_go_to_the_lowest_index(groups, topk_groups, score):
@@ -208,6 +254,25 @@ def test_route_backward(T, E, k, score, renormalize, scale, dtype):
     assert dx.dtype == logits.dtype and dx.shape == logits.shape
     ref, mag = grad64(logits, idx, dw, score, renormalize, scale)
     assert within(dx, ref, 48 * U * mag)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(4097, 256, 8), (4098, 255, 8), (4099, 130, 16), (4100, 64, 6), (4111, 7, 3),
+                                   (5000, 192, 1)])
+def test_route_backward_many(T, E, k, score, dtype):
+    """Bit for bit what a few of the tokens alone give (those are checked against the formula)."""
+    g = rng(T * E + k)
+    logits = randn(g, T, E).to(DT[dtype])
+    dw = randn(g, T, k)
+    _, idx = fq.moe_route(logits, k, score=score)
+    idx[5, 0] = -1
+    for renormalize in (True, False):
+        dx = fq.moe_route_backward(dw, logits, idx, score=score, renormalize=renormalize, scale=2.5)
+        for part in (slice(0, 64), slice(T - 31, T)):
+            few = fq.moe_route_backward(dw[part].contiguous(), logits[part].contiguous(), idx[part].contiguous(),
+                                        score=score, renormalize=renormalize, scale=2.5)
+            assert torch.equal(dx[part], few)
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
