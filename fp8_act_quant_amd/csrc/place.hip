@@ -11,6 +11,8 @@
 //
 // moe_combine: y[t] = sum_j w[t, j] h[slots[t, j]], and its gradient. One pass over h, 16 bytes
 // a lane; memory bound.
+#include <cmath>
+
 #include <fp8q.h>
 
 #include "device_common.h"
@@ -22,8 +24,10 @@ namespace {
 constexpr int kMaxExperts = (int)kMaxGroupedExperts;
 constexpr int PW = 16;               // waves of a placement workgroup
 constexpr int PT = 64 * PW;
-constexpr int64_t kOneChunk = 16384; // pairs that one workgroup places by itself
-constexpr int64_t kChunk = 2048;    // pairs of a chunk where there are several
+// Pairs that one workgroup places by itself, in one launch (4096 pairs of 256 experts 5.5 us, 8192 9.3;
+// two launches 7.3 and 7.5)
+constexpr int64_t kOneChunk = 6144;
+constexpr int64_t kChunk = 1024;    // pairs of a chunk where there are several
 constexpr int64_t kMaxChunks = 256;
 
 struct PlaceArgs {
@@ -37,21 +41,32 @@ struct PlaceArgs {
     int E, first, k, chunks;
 };
 
-// this wave's pairs, and its counts by expert into hist[wave]
-__device__ __forceinline__ void count_segment(const PlaceArgs &a, int64_t p0, int64_t p1, uint32_t *hist, int lane) {
-    for (int64_t p = p0 + lane; p < p1; p += 64) {
-        const int e = a.experts[p] - a.first;
-        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&hist[e], 1u);
-    }
+// Pairs are read kBatch times 64 at a time, so that their latencies overlap: a lane's experts of
+// the pairs p + lane, p + 64 + lane, ..., -1 where there is none
+constexpr int kBatch = 4;
+__device__ __forceinline__ void load_batch(const PlaceArgs &a, int64_t p, int64_t p1, int (&e)[kBatch]) {
+    const int64_t i = p + (threadIdx.x & 63);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) e[u] = i + 64 * u < p1 ? a.experts[i + 64 * u] - a.first : -1;
+}
+__device__ __forceinline__ void count_batch(const PlaceArgs &a, const int (&e)[kBatch], uint32_t *hist) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+        if ((uint32_t)e[u] < (uint32_t)a.E) atomicAdd(&hist[e[u]], 1u);
 }
 
 __global__ __launch_bounds__(PT) void place_count_kernel(PlaceArgs a) {
     __shared__ uint32_t hist[kMaxExperts];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.E; e += PT) hist[e] = 0;
+    const int wave = threadIdx.x >> 6;
+    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg, p1 = min(p0 + a.seg, a.pairs);
+    int e[kBatch];
+    load_batch(a, p0, p1, e);
+    for (int x = threadIdx.x; x < a.E; x += PT) hist[x] = 0;
     __syncthreads();
-    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg;
-    count_segment(a, p0, min(p0 + a.seg, a.pairs), hist, lane);
+    for (int64_t p = p0; p < p1; p += 64 * kBatch) {
+        if (p != p0) load_batch(a, p, p1, e);
+        count_batch(a, e, hist);
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += PT) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
 }
@@ -82,32 +97,41 @@ __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
     __shared__ uint32_t total[kMaxExperts], before[kMaxExperts];   // several chunks: of all, of the earlier ones
     __shared__ uint32_t scratch[PW];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg, p1 = min(p0 + a.seg, a.pairs);
+    int batch[kBatch];
+    load_batch(a, p0, p1, batch);
     for (int e = threadIdx.x; e < a.E; e += PT) {
 #pragma unroll
         for (int w = 0; w < PW; ++w) hist[w][e] = 0;
         total[e] = before[e] = 0;
     }
     __syncthreads();
-    const int64_t p0 = ((int64_t)blockIdx.x * PW + wave) * a.seg, p1 = min(p0 + a.seg, a.pairs);
-    count_segment(a, p0, p1, hist[wave], lane);
     if (a.chunks > 1) {
-        // the whole table [chunks][E], 8 loads in flight; sums of integers, whose order does
-        // not matter
-        const int n = a.chunks * a.E, own = blockIdx.x * a.E;
-        for (int i0 = threadIdx.x; i0 < n; i0 += 8 * PT) {
-            uint32_t c[8];
+        // the columns of the table [chunks][E], a column's chunks dealt to several threads, 8 loads in
+        // flight; sums of integers, whose order does not matter
+        const int width = min(a.E, PT), split = PT / width, part = threadIdx.x / width;
+        for (int e = threadIdx.x - part * width; e < a.E && part < split; e += width) {
+            uint32_t sum = 0, earlier = 0;
+            for (int c0 = part; c0 < a.chunks; c0 += 8 * split) {
+                uint32_t n[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) c[u] = i0 + u * PT < n ? a.counts[i0 + u * PT] : 0u;
+                for (int u = 0; u < 8; ++u) {
+                    const int c = c0 + u * split;
+                    n[u] = c < a.chunks ? a.counts[(int64_t)c * a.E + e] : 0u;
+                }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int i = i0 + u * PT;
-                if (c[u]) {
-                    const int e = (int)((uint32_t)i % (uint32_t)a.E);
-                    atomicAdd(&total[e], c[u]);
-                    if (i < own) atomicAdd(&before[e], c[u]);
+                for (int u = 0; u < 8; ++u) {
+                    sum += n[u];
+                    earlier += c0 + u * split < (int)blockIdx.x ? n[u] : 0u;
                 }
             }
+            atomicAdd(&total[e], sum);
+            atomicAdd(&before[e], earlier);
         }
+    }
+    for (int64_t p = p0; p < p1; p += 64 * kBatch) {
+        if (p != p0) load_batch(a, p, p1, batch);
+        count_batch(a, batch, hist[wave]);
     }
     __syncthreads();
 
@@ -150,38 +174,48 @@ __global__ __launch_bounds__(PT) void place_kernel(PlaceArgs a) {
 
     uint32_t *next = hist[wave];
     const int bits = 32 - __builtin_clz(a.E);
-    for (int64_t p = p0; p < p1; p += 64) {
-        const int64_t i = p + lane;
-        const bool in = i < p1;
-        const int e = in ? a.experts[i] - a.first : -1;
-        const bool there = (uint32_t)e < (uint32_t)a.E;
-        const uint64_t placed = __ballot(there);
-        uint32_t lo = (uint32_t)placed, hi = (uint32_t)(placed >> 32);   // the lanes with this lane's expert
-        for (int b = 0; b < bits; ++b) {
-            const uint32_t bit = (uint32_t)__builtin_amdgcn_sbfe(e, b, 1);   // 0 or all ones
-            const uint64_t set = __ballot(bit != 0);
-            lo &= ~((uint32_t)set ^ bit);
-            hi &= ~((uint32_t)(set >> 32) ^ bit);
-        }
-        if (there) {
-            const uint32_t r = next[e] + __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
-            a.slots[i] = (int32_t)r;
-            a.rows[r] = (int32_t)((uint32_t)i / (uint32_t)a.k);
-            // (LDS accesses of a wave run in order; the fence keeps the compiler's order)
+    for (int64_t p = p0; p < p1; p += 64 * kBatch) {
+        if (p1 - p0 > 64 * kBatch) load_batch(a, p, p1, batch);   // (otherwise they are still there)
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (p + 64 * u >= p1) break;
+            const int64_t i = p + 64 * u + lane;
+            const int e = batch[u];
+            const bool there = (uint32_t)e < (uint32_t)a.E;
+            const uint64_t placed = __ballot(there);
+            uint32_t lo = (uint32_t)placed, hi = (uint32_t)(placed >> 32);   // the lanes with this lane's expert
+            for (int b = 0; b < bits; ++b) {
+                const uint32_t bit = (uint32_t)__builtin_amdgcn_sbfe(e, b, 1);   // 0 or all ones
+                const uint64_t set = __ballot(bit != 0);
+                lo &= ~((uint32_t)set ^ bit);
+                hi &= ~((uint32_t)(set >> 32) ^ bit);
+            }
+            if (there) {
+                const uint32_t r = next[e] + __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
+                a.slots[i] = (int32_t)r;
+                a.rows[r] = (int32_t)((uint32_t)i / (uint32_t)a.k);
+                // (LDS accesses of a wave run in order; the fence keeps the compiler's order)
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const uint64_t same = ((uint64_t)hi << 32) | lo;
+                if ((same >> lane) == 1ull) next[e] = r + 1;   // the last of these lanes
+            } else if (i < p1) {
+                a.slots[i] = -1;
+            }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            const uint64_t same = ((uint64_t)hi << 32) | lo;
-            if ((same >> lane) == 1ull) next[e] = r + 1;   // the last of these lanes
-        } else if (in) {
-            a.slots[i] = -1;
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
-int64_t chunks_of(int64_t pairs) {
+// Where there are several chunks, each of their workgroups reads the whole table of counts, and
+// its waves walk their pairs one after another: the time is some a * chunks * E + b * pairs /
+// chunks, least at chunks = sqrt(b pairs / (a E)). Measured best, us: 131072 pairs of 256 experts 10.0 at
+// 64 chunks (32: 10.1, 128: 11.7), of 32 experts 7.2 at 128 (32: 8.5), of 1024 experts 15.0 at 32 (64: 18.2,
+// 128: 27); 524288 pairs of 256 experts 15.0 at 128 (64: 16.6, 256: 19).
+int64_t chunks_of(int64_t pairs, int64_t E) {
     if (pairs <= kOneChunk) return 1;
-    const int64_t c = (pairs + kChunk - 1) / kChunk;
-    return c < kMaxChunks ? c : kMaxChunks;
+    const int64_t most = (pairs + kChunk - 1) / kChunk, best = (int64_t)std::sqrt(6.0 * (double)pairs / (double)E);
+    const int64_t c = best < most ? best : most;
+    return c < 2 ? 2 : (c < kMaxChunks ? c : kMaxChunks);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -405,14 +439,14 @@ __global__ __launch_bounds__(THREADS) void combine_grad_kernel(CombineArgs a) {
 }  // namespace
 
 size_t moe_place_workspace_bytes(int64_t pairs, int64_t E) {
-    const int64_t c = chunks_of(pairs);
+    const int64_t c = chunks_of(pairs, E);
     return c == 1 ? 0 : (size_t)(c * E * 4);
 }
 
 hipError_t launch_moe_place(const int32_t *experts, int64_t *offsets, int32_t *rows, int32_t *slots, int64_t T, int k,
                             int E, int first, void *workspace, hipStream_t stream) {
     PlaceArgs a{experts, offsets, rows, slots, static_cast<uint32_t *>(workspace), T * k, 0, E, first, k, 0};
-    a.chunks = (int)chunks_of(a.pairs);
+    a.chunks = (int)chunks_of(a.pairs, E);
     const int64_t waves = (int64_t)a.chunks * PW;
     a.seg = ((a.pairs + waves - 1) / waves + 63) / 64 * 64;
     if (a.chunks > 1) {
