@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
     return v;
 }
 
-// WAVES waves to a row, which they keep in registers between the maximum and the codes where
+// Bound by memory: 16384 x 7168 54 us, 6.5 TB/s. WAVES waves to a row, which they keep in registers between the maximum and the codes where
 // it has at most 512 * WAVES * NV elements (NV > 0), and read a second time where it is longer.
 template <int WAVES, int NV>
 __global__ __launch_bounds__(256) void row_quant_kernel(const uint16_t *x, int8_t *q, float *s, int64_t M, int64_t K) {
@@ -153,7 +153,7 @@ struct Int8Args {
 };
 
 constexpr int kNonTemporal = 2;   // cache policy of buffer loads
-constexpr int64_t kLastLevelCache = 256 << 20;
+constexpr int64_t kLastLevelCache = 256 << 20;   // bytes
 
 // A past-the-end offset: loads there return zero (every buffer here is shorter)
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
@@ -196,10 +196,10 @@ __device__ __forceinline__ void expert_rows(const Int8Args &g, int e, int64_t &r
 // Grouped work order. An expert's rows are cut into blocks of BM, the last of them short. Its tiles
 // are numbered with the row block varying fastest, experts one after another: neighbours then
 // read the same weight panel, and an expert's rows stay in the L2 of the XCD that walks it. The
-// numbers are dealt to the XCDs in contiguous, equal runs. (64 experts' 4096 x 7168, 12288 rows:
-// 508 us; numbered by size, long tiles first, 542, an expert's blocks then being read through
-// several XCDs; runs of equal cost instead of equal counts 536, the grid's larger bound costing
-// more than the balance gains.)
+// numbers are dealt to the XCDs in contiguous, equal runs. (64 experts' 4096 x 7168, 12288 rows, before
+// the non-temporal accesses: 508 us; numbered by size, long tiles first, 542, an expert's blocks then
+// being read through several XCDs; runs of equal cost instead of equal counts 536, the grid's larger
+// bound costing more than the balance gains.)
 //
 // Each wave works this out by itself, 64 experts at a time.
 __device__ __forceinline__ int wave_scan(int v) {   // inclusive prefix sum over the lanes
@@ -285,7 +285,8 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
 // QUANT: the rows come as bf16 and are quantised here: every workgroup does it for itself, in LDS,
 // while its first reads of W are on their way, which costs less than a launch of its own. 1: at
 // most 4 rows of at most 8192 elements, each shared by the waves. 2: at most 8 rows of at most
-// 2048, each a wave's own. 1 x 7168 x 7168: 10 us in all, of which the 51 MB of W are 9 at 5.7 TB/s.
+// 2048, each a wave's own. Bound by the read of W: 1 x 7168 x 7168 12 us, of which its 51 MB are 9 at
+// 5.7 TB/s; 1 x 4096 x 2048 4.0 us, of which 3 are the launch.
 constexpr int kFewRows = 16;
 constexpr int few_quant_rows(int quant) { return quant == 1 ? 2 : 8; }
 constexpr int few_quant_k(int quant) { return quant == 1 ? 8192 : 2048; }
@@ -465,7 +466,10 @@ struct TileAt {
     int64_t m0, m1, n0;   // first row, end of the rows (not of the tile), first channel
     const int8_t *w;      // the tile's weight and its scales
     const float *sw;
-    bool stream;          // its W panel is read once in this call and by no next one: non-temporally
+    // Its W panel is read once in this call, and is gone from the caches by the next one: copied
+    // non-temporally (64 experts' 4096 x 7168 at 1.5 rows 203 -> 177 us; a W that stays in the caches
+    // 11.0 -> 16.5, and one read by two row blocks 512 -> 560: neither is)
+    bool stream;
 };
 
 // Tile of a workgroup. Workgroup b runs on XCD b % 8, and each XCD takes a contiguous run of the
@@ -674,7 +678,7 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (
 // the same.
 //
 // What bounds it: 16384 x 7168 x 7168 takes 500 us on zeros (3.4 POP/s: the matrix unit busy 0.78 of
-// the cycles) and 640 us on normal data, at a lower clock (about 1.6 GHz): the power limit. The
+// the cycles) and 600 us on normal data (2.8 POP/s), at a lower clock (about 1.6 GHz): the power limit. The
 // 32x32x32 instruction, at half the K and so twice the accumulator traffic, has fewer cycles
 // and yet takes 685 us.
 template <class T, int FULL, int VARIANT, int STREAM, int OUT_BF16>
@@ -807,7 +811,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // Smaller tiles of 4 waves, for shapes with too few of the large ones. Their time is K's steps one
-// after another, each waiting for memory, so as many stages as fit are in flight (128 KB a CU).
+// after another, each waiting for memory, so as many stages as fit are in flight (128 KB or more a
+// CU: 64 experts' 4096 x 7168 at 1.5 rows, 32 x 128, 158 us, W read at 7.0 TB/s; 64 x 7168 x 7168 11.2 us).
 // Two register sets hold the fragments of two steps: the MFMAs of step ks take one while the
 // other is filled with step ks + 1. A stage buffer is free once its step is in registers
 // everywhere (lgkmcnt, then the barrier), and takes the copies of step ks + NSTAGE; steps past
@@ -995,7 +1000,10 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     }
 }
 
-// Whether a linear layer is one launch, and as which of int8_few_kernel's forms
+// Whether a linear layer is one launch, and as which of int8_few_kernel's forms. One launch against
+// two, us: form 2, 8 x 4096 x 2048 5.6 / 7.0, 16 rows 8.3 / 7.3, 8 x 32768 x 2048 17 / 16 (the rows are quantised
+// over and over); form 1, 1 x 7168 x 7168 12.5 / 13.8, 2 x 4096 x 7168 10.0 / 10.7, 3 rows 11.5 / 10.7, 1 x 10240 x
+// 7168 17.1 / 16.4 (past two workgroups a CU).
 static int one_launch(int64_t M, int64_t N, int64_t K) {
     const int64_t units = (N + 15) / 16;
     if (M <= few_quant_rows(2) && K <= few_quant_k(2) && units <= 1024) return 2;

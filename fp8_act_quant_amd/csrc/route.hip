@@ -37,19 +37,20 @@ struct RouteArgs {
     float scale;
 };
 
-// Order-preserving integer key of a number: a > b as floats is key(a) > key(b) as unsigned. Every
-// number's key is above 0; 0 stands for "no candidate". (A choice is never -0: scores are +0 at the
-// least, and +0 + -0 = +0.)
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// Order-preserving integer key of a number: a > b as floats is key(a) > key(b) as unsigned. Every key
+// is above 0 (that of the NaN of all ones by the maximum); 0 stands for "no candidate", so that top_k
+// candidates are found whatever the logits hold. (A choice is never -0: scores are +0 at the least,
+// and +0 + -0 = +0.)
 __device__ __forceinline__ uint32_t key_of(float c) {
     const uint32_t u = __float_as_uint(c);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return umax(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u), 1u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // v of another lane of the same 16 (all of whose lanes are active)
 template <int CTRL>
@@ -255,7 +256,7 @@ __device__ __forceinline__ void merge2(uint32_t &m1, uint32_t &m2, uint32_t o1, 
 // selected expert is always some lane's first: a maximum over the first ones, then that lane
 // moves up. About 20 operations per selected expert; with more experts a lane the sorting
 // would cost more than it saves, and each step looks at all of them. Bound by these operations
-// (some 400 a token), not by the 4 E bytes it reads.
+// (some 400 a token), not by the 4 E bytes it reads: 16384 tokens' 256 experts 12.4 us, 1.4 TB/s.
 template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
     typedef float piece __attribute__((ext_vector_type(V)));
@@ -539,7 +540,9 @@ struct RouteGradArgs {
 //     (renormalised), or g_j
 //     sigmoid: dx_j = ds_j s_j (1 - s_j), 0 for the experts that were not selected
 //     softmax: dx_i = s_i (ds_i - sum_j ds_j s_j), ds_i = 0 for those
-// The row of ds goes through LDS, from the k selected experts' lanes to the experts' lanes.
+// The row of ds goes through LDS, from the k selected experts' lanes to the experts' lanes. Bound
+// by its operations with few tokens to a chip's worth of waves (softmax, 16384 tokens' 256 experts
+// 9.6 us), in teams by memory (65536 tokens 22 us, 6.1 TB/s).
 template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a) {
     typedef float piece __attribute__((ext_vector_type(V)));

@@ -153,6 +153,18 @@ def test_route_many(T, E, k, groups, topk_groups, group_score, biased, score, dt
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bits", [0xFFFFFFFF, 0x7FC00000, 0x7F800000])
+@pytest.mark.parametrize("T", [9, 8195])
+def test_route_experts_in_range_whatever_the_logits(T, bits, score):
+    logits = randn(rng(6), T, 250)
+    logits.view(torch.int32)[::2] = bits if bits < 1 << 31 else bits - (1 << 32)
+    for k, groups, topk_groups, group_score in ((8, 1, 1, "max"), (10, 10, 2, "top2"), (16, 10, 3, "max")):
+        _, e = fq.moe_route(logits, k, score=score, groups=groups, topk_groups=topk_groups, group_score=group_score)
+        assert 0 <= int(e.min()) and int(e.max()) < 250
+        assert bool((torch.sort(e, dim=-1).values.diff(dim=-1) > 0).all())
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_many_masked_and_tied(score):
     """Experts at -inf, rows of one value, large logits and rows with many ties beside ordinary rows."""
     T, E, k = 8195, 256, 8
