@@ -1044,9 +1044,10 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
     //      512 x 1024 at 30 / 96 / 192  10 / 17 / 28,  11 / 17 / 22,  13 / 15 / 27,  13 / 22 / 25
     // With few tiles the smallest that still all run at once: 29 experts' 169 x 4912 at 38 rows 32 x 64
     // 12, 64 x 64 15, 64 x 128 21; 53 experts' 106 x 3328 at 72 rows 11, 10, 13; 48 experts' 300 x 4000 at
-    // 52 rows 64 x 128 19, 128 x 256 34. Between the last two by rounds of 256 tiles, blocks of 256
-    // rows taking 1.5 times as long (few are full) but reading W less often: 32 experts' 1408 x 2048 at
-    // 250 rows 42 against 59; 8 experts' 4096 x 7168 at 128 rows 48 / 79, at 256 92 / 81.
+    // 52 rows 64 x 128 19, 128 x 256 34. Between the last two by rounds of 256 tiles where they are few,
+    // blocks of 256 rows taking 1.5 times as long (few are full): 32 experts' 1408 x 2048 at 250 rows 42
+    // against 59; 8 experts' 4096 x 7168 at 128 rows 48 / 79, at 256 92 / 81. With many rounds the larger
+    // blocks, which read W less often (64 experts of 144 rows each 468 / 372).
     const int64_t mean = M / experts;
     auto tiles = [&](int bm, int bn) {   // an expert's last row block counted as half
         return (M / bm + (experts < M ? experts : M) / 2) * ((N + bn - 1) / bn);
@@ -1055,8 +1056,8 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
     if (mean < 16) return launch_deep<32, 128, 4, 1>(g, out_bf16, stream);
     if (tiles(64, 64) <= 256) return launch_deep<64, 64, 5, 1>(g, out_bf16, stream);
     if (mean < 32 || tiles(64, 128) <= 512) return launch_deep<64, 128, 3, 1>(g, out_bf16, stream);
-    if (2 * ((tiles(128, 256) + 255) / 256) <= 3 * ((tiles(256, 256) + 255) / 256))
-        return launch_turns<128, 1>(g, out_bf16, stream);
+    const int64_t rounds128 = (tiles(128, 256) + 255) / 256, rounds256 = (tiles(256, 256) + 255) / 256;
+    if (rounds128 <= 2 && 2 * rounds128 <= 3 * rounds256) return launch_turns<128, 1>(g, out_bf16, stream);
     return launch_turns<256, 1>(g, out_bf16, stream);
 }
 
