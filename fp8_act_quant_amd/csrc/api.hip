@@ -470,9 +470,9 @@ const char *fp8q_strerror(int status) {
     switch (status) {
     case FP8Q_OK: return "ok";
     case FP8Q_ERR_NULL: return "a required pointer is NULL";
-    case FP8Q_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 128, or too large)";
+    case FP8Q_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 128 (8-bit integers: 16), or too large)";
     case FP8Q_ERR_ALIGN: return "pointer alignment below what the entry point requires";
-    case FP8Q_ERR_DTYPE: return "unknown output dtype";
+    case FP8Q_ERR_DTYPE: return "unknown element type or flag";
     case FP8Q_ERR_UNSUPPORTED: return "no gfx950 device is current";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_WORKSPACE:

@@ -36,7 +36,8 @@
  *     call returns a non-zero FP8Q_ERR_* code and enqueues nothing. A failed launch
  *     returns FP8Q_ERR_LAUNCH. Faults during execution surface at the caller's stream
  *     synchronisation. No C++ exception crosses this interface.
- *   - Sizes are int64_t. K must be a non-negative multiple of 128. A zero M or N (or, for
+ *   - Sizes are int64_t. K must be a non-negative multiple of 128 (of 16 for the 8-bit integer
+ *     calls; the routed-expert calls have rows of any length). A zero M or N (or, for
  *     the quantisers, K) is a valid empty call that enqueues nothing; null pointers are
  *     then allowed.
  *   - The calls are stateless and may be issued concurrently from several host threads.
@@ -54,9 +55,9 @@ extern "C" {
 /* Status codes. */
 #define FP8Q_OK 0
 #define FP8Q_ERR_NULL 1        /* a required pointer is NULL                                */
-#define FP8Q_ERR_SHAPE 2       /* negative size, K not a multiple of 128, or size too large */
+#define FP8Q_ERR_SHAPE 2       /* negative size, K not a multiple of 128 (8-bit integers: 16), or too large */
 #define FP8Q_ERR_ALIGN 3       /* pointer alignment below what the entry point requires     */
-#define FP8Q_ERR_DTYPE 4       /* unknown output dtype                                      */
+#define FP8Q_ERR_DTYPE 4       /* unknown element type or flag                              */
 #define FP8Q_ERR_UNSUPPORTED 5 /* no gfx950 device is current                               */
 #define FP8Q_ERR_LAUNCH 6      /* the kernel launch failed                                  */
 #define FP8Q_ERR_WORKSPACE 7   /* more scratch needed than fp8_block_gemm_noalloc holds, or
