@@ -230,6 +230,64 @@ def test_grouped(sizes, N, K, gather, out):
     grouped_check(y, a, sa, w, sw, offsets, rows, out)
 
 
+def uneven(E, mean, seed):
+    """Rows of E experts, some of them without any, `mean` on average."""
+    r = np.random.default_rng(seed).gamma(1.5, mean / 1.5, E).astype(int)
+    r[E // 2] = 0
+    r[0] += max(0, E * mean - int(r.sum()))
+    return r.tolist()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("E,N,K,mean", [
+    (40, 1024, 7168, 3), (40, 1024, 7168, 20), (64, 1024, 7168, 60), (40, 1024, 7168, 360), (16, 256, 70000, 10),
+    (16, 256, 70000, 100),
+])
+def test_grouped_weights_larger_than_the_caches(E, N, K, mean, out):
+    """Over 256 MB of weights, at each size of block."""
+    sizes = uneven(E, mean, E + mean)
+    R = sum(sizes)
+    g = rng(R)
+    tokens = max(1, R // 2)
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int64, device="cuda")
+    rows = torch.randint(0, tokens, (R,), generator=g, device="cuda", dtype=torch.int32)
+    a, sa, w, sw = codes(g, tokens, K), scales(g, tokens), codes(g, E, N, K), scales(g, E, N)
+    y = fq.int8_grouped_gemm(a, sa, w, sw, offsets, rows=rows, out_dtype=DT[out])
+    grouped_check(y, a, sa, w, sw, offsets, rows, out)
+
+
+@pytest.mark.parametrize("E,N,K,mean", [
+    (40, 169, 1040, 38), (60, 106, 528, 72), (50, 300, 400, 52), (30, 1408, 272, 250), (8, 2000, 144, 128),
+    (70, 1000, 656, 9), (64, 512, 1024, 200), (200, 600, 256, 5), (12, 1300, 3216, 700),
+])
+def test_grouped_sizes_of_blocks(E, N, K, mean):
+    """Numbers of tiles on both sides of where the size of the blocks changes."""
+    sizes = uneven(E, mean, E + mean)
+    R = sum(sizes)
+    g = rng(R)
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int64, device="cuda")
+    a, sa, w, sw = codes(g, R, K), scales(g, R), codes(g, E, N, K), scales(g, E, N)
+    for out in ("f32", "bf16"):
+        y = fq.int8_grouped_gemm(a, sa, w, sw, offsets, out_dtype=DT[out])
+        grouped_check(y, a, sa, w, sw, offsets, None, out)
+
+
+@pytest.mark.parametrize("N", [512, 500, 504, 511])
+def test_large_outputs_of_any_row_length(N):
+    """Rows that are whole 64-byte blocks or not, in an output that begins anywhere that 4 bytes allow."""
+    M, K = 5000, 272
+    g = rng(N)
+    a, w, sa, sw = codes(g, M, K), codes(g, N, K), scales(g, M), scales(g, N)
+    for out in ("f32", "bf16"):
+        check(fq.int8_gemm(a, sa, w, sw, out_dtype=DT[out]), a, sa, w, sw, None, out)
+        buf = torch.full((M * N + 64,), 7.0, dtype=DT[out], device="cuda")
+        at = 4 // buf.element_size()
+        y = buf[at:at + M * N].view(M, N)
+        fq.int8_gemm(a, sa, w, sw, out_dtype=DT[out], out=y)
+        check(y, a, sa, w, sw, None, out)
+        assert (buf[:at] == 7).all() and (buf[at + M * N:] == 7).all()
+
+
 @pytest.mark.parametrize("sizes", [[2, 0, 3], [150, 30, 0, 90]])
 def test_grouped_rows_no_expert_owns(sizes):
     """Rows past the last offset are not written; rows of no token (-1, past the end) are rows
