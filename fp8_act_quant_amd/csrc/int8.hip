@@ -277,7 +277,7 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
     }
 }
 
-// At most 16 rows (a decode step): every byte of W meets all of them once, so the read of W is
+// At most 8 rows (a decode step): every byte of W meets all of them once, so the read of W is
 // what counts. A workgroup takes 16 channels; its 4 waves take a quarter of K each, W straight
 // from memory into MFMA operands (nothing of it is used twice), 2 U steps of 64 bytes in flight.
 // The quarters are added in LDS, exactly.
@@ -287,7 +287,7 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
 // most 4 rows of at most 8192 elements, each shared by the waves. 2: at most 8 rows of at most
 // 2048, each a wave's own. Bound by the read of W: 1 x 7168 x 7168 12 us, of which its 51 MB are 9 at
 // 5.7 TB/s; 1 x 4096 x 2048 4.0 us, of which 3 are the launch.
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 8;   // of int8_gemm
 constexpr int few_quant_rows(int quant) { return quant == 1 ? 2 : 8; }
 constexpr int few_quant_k(int quant) { return quant == 1 ? 8192 : 2048; }
 
@@ -825,41 +825,48 @@ __device__ __forceinline__ u32x4 read_piece(const uint8_t *stage, int f, int wm,
 
 // A wave issues in order, and a copy waits for the CU's one address unit (16 cycles a copy): queued
 // in a row ahead of the MFMAs, the copies and LDS reads add to their time instead of hiding
-// behind it. So each row group's MFMAs are preceded by their share of both.
-template <class T, class Dma>
+// behind it. So each row group's MFMAs are preceded by their share of both. A step is S times 128
+// bytes of K: with the smallest tile the barrier and the LDS latency of a step take longer than
+// its copies, so it is made of two (64 x 576 x 7168 8.8 -> 7.3 us; 32 x 64 tiles gain nothing).
+template <class T, int S, class Dma>
 __device__ __forceinline__ void deep_step(int ks, const Dma &dma, uint8_t *stage, const uint8_t *stage1, int wm,
                                           int w_base, int lo, int hi,
-                                          const u32x4 (&wf)[T::SUB_N][2], const u32x4 (&xf)[T::SUB_M][2],
-                                          u32x4 (&wf_next)[T::SUB_N][2], u32x4 (&xf_next)[T::SUB_M][2],
+                                          const u32x4 (&wf)[S][T::SUB_N][2], const u32x4 (&xf)[S][T::SUB_M][2],
+                                          u32x4 (&wf_next)[S][T::SUB_N][2], u32x4 (&xf_next)[S][T::SUB_M][2],
                                           i32x4 (&acc)[T::SUB_M][T::SUB_N]) {
-    constexpr int GROUPS = 2 * T::SUB_M, READS = 2 * (T::SUB_M + T::SUB_N);
+    constexpr int PER = 2 * T::SUB_M, GROUPS = PER * S, RPER = 2 * (T::SUB_M + T::SUB_N), READS = RPER * S;
+    constexpr int COPIES = T::IPW * S, AHEAD = T::NSTAGE / S;
     __builtin_amdgcn_sched_barrier(0);          // the waits stay behind the previous step's MFMAs
     wait_lgkm0();                               // step ks is in registers
-    wait_vmcnt<T::IPW * (T::NSTAGE - 2)>();     // step ks + 1 has landed
+    wait_vmcnt<COPIES * (AHEAD - 2)>();         // step ks + 1 has landed
     lds_barrier();
 #pragma unroll
     for (int q = 0; q < GROUPS; ++q) {
 #pragma unroll
         for (int r = q * READS / GROUPS; r < (q + 1) * READS / GROUPS; ++r) {
-            const u32x4 v = read_piece<T>(stage1, r / 2, wm, w_base, r & 1 ? hi : lo);
-            if (r / 2 < T::SUB_N) wf_next[r / 2][r & 1] = v;
-            else xf_next[r / 2 - T::SUB_N][r & 1] = v;
+            const int sub = r / RPER, f = r % RPER / 2;
+            const u32x4 v = read_piece<T>(stage1 + sub * T::STAGE, f, wm, w_base, r & 1 ? hi : lo);
+            if (f < T::SUB_N) wf_next[sub][f][r & 1] = v;
+            else xf_next[sub][f - T::SUB_N][r & 1] = v;
         }
-        dma.issue(stage, ks + T::NSTAGE, q * T::IPW / GROUPS, (q + 1) * T::IPW / GROUPS - q * T::IPW / GROUPS);
-        const int h = q / T::SUB_M, i = q % T::SUB_M;
 #pragma unroll
-        for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = mfma_i8(wf[j][h], xf[i][h], acc[i][j]);
+        for (int c = q * COPIES / GROUPS; c < (q + 1) * COPIES / GROUPS; ++c)
+            dma.issue(stage + c / T::IPW * T::STAGE, (ks + AHEAD) * S + c / T::IPW, c % T::IPW, 1);
+        const int sub = q / PER, h = q % PER / T::SUB_M, i = q % T::SUB_M;
+#pragma unroll
+        for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = mfma_i8(wf[sub][j][h], xf[sub][i][h], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <class T, int VARIANT, int STREAM, int OUT_BF16>
+template <class T, int S, int VARIANT, int STREAM, int OUT_BF16>
 __device__ __forceinline__ void deep(const Int8Args &g, const TileAt &at, uint8_t *smem) {
-    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, NSTAGE = T::NSTAGE;
+    constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, NSTAGE = T::NSTAGE, RPER = 2 * (SUB_M + SUB_N);
+    static_assert(NSTAGE % S == 0 && NSTAGE / S >= 3, "stages");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
-    const int nks = (int)((g.K + KB - 1) / KB);
+    const int nks = (int)((g.K + KB * S - 1) / (KB * S));
     const Int8Dma<T, VARIANT, STREAM> dma(g, at, wave, lane);
 
     i32x4 acc[SUB_M][SUB_N];
@@ -874,23 +881,24 @@ __device__ __forceinline__ void deep(const Int8Args &g, const TileAt &at, uint8_
 
 #pragma unroll
     for (int s = 0; s < NSTAGE; ++s) dma.issue(smem + s * T::STAGE, s);
-    wait_vmcnt<T::IPW *(NSTAGE - 1)>();
+    wait_vmcnt<T::IPW *(NSTAGE - S)>();
     lds_barrier();
-    u32x4 wf0[SUB_N][2], xf0[SUB_M][2], wf1[SUB_N][2], xf1[SUB_M][2];
+    u32x4 wf0[S][SUB_N][2], xf0[S][SUB_M][2], wf1[S][SUB_N][2], xf1[S][SUB_M][2];
 #pragma unroll
-    for (int r = 0; r < 2 * (SUB_M + SUB_N); ++r) {
-        const u32x4 v = read_piece<T>(smem, r / 2, wm, w_base, r & 1 ? hi : lo);
-        if (r / 2 < SUB_N) wf0[r / 2][r & 1] = v;
-        else xf0[r / 2 - SUB_N][r & 1] = v;
+    for (int r = 0; r < RPER * S; ++r) {
+        const int sub = r / RPER, f = r % RPER / 2;
+        const u32x4 v = read_piece<T>(smem + sub * T::STAGE, f, wm, w_base, r & 1 ? hi : lo);
+        if (f < SUB_N) wf0[sub][f][r & 1] = v;
+        else xf0[sub][f - SUB_N][r & 1] = v;
     }
     uint8_t *const end = smem + NSTAGE * T::STAGE;
     uint8_t *stage = smem;
     for (int ks = 0; ks < nks; ks += 2) {
         // (with an odd number of steps the last one here multiplies zeros)
-        uint8_t *stage1 = stage + T::STAGE == end ? smem : stage + T::STAGE;
-        uint8_t *stage2 = stage1 + T::STAGE == end ? smem : stage1 + T::STAGE;
-        deep_step<T>(ks, dma, stage, stage1, wm, w_base, lo, hi, wf0, xf0, wf1, xf1, acc);
-        deep_step<T>(ks + 1, dma, stage1, stage2, wm, w_base, lo, hi, wf1, xf1, wf0, xf0, acc);
+        uint8_t *stage1 = stage + S * T::STAGE == end ? smem : stage + S * T::STAGE;
+        uint8_t *stage2 = stage1 + S * T::STAGE == end ? smem : stage1 + S * T::STAGE;
+        deep_step<T, S>(ks, dma, stage, stage1, wm, w_base, lo, hi, wf0, xf0, wf1, xf1, acc);
+        deep_step<T, S>(ks + 1, dma, stage1, stage2, wm, w_base, lo, hi, wf1, xf1, wf0, xf0, acc);
         stage = stage2;
     }
     wait_lgkm0();
@@ -905,8 +913,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
     TileAt at;
     if (!find_tile<T, GROUPED>(g, at)) return;
-    if (GROUPED && at.stream) deep<T, VARIANT, GROUPED, OUT_BF16>(g, at, smem);
-    else deep<T, VARIANT, 0, OUT_BF16>(g, at, smem);
+    constexpr int S = BN == 32 ? 2 : 1;
+    if (GROUPED && at.stream) deep<T, S, VARIANT, GROUPED, OUT_BF16>(g, at, smem);
+    else deep<T, S, VARIANT, 0, OUT_BF16>(g, at, smem);
 }
 
 template <int U, int QUANT>
@@ -969,10 +978,9 @@ hipError_t launch_int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, 
 
 hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const float *bias,
                             void *y, bool out_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-    // Few tiles of 32 x 64 and few rows: 16 channels a workgroup use more of the CUs (16 x 1536 x 7168:
-    // 9.3 us against 10.1; 16 x 7168 x 7168, 112 tiles: 15.9 against 10.6).
-    const int64_t tiles32 = (M + 31) / 32 * ((N + 63) / 64);
-    if (M <= kFewRows && tiles32 <= 64)
+    // Few rows: against the tiles, us, W from memory: 1 x 1536 x 7168 6.7 / 9.1, 4 rows 7.3 / 9.1, 16 rows 9.5 / 9.2;
+    // 1 x 4096 x 7168 7.6 / 10.5; 1 x 7168 x 7168 (two workgroups on most CUs) 12.6 / 11.8.
+    if (M <= kFewRows && N <= 4096)
         return launch_few<8, 0>({a, sa, nullptr, w, sw, bias, y, N, (int)M, (int)K}, out_bf16, stream);
     const Int8Args g{a, sa, w, sw, bias, y, nullptr, nullptr, M, N, K, M, 0, 0, 0, 1, false};
     // The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps. The
@@ -984,18 +992,20 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
         const double rounds = (double)((tiles + 255) / 256);
         return steps * (first + more * (rounds - 1.0)) + end * rounds;
     };
-    const double t[6] = {time(32, 64, 0.155, 0.125, 1.1), time(64, 64, 0.21, 0.18, 1.4),
-                         time(64, 128, 0.34, 0.27, 1.5),  time(128, 128, 0.45, 0.53, 5.0),
-                         time(128, 256, 0.75, 0.83, 5.7), time(256, 256, 1.3, 1.5, 8.0)};
+    const double t[7] = {time(32, 32, 0.105, 0.085, 1.0), time(32, 64, 0.155, 0.125, 1.1),
+                         time(64, 64, 0.21, 0.18, 1.4),   time(64, 128, 0.34, 0.27, 1.5),
+                         time(128, 128, 0.45, 0.53, 5.0), time(128, 256, 0.75, 0.83, 5.7),
+                         time(256, 256, 1.3, 1.5, 8.0)};
     int best = 0;
-    for (int i = 1; i < 6; ++i)
+    for (int i = 1; i < 7; ++i)
         if (t[i] < t[best]) best = i;
     switch (best) {
-    case 0: return launch_deep<32, 64, 6, 0>(g, out_bf16, stream);
-    case 1: return launch_deep<64, 64, 5, 0>(g, out_bf16, stream);
-    case 2: return launch_deep<64, 128, 3, 0>(g, out_bf16, stream);
-    case 3: return launch_deep<128, 128, 4, 0>(g, out_bf16, stream);
-    case 4: return launch_turns<128, 0>(g, out_bf16, stream);
+    case 0: return launch_deep<32, 32, 8, 0>(g, out_bf16, stream);
+    case 1: return launch_deep<32, 64, 6, 0>(g, out_bf16, stream);
+    case 2: return launch_deep<64, 64, 5, 0>(g, out_bf16, stream);
+    case 3: return launch_deep<64, 128, 3, 0>(g, out_bf16, stream);
+    case 4: return launch_deep<128, 128, 4, 0>(g, out_bf16, stream);
+    case 5: return launch_turns<128, 0>(g, out_bf16, stream);
     default: return launch_turns<256, 0>(g, out_bf16, stream);
     }
 }
@@ -1042,8 +1052,9 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
     //     4096 x 7168   32 x 128 158 / 280 / 326 / 432 / 606 / 976    64 x 128 165 / 287 / 296 / 365 / 482 / 689
     //                  128 x 256 189 / 286 / 303 / 357 / 407 / 562   256 x 256 190 / 286 / 304 / 336 / 389 / 500
     //      512 x 1024 at 30 / 96 / 192  10 / 17 / 28,  11 / 17 / 22,  13 / 15 / 27,  13 / 22 / 25
-    // With few tiles the smallest that still all run at once: 29 experts' 169 x 4912 at 38 rows 32 x 64
-    // 12, 64 x 64 15, 64 x 128 21; 53 experts' 106 x 3328 at 72 rows 11, 10, 13; 48 experts' 300 x 4000 at
+    // With few tiles the smallest that still all run at once (a CU reads some 65 GB/s from memory, so the
+    // more of them the better): 12 experts' 412 x 4752 at 16 rows 32 x 32 11, 32 x 64 17, 64 x 64 17; 29 experts'
+    // 169 x 4912 at 38 rows 32 x 64 12, 64 x 64 15, 64 x 128 21; 53 experts' 106 x 3328 at 72 rows 11, 10, 13; 48 experts' 300 x 4000 at
     // 52 rows 64 x 128 19, 128 x 256 34. Between the last two by rounds of 256 tiles where they are few,
     // blocks of 256 rows taking 1.5 times as long (few are full): 32 experts' 1408 x 2048 at 250 rows 42
     // against 59; 8 experts' 4096 x 7168 at 128 rows 48 / 79, at 256 92 / 81. With many rounds the larger
@@ -1052,6 +1063,7 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
     auto tiles = [&](int bm, int bn) {   // an expert's last row block counted as half
         return (M / bm + (experts < M ? experts : M) / 2) * ((N + bn - 1) / bn);
     };
+    if (tiles(32, 32) <= 256) return launch_deep<32, 32, 8, 1>(g, out_bf16, stream);
     if (tiles(32, 64) <= 256) return launch_deep<32, 64, 6, 1>(g, out_bf16, stream);
     if (mean < 16) return launch_deep<32, 128, 4, 1>(g, out_bf16, stream);
     if (tiles(64, 64) <= 256) return launch_deep<64, 64, 5, 1>(g, out_bf16, stream);
