@@ -282,14 +282,10 @@ __device__ __forceinline__ void store4(void *y, int64_t at, const f32x4 &v, int6
 // from memory into MFMA operands (nothing of it is used twice), 2 U steps of 64 bytes in flight.
 // The quarters are added in LDS, exactly.
 //
-// QUANT: the rows come as bf16 and are quantised here: every workgroup does it for itself, in LDS,
-// while its first reads of W are on their way, which costs less than a launch of its own. 1: at
-// most 4 rows of at most 8192 elements, each shared by the waves. 2: at most 8 rows of at most
-// 2048, each a wave's own. Bound by the read of W: 1 x 7168 x 7168 12 us, of which its 51 MB are 9 at
-// 5.7 TB/s; 1 x 4096 x 2048 4.0 us, of which 3 are the launch.
-constexpr int kFewRows = 8;   // of int8_gemm
-constexpr int few_quant_rows(int quant) { return quant == 1 ? 2 : 8; }
-constexpr int few_quant_k(int quant) { return quant == 1 ? 8192 : 2048; }
+// QUANT: the rows, of at most 2048 elements, come as bf16 and are quantised here: every workgroup does
+// it for itself, in LDS, a row by a wave, while its first reads of W are on their way, which costs less
+// than a launch of its own. 1 x 4096 x 2048 4.0 us, of which 3 are the launch; 8 rows 5.6.
+constexpr int kFewRows = 8, kFewQuantK = 2048;
 
 struct Int8FewArgs {
     const int8_t *a;       // QUANT: null
@@ -305,10 +301,10 @@ struct Int8FewArgs {
 
 template <int U, int QUANT, int OUT_BF16>
 __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
-    constexpr int QROWS = few_quant_rows(QUANT), QK = few_quant_k(QUANT), PITCH = QK + 16;
+    constexpr int PITCH = kFewQuantK + 16;
     __shared__ i32x4 part[4][64];
-    __shared__ __attribute__((aligned(16))) uint8_t codes[QUANT ? QROWS * PITCH : 16];
-    __shared__ uint32_t tops[QUANT == 1 ? 4 : 1][QUANT ? QROWS : 1];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[QUANT ? kFewRows * PITCH : 16];
+    __shared__ uint32_t tops[kFewRows];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
@@ -342,7 +338,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
             u32x4 x = {0, 0, 0, 0};
             if constexpr (QUANT) {
                 // (past K: whatever lies there, against zeros of W; always inside `codes`)
-                const int k = min((s + u) * 64 + kg * 16, QK);
+                const int k = min((s + u) * 64 + kg * 16, kFewQuantK);
                 if (row < M) x = *reinterpret_cast<const u32x4 *>(codes + row * PITCH + k);
             } else {
                 x = av[b][u];
@@ -352,18 +348,16 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
     };
     float scale = 0.0f;   // of this lane's row
     if constexpr (QUANT) {
-        // piece i of row j of this thread's: of all rows (1) or every fourth (2)
-        constexpr int ROWS = 2, STRIDE = QUANT == 1 ? 256 : 64, NV = QK / 8 / STRIDE;
-        const int first = QUANT == 1 ? 0 : wave, next = QUANT == 1 ? 1 : 4, at = QUANT == 1 ? threadIdx.x : lane;
+        constexpr int ROWS = kFewRows / 4, NV = kFewQuantK / 512;   // of a wave: every fourth row
         u32x4 v[ROWS][NV];
         // the rows first: loads return in order, and these are needed before W
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            const int m = first + next * j;
+            const int m = wave + 4 * j;
             if (m < M) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int p = at + STRIDE * i;
+                    const int p = lane + 64 * i;
                     v[j][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                             ra, 8 * p < K ? (uint32_t)(2 * (m * K + 8 * p)) : kNowhere, 0, 0));
                 }
@@ -373,48 +367,28 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
         load(0, s0);
         load(1, s0 + U);
         __builtin_amdgcn_sched_barrier(0);
-        uint32_t top[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            const int m = first + next * j;
+            const int m = wave + 4 * j;
             if (m < M) {
-                top[j] = 0;
+                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const uint32_t b = absmax_bits8(v[j][i]);
-                    top[j] = top[j] > b ? top[j] : b;
+                    top = top > b ? top : b;
                 }
-                top[j] = wave_umax(top[j]);
-                if (lane == 0) tops[QUANT == 1 ? wave : 0][m] = top[j];
-            }
-        }
-        if constexpr (QUANT == 1) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                if (j < M) {
-                    top[j] = tops[0][j];
-#pragma unroll
-                    for (int w = 1; w < 4; ++w) top[j] = top[j] > tops[w][j] ? top[j] : tops[w][j];
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-            const int m = first + next * j;
-            if (m < M) {
-                const RowScale r = row_scale(top[j]);
-                if constexpr (QUANT == 1) scale = row == m ? r.s : scale;
+                top = wave_umax(top);
+                if (lane == 0) tops[m] = top;
+                const RowScale r = row_scale(top);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int p = at + STRIDE * i;
+                    const int p = lane + 64 * i;
                     if (8 * p < K) *reinterpret_cast<u32x2 *>(codes + m * PITCH + 8 * p) = codes8(v[j][i], r);
                 }
             }
         }
         __syncthreads();
-        if constexpr (QUANT == 2)
-            if (row < M) scale = row_scale(tops[0][row]).s;
+        if (row < M) scale = row_scale(tops[row]).s;
     } else {
         load(0, s0);
         if (row < M && K > 0) scale = g.sa[row];
@@ -810,6 +784,126 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 }
 
+// One or two rows of up to 8192 elements, as bf16 (a decoded token): 32 channels a workgroup. W comes
+// through LDS, in stages of four times 128 bytes of K, while the rows are quantised into LDS by every
+// workgroup for itself. Waves 0 and 1 take 16 channels each and the first half of every 128 bytes,
+// waves 2 and 3 the other half. Bound by the read of W: 1 x 7168 x 7168 9.8 us, of which its 51 MB
+// are 9 at 5.7 TB/s (with W straight into registers, half a line of a row at a time, 12.1). Three stages,
+// so that two workgroups share a CU: with four 1 x 10240 x 7168 takes 17.2 instead of 13.4.
+constexpr int kRowRows = 2, kRowK = 8192;
+template <int OUT_BF16>
+__global__ __launch_bounds__(256) void int8_row_kernel(Int8FewArgs g) {
+    constexpr int BN = 32, SUBS = 4, STAGES = 3, STEP = BN * KB, STAGE = SUBS * STEP, PITCH = kRowK + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t ring[STAGES * STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kRowRows * PITCH];
+    __shared__ uint32_t tops[4][kRowRows];
+    __shared__ i32x4 part[2][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 15, kg = lane >> 4, K = g.K, M = g.M;
+    const int64_t n0 = (int64_t)blockIdx.x * BN;
+    const int nw = (int)(g.N - n0 < BN ? g.N - n0 : BN);
+    const rsrc_t rw = make_rsrc(g.w + n0 * K, (int64_t)nw * K), rx = make_rsrc(g.x, (int64_t)M * K * 2);
+
+    constexpr int NV = kRowK / 8 / 256;   // pieces of 8 elements a thread keeps of a row
+    u32x4 v[kRowRows][NV];
+    // the rows first: loads return in order, and these are needed before W
+#pragma unroll
+    for (int m = 0; m < kRowRows; ++m) {
+        if (m < M) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int p = threadIdx.x + 256 * i;
+                v[m][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                        rx, 8 * p < K ? (uint32_t)(2 * (m * K + 8 * p)) : kNowhere, 0, 0));
+            }
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // Copies of a stage: each wave 8 rows of W, lane L the physical chunk L % 8 of row L / 8; bytes past K,
+    // and channels past N, read as zero, which makes what `codes` holds there count for nothing
+    const int chunk_byte = swz_chunk(lane >> 3, lane & 7) << 4;
+    const uint32_t off = (uint32_t)((8 * wave + (lane >> 3)) * K) + chunk_byte;
+    auto copy = [&](uint8_t *stage, int ks) {
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) {
+            const int koff = __builtin_amdgcn_readfirstlane((ks * SUBS + s) * KB);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(stage + s * STEP + 8 * wave * KB), 16,
+                                                     koff + chunk_byte >= K ? kNowhere : off, koff, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) copy(ring + s * STAGE, s);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < kRowRows; ++m) {
+        if (m < M) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const uint32_t b = absmax_bits8(v[m][i]);
+                top = top > b ? top : b;
+            }
+            top = wave_umax(top);
+            if (lane == 0) tops[wave][m] = top;
+        }
+    }
+    wait_lgkm0();   // (a barrier that waits for LDS, not for the copies)
+    lds_barrier();
+    float scale = 0.0f;   // of this lane's row
+#pragma unroll
+    for (int m = 0; m < kRowRows; ++m) {
+        if (m < M) {
+            uint32_t top = tops[0][m];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) top = top > tops[w][m] ? top : tops[w][m];
+            const RowScale r = row_scale(top);
+            scale = row == m ? r.s : scale;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int p = threadIdx.x + 256 * i;
+                if (8 * p < K) *reinterpret_cast<u32x2 *>(codes + m * PITCH + 8 * p) = codes8(v[m][i], r);
+            }
+        }
+    }
+
+    const int cg = wave & 1, half = wave >> 1;
+    const int w_at = (16 * cg + row) * KB + (swz_chunk(row, 4 * half + kg) << 4);
+    const uint8_t *x_at = codes + (row < M ? row : 0) * PITCH + 64 * half + 16 * kg;
+    i32x4 acc = {0, 0, 0, 0};
+    const int nks = (K + SUBS * KB - 1) / (SUBS * KB);
+    uint8_t *stage = ring, *last = ring + (STAGES - 1) * STAGE;   // `last`: of the step before
+    for (int ks = 0; ks < nks; ++ks) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_lgkm0();                                // (the codes, and the step before's reads)
+        wait_vmcnt<SUBS *(STAGES - 2)>();            // this step has landed
+        lds_barrier();
+        copy(last, ks + STAGES - 1);
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + s * STEP + w_at);
+            u32x4 x = {0, 0, 0, 0};
+            if (row < M) x = *reinterpret_cast<const u32x4 *>(x_at + (ks * SUBS + s) * KB);
+            acc = mfma_i8(w, x, acc);
+        }
+        last = stage;
+        stage = stage + STAGE == ring + STAGES * STAGE ? ring : stage + STAGE;
+    }
+    wait_vmcnt<0>();
+    if (half == 1) part[cg][lane] = acc;
+    __syncthreads();
+    const int64_t n = n0 + 16 * cg + 4 * kg;
+    if (half == 1 || row >= M || n >= g.N) return;
+    const i32x4 sum = acc + part[cg][lane];
+    f32x4 out;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t nr = n + r < g.N ? n + r : g.N - 1;
+        out[r] = (float)sum[r] * scale * g.sw[nr] + (g.bias ? g.bias[nr] : 0.0f);
+    }
+    store4<OUT_BF16>(g.y, row * g.N + n, out, g.N - n);
+}
+
 // Smaller tiles of 4 waves, for shapes with too few of the large ones. Their time is K's steps one
 // after another, each waiting for memory, so as many stages as fit are in flight (128 KB or more a
 // CU: 64 experts' 4096 x 7168 at 1.5 rows, 32 x 128, 158 us, W read at 7.0 TB/s; 64 x 7168 x 7168 11.2 us).
@@ -1010,14 +1104,12 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     }
 }
 
-// Whether a linear layer is one launch, and as which of int8_few_kernel's forms. One launch against
-// two, us: form 2, 8 x 4096 x 2048 5.6 / 7.0, 16 rows 8.3 / 7.3, 8 x 32768 x 2048 17 / 16 (the rows are quantised
-// over and over); form 1, 1 x 7168 x 7168 12.5 / 13.8, 2 x 4096 x 7168 10.0 / 10.7, 3 rows 11.5 / 10.7, 1 x 10240 x
-// 7168 17.1 / 16.4 (past two workgroups a CU).
+// Whether a linear layer is one launch, and by which kernel (1: int8_row_kernel, 2: int8_few_kernel). One
+// launch against two, us: 2, 8 x 4096 x 2048 5.6 / 7.0, 16 rows 8.3 / 7.3, 8 x 32768 x 2048 17 / 16 (the rows are
+// quantised over and over); 1, 1 x 512 x 2560 4.4 / 6.1, 1 x 7168 x 7168 10.0 / 13.1, 2 x 32768 x 7168 42.8 / 44.7.
 static int one_launch(int64_t M, int64_t N, int64_t K) {
-    const int64_t units = (N + 15) / 16;
-    if (M <= few_quant_rows(2) && K <= few_quant_k(2) && units <= 1024) return 2;
-    if (M <= few_quant_rows(1) && K <= few_quant_k(1) && units <= 512) return 1;
+    if (M <= kFewRows && K <= kFewQuantK && N <= 16384) return 2;
+    if (M <= kRowRows && K <= kRowK) return 1;
     return 0;
 }
 
@@ -1030,10 +1122,15 @@ hipError_t launch_int8_linear(const uint16_t *x, const int8_t *w, const float *s
                               bool out_bf16, int64_t M, int64_t N, int64_t K, void *workspace, hipStream_t stream) {
     const Int8FewArgs few{nullptr, nullptr, x, w, sw, bias, y, N, (int)M, (int)K};
     switch (one_launch(M, N, K)) {
-    case 1:   // (2 U steps cover a wave's quarter of K, all in flight at once)
-        if (K <= 4096) return launch_few<8, 1>(few, out_bf16, stream);
-        return launch_few<14, 1>(few, out_bf16, stream);
-    case 2: return launch_few<4, 2>(few, out_bf16, stream);
+    case 1: {
+        const int64_t units = (N + 31) / 32;
+        if (units * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
+        const dim3 grid((unsigned)units), block(256);
+        if (out_bf16) int8_row_kernel<1><<<grid, block, 0, stream>>>(few);
+        else int8_row_kernel<0><<<grid, block, 0, stream>>>(few);
+        return hipGetLastError();
+    }
+    case 2: return launch_few<4, 1>(few, out_bf16, stream);
     }
     int8_t *q = static_cast<int8_t *>(workspace);
     float *s = reinterpret_cast<float *>(q + M * K);
