@@ -165,6 +165,17 @@ def test_quant_zero_rows_and_empty():
     assert q.shape == (0, 32) and s.shape == (0,)
 
 
+@pytest.mark.parametrize("M,K", [(512, 1040), (513, 1040), (600, 2048), (515, 512), (514, 2064), (130, 20000)])
+def test_quant_many_rows(M, K):
+    g = rng(M + K)
+    x = (torch.randn((M, K), generator=g, device="cuda") * torch.logspace(-3, 3, M, device="cuda")[:, None]).bfloat16()
+    x[M // 2] = 0
+    q, s = fq.int8_quant(x)
+    rq, rs = quant_ref(x)
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("shape,N", [((1, 256), 96), ((2, 3, 1536), 200), ((300, 512), 576), ((1, 16), 1),
                                      ((2, 1040), 33), ((3, 7168), 130), ((4, 8192), 100), ((4, 8208), 100),
