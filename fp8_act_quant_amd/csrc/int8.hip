@@ -418,22 +418,20 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8FewArgs g) {
 }
 
 // Many rows: tiles of BM x BN in LDS, NW waves in a WAVES_M x (NW / WAVES_M) grid. Tile rows go to
-// the waves in runs of RUN, so that with 256 rows the first 128 are every wave's first 64 and the
-// next 128 its next: row group i (16 rows) of the waves in row wm of the grid starts at tile row
-// row(wm, i).
+// the waves in groups of 16 in turn, so that a tile with fewer rows is shared evenly, and of 256 rows
+// the first 128 are every wave's first half: group i of the waves in row wm of the grid starts at tile
+// row row(wm, i).
 template <int BM_, int BN_, int NW_, int WAVES_M_, int NSTAGE_>
 struct Int8Tile {
     static constexpr int BM = BM_, BN = BN_, NW = NW_, WAVES_M = WAVES_M_, WAVES_N = NW_ / WAVES_M_;
     static constexpr int NSTAGE = NSTAGE_;
-    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, RUN = WM < 64 ? WM : 64;
+    static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
     static constexpr int SUB_M = WM / 16, SUB_N = WN / 16;
     static constexpr int A_BYTES = BM * KB, W_BYTES = BN * KB, STAGE = A_BYTES + W_BYTES;
     static constexpr int A_INSTR = BM / (8 * NW), W_INSTR = BN / (8 * NW), IPW = A_INSTR + W_INSTR;
     static_assert(WAVES_M * WAVES_N == NW && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile shape");
     static_assert(STAGE * NSTAGE <= 160 * 1024 && IPW * (NSTAGE - 1) < 64, "LDS budget, vmcnt range");
-    __device__ static __forceinline__ constexpr int row(int wm, int i) {
-        return i / (RUN / 16) * (RUN * WAVES_M) + wm * RUN + i % (RUN / 16) * 16;
-    }
+    __device__ static __forceinline__ constexpr int row(int wm, int i) { return 16 * (i * WAVES_M + wm); }
 };
 
 // A workgroup's tile
