@@ -34,7 +34,7 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
                 bias: torch.Tensor | None = None, out_dtype=torch.bfloat16) -> torch.Tensor:
     """y = x . weight^T (+ bias) for bf16 activations x [..., K] and an 8-bit weight [N, K] with
     one scale per channel [N] (as int8_quant gives them): int8_gemm of int8_quant(x), bit for
-    bit, in one call (at most 4 tokens: in one launch)."""
+    bit, in one call (a few tokens: in one launch)."""
     return native.linear(x, weight, weight_scale, bias, out_code(out_dtype))
 
 

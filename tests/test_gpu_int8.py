@@ -299,6 +299,33 @@ def test_large_outputs_of_any_row_length(N):
         assert (buf[:at] == 7).all() and (buf[at + M * N:] == 7).all()
 
 
+def test_offsets_past_32_bits():
+    """An output of more than 2^31 elements, experts' weights and rows of more than 2^32 bytes: the
+    ends of each."""
+    g = rng(9)
+    M, N, K = 70000, 32768, 16
+    a, w, sa, sw = codes(g, M, K), codes(g, N, K), scales(g, M), scales(g, N)
+    y = fq.int8_gemm(a, sa, w, sw, out_dtype=torch.bfloat16)
+    for part in (slice(0, 5), slice(M // 2, M // 2 + 5), slice(M - 5, M)):
+        check(y[part], a[part], sa[part], w, sw, None, "bf16")
+    del y
+    E, N, K = 70, 8192, 8192
+    w, sw = codes(g, E, N, K), scales(g, E, N)
+    sizes = [0] * E
+    sizes[0], sizes[40], sizes[E - 1] = 3, 40, 5
+    offsets = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int64, device="cuda")
+    a, sa = codes(g, 48, K), scales(g, 48)
+    grouped_check(fq.int8_grouped_gemm(a, sa, w, sw, offsets, out_dtype=torch.float32), a, sa, w, sw, offsets, None, "f32")
+    del w
+    M, K = 300000, 8192
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, K), generator=g, device="cuda").bfloat16()
+    q, s = fq.int8_quant(x)
+    rq, rs = quant_ref(x[-3:])
+    assert np.array_equal(q[-3:].cpu().numpy(), rq) and np.array_equal(s[-3:].cpu().numpy(), rs)
+    assert not bool(s[:-3].any())
+
+
 @pytest.mark.parametrize("sizes", [[2, 0, 3], [150, 30, 0, 90]])
 def test_grouped_rows_no_expert_owns(sizes):
     """Rows past the last offset are not written; rows of no token (-1, past the end) are rows

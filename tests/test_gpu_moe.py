@@ -413,6 +413,40 @@ def test_combine_backward(T, k, H, E, n, dtype):
     assert abs(float(dw[T // 2, k // 2]) - float(num)) <= 1e-4 * H ** 0.5
 
 
+def test_offsets_past_32_bits():
+    """Rows, tokens and logits whose elements are more than 2^32: the last of each."""
+    g = rng(11)
+    T, k, H = 40000, 8, 14336
+    h = torch.zeros((T * k, H), dtype=torch.bfloat16, device="cuda")
+    h[-64:] = randn(g, 64, H).bfloat16()
+    slots = torch.arange(T * k, device="cuda", dtype=torch.int32).view(T, k)
+    w = randn(g, T, k)
+    y = fq.moe_combine(h, slots, w)
+    ref = (w[-8:, :, None].double() * h[-64:].view(8, k, H).double()).sum(1)
+    mag = (w[-8:, :, None].double() * h[-64:].view(8, k, H).double()).abs().sum(1)
+    assert not bool(y[:-8].any())
+    lo, hi = (ref - 16 * U * mag).bfloat16(), (ref + 16 * U * mag).bfloat16()
+    assert bool(((y[-8:] >= lo) & (y[-8:] <= hi)).all())
+    dy = randn(g, T, H).bfloat16()
+    dh, dw = fq.moe_combine_backward(dy, h, slots, w)
+    assert torch.equal(dh[-k:], (w[-1][:, None] * dy[-1].float()).bfloat16())
+    ref = (h[-64:].view(8, k, H).double() * dy[-8:, None].double()).sum(-1)
+    mag = (h[-64:].view(8, k, H).double() * dy[-8:, None].double()).abs().sum(-1)
+    assert bool(((dw[-8:] - ref).abs() <= H * U * mag).all()) and not bool(dw[:-8].any())
+    del h, dh, dy, y
+    T, E = 4200000, 1024
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    logits[-5:] = randn(g, 5, E).bfloat16()
+    for n in (E, 250):   # (a wave to a token, and 16 lanes)
+        part = logits if n == E else logits.view(-1)[:T * E // n * n].view(-1, n)[-(1 << 24) + 1:]
+        wp, ep = fq.moe_route(part, 4)
+        wl, el = fq.moe_route(part[-9:].contiguous(), 4)
+        assert torch.equal(ep[-9:], el) and torch.equal(wp[-9:], wl)
+        assert bool((ep[:100] == torch.arange(4, device="cuda", dtype=torch.int32)).all())
+    dx = fq.moe_route_backward(wp, part, ep)
+    assert torch.equal(dx[-9:], fq.moe_route_backward(wl, part[-9:].contiguous(), el))
+
+
 def test_gather_gradient_is_combine_without_weights():
     """x[rows]'s gradient: each token's rows of it, added up."""
     g = rng(9)
