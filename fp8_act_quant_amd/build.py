@@ -72,7 +72,7 @@ def build_binding(verbose: bool = False) -> str:
            *(f for d in (os.path.join(top, "include"), os.path.join(rocm, "include"),
                          sysconfig.get_paths()["include"]) for f in ("-isystem", d)),
            "-I", INCLUDE, os.path.join(CSRC, "binding.cpp"), "-o", tmp,
-           "-L", os.path.join(top, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+           "-L", os.path.join(top, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
            "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

