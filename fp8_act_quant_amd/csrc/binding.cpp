@@ -4,7 +4,7 @@
 //
 // Native because these calls are small: a decode step's kernel takes 3 us, and checks, allocations
 // and ctypes in Python took 6 us a call around the 3 us that the launch itself takes; here they
-// take about 1.5 us. Names, defaults and documentation are in moe.py and int8.py.
+// take about 1 us. Names, defaults and documentation are in moe.py and int8.py.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
