@@ -898,7 +898,7 @@ __global__ __launch_bounds__(256) void int8_row_kernel(Int8FewArgs g) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int64_t nr = n + r < g.N ? n + r : g.N - 1;
-        out[r] = (float)sum[r] * scale * g.sw[nr] + (g.bias ? g.bias[nr] : 0.0f);
+        out[r] = (float)sum[r] * scale * (K > 0 ? g.sw[nr] : 0.0f) + (g.bias ? g.bias[nr] : 0.0f);
     }
     store4<OUT_BF16>(g.y, row * g.N + n, out, g.N - n);
 }

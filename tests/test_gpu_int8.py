@@ -449,3 +449,24 @@ def test_refusals():
         fq.int8_grouped_gemm(a, sa, w3, sw[None], off, rows=torch.zeros(4, dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
         fq.int8_grouped_gemm(a, sa, w3, sw[None], off, rows=torch.zeros((2, 2), dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 9])
+def test_linear_of_no_depth(M):
+    """K = 0: the bias, or zeros, whatever the scales hold, at channel counts of every kernel; from the C
+    interface also without x, weight and scales."""
+    for N in (40, 16400):
+        bias = torch.randn(N, generator=rng(N), device="cuda")
+        x = torch.empty((M, 0), dtype=torch.bfloat16, device="cuda")
+        w = torch.empty((N, 0), dtype=torch.int8, device="cuda")
+        for bad in (torch.nan, torch.inf):
+            for b in (None, bias):
+                for out in DT.values():
+                    y = fq.int8_linear(x, w, torch.full((N,), bad, device="cuda"), b, out_dtype=out)
+                    assert torch.equal(y, (torch.zeros_like(bias) if b is None else b).to(out).expand(M, N))
+        y = torch.full((M, N), 7.0, device="cuda")
+        size = fq.lib.int8_linear_workspace_bytes(M, N, 0)
+        ws = torch.empty(size + 16, dtype=torch.uint8, device="cuda")
+        assert fq.lib.int8_linear(None, None, None, bias.data_ptr(), y.data_ptr(), 0, M, N, 0, ws.data_ptr(), size,
+                                  torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(y, bias.expand(M, N))
