@@ -410,8 +410,9 @@ __global__ __launch_bounds__(THREADS) void combine_grad_kernel(CombineArgs a) {
                 if (slot[u] >= 0) {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        const float gi = WHOLE || i >= at.again ? g.v[i] : 0.0f;   // (counted once)
-                        dot[u] = __builtin_fmaf(gi, p[u].v[i], dot[u]);
+                        // counted once: neither factor of the other time, either may be infinite
+                        const bool once = WHOLE || i >= at.again;
+                        dot[u] = __builtin_fmaf(once ? g.v[i] : 0.0f, once ? p[u].v[i] : 0.0f, dot[u]);
                         out.v[i] = w[u] * g.v[i];
                     }
                     if (whole) out.store(a.dh, (int64_t)slot[u] * a.H + at.col);

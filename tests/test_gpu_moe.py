@@ -551,3 +551,37 @@ def test_refusals():
         fq.moe_combine_backward(torch.zeros((3, 32), device="cuda"), h, i, w)
     with pytest.raises(TypeError):
         fq.moe_combine_backward(torch.zeros((4, 32), device="cuda").bfloat16(), h, i, w)
+
+
+def overlapped(H, dtype):
+    """The columns that the last 16-byte piece of a row of H elements shares with the piece before, the first and the last."""
+    n = 4 if dtype == "f32" else 8
+    return [*range(H - n, H // n * n), 0, H - 1]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(5, 1447), (300, 515), (1100, 515), (3, 10), (7, 1448)])
+def test_combine_backward_of_infinities(T, H, dtype):
+    """An infinity in a row of h, or in dy, gives the dot product that the definition has: an infinity
+    of its sign wherever it stands (each element counts once), and numbers elsewhere."""
+    g = rng(T + H)
+    k = 3
+    _, _, slots = placed(g, T, k, 8)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    at = slots.long()
+    for col in overlapped(H, dtype):
+        for sign in (1.0, -1.0):
+            h, dy = randn(g, T * k, H).to(DT[dtype]), randn(g, T, H).to(DT[dtype])
+            h[at[T // 2, 1], col] = sign * torch.inf
+            dh, dw = fq.moe_combine_backward(dy, h, slots, w)
+            terms = h.double()[at] * dy.double()[:, None]
+            ref, mag = terms.sum(-1), terms.abs().sum(-1)
+            there = torch.isfinite(ref)
+            assert int((~there).sum()) == 1 and torch.equal(dw[~there].double(), ref[~there]), (col, sign)
+            assert ((dw.double() - ref).abs()[there] <= (H + 1) * U * mag[there]).all()
+            assert torch.isfinite(dh).all()
+            h[at[T // 2, 1], col] = 1.0
+            dy[0, col] = sign * torch.inf
+            dw = fq.moe_combine_backward(dy, h, slots, w)[1]
+            assert torch.equal(dw[0].double(), (h.double()[at[0]] * dy[0].double()).sum(-1)), (col, sign)
+            assert torch.isfinite(dw[1:]).all()
