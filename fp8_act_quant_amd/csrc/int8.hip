@@ -1067,8 +1067,18 @@ hipError_t launch_int8_quant(const uint16_t *x, int8_t *q, float *s, int64_t M, 
     else if (K <= 2048 && M <= 512) row_quant_kernel<4, 1><<<one, block, 0, stream>>>(x, q, s, M, K);
     else if (K <= 2048) row_quant_kernel<1, 4><<<four, block, 0, stream>>>(x, q, s, M, K);
     else if (K <= 8192) row_quant_kernel<4, 4><<<one, block, 0, stream>>>(x, q, s, M, K);
-    else if (K <= 32768) row_quant_kernel<16, 4><<<one, large, 0, stream>>>(x, q, s, M, K);
-    else row_quant_kernel<16, 0><<<one, large, 0, stream>>>(x, q, s, M, K);
+    else {
+        // A grid counts at most 2^32 - 1 threads (more are not refused: their number wraps), so 2^22 rows
+        // and more of 1024 threads each are several launches
+        constexpr int64_t kRows = 0xFFFFFFFFll / 1024;
+        for (int64_t m = 0; m < M; m += kRows) {
+            const int64_t n = M - m < kRows ? M - m : kRows;
+            const dim3 grid((unsigned)n);
+            if (K <= 32768) row_quant_kernel<16, 4><<<grid, large, 0, stream>>>(x + m * K, q + m * K, s + m, n, K);
+            else row_quant_kernel<16, 0><<<grid, large, 0, stream>>>(x + m * K, q + m * K, s + m, n, K);
+            if (hipError_t e = hipGetLastError()) return e;
+        }
+    }
     return hipGetLastError();
 }
 

@@ -470,3 +470,21 @@ def test_linear_of_no_depth(M):
         assert fq.lib.int8_linear(None, None, None, bias.data_ptr(), y.data_ptr(), 0, M, N, 0, ws.data_ptr(), size,
                                   torch.cuda.current_stream().cuda_stream) == 0
         assert torch.equal(y, bias.expand(M, N))
+
+
+def test_quant_of_more_rows_than_one_grid():
+    """2^22 and some rows of more than 8192 elements: 1024 threads each, of which a grid counts 2^32 - 1."""
+    M, K = (1 << 22) + 5, 8208
+    g = rng(7)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    parts = [slice(0, 3), slice(M // 2, M // 2 + 3), slice((1 << 22) - 4, M)]
+    for p in parts:
+        x[p] = torch.randn(x[p].shape, generator=g, device="cuda").bfloat16()
+    q, s = fq.int8_quant(x)
+    assert int((s != 0).sum()) == 15
+    for p in parts:
+        rq, rs = quant_ref(x[p])
+        assert np.array_equal(s[p].cpu().numpy().view(np.uint32), rs.view(np.uint32))
+        assert np.array_equal(q[p].cpu().numpy(), rq)
+    del x, q, s
+    torch.cuda.empty_cache()
