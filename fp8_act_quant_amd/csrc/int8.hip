@@ -15,6 +15,7 @@
 // Grouped products. Expert e owns the rows offsets[e] .. offsets[e + 1] - 1 of Y; row r's
 // token is rows[r] (the gather is part of the loads, a token is quantised once however many
 // experts take it), or r itself.
+#include <cmath>
 #include <type_traits>
 
 #include <fp8q.h>
@@ -1093,18 +1094,21 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
     // constants are fitted to times at K = 512 and 7168, N = 1536 and 7168, M = 16 to 4096 (us): the
     // first round's step, a later round's (less where two workgroups share a CU's waits), the epilogue.
     const double steps = (double)((K + KB - 1) / KB);
-    auto time = [&](int bm, int bn, double first, double more, double end) {
+    // (Tiles whose grid would pass 2^32 - 1 threads are left out: 2^30 rows have too many of 64.)
+    auto time = [&](int bm, int bn, double first, double more, double end, int threads = 256) {
         const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+        if (tiles * threads > 0xFFFFFFFFll) return HUGE_VAL;
         const double rounds = (double)((tiles + 255) / 256);
         return steps * (first + more * (rounds - 1.0)) + end * rounds;
     };
     const double t[7] = {time(32, 32, 0.105, 0.085, 1.0), time(32, 64, 0.155, 0.125, 1.1),
                          time(64, 64, 0.21, 0.18, 1.4),   time(64, 128, 0.34, 0.27, 1.5),
-                         time(128, 128, 0.45, 0.53, 5.0), time(128, 256, 0.75, 0.83, 5.7),
-                         time(256, 256, 1.3, 1.5, 8.0)};
+                         time(128, 128, 0.45, 0.53, 5.0), time(128, 256, 0.75, 0.83, 5.7, 512),
+                         time(256, 256, 1.3, 1.5, 8.0, 512)};
     int best = 0;
     for (int i = 1; i < 7; ++i)
         if (t[i] < t[best]) best = i;
+    if (t[best] == HUGE_VAL) return hipErrorInvalidValue;
     switch (best) {
     case 0: return launch_deep<32, 32, 8, 0>(g, out_bf16, stream);
     case 1: return launch_deep<32, 64, 6, 0>(g, out_bf16, stream);

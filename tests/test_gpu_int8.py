@@ -488,3 +488,16 @@ def test_quant_of_more_rows_than_one_grid():
         assert np.array_equal(q[p].cpu().numpy(), rq)
     del x, q, s
     torch.cuda.empty_cache()
+
+
+def test_gemm_of_more_rows_than_a_grid_of_small_tiles():
+    """2^30 and some rows: more tiles of 64 rows than a grid's 2^32 - 1 threads hold."""
+    M, N, K = (1 << 30) + 70, 16, 16
+    g = rng(8)
+    a = torch.empty((M, K), dtype=torch.int8, device="cuda").random_(-128, 128, generator=g)
+    sa, w, sw = scales(g, M), codes(g, N, K), scales(g, N)
+    y = fq.int8_gemm(a, sa, w, sw, out_dtype=torch.bfloat16)
+    for p in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
+        check(y[p], a[p], sa[p], w, sw, None, "bf16")
+    del a, sa, y
+    torch.cuda.empty_cache()
