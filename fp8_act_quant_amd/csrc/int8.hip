@@ -790,10 +790,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // waves 2 and 3 the other half. Bound by the read of W: 1 x 7168 x 7168 9.8 us, of which its 51 MB
 // are 9 at 5.7 TB/s (with W straight into registers, half a line of a row at a time, 12.1). Three stages,
 // so that two workgroups share a CU: with four 1 x 10240 x 7168 takes 17.2 instead of 13.4.
-constexpr int kRowRows = 2, kRowK = 8192;
+constexpr int kRowRows = 2, kRowK = 8192, kRowN = 32;
 template <int OUT_BF16>
 __global__ __launch_bounds__(256) void int8_row_kernel(Int8FewArgs g) {
-    constexpr int BN = 32, SUBS = 4, STAGES = 3, STEP = BN * KB, STAGE = SUBS * STEP, PITCH = kRowK + 16;
+    constexpr int BN = kRowN, SUBS = 4, STAGES = 3, STEP = BN * KB, STAGE = SUBS * STEP, PITCH = kRowK + 16;
     __shared__ __attribute__((aligned(16))) uint8_t ring[STAGES * STAGE];
     __shared__ __attribute__((aligned(16))) uint8_t codes[kRowRows * PITCH];
     __shared__ uint32_t tops[4][kRowRows];
@@ -1123,9 +1123,11 @@ hipError_t launch_int8_gemm(const int8_t *a, const float *sa, const int8_t *w, c
 // Whether a linear layer is one launch, and by which kernel (1: int8_row_kernel, 2: int8_few_kernel). One
 // launch against two, us: 2, 8 x 4096 x 2048 5.6 / 7.0, 16 rows 8.3 / 7.3, 8 x 32768 x 2048 17 / 16 (the rows are
 // quantised over and over); 1, 1 x 512 x 2560 4.4 / 6.1, 1 x 7168 x 7168 10.0 / 13.1, 2 x 32768 x 7168 42.8 / 44.7.
+// (A grid counts at most 2^32 - 1 threads.)
+constexpr int64_t kRowMaxN = 0xFFFFFFFFll / 256 * kRowN;
 static int one_launch(int64_t M, int64_t N, int64_t K) {
     if (M <= kFewRows && K <= kFewQuantK && N <= 16384) return 2;
-    if (M <= kRowRows && K <= kRowK) return 1;
+    if (M <= kRowRows && K <= kRowK && N <= kRowMaxN) return 1;
     return 0;
 }
 
@@ -1139,9 +1141,7 @@ hipError_t launch_int8_linear(const uint16_t *x, const int8_t *w, const float *s
     const Int8FewArgs few{nullptr, nullptr, x, w, sw, bias, y, N, (int)M, (int)K};
     switch (one_launch(M, N, K)) {
     case 1: {
-        const int64_t units = (N + 31) / 32;
-        if (units * 256 > 0xFFFFFFFFll) return hipErrorInvalidValue;
-        const dim3 grid((unsigned)units), block(256);
+        const dim3 grid((unsigned)((N + kRowN - 1) / kRowN)), block(256);
         if (out_bf16) int8_row_kernel<1><<<grid, block, 0, stream>>>(few);
         else int8_row_kernel<0><<<grid, block, 0, stream>>>(few);
         return hipGetLastError();

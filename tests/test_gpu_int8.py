@@ -501,3 +501,17 @@ def test_gemm_of_more_rows_than_a_grid_of_small_tiles():
         check(y[p], a[p], sa[p], w, sw, None, "bf16")
     del a, sa, y
     torch.cuda.empty_cache()
+
+
+def test_linear_of_more_channels_than_one_launch():
+    """2^29 and some channels for one row: the ends and the middle."""
+    N, K = (1 << 29) + 50, 16
+    g = rng(12)
+    w = torch.empty((N, K), dtype=torch.int8, device="cuda").random_(-128, 128, generator=g)
+    ws, x = scales(g, N), torch.randn((1, K), generator=g, device="cuda").bfloat16()
+    y = fq.int8_linear(x, w, ws, out_dtype=torch.float32)
+    q, s = (torch.from_numpy(v).cuda() for v in quant_ref(x))
+    for p in (slice(0, 300), slice(N // 2, N // 2 + 300), slice(N - 300, N)):
+        check(y[:, p], q, s, w[p], ws[p], None, "f32")
+    del w, ws, y
+    torch.cuda.empty_cache()

@@ -124,3 +124,14 @@ def test_int8_validation(L):
     for bad in (dict(off=FAKE + 4), dict(rows=FAKE + 2), dict(w=FAKE + 8)):
         assert grouped(**bad) == L.FP8Q_ERR_ALIGN
     assert grouped(M=0, tokens=7) == L.FP8Q_OK
+
+
+def test_linear_layers_wider_than_one_launch(L):
+    """One or two rows of more channels than the one-launch kernel's grid holds take two launches, for which
+    they need a workspace (and are refused without one)."""
+    lib = L.lib
+    most = (2 ** 32 - 1) // 256 * 32
+    for M in (1, 2):
+        assert lib.int8_linear_workspace_bytes(M, most, 2064) == 0
+        assert lib.int8_linear_workspace_bytes(M, most + 1, 2064) >= M * 2068
+        assert lib.int8_linear(FAKE, FAKE, FAKE, None, FAKE, 0, M, most + 1, 2064, None, 0, None) == L.FP8Q_ERR_WORKSPACE
