@@ -585,3 +585,27 @@ def test_combine_backward_of_infinities(T, H, dtype):
             dw = fq.moe_combine_backward(dy, h, slots, w)[1]
             assert torch.equal(dw[0].double(), (h.double()[at[0]] * dy[0].double()).sum(-1)), (col, sign)
             assert torch.isfinite(dw[1:]).all()
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(9, 24, 5), (4100, 24, 5), (4100, 256, 8), (5, 1024, 32)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_backward_of_small_scores(T, E, k, score, renormalize):
+    """Selected scores near fp32's smallest numbers, whose sum has no reciprocal there: the gradient of the
+    renormalised weights is an ordinary number (each score over the sum is).
+
+    Bound: such a score, down to 2^-127.4, is off by expf's 2 ulp (2^-148) and a rounding (2^-150): within
+    2^-20.2 = 14 u of its value; score over sum within 3 * 14 u + 8 u, the difference from the mean within
+    2 * 50 u, their product and its sum within 160 u of the magnitudes."""
+    g = rng(T + E + k)
+    logits = -88.3 + 1.5 * torch.rand((T, E), generator=g, device="cuda")
+    idx = torch.rand((T, E - 1), generator=g, device="cuda").topk(k, dim=-1).indices.to(torch.int32)
+    if score == "softmax":
+        logits[:, -1] = 0.0
+    dw = 8.0 * randn(g, T, k)
+    dx = fq.moe_route_backward(dw, logits, idx, score=score, renormalize=renormalize, scale=2.5)
+    ref, mag = grad64(logits, idx, dw, score, renormalize, 2.5)
+    assert torch.isfinite(dx).all()
+    assert ((dx.double() - ref).abs() <= 160 * U * mag + 1e-37).all()
+    if renormalize:
+        assert float(ref.abs().max()) > 0.1
