@@ -18,8 +18,23 @@ import torch
 from . import _lib
 from ._lib import (FP8Q_GEMM_EXACT_SLICES, FP8Q_GEMM_FP8_PRODUCTS, FP8Q_OUT_BF16, FP8Q_OUT_F32, FP8Q_SA_KMAJOR,
                    Fp8qError, check, lib)
-from .int8 import int8_gemm, int8_grouped_gemm, int8_linear, int8_quant
-from .moe import moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward
+
+try:
+    from .int8 import int8_gemm, int8_grouped_gemm, int8_linear, int8_quant
+    from .moe import moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward
+except ImportError as _e:
+    # These go through the native binding, which is built for one Python and torch; everything else needs only
+    # libfp8q.so and works without it. Without it they raise its error when they are called.
+    def _missing(name: str, why: str = str(_e)):
+        def call(*args, **kwargs):
+            raise ImportError(f"{name}: {why}")
+        call.__name__ = name
+        return call
+
+    int8_gemm, int8_grouped_gemm, int8_linear, int8_quant = map(
+        _missing, ("int8_gemm", "int8_grouped_gemm", "int8_linear", "int8_quant"))
+    moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward = map(
+        _missing, ("moe_combine", "moe_combine_backward", "moe_place", "moe_route", "moe_route_backward"))
 
 BLOCK = 128
 

@@ -1,7 +1,12 @@
 """Host-side validation of the routed-expert and 8-bit integer entry points (no GPU needed):
 every call below is refused, or is an empty call, before a device is touched."""
+import os
+import subprocess
+import sys
+
 import pytest
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000  # never dereferenced
 
 
@@ -135,3 +140,32 @@ def test_linear_layers_wider_than_one_launch(L):
         assert lib.int8_linear_workspace_bytes(M, most, 2064) == 0
         assert lib.int8_linear_workspace_bytes(M, most + 1, 2064) >= M * 2068
         assert lib.int8_linear(FAKE, FAKE, FAKE, None, FAKE, 0, M, most + 1, 2064, None, 0, None) == L.FP8Q_ERR_WORKSPACE
+
+
+def test_package_without_the_native_binding():
+    """Where the binding cannot be loaded the calls that need it say so, and the others are there."""
+    code = """
+import sys
+sys.modules["fp8_act_quant_amd._native"] = None      # its import fails
+import fp8_act_quant_amd as fq
+from fp8_act_quant_amd import *
+assert callable(act_quant) and callable(fq.fp8_gemm) and fq.lib.fp8q_version() >> 16 == 1
+for name in ("moe_route", "moe_route_backward", "moe_place", "moe_combine", "moe_combine_backward", "int8_quant",
+             "int8_gemm", "int8_linear", "int8_grouped_gemm"):
+    assert getattr(fq, name).__name__ == name
+    try:
+        getattr(fq, name)(None, 1)
+    except ImportError as e:
+        assert name in str(e) and "native binding" in str(e)
+    else:
+        raise SystemExit(name)
+print("fine")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert out.stdout == "fine\n", out.stderr
+
+
+def test_package_with_the_native_binding():
+    import fp8_act_quant_amd as fq
+    from fp8_act_quant_amd import int8, moe
+    assert fq.moe_route is moe.moe_route and fq.int8_linear is int8.int8_linear
