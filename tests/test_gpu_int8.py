@@ -515,3 +515,22 @@ def test_linear_of_more_channels_than_one_launch():
         check(y[:, p], q, s, w[p], ws[p], None, "f32")
     del w, ws, y
     torch.cuda.empty_cache()
+
+
+def test_outputs_are_filled_in_deterministic_mode():
+    """Where torch fills uninitialised memory with NaN (deterministic algorithms), what no expert owns
+    is filled too."""
+    g = rng(10)
+    a, sa, w, sw = codes(g, 9, 64), scales(g, 9), codes(g, 2, 32, 64), scales(g, 2, 32)
+    offsets = torch.tensor([0, 2, 5], device="cuda")
+    slots = torch.tensor([[0, -1], [3, 1]], dtype=torch.int32, device="cuda")
+    h, dy, weights = torch.ones((9, 32), device="cuda"), torch.ones((2, 32), device="cuda"), torch.ones((2, 2), device="cuda")
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        y = fq.int8_grouped_gemm(a, sa, w, sw, offsets, out_dtype=torch.float32)
+        dh, _ = fq.moe_combine_backward(dy, h, slots, weights)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert torch.isnan(y[5:]).all() and not torch.isnan(y[:5]).any()
+    assert torch.isnan(dh[[2, 4, 5, 6, 7, 8]]).all() and (dh[[0, 1, 3]] == 1).all()
