@@ -609,3 +609,52 @@ def test_route_backward_of_small_scores(T, E, k, score, renormalize):
     assert ((dx.double() - ref).abs() <= 160 * U * mag + 1e-37).all()
     if renormalize:
         assert float(ref.abs().max()) > 0.1
+
+
+@pytest.mark.parametrize("dtype,H", [("bf16", 7161), ("f32", 7161), ("f32", 7168), ("bf16", 7168)])
+def test_combine_of_more_rows_than_the_caches_hold(H, dtype):
+    """Over 256 MB of rows, whose lengths are whole 16-byte pieces or not."""
+    g = rng(H)
+    T, k, E = 2401, 8, 64
+    _, _, slots = placed(g, T, k, E, 60)
+    h, dy = randn(g, T * k, H).to(DT[dtype]), randn(g, T, H).to(DT[dtype])
+    w = torch.rand((T, k), generator=g, device="cuda")
+    y = fq.moe_combine(h, slots, w)
+    dh, dw = fq.moe_combine_backward(dy, h, slots, w)
+    ref, mag = torch.zeros((2, T, H), dtype=torch.float64, device="cuda")
+    for j in range(k):
+        there = slots[:, j] >= 0
+        hj = torch.where(there[:, None], h[slots[:, j].clamp(min=0).long()].double(), 0.0)
+        term = w[:, j, None].double() * hj
+        ref += term
+        mag += term.abs()
+        dot = hj * dy.double()
+        assert ((dw[:, j].double() - dot.sum(-1)).abs() <= (H + 1) * U * dot.abs().sum(-1) + 1e-37).all()
+        ref_h = (w[:, j, None].double() * dy.double())[there]
+        assert within(dh[slots[there, j].long()], ref_h, U * ref_h.abs())
+    assert within(y, ref, (k + 1) * U * mag)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E", [(33, 256), (4097, 64), (8195, 256), (6, 1024)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_of_views_off_a_16_byte_boundary(T, E, score, dtype):
+    """Logits and biases one element past an aligned start: bit for bit what aligned copies give, forward and
+    backward, with a wave or 16 lanes to a token."""
+    g = rng(T + E)
+    logits = randn(g, T * E + 1).to(DT[dtype])[1:].view(T, E)
+    bias = (0.1 * randn(g, E + 1))[1:]
+    kw = dict(score=score, groups=4, topk_groups=2)
+    w, e = fq.moe_route(logits, 8, bias=bias, **kw)
+    for x, b in ((logits.clone(), bias), (logits, bias.clone()), (logits.clone(), bias.clone())):
+        wa, ea = fq.moe_route(x, 8, bias=b, **kw)
+        assert torch.equal(w, wa) and torch.equal(e, ea)
+    dw = randn(g, T, 8)
+    dx = fq.moe_route_backward(dw, logits, e, score=score)
+    assert torch.equal(dx, fq.moe_route_backward(dw, logits.clone(), e, score=score))
+    # and an output that starts off the boundary, which only the C interface can ask for
+    out = torch.full((T * E + 2,), 7.0, dtype=DT[dtype], device="cuda")
+    status = fq.lib.moe_route_backward(dw.data_ptr(), logits.data_ptr(), int(dtype == "bf16"), e.data_ptr(),
+                                       out[1:].data_ptr(), T, E, 8, 1.0, int(score == "softmax"),
+                                       torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and torch.equal(out[1:-1].view(T, E), dx) and out[0] == 7 and out[-1] == 7
