@@ -35,9 +35,11 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // A row's scale and what its codes are formed with. RN(x / s) comes from the rounded reciprocal
 // and two corrections (fast_quotient's steps, of which only the sign of a zero is left out); that
-// it gives the same code as the division for every bf16 x and maximum is checked exhaustively.
-// It needs s >= 2^-92; smaller scales take the division, and a clamp, since a scale below the
-// normal range may be off by more than the half step that separates 127 from 127.5.
+// it gives the same code as the division is tested for every pair of significands of x and maximum,
+// at 23 of the maximum's exponents (the significands decide while nothing leaves the normal range). It
+// needs s >= 2^-92, on both sides of which those exponents lie; smaller scales take the division, and a
+// clamp, since a scale below the normal range may be off by more than the half step that separates
+// 127 from 127.5.
 struct RowScale {
     float s, d, y;
     bool fast;

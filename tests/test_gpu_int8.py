@@ -534,3 +534,24 @@ def test_outputs_are_filled_in_deterministic_mode():
         torch.use_deterministic_algorithms(before)
     assert torch.isnan(y[5:]).all() and not torch.isnan(y[:5]).any()
     assert torch.isnan(dh[[2, 4, 5, 6, 7, 8]]).all() and (dh[[0, 1, 3]] == 1).all()
+
+
+def test_quant_exponents_around_the_quotients_limit():
+    """Every (x, amax) pair of bf16 significands where the scale passes 2^-92, from where the quotient takes
+    another way."""
+    frac = torch.arange(128, dtype=torch.int32)
+    rows = []
+    for top_exp in range(38, 47):
+        for f in range(128):
+            top = (top_exp << 7) | f
+            body = torch.cat([((top_exp - d) << 7) | frac for d in range(10)])
+            body = torch.where(body <= top, body, 0)
+            rows.append(torch.cat([torch.tensor([top], dtype=torch.int32), body, body | 0x8000,
+                                   torch.zeros(15, dtype=torch.int32)]))
+    bits = torch.stack(rows)
+    x = torch.where(bits >= 0x8000, bits - 0x10000, bits).to(torch.int16).view(torch.bfloat16).cuda()
+    q, s = fq.int8_quant(x)
+    rq, rs = quant_ref(x)
+    assert rs.min() < 2.0 ** -92 < rs.max()
+    assert np.array_equal(s.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(q.cpu().numpy(), rq)

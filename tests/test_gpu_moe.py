@@ -658,3 +658,19 @@ def test_route_of_views_off_a_16_byte_boundary(T, E, score, dtype):
                                        out[1:].data_ptr(), T, E, 8, 1.0, int(score == "softmax"),
                                        torch.cuda.current_stream().cuda_stream)
     assert status == 0 and torch.equal(out[1:-1].view(T, E), dx) and out[0] == 7 and out[-1] == 7
+
+
+@pytest.mark.parametrize("n", [2000, 1 << 22])
+def test_sigmoid_scores_are_the_divided_form(n):
+    """One expert's score is its sigmoid, bit for bit 1 / (1 + exp(-x)) with the addition and the quotient rounded
+    to nearest (by numpy): dense logits from where the score is 1 to where it is the smallest number and 0, and
+    logits that give every binade of the quotient's divisor. (A few tokens and many: both kernels.)"""
+    logits = torch.cat([torch.linspace(-89.5, 20.0, n, device="cuda"), torch.linspace(-88.8, -86.9, n, device="cuda"),
+                        10.0 * randn(rng(n), n), -torch.linspace(0.0, 88.0, 129, device="cuda")])
+    with np.errstate(over="ignore"):
+        ref = np.float32(1) / (np.float32(1) + torch.exp(-logits).cpu().numpy())
+    for t0 in range(0, logits.numel(), 1000 if n == 2000 else n):
+        part = logits[t0:t0 + (1000 if n == 2000 else n)]
+        w, e = fq.moe_route(part[:, None].contiguous(), 1, renormalize=False)
+        assert not bool(e.any())
+        assert np.array_equal(w[:, 0].cpu().numpy().view(np.uint32), ref[t0:t0 + part.numel()].view(np.uint32))
