@@ -256,7 +256,7 @@ __device__ __forceinline__ void merge2(uint32_t &m1, uint32_t &m2, uint32_t o1, 
 // selected expert is always some lane's first: a maximum over the first ones, then that lane
 // moves up. About 20 operations per selected expert; with more experts a lane the sorting
 // would cost more than it saves, and each step looks at all of them. Bound by these operations
-// (some 400 a token), not by the 4 E bytes it reads: 16384 tokens' 256 experts 12.4 us, 1.4 TB/s.
+// (some 400 a token), not by the 4 E bytes it reads: 16384 tokens' 256 experts 13.0 us, 1.4 TB/s.
 template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
     typedef float piece __attribute__((ext_vector_type(V)));
@@ -386,8 +386,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a) {
 // route_kernel, each of them for four tokens at once and over 16 lanes instead of 64. Of a lane's
 // up to 16 experts every four are sorted; a step takes the largest of their first ones. A team's
 // first lane among those at the maximum is the lowest set bit of its 16 in a ballot. Bound by its
-// operations too (about 220 a token; a third of them the scores): 16384 tokens' 256 experts 9.2 us
-// against 12.4 with a wave to a token, of which 3 are the launch.
+// operations too (237 a token; a third of them the scores): 16384 tokens' 256 experts 10.4 us
+// against 13.0 with a wave to a token, of which 3 are the launch.
 __device__ __forceinline__ uint64_t first_of_teams(uint64_t m) {   // (no 16 bits of m are all clear)
     return m & (~m + 0x0001000100010001ull);
 }
@@ -543,7 +543,7 @@ struct RouteGradArgs {
 // d_j is the derivative by the score times the score: the former alone passes fp32's range where S is
 // as small as its smallest numbers, r_j is at most 1. The row of d goes through LDS, from the k selected experts' lanes to the experts' lanes. Bound
 // by its operations with few tokens to a chip's worth of waves (softmax, 16384 tokens' 256 experts
-// 9.6 us), in teams by memory (65536 tokens 22 us, 6.1 TB/s).
+// 10.2 us), in teams by memory (65536 tokens 27 us, 5.1 TB/s; 22 where the caches still hold the logits).
 template <int V, int BF16, int SOFTMAX, int FULL>
 __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a) {
     typedef float piece __attribute__((ext_vector_type(V)));
@@ -776,9 +776,9 @@ hipError_t launch_moe_route(const void *logits, bool bf16, const float *bias, fl
                 scale};
     for (int g = 1; g < groups; g <<= 1) --a.lane_shift;
     // Teams from the number of tokens on at which their waves fill the chip. A wave to a token
-    // against teams, us: 256 experts (16 a lane) at 4096 / 8192 / 16384 / 65536 tokens 5.2 / 7.5 / 12.4 / 41
-    // against 5.4 / 6.5 / 9.2 / 26; 64 experts (4 a lane) at 2048 / 8192 / 65536 3.9 / 4.8 / 23 against
-    // 4.0 / 4.0 / 10.
+    // against teams, us, three sets of inputs in turn: 256 experts (16 a lane) at 4096 / 8192 / 16384 / 65536
+    // tokens 5.5 / 7.7 / 13.0 / 41 against 5.6 / 6.7 / 10.4 / 27; 64 experts (4 a lane) at 2048 / 8192 / 65536
+    // 4.2 / 5.6 / 27 against 4.3 / 4.8 / 12.
     const int v4 = ((a.per - 1) >> max(a.lane_shift - 2, 0)) + 1, quads = (v4 + 3) / 4;   // of a lane of 16
     if (T >= 2048 * quads && k <= 16 && groups <= 16 && quads <= 4) {
         a.lane_shift -= 2;
@@ -806,9 +806,9 @@ hipError_t launch_moe_route_backward(const float *dweights, const void *logits, 
                                      float scale, hipStream_t stream) {
     const RouteGradArgs a{dweights, logits, experts, dlogits, T, E, k, renormalize, scale};
     const dim3 grid((unsigned)((T + kWaves - 1) / kWaves));
-    // Teams or a wave to a token, us: softmax, 256 experts at 2048 / 8192 / 65536 tokens 4.0 / 5.0 / 22 against
-    // 4.0 / 6.0 / 30, 64 experts 3.9 / 3.9 / 8 against 3.9 / 4.4 / 21. (Rows that are no whole quads are
-    // loaded by elements: 255 experts, 16384 tokens 12.2 against 11.0.)
+    // Teams or a wave to a token, us, three sets of inputs in turn: softmax, 256 experts at 4096 / 8192 / 65536
+    // tokens 4.7 / 5.6 / 27 against 4.7 / 6.3 / 33, 64 experts at 8192 / 65536 4.9 / 9.3 against 4.9 / 22. (Rows
+    // that are no whole quads are loaded by elements: 255 experts, 16384 tokens 12.5 against 11.1.)
     if (T >= 4096 && k <= 16 && E <= (E % 4 == 0 ? 256 : 192)) {
         const dim3 teams((unsigned)((T + 4 * kWaves - 1) / (4 * kWaves)));
         if (E <= 64) route_grad_v<4, 1>(a, bf16, softmax, teams, stream);

@@ -316,7 +316,8 @@ size_t moe_place_workspace_bytes(int64_t T, int64_t top_k, int64_t experts);
 /* moe_combine -- y[t] = sum over j of weights[t, j] * h[slots[t, j]].
  *   h [rows, H] and y [T, H] of type dtype; slots [T, top_k] int32, entries outside
  *   [0, rows) adding nothing; weights [T, top_k] fp32, or NULL for all 1 (the gradient of
- *   the gather by moe_place's rows). Summed in fp32 in the order of j, rounded once. Any
+ *   the gather by moe_place's rows). Summed in fp32 in the order of j, rounded once. Infinities
+ *   and NaN in the named rows count as in that arithmetic, here and in the gradient. Any
  *   alignment of the element type (16-byte rows are faster). */
 int moe_combine(const void *h, int dtype, const int32_t *slots, const float *weights, void *y, int64_t T,
                 int64_t top_k, int64_t rows, int64_t H, void *stream);
