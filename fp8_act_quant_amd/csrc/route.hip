@@ -524,6 +524,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_teams_kernel(RouteArgs a) {
     }
 }
 
+// Scores whose sum is less are scaled up by kUp, so that neither they nor quotients by their sum leave
+// fp32's range
+constexpr float kSmallSum = 0x1p-64f, kUp = 0x1p64f;
+
 struct RouteGradArgs {
     const float *dweights;
     const void *logits;
@@ -536,12 +540,13 @@ struct RouteGradArgs {
 };
 
 // Gradient of the logits, one wave per token (the selection itself has none):
-//     g_j = scale * dw_j;   r_j = s_j / S, S = sum of the selected s (renormalised), or s_j
-//     d_j = r_j (g_j - sum_i g_i r_i)   (renormalised), or r_j g_j
-//     sigmoid: dx_j = d_j (1 - s_j), 0 for the experts that were not selected
-//     softmax: dx_i = d_i - s_i sum_j d_j, d_i = 0 for those
-// d_j is the derivative by the score times the score: the former alone passes fp32's range where S is
-// as small as its smallest numbers, r_j is at most 1. The row of d goes through LDS, from the k selected experts' lanes to the experts' lanes. Bound
+//     g_j = scale * dw_j;   ds_j = (g_j - sum_i g_i s_i / S) / S, S = sum of the selected s
+//     (renormalised), or g_j
+//     sigmoid: dx_j = ds_j s_j (1 - s_j), 0 for the experts that were not selected
+//     softmax: dx_i = s_i (ds_i - sum_j ds_j s_j), ds_i = 0 for those
+// ds passes fp32's range where S is about as small as its smallest numbers: there the scores are
+// scaled up by a power of two and ds is that much smaller, which leaves the products as they are.
+// The row of ds goes through LDS, from the k selected experts' lanes to the experts' lanes. Bound
 // by its operations with few tokens to a chip's worth of waves (softmax, 16384 tokens' 256 experts
 // 10.2 us), in teams by memory (65536 tokens 27 us, 5.1 TB/s; 22 where the caches still hold the logits).
 template <int V, int BF16, int SOFTMAX, int FULL>
@@ -571,13 +576,26 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a
     rows[wave][lane] = zero;
 
     const float s = there ? score_of<SOFTMAX>(xe, top, total) : 0.0f;
-    const float sum = a.renormalize ? wave_sum(s) : 1.0f;
-    const float part = sum != 0.0f ? s / sum : 0.0f;
-    float d = dw * a.scale;
-    if (a.renormalize) d -= wave_sum(d * part);
-    d = there ? d * part : 0.0f;
-    const float all = SOFTMAX ? wave_sum(d) : 0.0f;
-    if constexpr (!SOFTMAX) d *= 1.0f - s;
+    float d = dw * a.scale, z = s;   // z: the score, scaled up if need be
+    bool small = false;
+    if (a.renormalize) {
+        float sum = wave_sum(s);
+        small = sum < kSmallSum;
+        z = small ? s * kUp : s;
+        sum = small ? sum * kUp : sum;
+        const float dot = wave_sum(d * z);
+        d = there && sum != 0.0f ? (d - dot / sum) / sum : 0.0f;
+    }
+    float all = SOFTMAX ? wave_sum(d * z) : 0.0f;
+    if constexpr (SOFTMAX) {
+        if (__any(small)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = small ? p[i] * kUp : p[i];
+            all = small ? all / kUp : all;
+        }
+    } else {
+        d *= z * (1.0f - s);
+    }
     // (LDS accesses of a wave run in order; the fences keep the compiler's order)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (there) reinterpret_cast<float *>(rows[wave])[e] = d;
@@ -586,7 +604,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteGradArgs a
     piece g = rows[wave][lane];
     if constexpr (SOFTMAX) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = __builtin_fmaf(-p[i], all, g[i]);
+        for (int i = 0; i < V; ++i) g[i] = p[i] * (g[i] - all);
     }
     if constexpr (BF16) {
         typedef uint16_t half_piece __attribute__((ext_vector_type(V)));
@@ -676,13 +694,26 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_teams_kernel(RouteGrad
     for (int q = 0; q < Q; ++q) rows[wave][team][16 * q + tl] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const float s = there ? score_of<SOFTMAX>(xe, top, total) : 0.0f;
-    const float sum = a.renormalize ? team_sum(s) : 1.0f;
-    const float part = sum != 0.0f ? s / sum : 0.0f;
-    float d = dw * a.scale;
-    if (a.renormalize) d -= team_sum(d * part);
-    d = there ? d * part : 0.0f;
-    const float all = SOFTMAX ? team_sum(d) : 0.0f;
-    if constexpr (!SOFTMAX) d *= 1.0f - s;
+    float d = dw * a.scale, z = s;   // z: the score, scaled up if need be
+    bool small = false;
+    if (a.renormalize) {
+        float sum = team_sum(s);
+        small = sum < kSmallSum;
+        z = small ? s * kUp : s;
+        sum = small ? sum * kUp : sum;
+        const float dot = team_sum(d * z);
+        d = there && sum != 0.0f ? (d - dot / sum) / sum : 0.0f;
+    }
+    float all = SOFTMAX ? team_sum(d * z) : 0.0f;
+    if constexpr (SOFTMAX) {
+        if (__any(small)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = small ? p[i] * kUp : p[i];
+            all = small ? all / kUp : all;
+        }
+    } else {
+        d *= z * (1.0f - s);
+    }
     // (LDS accesses of a wave run in order; the fences keep the compiler's order)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (there) reinterpret_cast<float *>(rows[wave][team])[e] = d;
@@ -694,7 +725,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_teams_kernel(RouteGrad
         f32x4 g = rows[wave][team][16 * q + tl];
         if constexpr (SOFTMAX) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = __builtin_fmaf(-p[4 * q + i], all, g[i]);
+            for (int i = 0; i < 4; ++i) g[i] = p[4 * q + i] * (g[i] - all);
         }
         if (!real) continue;
         store_quad<BF16, QUADS>(a.dlogits, row + first, a.E - first, g);

@@ -674,3 +674,30 @@ def test_sigmoid_scores_are_the_divided_form(n):
         w, e = fq.moe_route(part[:, None].contiguous(), 1, renormalize=False)
         assert not bool(e.any())
         assert np.array_equal(w[:, 0].cpu().numpy().view(np.uint32), ref[t0:t0 + part.numel()].view(np.uint32))
+
+
+@pytest.mark.parametrize("T", [9, 4100])
+@pytest.mark.parametrize("k", [1, 2])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_backward_steps(score, k, T):
+    """Ordinary scores: the formula's steps, each rounded to nearest in fp32, bit for bit. (With one or two
+    experts sums have one order. One renormalised weight does not depend on the logits: what is left of its
+    gradient is those steps' rounding.)"""
+    E = 24
+    g = rng(T + k)
+    logits, dw = randn(g, T, E), randn(g, T, k)
+    w, e = fq.moe_route(logits, E, score=score, renormalize=False)
+    s = torch.empty_like(w).scatter_(1, e.long(), w).cpu().numpy()
+    idx = torch.rand((T, E), generator=g, device="cuda").topk(k, dim=-1).indices
+    at = idx.cpu().numpy()
+    sel, d = np.take_along_axis(s, at, 1), dw.cpu().numpy() * np.float32(2.5)
+    total, dot = sel.sum(1, keepdims=True), (d * sel).sum(1, keepdims=True)
+    d = (d - dot / total) / total
+    dx = np.zeros_like(s)
+    if score == "sigmoid":
+        np.put_along_axis(dx, at, d * (sel * (1 - sel)), 1)
+    else:
+        np.put_along_axis(dx, at, d, 1)
+        dx = s * (dx - (d * sel).sum(1, keepdims=True))
+    got = fq.moe_route_backward(dw, logits, idx.to(torch.int32), score=score, scale=2.5).cpu().numpy()
+    assert got.dtype == dx.dtype == np.float32 and np.array_equal(got, dx)
