@@ -20,6 +20,8 @@ from ._lib import (FP8Q_GEMM_EXACT_SLICES, FP8Q_GEMM_FP8_PRODUCTS, FP8Q_OUT_BF16
                    Fp8qError, check, lib)
 
 try:
+    from .block import (adapter_add, adapter_linear, gated_linear, gated_linear_backward, residual_norm,
+                        residual_norm_backward, rms_norm, rms_norm_backward)
     from .int8 import int8_gemm, int8_grouped_gemm, int8_linear, int8_quant
     from .moe import moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward
 except ImportError as _e:
@@ -35,6 +37,10 @@ except ImportError as _e:
         _missing, ("int8_gemm", "int8_grouped_gemm", "int8_linear", "int8_quant"))
     moe_combine, moe_combine_backward, moe_place, moe_route, moe_route_backward = map(
         _missing, ("moe_combine", "moe_combine_backward", "moe_place", "moe_route", "moe_route_backward"))
+    adapter_add, adapter_linear, gated_linear, gated_linear_backward = map(
+        _missing, ("adapter_add", "adapter_linear", "gated_linear", "gated_linear_backward"))
+    residual_norm, residual_norm_backward, rms_norm, rms_norm_backward = map(
+        _missing, ("residual_norm", "residual_norm_backward", "rms_norm", "rms_norm_backward"))
 
 BLOCK = 128
 
@@ -43,6 +49,8 @@ __all__ = [
     "linear", "gemm_workspace_bytes", "lib", "act_quant_t", "weight_transpose", "fp8_gemm_rowwise",
     "linear_backward", "bf16_gemm", "moe_route", "moe_route_backward", "moe_place", "moe_combine",
     "moe_combine_backward", "int8_quant", "int8_gemm", "int8_linear", "int8_grouped_gemm",
+    "rms_norm", "rms_norm_backward", "residual_norm", "residual_norm_backward", "gated_linear",
+    "gated_linear_backward", "adapter_linear", "adapter_add",
 ]
 
 

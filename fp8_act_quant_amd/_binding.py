@@ -1,4 +1,4 @@
-"""The native binding of the routed-expert and 8-bit integer operators (csrc/binding.cpp): it
+"""The native binding of the routed-expert, 8-bit integer and dense-block operators (csrc/binding.cpp): it
 checks arguments, allocates outputs with torch and calls libfp8q.so. No fallback: if it is
 missing the import fails."""
 from __future__ import annotations

@@ -32,6 +32,10 @@ FP8Q_MOE_SOFTMAX = 1
 FP8Q_MOE_GROUP_MAX = 2
 FP8Q_MOE_KEEP_SCORES = 4
 
+FP8Q_NORM_GATES = 1
+FP8Q_ACT_SILU = 0
+FP8Q_ACT_GELU = 1
+
 # name -> (restype, argtypes); the exports of include/fp8q.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -65,6 +69,16 @@ SIGNATURES = {
     "int8_linear": (_INT, [_P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "int8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "int8_grouped_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P]),
+    "residual_norm": (_INT, [_P, _P, _INT, _P, _P, _P, _INT, _F32, _F32, _P, _P, _I64, _I64, _P]),
+    "residual_norm_backward": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _INT, _F32, _F32, _P, _P, _P, _P, _P, _I64, _I64,
+                                      _P, ctypes.c_size_t, _P]),
+    "residual_norm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "gated_linear": (_INT, [_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _P]),
+    "gated_linear_backward": (_INT, [_P, _P, _P, _P, _INT, _P, _INT, _P, _INT, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "gated_linear_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "adapter_linear": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t,
+                              _P]),
+    "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "fp8q_gemm_force_config": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "fp8q_gemm_config_name": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8q_gemm_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, _P, _P]),

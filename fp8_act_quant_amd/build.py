@@ -1,5 +1,5 @@
 """Build libfp8q.so (the HIP kernels and the C ABI) in-tree for gfx950 with hipcc, and _native.so,
-the Python binding of the routed-expert and 8-bit operators, against it and torch."""
+the Python binding of the routed-expert, 8-bit and dense-block operators, against it and torch."""
 from __future__ import annotations
 
 import os
@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 BINDING = os.path.join(PKG, "_native.so")
 
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "transpose.hip", "bf16_gemm.hip", "route.hip", "place.hip",
-           "int8.hip"]
+           "int8.hip", "norm.hip", "gated.hip", "adapter.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

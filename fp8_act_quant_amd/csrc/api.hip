@@ -93,6 +93,28 @@ int int8_ok(int dtype, int64_t M, int64_t N, int64_t K) {
     return FP8Q_OK;
 }
 
+int norm_ok(int dtype, int flags, int64_t T, int64_t H) {
+    if (!is_type(dtype) || (flags & ~FP8Q_NORM_GATES)) return FP8Q_ERR_DTYPE;
+    if (T < 0 || H < fp8q::kMinNormH || H > fp8q::kMaxNormH || T > kMaxElems / H) return FP8Q_ERR_SHAPE;
+    return FP8Q_OK;
+}
+
+// The dense block's products: rows of operands are 16-byte pieces, addressed within a tile by 32-bit byte
+// offsets (256 rows of 2 K bytes), 32 of a tile's rows at the least are a workgroup of 256 threads or more
+constexpr int64_t kDenseStep = 8, kMaxDenseK = ((int64_t)1 << 23) - kDenseStep, kMaxDenseRows = (int64_t)1 << 26;
+constexpr int64_t kMaxDenseN = (int64_t)1 << 28;
+
+bool gated_ok(int64_t M, int64_t F, int64_t K) {
+    return M >= 0 && F >= 0 && K >= 0 && F % kDenseStep == 0 && K % kDenseStep == 0 && K <= kMaxDenseK &&
+           2 * F <= kMaxDenseK && M <= kMaxDenseRows;
+}
+
+bool adapter_ok(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank) {
+    return M >= 0 && N >= 0 && K >= 0 && K % kDenseStep == 0 && K <= kMaxDenseK && M <= kMaxDenseRows &&
+           N <= kMaxDenseN && adapters >= 0 && adapters <= INT32_MAX && rank >= kDenseStep && rank % kDenseStep == 0 &&
+           rank <= fp8q::kMaxRank;   // (an adapter's A is below 2^32 - 2^12 bytes)
+}
+
 int finish(hipError_t e) { return e == hipSuccess ? FP8Q_OK : FP8Q_ERR_LAUNCH; }
 
 }  // namespace
@@ -444,6 +466,106 @@ int int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const f
     if (int e = check_device()) return e;
     return finish(fp8q::launch_int8_grouped_gemm(a, sa, w, sw, offsets, rows, y, y_dtype == FP8Q_OUT_BF16, experts, M,
                                                  tokens, N, K, static_cast<hipStream_t>(stream)));
+}
+
+int residual_norm(const void *x, const void *y, int dtype, const float *weight, const float *post, const void *gate,
+                  int flags, float scale, float eps, void *t, void *z, int64_t T, int64_t H, void *stream) {
+    if (int e = norm_ok(dtype, flags, T, H)) return e;
+    if (T == 0) return FP8Q_OK;
+    if (!x || (weight ? !z : !t)) return FP8Q_ERR_NULL;
+    const bool gates = gate && (flags & FP8Q_NORM_GATES);
+    const uintptr_t size = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+    if (misaligned(x, size) || misaligned(y, size) || misaligned(t, size) || misaligned(z, size) ||
+        misaligned(gate, gates ? size : 4) || misaligned(weight, 4) || misaligned(post, 4))
+        return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_residual_norm(x, y, dtype == FP8Q_OUT_BF16, weight, y ? post : nullptr,
+                                             y && !gates ? static_cast<const float *>(gate) : nullptr,
+                                             y && gates ? gate : nullptr, scale, eps, t, weight ? z : nullptr, T, H,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+size_t residual_norm_backward_workspace_bytes(int64_t T, int64_t H) {
+    return norm_ok(FP8Q_OUT_F32, 0, T, H) ? 0 : fp8q::residual_norm_grad_workspace_bytes(T, H);
+}
+
+int residual_norm_backward(const void *dt, const void *dz, const void *t, const void *y, int dtype, const float *weight,
+                           const float *post, const void *gate, int flags, float scale, float eps, void *dx, void *dy,
+                           float *dweight, float *dpost, void *dgate, int64_t T, int64_t H, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    if (int e = norm_ok(dtype, flags, T, H)) return e;
+    if (!y && T > 0) post = nullptr, gate = nullptr;   // (no rows: the sums are wanted whatever y points to)
+    const bool gates = gate && (flags & FP8Q_NORM_GATES);
+    if ((weight && !dweight) || (post && !dpost) || (gate && !dgate && (!gates || T > 0))) return FP8Q_ERR_NULL;
+    if (T > 0 && (!dx || (y && !dy) || (weight && (!dz || !t)) || (!weight && !dt))) return FP8Q_ERR_NULL;
+    const uintptr_t size = dtype == FP8Q_OUT_BF16 ? 2 : 4;
+    if (misaligned(dt, size) || misaligned(dz, size) || misaligned(t, size) || misaligned(y, size) ||
+        misaligned(dx, size) || misaligned(dy, size) || misaligned(gate, gates ? size : 4) ||
+        misaligned(dgate, gates ? size : 4) || misaligned(weight, 4) || misaligned(post, 4) || misaligned(dweight, 4) ||
+        misaligned(dpost, 4) || misaligned(workspace, 16))
+        return FP8Q_ERR_ALIGN;
+    if (fp8q::residual_norm_grad_workspace_bytes(T, H) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_residual_norm_backward(
+        dt, dz, t, y, dtype == FP8Q_OUT_BF16, weight, post, gate && !gates ? static_cast<const float *>(gate) : nullptr,
+        gates ? gate : nullptr, scale, eps, dx, dy, weight ? dweight : nullptr, post ? dpost : nullptr,
+        gate && !gates ? static_cast<float *>(dgate) : nullptr, gates ? dgate : nullptr, T, H, workspace,
+        static_cast<hipStream_t>(stream)));
+}
+
+int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uint16_t *gu, int act, int64_t M,
+                 int64_t F, int64_t K, void *stream) {
+    if (!is_type(h_dtype) || (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU)) return FP8Q_ERR_DTYPE;
+    if (!gated_ok(M, F, K)) return FP8Q_ERR_SHAPE;
+    if (M == 0 || F == 0) return FP8Q_OK;
+    if (!h || (K > 0 && (!x || !w))) return FP8Q_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(h, 4) || misaligned(gu, 4)) return FP8Q_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_gated_linear(x, w, h, h_dtype == FP8Q_OUT_BF16, gu, act == FP8Q_ACT_GELU, M, F, K,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F) {
+    return gated_ok(M, F, 0) ? (size_t)(M * F * 4) : 0;
+}
+
+int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
+                          int dx_dtype, void *dw, int dw_dtype, int64_t M, int64_t F, int64_t K, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    if (!is_type(dx_dtype) || !is_type(dw_dtype) || (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU)) return FP8Q_ERR_DTYPE;
+    if (!gated_ok(M, F, K)) return FP8Q_ERR_SHAPE;
+    if (K == 0 || (!dx && !dw)) return FP8Q_OK;
+    if (M > 0 && F > 0 && (!dh || !w || !x)) return FP8Q_ERR_NULL;
+    if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(gu, 16) || misaligned(dx, 4) ||
+        misaligned(dw, 4) || misaligned(workspace, 16))
+        return FP8Q_ERR_ALIGN;
+    if (gated_linear_backward_workspace_bytes(M, F) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_gated_linear_backward(dh, x, w, gu, act == FP8Q_ACT_GELU, dx, dx_dtype == FP8Q_OUT_BF16, dw,
+                                                     dw_dtype == FP8Q_OUT_BF16, M, F, K, workspace,
+                                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank) {
+    return adapter_ok(M, 0, 0, 0, rank) ? fp8q::adapter_linear_workspace_bytes(M, rank) : 0;
+}
+
+int adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a, const uint16_t *b,
+                   const float *scales, const int32_t *ids, const void *base, void *y, int y_dtype, int64_t M,
+                   int64_t N, int64_t K, int64_t adapters, int64_t rank, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+    if (!is_type(y_dtype)) return FP8Q_ERR_DTYPE;
+    if (!adapter_ok(M, N, K, adapters, rank)) return FP8Q_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (!y || !ids || (K > 0 && !x) || (K > 0 && !w && !base) || (adapters > 0 && (!b || (K > 0 && !a)))) return FP8Q_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(a, 16) || misaligned(b, 16) || misaligned(bias, 4) ||
+        misaligned(scales, 4) || misaligned(ids, 4) || misaligned(base, 4) || misaligned(y, 4) || misaligned(workspace, 16))
+        return FP8Q_ERR_ALIGN;
+    if (adapters > 0 && fp8q::adapter_linear_workspace_bytes(M, rank) > (workspace ? workspace_bytes : 0))
+        return FP8Q_ERR_WORKSPACE;
+    if (int e = check_device()) return e;
+    return finish(fp8q::launch_adapter_linear(x, w, bias, a, b, scales, ids, base, y, y_dtype == FP8Q_OUT_BF16, M, N, K,
+                                              adapters, rank, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int fp8q_gemm_force_config(int config, int splits) {

@@ -1,10 +1,11 @@
-// binding.cpp -- the Python calls of the routed-expert and 8-bit integer operators: argument
+// binding.cpp -- the Python calls of the routed-expert, 8-bit integer and dense-block operators: argument
 // checks, outputs and workspaces from torch's allocator, one call of the C ABI (fp8q.h) on the
 // tensors' device and torch's current stream there.
 //
 // Native because these calls are small: a decode step's kernel takes 3 us, and checks, allocations
 // and ctypes in Python took 6 us a call around the 3 us that the launch itself takes; here they
-// take about 1 us. Names, defaults and documentation are in moe.py and int8.py.
+// take about 1 us. Names, defaults and documentation are in moe.py, int8.py and
+// block.py.
 #include <Python.h>
 
 #include <ATen/Context.h>
@@ -173,10 +174,11 @@ PyObject *pack(std::initializer_list<Tensor> ts) {
     PyObject *r = PyTuple_New((Py_ssize_t)ts.size());
     if (!r) throw Raised{};
     Py_ssize_t i = 0;
-    for (const Tensor &t : ts) PyTuple_SET_ITEM(r, i++, wrap(t));
+    for (const Tensor &t : ts) PyTuple_SET_ITEM(r, i++, wrap(t));   // (an undefined tensor is None)
     return r;
 }
 
+constexpr int64_t kMinNormH = 8, kMaxNormH = 16384, kDenseStep = 8, kMaxRank = 256;
 constexpr int64_t kMaxExperts = 1024, kMaxTopK = 32, kMaxGroups = 64, kStep = 16, kMaxK = (int64_t)1 << 17;
 
 // ---- routing -------------------------------------------------------------------------------
@@ -391,6 +393,159 @@ PyObject *grouped_gemm(PyObject *const *a) {
     return wrap(y);
 }
 
+// ---- the dense block -----------------------------------------------------------------------
+
+struct Norm {   // the arguments that residual_norm and its gradient share
+    const Tensor *weight = nullptr, *post = nullptr, *gate = nullptr;
+    int flags = 0;
+    float scale, eps;
+    int64_t H;
+    Norm(const Tensor &x, const char *name, PyObject *w, PyObject *p, PyObject *g, PyObject *s, PyObject *e)
+        : scale(real(s)), eps(real(e)) {
+        if (x.dim() < 1 || x.size(-1) < kMinNormH || x.size(-1) > kMaxNormH)
+            raise(PyExc_ValueError, "%s must be [..., H] with H from %d to %d", name, (int)kMinNormH, (int)kMaxNormH);
+        if (!(eps >= 0.0f)) raise(PyExc_ValueError, "eps must not be negative");
+        H = x.size(-1);
+        if (w != Py_None) shaped(*(weight = &need(w, "weight", ScalarType::Float, 4, &x)), "weight", {H});
+        if (p != Py_None) shaped(*(post = &need(p, "post", ScalarType::Float, 4, &x)), "post", {H});
+        if (g == Py_None) return;
+        // one per channel, or per element
+        if (tensor(g, "gate").dim() == 1 && THPVariable_Unpack(g).scalar_type() == ScalarType::Float) {
+            shaped(*(gate = &need(g, "gate", ScalarType::Float, 4, &x)), "gate", {H});
+        } else {
+            shaped(*(gate = &need(g, "gate", x.scalar_type(), x.element_size(), &x)), "gate", x.sizes());
+            flags = FP8Q_NORM_GATES;
+        }
+    }
+};
+const Tensor *beside_of(PyObject *o, const char *name, const Tensor &x) {   // of x's type and shape, or None
+    if (o == Py_None) return nullptr;
+    const Tensor &t = need(o, name, x.scalar_type(), x.element_size(), &x);
+    shaped(t, name, x.sizes());
+    return &t;
+}
+void *out_of(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// (x, y or None, weight or None, post or None, gate or None, scale, eps)
+PyObject *norm(PyObject *const *a) {
+    const Tensor &x = need_float(a[0], "x");
+    const Tensor *y = beside_of(a[1], "y", x);
+    const Norm n(x, "x", a[2], a[3], a[4], a[5], a[6]);
+    if (!y && !n.weight) raise(PyExc_ValueError, "weight must be given");
+    const Tensor t = y ? like(x, x.sizes(), x.scalar_type()) : Tensor(),
+                 z = n.weight ? like(x, x.sizes(), x.scalar_type()) : Tensor();
+    const On on(x);
+    check("residual_norm",
+          residual_norm(x.data_ptr(), data(y), code_of(x), static_cast<const float *>(data(n.weight)),
+                        static_cast<const float *>(data(n.post)), data(n.gate), n.flags, n.scale, n.eps, out_of(t),
+                        out_of(z), rows_of(x), n.H, on.stream()));
+    return y ? pack({t, z}) : wrap(z);
+}
+
+// (dt or None, dz or None, t, y or None, weight or None, post or None, gate or None, scale, eps)
+PyObject *norm_backward(PyObject *const *a) {
+    const Tensor &t = need_float(a[2], "t");
+    const Tensor *y = beside_of(a[3], "y", t), *dt = beside_of(a[0], "dt", t), *dz = beside_of(a[1], "dz", t);
+    const Norm n(t, "t", a[4], a[5], a[6], a[7], a[8]);
+    if ((dz != nullptr) != (n.weight != nullptr)) raise(PyExc_ValueError, "dz and weight go together");
+    if (!dt && !dz) raise(PyExc_ValueError, "dt or dz must be given");
+    const int64_t T = rows_of(t);
+    const Tensor dx = like(t, t.sizes(), t.scalar_type()), dy = y ? like(t, t.sizes(), t.scalar_type()) : Tensor(),
+                 dw = n.weight ? like(t, {n.H}, ScalarType::Float) : Tensor(),
+                 dp = y && n.post ? like(t, {n.H}, ScalarType::Float) : Tensor(),
+                 dg = y && n.gate ? like(t, n.gate->sizes(), n.gate->scalar_type()) : Tensor();
+    const size_t bytes = residual_norm_backward_workspace_bytes(T, n.H);
+    const Tensor ws = bytes ? like(t, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
+    const On on(t);
+    check("residual_norm_backward",
+          residual_norm_backward(data(dt), data(dz), t.data_ptr(), data(y), code_of(t),
+                                 static_cast<const float *>(data(n.weight)), static_cast<const float *>(data(n.post)),
+                                 data(n.gate), n.flags, n.scale, n.eps, dx.data_ptr(), out_of(dy),
+                                 static_cast<float *>(out_of(dw)), static_cast<float *>(out_of(dp)), out_of(dg), T, n.H,
+                                 out_of(ws), bytes, on.stream()));
+    return pack({dx, dy, dw, dp, dg});
+}
+
+struct Gated {
+    const Tensor &x, &w;
+    int64_t M, F, K;
+    Gated(PyObject *xo, PyObject *wo)
+        : x(need(xo, "x", ScalarType::BFloat16, 16)), w(need(wo, "w", ScalarType::BFloat16, 16, &x)) {
+        if (x.dim() < 1 || w.dim() != 2 || w.size(1) != x.size(-1) || w.size(0) % 2)
+            raise(PyExc_ValueError, "w must be [2 F, K] with the activation's K");
+        M = rows_of(x), F = w.size(0) / 2, K = w.size(1);
+        if (F % kDenseStep || K % kDenseStep) raise(PyExc_ValueError, "F and K must be multiples of %d", (int)kDenseStep);
+    }
+    c10::SmallVector<int64_t, 6> shape(int64_t last) const {
+        c10::SmallVector<int64_t, 6> s(x.sizes().begin(), x.sizes().end());
+        s.back() = last;
+        return s;
+    }
+};
+
+// (x, w, act, keep, dtype code)
+PyObject *gated(PyObject *const *a) {
+    const Gated g(a[0], a[1]);
+    const int act = (int)integer(a[2], "act");
+    const bool keep = PyObject_IsTrue(a[3]) == 1;
+    const Tensor h = like(g.x, g.shape(g.F), type_of_code(a[4])),
+                 gu = keep ? like(g.x, g.shape(2 * g.F), ScalarType::BFloat16) : Tensor();
+    const On on(g.x);
+    check("gated_linear", gated_linear(ptr<uint16_t>(g.x), ptr<uint16_t>(g.w), h.data_ptr(), code_of(h),
+                                       static_cast<uint16_t *>(out_of(gu)), act, g.M, g.F, g.K, on.stream()));
+    return keep ? pack({h, gu}) : wrap(h);
+}
+
+// (dh, x, w, gu or None, act, dx dtype code, dw dtype code)
+PyObject *gated_backward(PyObject *const *a) {
+    const Gated g(a[1], a[2]);
+    const Tensor &dh = need(a[0], "dh", ScalarType::BFloat16, 16, &g.x);
+    shaped(dh, "dh", g.shape(g.F));
+    const Tensor *gu = nullptr;
+    if (a[3] != Py_None) shaped(*(gu = &need(a[3], "gu", ScalarType::BFloat16, 16, &g.x)), "gu", g.shape(2 * g.F));
+    const Tensor dx = like(g.x, g.x.sizes(), type_of_code(a[5])), dw = like(g.x, g.w.sizes(), type_of_code(a[6]));
+    const size_t bytes = gated_linear_backward_workspace_bytes(g.M, g.F);
+    const Tensor ws = bytes ? like(g.x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
+    const On on(g.x);
+    check("gated_linear_backward",
+          gated_linear_backward(ptr<uint16_t>(dh), ptr<uint16_t>(g.x), ptr<uint16_t>(g.w),
+                                static_cast<const uint16_t *>(data(gu)), (int)integer(a[4], "act"), dx.data_ptr(),
+                                code_of(dx), dw.data_ptr(), code_of(dw), g.M, g.F, g.K, out_of(ws), bytes, on.stream()));
+    return pack({dx, dw});
+}
+
+// (x, w or None, a, b, ids, scales or None, bias or None, base or None, dtype code, out or None): w or base
+PyObject *adapter(PyObject *const *a) {
+    const Tensor &x = need(a[0], "x", ScalarType::BFloat16, 16);
+    const Tensor &la = need(a[2], "a", ScalarType::BFloat16, 16, &x), &lb = need(a[3], "b", ScalarType::BFloat16, 16, &x);
+    if (x.dim() < 1 || la.dim() != 3 || lb.dim() != 3 || la.size(0) != lb.size(0) || la.size(1) != lb.size(2) ||
+        la.size(2) != x.size(-1))
+        raise(PyExc_ValueError, "a must be [adapters, rank, K] with the activation's K and b [adapters, N, rank]");
+    const int64_t M = rows_of(x), K = x.size(-1), L = la.size(0), r = la.size(1), N = lb.size(1);
+    if (K % kDenseStep) raise(PyExc_ValueError, "the last dimension must be a multiple of %d", (int)kDenseStep);
+    if (r < kDenseStep || r % kDenseStep || r > kMaxRank)
+        raise(PyExc_ValueError, "the rank must be a multiple of %d from %d to %d", (int)kDenseStep, (int)kDenseStep, (int)kMaxRank);
+    const Tensor &ids = need(a[4], "ids", ScalarType::Int, 4, &x);
+    shaped(ids, "ids", x.sizes().slice(0, x.dim() - 1));
+    const Tensor *scales = nullptr, *w = nullptr, *base = nullptr;
+    if (a[5] != Py_None) shaped(*(scales = &need(a[5], "scales", ScalarType::Float, 4, &x)), "scales", {L});
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = N;
+    if (a[1] != Py_None) shaped(*(w = &need(a[1], "w", ScalarType::BFloat16, 16, &x)), "w", {N, K});
+    else shaped(*(base = &need_float(a[7], "y", &x)), "y", shape);
+    const Tensor *bias = bias_of(a[6], N, x);
+    if (base && reinterpret_cast<uintptr_t>(base->data_ptr()) % 4) raise(PyExc_ValueError, "y must be 4-byte aligned");
+    const Tensor y = output(a[9], shape, base ? base->scalar_type() : type_of_code(a[8]), 4, x);
+    const size_t bytes = L ? adapter_linear_workspace_bytes(M, r) : 0;
+    const Tensor ws = bytes ? like(x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
+    const On on(x);
+    check("adapter_linear",
+          adapter_linear(ptr<uint16_t>(x), static_cast<const uint16_t *>(data(w)), static_cast<const float *>(data(bias)),
+                         ptr<uint16_t>(la), ptr<uint16_t>(lb), static_cast<const float *>(data(scales)), ptr<int32_t>(ids),
+                         data(base), y.data_ptr(), code_of(y), M, N, K, L, r, out_of(ws), bytes, on.stream()));
+    return wrap(y);
+}
+
 // ---- module --------------------------------------------------------------------------------
 
 template <PyObject *(*F)(PyObject *const *), int N>
@@ -410,9 +565,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {ENTRY(route, 7),    ENTRY(route_backward, 5), ENTRY(place, 3),
                          ENTRY(combine, 4),  ENTRY(combine_backward, 4), ENTRY(quant, 1),
                          ENTRY(gemm, 7),     ENTRY(linear, 5),         ENTRY(grouped_gemm, 8),
+                         ENTRY(norm, 7),     ENTRY(norm_backward, 9),  ENTRY(gated, 5),
+                         ENTRY(gated_backward, 7), ENTRY(adapter, 10),
                          {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Calls of the routed-expert and 8-bit integer operators", -1,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Calls of the routed-expert, 8-bit integer and dense-block operators", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,253 @@
+// gated.hip -- the gated projection of a feed-forward block: both projections, the activation and the
+// product in one kernel, and its gradient, for gfx950.
+//
+//     g = x Wg^T, u = x Wu^T  (W = [Wg; Wu]),  h = act(g) * u
+//     dg = dh * u * act'(g),  du = dh * act(g),  dx = [dg du] W,  dW = [dg du]^T x
+//
+// act is SiLU, a / (1 + e^-a), or GELU, a * Phi(a) with Phi by erfc (which keeps its relative precision
+// where Phi is small). Products are bf16 with fp32 sums (mm.h); activation and product are fp32 on the
+// sums, rounded once. The gradient's products take dg and du rounded to bf16, the matrix unit's type.
+//
+// The projections' columns are dealt so that a lane holds g and u of the same element: nothing of them
+// goes through memory unless the caller keeps them. The gradient forms dg and du from kept projections (a
+// pass over memory) or by the same product again with another epilogue, then takes two products whose
+// operands are transposed by their LDS reads.
+#include <cmath>
+
+#include <fp8q.h>
+
+#include "mm.h"
+
+namespace fp8q {
+namespace {
+
+struct GatedArgs {
+    MmArgs mm;            // N = F
+    void *h;              // [M, F]
+    uint16_t *gu;         // [M, 2 F] or null; the gradient: dg and du
+    const uint16_t *dh;   // the gradient: [M, F]
+    int gelu;
+};
+
+struct Activation {
+    float value, slope;
+};
+__device__ __forceinline__ Activation activate(float a, int gelu) {
+    if (gelu) {
+        const float p = 0.5f * erfcf(a * -0.70710678118654752f);
+        return {a * p, p + a * (expf(-0.5f * a * a) * 0.39894228040143268f)};
+    }
+    const float s = 1.0f / (1.0f + expf(-a));
+    return {a * s, s * (1.0f + a * (1.0f - s))};
+}
+
+// MODE 0, 1: h in fp32, bf16; 2: dg and du
+template <int BM, int BN, int NW, int NSTAGE, int MODE>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_kernel(GatedArgs g) {
+    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+    constexpr int HALF = T::SUB_N / 2;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    int64_t m0, n0;
+    find_tile<T, BN / 2>(g.mm, m0, n0);
+    f32x4 acc[T::SUB_M][T::SUB_N];
+    multiply<T, 0, 0, 1, MODE>(g.mm, m0, n0, smem, acc);
+    const int64_t M = g.mm.M, F = g.mm.N;
+    auto gate = [&](int i, int j) { return acc[i][j]; };
+    auto up = [&](int i, int j) { return acc[i][j + HALF]; };
+    if constexpr (MODE == 2) {
+        const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
+#pragma unroll
+        for (int i = 0; i < T::SUB_M; ++i) {
+            const int64_t m = m0 + T::row(wm, i) + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < HALF; ++j) {
+                const int64_t n = n0 + 16 * (wn * HALF + j) + 4 * (lane >> 4);
+                f32x4 dh = {0.f, 0.f, 0.f, 0.f};
+                if (m < M && n < F) dh = load4<1>(g.dh, m * F + n, F - n);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const Activation a = activate(acc[i][j][r], g.gelu);
+                    acc[i][j][r] = dh[r] * acc[i][j + HALF][r] * a.slope;
+                    acc[i][j + HALF][r] = dh[r] * a.value;
+                }
+            }
+        }
+    } else {
+        store_tile<T, MODE, HALF>(g.h, F, m0, M, n0, F, smem, [&](int i, int j) {
+            f32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = activate(acc[i][j][r], g.gelu).value * acc[i][j + HALF][r];
+            return v;
+        });
+    }
+    if (g.gu) {
+        store_tile<T, 1, HALF>(g.gu, 2 * F, m0, M, n0, F, smem, gate);
+        store_tile<T, 1, HALF>(g.gu + F, 2 * F, m0, M, n0, F, smem, up);
+    }
+}
+
+// At most 16 rows
+template <int MODE>
+__global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kFewStage * kFewStages];
+    __shared__ f32x4 part[2][64];
+    __shared__ f32x4 ups[64];
+    const int64_t n0 = (int64_t)blockIdx.x * (kFewN / 2);
+    const f32x4 acc = few<1, MODE>(g.mm, n0, smem, part);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (wave == 1) ups[lane] = acc;
+    __syncthreads();
+    const int64_t m = lane & 15, n = n0 + 4 * (lane >> 4), F = g.mm.N;
+    if (wave || m >= g.mm.M || n >= F) return;
+    const f32x4 up = ups[lane];
+    f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const Activation act = activate(acc[r], g.gelu);
+        a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
+        b[r] = dh[r] * act.value;
+    }
+    if constexpr (MODE == 2) {
+        store4<1>(g.gu, m * 2 * F + n, a, F - n);
+        store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
+    } else {
+        store4<MODE>(g.h, m * F + n, a, F - n);
+        if (g.gu) {
+            store4<1>(g.gu, m * 2 * F + n, acc, F - n);
+            store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
+        }
+    }
+}
+
+// dg and du from kept projections, 8 elements a thread (F is a multiple of 8): bound by memory
+__global__ __launch_bounds__(256) void gated_slope_kernel(const uint16_t *dh, const uint16_t *gu, uint16_t *d, int64_t n,
+                                                          int64_t F, int gelu) {
+    const int64_t step = (int64_t)gridDim.x * 256, per = F / 8;
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < n; p += step) {
+        const int64_t m = p / per, at = m * 2 * F + 8 * (p - m * per);
+        const u32x4 vh = *reinterpret_cast<const u32x4 *>(dh + 8 * p), vg = *reinterpret_cast<const u32x4 *>(gu + at),
+                    vu = *reinterpret_cast<const u32x4 *>(gu + at + F);
+        u32x4 a, b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Activation lo = activate(bf16lo_to_f32(vg[i]), gelu), hi = activate(bf16hi_to_f32(vg[i]), gelu);
+            const float hl = bf16lo_to_f32(vh[i]), hh = bf16hi_to_f32(vh[i]);
+            a[i] = pack_bf16x2(hl * bf16lo_to_f32(vu[i]) * lo.slope, hh * bf16hi_to_f32(vu[i]) * hi.slope);
+            b[i] = pack_bf16x2(hl * lo.value, hh * hi.value);
+        }
+        *reinterpret_cast<u32x4 *>(d + at) = a;
+        *reinterpret_cast<u32x4 *>(d + at + F) = b;
+    }
+}
+
+// dx (XT 0) and dW (XT 1): W's operand is K-strided in both
+struct ProductArgs {
+    MmArgs mm;
+    void *y;
+};
+template <int BM, int BN, int NW, int NSTAGE, int XT, int OUT_BF16>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_grad_kernel(ProductArgs g) {
+    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    int64_t m0, n0;
+    find_tile<T, BN>(g.mm, m0, n0);
+    f32x4 acc[T::SUB_M][T::SUB_N];
+    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc);
+    store_tile<T, OUT_BF16, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, [&](int i, int j) { return acc[i][j]; });
+}
+
+template <int BM, int BN, int NW, int NSTAGE>
+hipError_t launch_gated_tile(GatedArgs a, int mode, hipStream_t stream) {
+    if (!lay_out(a.mm, BM, BN / 2, NW * 64)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(NW * 64);
+    if (mode == 0) gated_kernel<BM, BN, NW, NSTAGE, 0><<<grid, block, 0, stream>>>(a);
+    else if (mode == 1) gated_kernel<BM, BN, NW, NSTAGE, 1><<<grid, block, 0, stream>>>(a);
+    else gated_kernel<BM, BN, NW, NSTAGE, 2><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps.
+double tile_time(int64_t M, int64_t N, int64_t K, int bm, int bn, double first, double more, double end) {
+    const double tiles = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn), rounds = std::ceil(tiles / 256.0);
+    return (double)((K + KSTEP - 1) / KSTEP) * (first + more * (rounds - 1.0)) + end * rounds;
+}
+int best_tile(const double *t, int n) {
+    int best = 0;
+    for (int i = 1; i < n; ++i)
+        if (t[i] < t[best]) best = i;
+    return best;
+}
+
+hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
+    const int64_t M = a.mm.M, F = a.mm.N, K = a.mm.K;
+    if (M <= kFewRows) {
+        const dim3 grid((unsigned)((F + kFewN / 2 - 1) / (kFewN / 2))), block(256);
+        if (mode == 0) gated_few_kernel<0><<<grid, block, 0, stream>>>(a);
+        else if (mode == 1) gated_few_kernel<1><<<grid, block, 0, stream>>>(a);
+        else gated_few_kernel<2><<<grid, block, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    const double t[5] = {tile_time(M, 2 * F, K, 32, 64, 0.155, 0.125, 1.1), tile_time(M, 2 * F, K, 64, 64, 0.21, 0.18, 1.4),
+                         tile_time(M, 2 * F, K, 128, 128, 0.45, 0.53, 5.0),
+                         tile_time(M, 2 * F, K, 128, 256, 0.75, 0.83, 5.7),
+                         tile_time(M, 2 * F, K, 256, 256, 1.3, 1.5, 8.0)};
+    switch (best_tile(t, 5)) {
+    case 0: return launch_gated_tile<32, 64, 4, 6>(a, mode, stream);
+    case 1: return launch_gated_tile<64, 64, 4, 5>(a, mode, stream);
+    case 2: return launch_gated_tile<128, 128, 4, 4>(a, mode, stream);
+    case 3: return launch_gated_tile<128, 256, 8, 3>(a, mode, stream);
+    default: return launch_gated_tile<256, 256, 8, 2>(a, mode, stream);
+    }
+}
+
+template <int BM, int BN, int NW, int NSTAGE, int XT>
+hipError_t launch_product_tile(ProductArgs a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a.mm, BM, BN, NW * 64)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(NW * 64);
+    if (out_bf16) gated_grad_kernel<BM, BN, NW, NSTAGE, XT, 1><<<grid, block, 0, stream>>>(a);
+    else gated_grad_kernel<BM, BN, NW, NSTAGE, XT, 0><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int XT>
+hipError_t launch_product(const ProductArgs &a, bool out_bf16, hipStream_t stream) {
+    const int64_t M = a.mm.M, N = a.mm.N, K = a.mm.K;
+    const double t[4] = {tile_time(M, N, K, 64, 64, 0.21, 0.18, 1.4), tile_time(M, N, K, 128, 128, 0.45, 0.53, 5.0),
+                         tile_time(M, N, K, 128, 256, 0.75, 0.83, 5.7), tile_time(M, N, K, 256, 256, 1.3, 1.5, 8.0)};
+    switch (best_tile(t, 4)) {
+    case 0: return launch_product_tile<64, 64, 4, 5, XT>(a, out_bf16, stream);
+    case 1: return launch_product_tile<128, 128, 4, 4, XT>(a, out_bf16, stream);
+    case 2: return launch_product_tile<128, 256, 8, 3, XT>(a, out_bf16, stream);
+    default: return launch_product_tile<256, 256, 8, 2, XT>(a, out_bf16, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
+                               int64_t M, int64_t F, int64_t K, hipStream_t stream) {
+    return launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, h, gu, nullptr, gelu}, h_bf16, stream);
+}
+
+hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,
+                                        bool gelu, void *dx, bool dx_bf16, void *dw, bool dw_bf16, int64_t M, int64_t F,
+                                        int64_t K, void *workspace, hipStream_t stream) {
+    uint16_t *const d = static_cast<uint16_t *>(workspace);   // [M, 2 F]
+    if (M > 0 && F > 0) {
+        if (gu) {
+            const int64_t n = M * F / 8, need = (n + 255) / 256;
+            gated_slope_kernel<<<dim3((unsigned)(need < 8192 ? need : 8192)), dim3(256), 0, stream>>>(dh, gu, d, n, F, gelu);
+            if (hipError_t e = hipGetLastError()) return e;
+        } else if (hipError_t e = launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, nullptr, d, dh, gelu}, 2, stream)) {
+            return e;
+        }
+    }
+    if (dx && M > 0 && K > 0)
+        if (hipError_t e = launch_product<0>({{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx}, dx_bf16, stream)) return e;
+    if (dw && F > 0 && K > 0)
+        if (hipError_t e = launch_product<1>({{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw}, dw_bf16, stream)) return e;
+    return hipSuccess;
+}
+
+}  // namespace fp8q

@@ -107,4 +107,35 @@ hipError_t launch_int8_grouped_gemm(const int8_t *a, const float *sa, const int8
                                     int64_t experts, int64_t M, int64_t tokens, int64_t N, int64_t K,
                                     hipStream_t stream);
 
+// Norms before and after a block with its gate and the residual (norm.hip). x, y (or null), gates (or
+// null) and the outputs bf16 or fp32 [T, H], the vectors fp32 [H] or null; 8 <= H <= 16384, at most one of gate and gates. The
+// gradient's workspace holds residual_norm_grad_workspace_bytes (any contents).
+constexpr int64_t kMinNormH = 8, kMaxNormH = 16384;
+hipError_t launch_residual_norm(const void *x, const void *y, bool bf16, const float *weight, const float *post,
+                                const float *gate, const void *gates, float scale, float eps, void *t, void *z,
+                                int64_t T, int64_t H, hipStream_t stream);
+size_t residual_norm_grad_workspace_bytes(int64_t T, int64_t H);
+hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const void *t, const void *y, bool bf16,
+                                         const float *weight, const float *post, const float *gate, const void *gates,
+                                         float scale, float eps, void *dx, void *dy, float *dweight, float *dpost,
+                                         float *dgate, void *dgates, int64_t T, int64_t H, void *workspace,
+                                         hipStream_t stream);
+
+// Gated projections (gated.hip): x [M, K], w [2 F, K], K and F multiples of 8 (K < 2^23, F < 2^22), the
+// gradient's workspace [M, 2 F] bf16.
+hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
+                               int64_t M, int64_t F, int64_t K, hipStream_t stream);
+hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,
+                                        bool gelu, void *dx, bool dx_bf16, void *dw, bool dw_bf16, int64_t M, int64_t F,
+                                        int64_t K, void *workspace, hipStream_t stream);
+
+// Linear layers with an adapter per token (adapter.hip): K and rank multiples of 8, rank <= kMaxRank; w, or base
+// of y's type; the workspace holds adapter_linear_workspace_bytes.
+constexpr int64_t kMaxRank = 256;
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank);
+hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a,
+                                 const uint16_t *b, const float *scales, const int32_t *ids, const void *base, void *y,
+                                 bool out_bf16, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank,
+                                 void *workspace, hipStream_t stream);
+
 }  // namespace fp8q

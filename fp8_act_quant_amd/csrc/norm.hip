@@ -1,0 +1,500 @@
+// norm.hip -- the norms before and after a block, with the block's gate and the residual, in one pass
+// over the rows, and their gradient.
+//
+//     n = y, or with `post` y * q * post, q = 1 / sqrt(mean(y^2) + eps)
+//     t = scale * x + gate * n                       gate: one per channel, per element, or 1
+//     z = t * r * weight, r = 1 / sqrt(mean(t^2) + eps)
+//
+// and from dt (of t besides z) and dz, with th = t * r and yh = y * q:
+//
+//     d = dt + r * (dz * weight - th * mean(dz * weight * th)),  dx = scale * d,  dweight = sum dz * th
+//     dn = d * gate,  dgate = d * n (summed over the rows for one per channel),  dpost = sum dn * yh
+//     dy = dn, or with `post` q * (dn * post - yh * mean(dn * post * yh))
+//
+// Bound by memory: four rows of H elements a token, six for the gradient. So a row is read once, into
+// registers, NT threads to a row and NV pieces of 8 elements a thread, and a workgroup walks many rows:
+// the per-channel vectors stay in registers too (read again for every row they would be more bytes
+// than the rows themselves), the next row's loads are on their way while a row is reduced, and the
+// gradient's sums over the rows are carried in registers. Squares, sums and every step are fp32; t
+// enters the second norm before its rounding. Outputs round once. The order of every sum is fixed.
+#include <fp8q.h>
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8q {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+// rows of any length: pieces lie at the alignment of an element
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+
+struct NormArgs {
+    const void *x, *y;          // the gradient: x is t
+    const void *dt, *dz;        // gradient only; dt may be null
+    const float *weight, *post; // [H] or null
+    const float *gate;          // [H] or null
+    const void *gates;          // [T, H] or null (at most one of gate, gates)
+    void *t, *z;                // the gradient: dx, dy
+    void *dgates;               // gradient: [T, H], or null
+    float *sums[3];             // gradient: dweight, dpost, dgate, each [partials][H] at `pitch`
+    int64_t pitch;
+    int64_t T;
+    int H;
+    float scale, eps;
+};
+
+// 8 elements as they come from memory
+template <int BF16>
+struct Raw {
+    u32x4 v[BF16 ? 1 : 2];
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (BF16) return i & 1 ? bf16hi_to_f32(v[0][i / 2]) : bf16lo_to_f32(v[0][i / 2]);
+        else return __uint_as_float(v[i / 4][i % 4]);
+    }
+};
+
+// Piece p of a row of H >= 8 elements. A row's last piece, where it is short, is the row's last 8
+// elements with those before the piece shifted out; what lies past the row counts as zeros.
+template <int BF16>
+__device__ __forceinline__ Raw<BF16> load8(const void *base, int64_t row, int p, int H) {
+    constexpr int N = BF16 ? 1 : 2;
+    Raw<BF16> r;
+#pragma unroll
+    for (int h = 0; h < N; ++h) r.v[h] = u32x4{0, 0, 0, 0};
+    if (8 * p >= H) return r;
+    const uint32_t off = 8 * p + 8 <= H ? 8 * p : H - 8;
+    const char *from = static_cast<const char *>(base) + row * H * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int h = 0; h < N; ++h)
+        r.v[h] = *reinterpret_cast<const u32x4_any *>(from + (uint32_t)(off * (BF16 ? 2 : 4) + 16 * h));
+    const int s = 8 * p - (int)off;
+    if (s) {
+        uint32_t u[4 * N];
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) u[i] = r.v[i / 4][i % 4];
+#pragma unroll
+        for (int bit = 4; bit; bit >>= 1) {
+            const int words = BF16 ? bit / 2 : bit;   // (half a word last, of bf16)
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i) {
+                const uint32_t up = words ? (i + words < 4 * N ? u[i + words] : 0)
+                                          : u[i] >> 16 | (i + 1 < 4 * N ? u[i + 1] << 16 : 0);
+                u[i] = s & bit ? up : u[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) r.v[i / 4][i % 4] = u[i];
+    }
+    return r;
+}
+
+template <int BF16>
+__device__ __forceinline__ void store8(void *base, int64_t row, int p, int H, const float (&v)[8]) {
+    const int left = H - 8 * p;
+    if (left <= 0) return;
+    if constexpr (BF16) {
+        uint16_t *q = reinterpret_cast<uint16_t *>(static_cast<char *>(base) + row * H * 2 + (uint32_t)(16 * p));
+        const u32x4 u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+        if (left >= 8) {
+            *reinterpret_cast<u32x4_any *>(q) = u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < left) q[i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
+        }
+    } else {
+        float *q = reinterpret_cast<float *>(static_cast<char *>(base) + row * H * 4 + (uint32_t)(32 * p));
+        if (left >= 8) {
+            *reinterpret_cast<u32x4_any *>(q) = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+            *reinterpret_cast<u32x4_any *>(q + 4) = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < left) q[i] = v[i];
+        }
+    }
+}
+
+// A per-channel vector's pieces of this thread, ones where there is none: kept in registers, or read
+// again for every row where a row takes too many of them
+template <int NT, int NV, bool KEEP>
+struct Channels {
+    Raw<0> kept[KEEP ? NV : 1];
+    const float *v;
+    int tid, H;
+    __device__ __forceinline__ Channels(const float *v_, int tid_, int H_) : v(v_), tid(tid_), H(H_) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) kept[i] = read(i);
+        }
+    }
+    __device__ __forceinline__ Raw<0> read(int i) const {
+        if (v) return load8<0>(v, 0, tid + i * NT, H);
+        Raw<0> r;
+        r.v[0] = r.v[1] = u32x4{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
+        return r;
+    }
+    __device__ __forceinline__ Raw<0> operator()(int i) const {
+        if constexpr (KEEP) return kept[i];
+        else return read(i);
+    }
+};
+
+// Sums of N values over the NT threads of a row, the same bits in all of them. `turn` alternates: the
+// values of one call stay readable until every thread is past the barrier of the next.
+template <int NT, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[3][NT / 64], int &turn) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], m, 64);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) part[turn][n][threadIdx.x >> 6] = v[n];
+        }
+        // (a barrier that waits for LDS, not for the next row's loads)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            v[n] = part[turn][n][0];
+#pragma unroll
+            for (int w = 1; w < NT / 64; ++w) v[n] += part[turn][n][w];
+        }
+        turn ^= 1;
+    }
+}
+
+// NT threads to a row: a wave (four rows a workgroup) or a workgroup
+template <int NT>
+constexpr int rows_of() { return NT == 64 ? 4 : 1; }
+
+// GATES: the gate is one per element
+template <int BF16, int NT, int NV, int GATES>
+__global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormArgs g) {
+    constexpr int ROWS = rows_of<NT>();
+    constexpr bool AHEAD = NV <= 2;   // the next row's loads a row ahead, the channels in registers
+    __shared__ float part[2][3][NT / 64];
+    const int tid = threadIdx.x % NT, H = g.H;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const float inv = 1.0f / (float)H;
+    int turn = 0;
+
+    Raw<BF16> x[NV], y[NV], gt[NV];
+    auto load = [&](int64_t m) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = load8<BF16>(g.x, m, tid + i * NT, H);
+            if (g.y) y[i] = load8<BF16>(g.y, m, tid + i * NT, H);
+            if constexpr (GATES) gt[i] = load8<BF16>(g.gates, m, tid + i * NT, H);
+        }
+    };
+    if (AHEAD && row < g.T) load(row);
+    const Channels<NT, NV, AHEAD> weight(g.weight, tid, H), post(g.post, tid, H), gate(g.gate, tid, H);
+    for (; row < g.T; row += step) {
+        if constexpr (!AHEAD) load(row);
+        float t[NV][8], n[NV][8];
+        Raw<BF16> gates[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (GATES) gates[i] = gt[i];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[i][e] = g.scale * x[i].at(e);
+                n[i][e] = g.y ? y[i].at(e) : 0.0f;
+            }
+        }
+        if (AHEAD && row + step < g.T) load(row + step);
+        if (g.y) {
+            float q = 1.0f;
+            if (g.post) {
+                float s[1] = {0.0f};
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(n[i][e], n[i][e], s[0]);
+                row_sums<NT>(s, part, turn);
+                q = 1.0f / __builtin_sqrtf(s[0] * inv + g.eps);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Raw<0> p = post(i), c = gate(i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t[i][e] = __builtin_fmaf(GATES ? gates[i].at(e) : c.at(e), n[i][e] * q * p.at(e), t[i][e]);
+            }
+        }
+        if (g.t) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) store8<BF16>(g.t, row, tid + i * NT, H, t[i]);
+        }
+        if (g.weight) {
+            float s[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(t[i][e], t[i][e], s[0]);   // (0 past the row's end)
+            row_sums<NT>(s, part, turn);
+            const float r = 1.0f / __builtin_sqrtf(s[0] * inv + g.eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Raw<0> w = weight(i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[i][e] = t[i][e] * r * w.at(e);
+                store8<BF16>(g.z, row, tid + i * NT, H, t[i]);
+            }
+        }
+    }
+}
+
+// The gradient. The sums over the rows leave as one partial row per workgroup, which a second kernel
+// adds up (with one workgroup they are the sums).
+template <int BF16, int NT, int NV, int GATES>
+__global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(NormArgs g) {
+    constexpr int ROWS = rows_of<NT>();
+    constexpr bool AHEAD = NV == 1 || (NV == 2 && BF16);
+    __shared__ float part[2][3][NT / 64];
+    __shared__ float across[ROWS > 1 ? 3 * NT * NV * 8 : 1];
+    const int tid = threadIdx.x % NT, H = g.H;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const float inv = 1.0f / (float)H;
+    int turn = 0;
+
+    struct Inputs {
+        Raw<BF16> t, dz, dt, y, gate;
+    };
+    Inputs next[NV];
+    const bool need_y = g.y && (g.post || g.sums[2] || GATES);
+    auto load = [&](int64_t m) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (g.weight) {
+                next[i].t = load8<BF16>(g.x, m, tid + i * NT, H);
+                next[i].dz = load8<BF16>(g.dz, m, tid + i * NT, H);
+            }
+            if (g.dt) next[i].dt = load8<BF16>(g.dt, m, tid + i * NT, H);
+            if (need_y) next[i].y = load8<BF16>(g.y, m, tid + i * NT, H);
+            if constexpr (GATES) next[i].gate = load8<BF16>(g.gates, m, tid + i * NT, H);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int h = 0; h < (BF16 ? 1 : 2); ++h) {   // what is not there counts as zeros
+            const u32x4 zero = {0, 0, 0, 0};
+            next[i].t.v[h] = next[i].dz.v[h] = next[i].dt.v[h] = next[i].y.v[h] = next[i].gate.v[h] = zero;
+        }
+    if (AHEAD && row < g.T) load(row);
+    const Channels<NT, NV, AHEAD> weight(g.weight, tid, H), post(g.post, tid, H), gate(g.gate, tid, H);
+    float sum[3][NV][8];
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[a][i][e] = 0.0f;
+
+    for (; row < g.T; row += step) {
+        if constexpr (!AHEAD) load(row);
+        Inputs in[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) in[i] = next[i];
+        if (AHEAD && row + step < g.T) load(row + step);
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Raw<0> w = weight(i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float t = in[i].t.at(e), y = in[i].y.at(e);
+                s[0] = __builtin_fmaf(t, t, s[0]);
+                s[1] = __builtin_fmaf(in[i].dz.at(e) * w.at(e), t, s[1]);
+                s[2] = __builtin_fmaf(y, y, s[2]);
+            }
+        }
+        row_sums<NT>(s, part, turn);
+        const float r = g.weight ? 1.0f / __builtin_sqrtf(s[0] * inv + g.eps) : 0.0f, mean = s[1] * inv * r;
+        const float q = g.post ? 1.0f / __builtin_sqrtf(s[2] * inv + g.eps) : 1.0f;
+        float d[NV][8], dot[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Raw<0> w = weight(i), p = post(i), c = gate(i);
+            float out[8], dg[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float th = in[i].t.at(e) * r, dz = in[i].dz.at(e), yh = in[i].y.at(e) * q;
+                sum[0][i][e] = __builtin_fmaf(dz, th, sum[0][i][e]);
+                d[i][e] = __builtin_fmaf(r, __builtin_fmaf(-th, mean, dz * w.at(e)), in[i].dt.at(e));
+                out[e] = g.scale * d[i][e];
+                dg[e] = d[i][e] * (yh * p.at(e));
+                if constexpr (!GATES) sum[2][i][e] += dg[e];
+                d[i][e] *= GATES ? in[i].gate.at(e) : c.at(e);       // dn
+                sum[1][i][e] = __builtin_fmaf(d[i][e], yh, sum[1][i][e]);
+                d[i][e] *= p.at(e);
+                dot[0] = __builtin_fmaf(d[i][e], yh, dot[0]);
+            }
+            store8<BF16>(g.t, row, tid + i * NT, H, out);
+            if constexpr (GATES) store8<BF16>(g.dgates, row, tid + i * NT, H, dg);
+        }
+        if (!g.y) continue;
+        if (g.post) {
+            row_sums<NT>(dot, part, turn);
+            const float m = dot[0] * inv;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[i][e] = q * __builtin_fmaf(-(in[i].y.at(e) * q), m, d[i][e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) store8<BF16>(g.z, row, tid + i * NT, H, d[i]);
+    }
+
+    // one partial row per workgroup; a workgroup's waves add theirs in order
+    if constexpr (ROWS > 1) {
+#pragma unroll
+        for (int w = 0; w < ROWS; ++w) {
+            if ((int)threadIdx.x / NT == w) {
+#pragma unroll
+                for (int a = 0; a < 3; ++a)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float *at = across + ((a * NV + i) * 8 + e) * NT + tid;
+                            if (w > 0) sum[a][i][e] += *at;
+                            *at = sum[a][i][e];
+                        }
+            }
+            __syncthreads();
+        }
+        if ((int)threadIdx.x / NT != ROWS - 1) return;
+    }
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        if (g.sums[a]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) store8<0>(g.sums[a] + blockIdx.x * g.pitch, 0, tid + i * NT, H, sum[a][i]);
+        }
+    }
+}
+
+// The partial rows added up: 64 channels a workgroup, 16 threads to a channel
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float *partials, int64_t n, int H, float *o0, float *o1,
+                                                         float *o2) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, a = blockIdx.y;
+    float *const out = a == 0 ? o0 : a == 1 ? o1 : o2;
+    const int col = blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (out && col < H) {
+        const float *p = partials + (int64_t)a * H + col;
+#pragma unroll 8
+        for (int64_t i = w; i < n; i += 16) s += p[i * 3 * H];
+    }
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && out && col < H) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += part[i][lane];
+        out[col] = s;
+    }
+}
+
+// calls f.run<NT, NV>() for rows of H elements
+template <class F>
+void for_length(int H, const F &f) {
+    if (H <= 512) f.template run<64, 1>();
+    else if (H <= 1024) f.template run<128, 1>();
+    else if (H <= 2048) f.template run<256, 1>();
+    else if (H <= 4096) f.template run<512, 1>();
+    else if (H <= 8192) f.template run<512, 2>();
+    else f.template run<512, 4>();
+}
+
+constexpr int64_t kCUs = 256;
+
+template <int BF16>
+struct Forward {
+    const NormArgs &a;
+    hipStream_t stream;
+    template <int NT, int NV>
+    void run() const {
+        constexpr int THREADS = NT * rows_of<NT>();
+        const int64_t need = (a.T + rows_of<NT>() - 1) / rows_of<NT>(), most = kCUs * (1024 / THREADS);
+        const dim3 grid((unsigned)(need < most ? need : most));
+        if (a.gates) residual_norm_kernel<BF16, NT, NV, 1><<<grid, dim3(THREADS), 0, stream>>>(a);
+        else residual_norm_kernel<BF16, NT, NV, 0><<<grid, dim3(THREADS), 0, stream>>>(a);
+    }
+};
+
+template <int BF16>
+struct Backward {
+    const NormArgs &a;
+    int64_t workgroups;
+    hipStream_t stream;
+    template <int NT, int NV>
+    void run() const {
+        const dim3 grid((unsigned)workgroups), block(NT * rows_of<NT>());
+        if (a.gates) residual_norm_grad_kernel<BF16, NT, NV, 1><<<grid, block, 0, stream>>>(a);
+        else residual_norm_grad_kernel<BF16, NT, NV, 0><<<grid, block, 0, stream>>>(a);
+    }
+};
+
+// Workgroups of the gradient, each of which leaves a partial row: one a CU, more only where each still
+// takes 32 rows (their partials are then some 6% of the rows' bytes).
+int64_t grad_workgroups(int64_t T, int64_t H) {
+    const int64_t need = H <= 512 ? (T + 3) / 4 : T;
+    const int64_t most = T / 32 > kCUs ? (T / 32 < 4 * kCUs ? T / 32 : 4 * kCUs) : kCUs;
+    return need < most ? need : most;
+}
+
+}  // namespace
+
+hipError_t launch_residual_norm(const void *x, const void *y, bool bf16, const float *weight, const float *post,
+                                const float *gate, const void *gates, float scale, float eps, void *t, void *z,
+                                int64_t T, int64_t H, hipStream_t stream) {
+    NormArgs a{};
+    a.x = x, a.y = y, a.weight = weight, a.post = post, a.gate = gate, a.gates = gates, a.scale = scale, a.eps = eps;
+    a.t = t, a.z = z, a.T = T, a.H = (int)H;
+    if (bf16) for_length((int)H, Forward<1>{a, stream});
+    else for_length((int)H, Forward<0>{a, stream});
+    return hipGetLastError();
+}
+
+size_t residual_norm_grad_workspace_bytes(int64_t T, int64_t H) {
+    const int64_t n = grad_workgroups(T, H);
+    return n > 1 ? (size_t)(n * 3 * H * 4) : 0;
+}
+
+hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const void *t, const void *y, bool bf16,
+                                         const float *weight, const float *post, const float *gate, const void *gates,
+                                         float scale, float eps, void *dx, void *dy, float *dweight, float *dpost,
+                                         float *dgate, void *dgates, int64_t T, int64_t H, void *workspace,
+                                         hipStream_t stream) {
+    NormArgs a{};
+    a.x = t, a.y = y, a.dt = dt, a.dz = dz, a.weight = weight, a.post = post, a.gate = gate, a.gates = gates;
+    a.scale = scale, a.eps = eps, a.t = dx, a.z = dy, a.dgates = dgates, a.T = T, a.H = (int)H;
+    const int64_t n = grad_workgroups(T, H);
+    float *const out[3] = {dweight, dpost, dgate}, *const partials = static_cast<float *>(workspace);
+    for (int i = 0; i < 3; ++i) a.sums[i] = out[i] ? (n > 1 ? partials + i * H : out[i]) : nullptr;
+    a.pitch = 3 * H;
+    if (n > 0) {
+        if (bf16) for_length((int)H, Backward<1>{a, n, stream});
+        else for_length((int)H, Backward<0>{a, n, stream});
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (n == 1 || !(dweight || dpost || dgate)) return hipSuccess;
+    // (with no rows the sums are zero)
+    norm_sums_kernel<<<dim3((unsigned)((H + 63) / 64), 3), dim3(1024), 0, stream>>>(partials, n, (int)H, dweight, dpost,
+                                                                                   dgate);
+    return hipGetLastError();
+}
+
+}  // namespace fp8q

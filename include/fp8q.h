@@ -37,7 +37,7 @@
  *     returns FP8Q_ERR_LAUNCH. Faults during execution surface at the caller's stream
  *     synchronisation. No C++ exception crosses this interface.
  *   - Sizes are int64_t. K must be a non-negative multiple of 128 (of 16 for the 8-bit integer
- *     calls; the routed-expert calls have rows of any length). A zero M or N (or, for
+ *     calls, of 8 for the dense block's; the routed-expert calls have rows of any length). A zero M or N (or, for
  *     the quantisers, K) is a valid empty call that enqueues nothing; null pointers are
  *     then allowed.
  *   - The calls are stateless and may be issued concurrently from several host threads.
@@ -55,13 +55,14 @@ extern "C" {
 /* Status codes. */
 #define FP8Q_OK 0
 #define FP8Q_ERR_NULL 1        /* a required pointer is NULL                                */
-#define FP8Q_ERR_SHAPE 2       /* negative size, K not a multiple of 128 (8-bit integers: 16), or too large */
+#define FP8Q_ERR_SHAPE 2       /* negative size, K not a multiple of 128 (8-bit integers: 16,
+                                  the dense block's calls: 8), or too large                  */
 #define FP8Q_ERR_ALIGN 3       /* pointer alignment below what the entry point requires     */
 #define FP8Q_ERR_DTYPE 4       /* unknown element type or flag                              */
 #define FP8Q_ERR_UNSUPPORTED 5 /* no gfx950 device is current                               */
 #define FP8Q_ERR_LAUNCH 6      /* the kernel launch failed                                  */
 #define FP8Q_ERR_WORKSPACE 7   /* more scratch needed than fp8_block_gemm_noalloc holds, or
-                                  a workspace smaller than moe_place or int8_linear need    */
+                                  a workspace smaller than the call's _workspace_bytes      */
 
 /* Output dtypes of fp8_block_gemm (low 8 bits of its y_dtype argument). */
 #define FP8Q_OUT_F32 0
@@ -369,6 +370,91 @@ size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int int8_grouped_gemm(const int8_t *a, const float *sa, const int8_t *w, const float *sw, const int64_t *offsets,
                       const int32_t *rows, void *y, int y_dtype, int64_t experts, int64_t M, int64_t tokens, int64_t N,
                       int64_t K, void *stream);
+
+/* ---- The dense block around the linear layers ------------------------------------------
+ * Norms before and after a block with its gate and the residual, gated projections, and
+ * linear layers with an adapter per token, each with the gradient that training needs (the
+ * adapters serve only). Element types (dtype) are FP8Q_OUT_F32 or FP8Q_OUT_BF16.
+ * (pomoai.com "DeepSeek-V3", the list of model classes: RMSNorm, the gated feed-forward and
+ * the block's residual additions stay in higher precision around the FP8 products.) */
+
+/* Flag of residual_norm and residual_norm_backward. */
+#define FP8Q_NORM_GATES 1      /* gate is [T, H] of type dtype (default: [H] fp32)               */
+
+/* residual_norm -- t = scale * x + gate * n, z = norm(t) * weight, with norm(v) = v / sqrt(mean(v^2)
+ * + eps) over a row and n = norm(y) * post, or y where post is NULL.
+ *   x, y, t, z [T, H] of type dtype; weight, post [H] fp32; gate [H] fp32, or [T, H] of type
+ *   dtype (FP8Q_NORM_GATES), or NULL for 1. With y NULL t is scale * x (post and gate are not
+ *   read). With weight NULL z is not written; t may be NULL where weight is not.
+ *   Squares are summed and every step is taken in fp32; z is formed from t before t's
+ *   rounding. 8 <= H <= 16384. Any alignment of the element type (16-byte rows are faster).
+ *   t may be x (a residual stream updated in place). */
+int residual_norm(const void *x, const void *y, int dtype, const float *weight, const float *post, const void *gate,
+                  int flags, float scale, float eps, void *t, void *z, int64_t T, int64_t H, void *stream);
+
+/* residual_norm_backward -- its gradient at t [T, H] (as residual_norm wrote it) and y.
+ *   dt [T, H]: the gradient with respect to t besides the one through z, or NULL for none; dz [T, H]
+ *      with respect to z, and weight (both NULL where the forward call had no weight; t is then
+ *      not read).
+ *   dx [T, H]; dy [T, H] (not written where y is NULL); fp32 [H]: dweight, dpost (not written
+ *   where weight, post is NULL), dgate (where gate is NULL not written; with FP8Q_NORM_GATES
+ *   [T, H] of type dtype). The sums over the rows are fp32, in a fixed order.
+ *   workspace: residual_norm_backward_workspace_bytes bytes of any contents, 16-byte aligned (NULL
+ *   where that is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at
+ *   the same time must not share it. T = 0 still writes the sums (all zero). */
+int residual_norm_backward(const void *dt, const void *dz, const void *t, const void *y, int dtype, const float *weight,
+                           const float *post, const void *gate, int flags, float scale, float eps, void *dx, void *dy,
+                           float *dweight, float *dpost, void *dgate, int64_t T, int64_t H, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t residual_norm_backward_workspace_bytes(int64_t T, int64_t H);
+
+/* Activations of gated_linear. */
+#define FP8Q_ACT_SILU 0        /* a / (1 + exp(-a))                                              */
+#define FP8Q_ACT_GELU 1        /* a * Phi(a), Phi the normal distribution (not its tanh form)    */
+
+/* gated_linear -- h = act(x Wg^T) * (x Wu^T), w = [Wg; Wu]: both projections of a feed-forward
+ * block, the activation and the product in one kernel.
+ *   x [M, K] and w [2 F, K] bf16 (16-byte aligned): rows 0 .. F - 1 of w are the gate's, the
+ *   others the up-projection's. h [M, F] of type h_dtype (4-byte aligned); gu [M, 2 F] bf16 (4-byte aligned), or
+ *   NULL: both projections, rounded, for gated_linear_backward.
+ *   K and F are multiples of 8, K < 2^23, F < 2^22, M <= 2^26. Products are exact in fp32 and summed in
+ *   fp32; activation and product are fp32 on the sums, rounded once. With K = 0 h is zeros. */
+int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uint16_t *gu, int act, int64_t M,
+                 int64_t F, int64_t K, void *stream);
+
+/* gated_linear_backward -- from dh [M, F] bf16: dx [M, K] of type dx_dtype and dw [2 F, K] of type
+ * dw_dtype (either may be NULL: not wanted).
+ *   gu as gated_linear wrote it, or NULL: the projections are computed again. The gradient of
+ *   the projections is rounded to bf16 (the matrix unit's type) on its way into dx and dw, whose
+ *   sums are fp32. dh, x, w, gu 16-byte aligned, dx and dw 4-byte.
+ *   workspace: gated_linear_backward_workspace_bytes bytes of any contents, 16-byte aligned (NULL
+ *   where that is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at
+ *   the same time must not share it. M = 0 still writes dw (zeros). */
+int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
+                          int dx_dtype, void *dw, int dw_dtype, int64_t M, int64_t F, int64_t K, void *workspace,
+                          size_t workspace_bytes, void *stream);
+size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F);
+
+/* adapter_linear -- y[m] = x[m] w^T + bias + scales[e] (x[m] a[e]^T) b[e]^T, e = ids[m]: a linear layer
+ * whose rows each have a low-rank adapter of their own (requests of many adapters in a batch).
+ *   x [M, K] bf16; w [N, K] bf16 (16-byte aligned both); bias [N] fp32 or NULL;
+ *   a [adapters, rank, K] and b [adapters, N, rank] bf16 (16-byte aligned); scales [adapters] fp32, or NULL
+ *   for 1; ids [M] int32 on the device: rows whose id is outside [0, adapters) have no adapter.
+ *   y [M, N] of type y_dtype (4-byte aligned).
+ *   With w NULL base [M, N] of type y_dtype takes the place of x w^T (the output of another
+ *   projection: FP8, 8-bit integers); it may be y itself.
+ *   K a multiple of 8 below 2^23, rank of 8 up to 256 (adapters of lower ranks padded with zeros),
+ *   adapters < 2^31, M <= 2^26, N <= 2^28. x a^T is kept in fp32 and enters the second product
+ *   with all its bits; sums are fp32, rounded once. What an adapter holds (infinities, NaN) reaches
+ *   only the rows that name it.
+ *   workspace: adapter_linear_workspace_bytes bytes of any contents, 16-byte aligned (NULL where
+ *   adapters is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at the
+ *   same time must not share it. */
+int adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a, const uint16_t *b,
+                   const float *scales, const int32_t *ids, const void *base, void *y, int y_dtype, int64_t M,
+                   int64_t N, int64_t K, int64_t adapters, int64_t rank, void *workspace, size_t workspace_bytes,
+                   void *stream);
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank);
 
 /* Workspace size in bytes that lets fp8_block_gemm use its split-K schedule for this
  * shape and y_dtype (including the mode bits); 0 if that call does not use one or the
