@@ -17,6 +17,8 @@
 // than the rows themselves), the next row's loads are on their way while a row is reduced, and the
 // gradient's sums over the rows are carried in registers. Squares, sums and every step are fp32; t
 // enters the second norm before its rounding. Outputs round once. The order of every sum is fixed.
+// 16384 x 7168 bf16 177 us, 5.3 TB/s (a copy of 1 GB: 5.15); the gradient of 4096 x 7168 94 us, 3.7 TB/s, of
+// 16384 x 2048 82 us, 4.9 TB/s.
 #include <fp8q.h>
 
 #include "device_common.h"
@@ -54,25 +56,27 @@ struct Raw {
     }
 };
 
-// Piece p of a row of H >= 8 elements. A row's last piece, where it is short, is the row's last 8
-// elements with those before the piece shifted out; what lies past the row counts as zeros.
+// Piece p of a row of H >= 8 elements, in two steps: a load that needs no branch (from the row's last 8
+// elements where the piece is short or past the end), and, once it is there, what lies before the piece shifted out
+// and zeros put past the row's end. (Done at once, the wait for the load would come before the work that is to hide it.)
 template <int BF16>
 __device__ __forceinline__ Raw<BF16> load8(const void *base, int64_t row, int p, int H) {
-    constexpr int N = BF16 ? 1 : 2;
-    Raw<BF16> r;
-#pragma unroll
-    for (int h = 0; h < N; ++h) r.v[h] = u32x4{0, 0, 0, 0};
-    if (8 * p >= H) return r;
     const uint32_t off = 8 * p + 8 <= H ? 8 * p : H - 8;
     const char *from = static_cast<const char *>(base) + row * H * (BF16 ? 2 : 4);
+    Raw<BF16> r;
 #pragma unroll
-    for (int h = 0; h < N; ++h)
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h)
         r.v[h] = *reinterpret_cast<const u32x4_any *>(from + (uint32_t)(off * (BF16 ? 2 : 4) + 16 * h));
-    const int s = 8 * p - (int)off;
-    if (s) {
+    return r;
+}
+template <int BF16>
+__device__ __forceinline__ Raw<BF16> settle(Raw<BF16> r, int p, int H) {
+    constexpr int N = BF16 ? 1 : 2;
+    const int s = 8 * p + 8 - H;   // elements past the end
+    if (s > 0) {
         uint32_t u[4 * N];
 #pragma unroll
-        for (int i = 0; i < 4 * N; ++i) u[i] = r.v[i / 4][i % 4];
+        for (int i = 0; i < 4 * N; ++i) u[i] = s >= 8 ? 0 : r.v[i / 4][i % 4];
 #pragma unroll
         for (int bit = 4; bit; bit >>= 1) {
             const int words = BF16 ? bit / 2 : bit;   // (half a word last, of bf16)
@@ -131,7 +135,7 @@ struct Channels {
         }
     }
     __device__ __forceinline__ Raw<0> read(int i) const {
-        if (v) return load8<0>(v, 0, tid + i * NT, H);
+        if (v) return settle<0>(load8<0>(v, 0, tid + i * NT, H), tid + i * NT, H);
         Raw<0> r;
         r.v[0] = r.v[1] = u32x4{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
         return r;
@@ -142,14 +146,28 @@ struct Channels {
     }
 };
 
+// The sum over a wave, in every lane: 16 lanes by DPP moves, then the four 16s
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v += moved<0xB1>(v);    // quad_perm [1,0,3,2]
+    v += moved<0x4E>(v);    // quad_perm [2,3,0,1]
+    v += moved<0x141>(v);   // row_half_mirror
+    v += moved<0x140>(v);   // row_mirror
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
 // Sums of N values over the NT threads of a row, the same bits in all of them. `turn` alternates: the
 // values of one call stay readable until every thread is past the barrier of the next.
 template <int NT, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[3][NT / 64], int &turn) {
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-#pragma unroll
-        for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], m, 64);
+    for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -203,11 +221,15 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormA
         Raw<BF16> gates[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (GATES) gates[i] = gt[i];
+            const int p = tid + i * NT;
+            if constexpr (GATES) gates[i] = settle(gt[i], p, H);
+            const Raw<BF16> xs = settle(x[i], p, H);
+            Raw<BF16> ys;
+            if (g.y) ys = settle(y[i], p, H);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                t[i][e] = g.scale * x[i].at(e);
-                n[i][e] = g.y ? y[i].at(e) : 0.0f;
+                t[i][e] = g.scale * xs.at(e);
+                n[i][e] = g.y ? ys.at(e) : 0.0f;
             }
         }
         if (AHEAD && row + step < g.T) load(row + step);
@@ -253,12 +275,47 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormA
     }
 }
 
+// The same in LDS, for the gradient, whose sums over the rows take the registers: 16 bytes of each of a
+// wave's lanes side by side, which meets no bank conflict. Without HOLD (rows too long) read again.
+template <int NT, int NV, bool HOLD>
+struct SharedChannels {
+    f32x4 *at;
+    const float *v;
+    int tid, H;
+    static constexpr int SIZE = HOLD ? 2 * NT * NV : 1;
+    __device__ __forceinline__ SharedChannels(f32x4 *lds, const float *v_, int tid_, int H_) : at(lds), v(v_), tid(tid_), H(H_) {
+        if constexpr (HOLD) {   // (a workgroup's waves write the same where each has a row)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Raw<0> r = Channels<NT, NV, false>(v, tid, H).read(i);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) at[(2 * i + h) * NT + tid] = __builtin_bit_cast(f32x4, r.v[h]);
+            }
+        }
+    }
+    __device__ __forceinline__ f32x4 operator()(int i, int h) const {   // half h of piece i
+        if constexpr (HOLD) return at[(2 * i + h) * NT + tid];
+        else return __builtin_bit_cast(f32x4, Channels<NT, NV, false>(v, tid, H).read(i).v[h]);
+    }
+};
+
+// keeps the compiler from holding what it has computed from v: that is computed again from v instead
+template <int BF16>
+__device__ __forceinline__ void forget(Raw<BF16> &v) {
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) asm volatile("" : "+v"(v.v[h]));
+}
+
 // The gradient. The sums over the rows leave as one partial row per workgroup, which a second kernel
 // adds up (with one workgroup they are the sums).
 template <int BF16, int NT, int NV, int GATES>
 __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(NormArgs g) {
     constexpr int ROWS = rows_of<NT>();
-    constexpr bool AHEAD = NV == 1 || (NV == 2 && BF16);
+    // a row's inputs stay in registers (where they fit), the next row's are on their way; else they are read
+    // again for each use, from the caches
+    constexpr bool KEEP = NT * NV <= 1024, AHEAD = KEEP && (NV == 1 || BF16);
+    typedef SharedChannels<NT, NV, KEEP> Vector;
+    __shared__ f32x4 channels[3][Vector::SIZE];
     __shared__ float part[2][3][NT / 64];
     __shared__ float across[ROWS > 1 ? 3 * NT * NV * 8 : 1];
     const int tid = threadIdx.x % NT, H = g.H;
@@ -270,29 +327,34 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
     struct Inputs {
         Raw<BF16> t, dz, dt, y, gate;
     };
-    Inputs next[NV];
+    Inputs next[AHEAD ? NV : 1];
     const bool need_y = g.y && (g.post || g.sums[2] || GATES);
-    auto load = [&](int64_t m) {
+    auto read = [&](int64_t m, int i) {
+        Inputs p;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (g.weight) {
-                next[i].t = load8<BF16>(g.x, m, tid + i * NT, H);
-                next[i].dz = load8<BF16>(g.dz, m, tid + i * NT, H);
-            }
-            if (g.dt) next[i].dt = load8<BF16>(g.dt, m, tid + i * NT, H);
-            if (need_y) next[i].y = load8<BF16>(g.y, m, tid + i * NT, H);
-            if constexpr (GATES) next[i].gate = load8<BF16>(g.gates, m, tid + i * NT, H);
+        for (int h = 0; h < (BF16 ? 1 : 2); ++h)   // what is not there counts as zeros
+            p.t.v[h] = p.dz.v[h] = p.dt.v[h] = p.y.v[h] = p.gate.v[h] = u32x4{0, 0, 0, 0};
+        if (g.weight) {
+            p.t = load8<BF16>(g.x, m, tid + i * NT, H);
+            p.dz = load8<BF16>(g.dz, m, tid + i * NT, H);
         }
+        if (g.dt) p.dt = load8<BF16>(g.dt, m, tid + i * NT, H);
+        if (need_y) p.y = load8<BF16>(g.y, m, tid + i * NT, H);
+        if constexpr (GATES) p.gate = load8<BF16>(g.gates, m, tid + i * NT, H);
+        return p;
     };
+    auto settled = [&](Inputs p, int i) {
+        const int at = tid + i * NT;
+        p.t = settle(p.t, at, H), p.dz = settle(p.dz, at, H), p.dt = settle(p.dt, at, H), p.y = settle(p.y, at, H);
+        if constexpr (GATES) p.gate = settle(p.gate, at, H);
+        return p;
+    };
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int h = 0; h < (BF16 ? 1 : 2); ++h) {   // what is not there counts as zeros
-            const u32x4 zero = {0, 0, 0, 0};
-            next[i].t.v[h] = next[i].dz.v[h] = next[i].dt.v[h] = next[i].y.v[h] = next[i].gate.v[h] = zero;
-        }
-    if (AHEAD && row < g.T) load(row);
-    const Channels<NT, NV, AHEAD> weight(g.weight, tid, H), post(g.post, tid, H), gate(g.gate, tid, H);
+        for (int i = 0; i < NV; ++i)
+            if (row < g.T) next[i] = read(row, i);
+    }
+    const Vector weight(channels[0], g.weight, tid, H), post(channels[1], g.post, tid, H), gate(channels[2], g.gate, tid, H);
     float sum[3][NV][8];
 #pragma unroll
     for (int a = 0; a < 3; ++a)
@@ -302,58 +364,102 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
             for (int e = 0; e < 8; ++e) sum[a][i][e] = 0.0f;
 
     for (; row < g.T; row += step) {
-        if constexpr (!AHEAD) load(row);
-        Inputs in[NV];
+        Inputs in[KEEP ? NV : 1];
+        if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) in[i] = next[i];
-        if (AHEAD && row + step < g.T) load(row + step);
+            for (int i = 0; i < NV; ++i) {
+                in[i] = settled(AHEAD ? next[AHEAD ? i : 0] : read(row, i), i);
+            }
+        }
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (row + step < g.T) next[i] = read(row + step, i);
+        }
+        auto inputs = [&](int i) {
+            if constexpr (KEEP) {
+                if constexpr (BF16) forget(in[i].t), forget(in[i].dz), forget(in[i].y);
+                return in[i];
+            } else {
+                return settled(read(row, i), i);
+            }
+        };
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Raw<0> w = weight(i);
+            const Inputs p = inputs(i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float t = in[i].t.at(e), y = in[i].y.at(e);
-                s[0] = __builtin_fmaf(t, t, s[0]);
-                s[1] = __builtin_fmaf(in[i].dz.at(e) * w.at(e), t, s[1]);
-                s[2] = __builtin_fmaf(y, y, s[2]);
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 w = weight(i, h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float t = p.t.at(4 * h + e), y = p.y.at(4 * h + e);
+                    s[0] = __builtin_fmaf(t, t, s[0]);
+                    s[1] = __builtin_fmaf(p.dz.at(4 * h + e) * w[e], t, s[1]);
+                    s[2] = __builtin_fmaf(y, y, s[2]);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);   // a piece at a time, which takes fewer registers
         }
         row_sums<NT>(s, part, turn);
         const float r = g.weight ? 1.0f / __builtin_sqrtf(s[0] * inv + g.eps) : 0.0f, mean = s[1] * inv * r;
         const float q = g.post ? 1.0f / __builtin_sqrtf(s[2] * inv + g.eps) : 1.0f;
-        float d[NV][8], dot[1] = {0.0f};
+        // the gradient with respect to t
+        auto slope = [&](const Inputs &p, int e, float w) {
+            return __builtin_fmaf(r, __builtin_fmaf(-(p.t.at(e) * r), mean, p.dz.at(e) * w), p.dt.at(e));
+        };
+        float d[KEEP ? NV : 1][8], dot[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Raw<0> w = weight(i), p = post(i), c = gate(i);
-            float out[8], dg[8];
+            const Inputs p = inputs(i);
+            float out[8], dg[8], dn[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float th = in[i].t.at(e) * r, dz = in[i].dz.at(e), yh = in[i].y.at(e) * q;
-                sum[0][i][e] = __builtin_fmaf(dz, th, sum[0][i][e]);
-                d[i][e] = __builtin_fmaf(r, __builtin_fmaf(-th, mean, dz * w.at(e)), in[i].dt.at(e));
-                out[e] = g.scale * d[i][e];
-                dg[e] = d[i][e] * (yh * p.at(e));
-                if constexpr (!GATES) sum[2][i][e] += dg[e];
-                d[i][e] *= GATES ? in[i].gate.at(e) : c.at(e);       // dn
-                sum[1][i][e] = __builtin_fmaf(d[i][e], yh, sum[1][i][e]);
-                d[i][e] *= p.at(e);
-                dot[0] = __builtin_fmaf(d[i][e], yh, dot[0]);
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 w = weight(i, h), b = post(i, h), c = gate(i, h);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int e = 4 * h + f;
+                    const float yh = p.y.at(e) * q, v = slope(p, e, w[f]);
+                    sum[0][i][e] = __builtin_fmaf(p.dz.at(e), p.t.at(e) * r, sum[0][i][e]);
+                    out[e] = g.scale * v;
+                    dg[e] = v * (yh * b[f]);
+                    if constexpr (!GATES) sum[2][i][e] += dg[e];
+                    dn[e] = v * (GATES ? p.gate.at(e) : c[f]);
+                    sum[1][i][e] = __builtin_fmaf(dn[e], yh, sum[1][i][e]);
+                    dn[e] *= b[f];
+                    dot[0] = __builtin_fmaf(dn[e], yh, dot[0]);
+                    if constexpr (KEEP) d[i][e] = dn[e];
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
             store8<BF16>(g.t, row, tid + i * NT, H, out);
             if constexpr (GATES) store8<BF16>(g.dgates, row, tid + i * NT, H, dg);
         }
         if (!g.y) continue;
+        float m = 0.0f;
         if (g.post) {
             row_sums<NT>(dot, part, turn);
-            const float m = dot[0] * inv;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[i][e] = q * __builtin_fmaf(-(in[i].y.at(e) * q), m, d[i][e]);
+            m = dot[0] * inv;
         }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) store8<BF16>(g.z, row, tid + i * NT, H, d[i]);
+        for (int i = 0; i < NV; ++i) {
+            const Inputs p = inputs(i);
+            float out[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4 w, b, c;
+                if constexpr (!KEEP) w = weight(i, h), b = post(i, h), c = gate(i, h);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int e = 4 * h + f;
+                    float dn;
+                    if constexpr (KEEP) dn = d[i][e];
+                    else dn = slope(p, e, w[f]) * (GATES ? p.gate.at(e) : c[f]) * b[f];
+                    out[e] = g.post ? q * __builtin_fmaf(-(p.y.at(e) * q), m, dn) : dn;
+                }
+            }
+            store8<BF16>(g.z, row, tid + i * NT, H, out);
+        }
     }
 
     // one partial row per workgroup; a workgroup's waves add theirs in order
@@ -407,15 +513,15 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *partials, 
     }
 }
 
-// calls f.run<NT, NV>() for rows of H elements
-template <class F>
+// calls f.run<NT, NV>() for rows of H elements; those above 4096 by MID threads, above 8192 by LONG
+template <int MID, int LONG, class F>
 void for_length(int H, const F &f) {
     if (H <= 512) f.template run<64, 1>();
     else if (H <= 1024) f.template run<128, 1>();
     else if (H <= 2048) f.template run<256, 1>();
     else if (H <= 4096) f.template run<512, 1>();
-    else if (H <= 8192) f.template run<512, 2>();
-    else f.template run<512, 4>();
+    else if (H <= 8192) f.template run<MID, 8192 / 8 / MID>();
+    else f.template run<LONG, 16384 / 8 / LONG>();
 }
 
 constexpr int64_t kCUs = 256;
@@ -447,11 +553,12 @@ struct Backward {
     }
 };
 
-// Workgroups of the gradient, each of which leaves a partial row: one a CU, more only where each still
-// takes 32 rows (their partials are then some 6% of the rows' bytes).
+// Workgroups of the gradient, each of which leaves a partial row: as many as run at once, where that is worth
+// their partials. us with 256 / 512 / 1024 of them, bf16: 4096 x 7168 94 / 103 / 129, 4096 x 2048 34 / 28 / 32,
+// 4096 x 1024 33 / 24 / 21, 16384 x 512 30 / 26 / 29, 1024 x 1091 15 / 16 / 22.
 int64_t grad_workgroups(int64_t T, int64_t H) {
     const int64_t need = H <= 512 ? (T + 3) / 4 : T;
-    const int64_t most = T / 32 > kCUs ? (T / 32 < 4 * kCUs ? T / 32 : 4 * kCUs) : kCUs;
+    const int64_t most = H > 2048 ? kCUs : H > 512 && H <= 1024 && T >= 4096 ? 4 * kCUs : T >= 1536 ? 2 * kCUs : kCUs;
     return need < most ? need : most;
 }
 
@@ -463,8 +570,8 @@ hipError_t launch_residual_norm(const void *x, const void *y, bool bf16, const f
     NormArgs a{};
     a.x = x, a.y = y, a.weight = weight, a.post = post, a.gate = gate, a.gates = gates, a.scale = scale, a.eps = eps;
     a.t = t, a.z = z, a.T = T, a.H = (int)H;
-    if (bf16) for_length((int)H, Forward<1>{a, stream});
-    else for_length((int)H, Forward<0>{a, stream});
+    if (bf16) for_length<1024, 1024>((int)H, Forward<1>{a, stream});
+    else for_length<1024, 1024>((int)H, Forward<0>{a, stream});
     return hipGetLastError();
 }
 
@@ -486,8 +593,8 @@ hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const v
     for (int i = 0; i < 3; ++i) a.sums[i] = out[i] ? (n > 1 ? partials + i * H : out[i]) : nullptr;
     a.pitch = 3 * H;
     if (n > 0) {
-        if (bf16) for_length((int)H, Backward<1>{a, n, stream});
-        else for_length((int)H, Backward<0>{a, n, stream});
+        if (bf16) for_length<512, 512>((int)H, Backward<1>{a, n, stream});
+        else for_length<512, 512>((int)H, Backward<0>{a, n, stream});
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (n == 1 || !(dweight || dpost || dgate)) return hipSuccess;
