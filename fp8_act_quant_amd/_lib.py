@@ -78,7 +78,7 @@ SIGNATURES = {
     "gated_linear_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "adapter_linear": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t,
                               _P]),
-    "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "fp8q_gemm_force_config": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "fp8q_gemm_config_name": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8q_gemm_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, _P, _P]),

@@ -21,16 +21,18 @@
 namespace fp8q {
 namespace {
 
+constexpr int kMaxSplits = 8;   // parts of K in the adapters' first product
+
 struct AdapterArgs {
     MmArgs mm;
     const float *bias;       // [N] or null
     const uint16_t *a, *b;   // [adapters, rank, K], [adapters, N, rank]
     const float *scales;     // [adapters] or null
     const int32_t *ids;      // [M]
-    float *u;                // [M, rank]
+    float *u;                // [splits, M, rank]
     const void *base;        // [M, N] of y's type: added instead of a product with W
     void *y;
-    int adapters, rank;
+    int adapters, rank, splits;
 };
 
 // an adapter's number, -1 where there is none
@@ -39,77 +41,132 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs &g, int64_t m) {
     return e >= 0 && e < g.adapters ? e : -1;
 }
 
-// u of 16 RG rows: WAVES waves take a part of K each, the operands straight from memory (16 bytes a lane),
-// and their sums are added in LDS, in order. The rows' adapters are taken one after another, workgroup
-// blockIdx.y those numbered blockIdx.y, blockIdx.y + gridDim.y, ... among them. RB blocks of 16 ranks at a time.
-template <int RG, int RB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void adapter_shrink_kernel(AdapterArgs g) {
-    constexpr int U = RG + RB <= 2 ? 4 : 2;   // steps of 64 k on their way
-    __shared__ f32x4 part[WAVES][RG * RB][64];
+// u in two ways. K is cut into `splits` parts, whose sums are kept apart (u[part]) and added where u is used.
+//
+// Few rows, which may all have different adapters: a workgroup takes one row and one part of K, its 4 waves a
+// quarter of that each, A straight from memory into the matrix unit's registers (16 RB ranks at a time), whose
+// other operand is the row 16 times. Bound by latency and the reads of A.
+template <int RB>
+__global__ __launch_bounds__(256) void adapter_row_kernel(AdapterArgs g) {
+    constexpr int U = RB == 1 ? 4 : 2;   // steps of 64 k on their way
+    __shared__ f32x4 part[4][RB][4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * RG), K = g.mm.K;
-    const int id = lane < 16 * RG ? adapter_of(g, m0 + lane) : -1;
-    const int64_t rows = g.mm.M - m0 < 16 * RG ? g.mm.M - m0 : 16 * RG;
-    const rsrc_t rx = make_rsrc(g.mm.x + m0 * K, 2 * rows * K);
-    const int steps = (int)((K + KSTEP - 1) / KSTEP), s0 = wave * steps / WAVES, s1 = (wave + 1) * steps / WAVES;
+    const int64_t m = blockIdx.x, K = g.mm.K;
+    const int e = adapter_of(g, m);
+    if (e < 0) return;
+    const rsrc_t rx = make_rsrc(g.mm.x + m * K, 2 * K), ra = make_rsrc(g.a + (int64_t)e * g.rank * K, 2 * g.rank * K);
+    const int steps = (int)((K + KSTEP - 1) / KSTEP), parts = 4 * g.splits, p = 4 * blockIdx.y + wave;
+    const int s0 = (int)((int64_t)p * steps / parts), s1 = (int)((int64_t)(p + 1) * steps / parts);
     const uint32_t pitch = (uint32_t)(2 * K);
+    for (int r0 = 0; r0 < g.rank; r0 += 16 * RB) {
+        f32x4 acc[RB];
+#pragma unroll
+        for (int j = 0; j < RB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int s = s0; s < s1; s += U) {
+            u32x4 xf[U][2], af[U][2][RB];
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t k = (uint32_t)((s + v) * KB + 64 * h + 16 * kg);
+                    const bool in = s + v < s1 && k < pitch;
+                    xf[v][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? k : kNowhere, 0, 0));
+#pragma unroll
+                    for (int j = 0; j < RB; ++j) {
+                        const int r = r0 + 16 * j + row;
+                        af[v][h][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                            ra, in && r < g.rank ? r * pitch + k : kNowhere, 0, 0));
+                    }
+                }
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < RB; ++j) acc[j] = mfma_bf16(af[v][h][j], xf[v][h], acc[j]);
+        }
+        __syncthreads();
+        if (row == 0) {
+#pragma unroll
+            for (int j = 0; j < RB; ++j) part[wave][j][kg] = acc[j];
+        }
+        __syncthreads();
+        const int r = r0 + 4 * (int)threadIdx.x;
+        if (threadIdx.x < 4 * RB && r < g.rank) {
+            f32x4 sum = part[0][threadIdx.x / 4][threadIdx.x % 4];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) sum += part[w][threadIdx.x / 4][threadIdx.x % 4];
+            const float scale = g.scales ? g.scales[e] : 1.0f;
+            *reinterpret_cast<f32x4 *>(g.u + ((int64_t)blockIdx.y * g.mm.M + m) * g.rank + r) = sum * scale;
+        }
+    }
+}
+
+// Many rows: tiles of 32 rows x 64 ranks (mm.h), for each of the rows' adapters, of which workgroup
+// blockIdx.z takes those numbered blockIdx.z, blockIdx.z + gridDim.z, ...: mostly there is one.
+using ShrinkTile = Tile<32, 64, 4, 2, 6>;
+__global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterArgs g) {
+    using T = ShrinkTile;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * T::NSTAGE];
+    const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
+    const int64_t m0 = (int64_t)blockIdx.x * T::BM, K = g.mm.K;
+    const int steps = (int)((K + KSTEP - 1) / KSTEP), blocks = (g.rank + T::BN - 1) / T::BN;
+    const int part = blockIdx.y / blocks, r0 = (blockIdx.y - part * blocks) * T::BN;
+    const int64_t k0 = (int64_t)part * steps / g.splits * KSTEP, k1 = (int64_t)(part + 1) * steps / g.splits * KSTEP;
+    MmArgs mm = g.mm;
+    mm.x += k0;
+    mm.N = g.rank;
+    mm.K = (k1 < K ? k1 : K) - k0;
+    const int id = lane < T::BM ? adapter_of(g, m0 + lane) : -1;
     int number = 0;
     for (uint64_t left = __ballot(id >= 0); left; ++number) {
         const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         left &= ~__ballot(id == e);
-        if (number % gridDim.y != blockIdx.y) continue;
-        const rsrc_t ra = make_rsrc(g.a + (int64_t)e * g.rank * K, 2 * g.rank * K);
-        for (int r0 = 0; r0 < g.rank; r0 += 16 * RB) {
-            f32x4 acc[RG][RB];
+        if (number % gridDim.z != blockIdx.z) continue;
+        mm.w = g.a + (int64_t)e * g.rank * K + k0;
+        f32x4 acc[T::SUB_M][T::SUB_N];
+        multiply<T, 0, 0, 0, 2>(mm, m0, r0, smem, acc, []() {});
+        const float scale = g.scales ? g.scales[e] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < RG; ++i)
+        for (int i = 0; i < T::SUB_M; ++i) {
+            const int within = T::row(wm, i) + (lane & 15);
+            if (__shfl(id, within, 64) != e) continue;
 #pragma unroll
-                for (int j = 0; j < RB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int s = s0; s < s1; s += U) {
-                u32x4 xf[U][2][RG], af[U][2][RB];
-#pragma unroll
-                for (int v = 0; v < U; ++v)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t k = (uint32_t)((s + v) * KB + 64 * h + 16 * kg);
-                        const bool in = s + v < s1 && k < pitch;
-#pragma unroll
-                        for (int i = 0; i < RG; ++i)
-                            xf[v][h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                rx, in ? (16 * i + row) * pitch + k : kNowhere, 0, 0));
-#pragma unroll
-                        for (int j = 0; j < RB; ++j)
-                            af[v][h][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                ra, in && r0 + 16 * j + row < g.rank ? (r0 + 16 * j + row) * pitch + k : kNowhere, 0, 0));
-                    }
-#pragma unroll
-                for (int v = 0; v < U; ++v)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < RG; ++i)
-#pragma unroll
-                            for (int j = 0; j < RB; ++j) acc[i][j] = mfma_bf16(af[v][h][j], xf[v][h][i], acc[i][j]);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < RG; ++i)
-#pragma unroll
-                for (int j = 0; j < RB; ++j) part[wave][i * RB + j][lane] = acc[i][j];
-            __syncthreads();
-            const float scale = g.scales ? g.scales[e] : 1.0f;
-            for (int b = wave; b < RG * RB; b += WAVES) {
-                f32x4 sum = part[0][b][lane];
-#pragma unroll
-                for (int w = 1; w < WAVES; ++w) sum += part[w][b][lane];
-                const int within = 16 * (b / RB) + row, r = r0 + 16 * (b % RB) + 4 * kg;
-                if (__shfl(id, within, 64) == e && r < g.rank)
-                    *reinterpret_cast<f32x4 *>(g.u + (m0 + within) * g.rank + r) = sum * scale;
+            for (int j = 0; j < T::SUB_N; ++j) {
+                const int r = r0 + wn * T::WN + 16 * j + 4 * (lane >> 4);
+                if (r < g.rank)
+                    *reinterpret_cast<f32x4 *>(g.u + ((int64_t)part * g.mm.M + m0 + within) * g.rank + r) = acc[i][j] * scale;
             }
         }
     }
+}
+
+// 32 ranks of the u of ROWS rows into LDS (fp32, pitch UP), the parts of K added in order; zeros past the rank
+// and where a row has no adapter. Read by each lane for itself from memory they took longer than all
+// else that an adapter costs (1021 x 1533, 8 parts: 27 us, now 7). Between two barriers.
+constexpr int kChunk = 32, UP = kChunk + 4;
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void stage_u(const AdapterArgs &g, int64_t m0, int r0, float *lds) {
+    __syncthreads();
+    for (int p = threadIdx.x; p < ROWS * (kChunk / 4); p += THREADS) {
+        const int row = p / (kChunk / 4), r = r0 + 4 * (p % (kChunk / 4));
+        const int64_t m = m0 + row;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (r < g.rank && adapter_of(g, m) >= 0) {
+            const float *from = g.u + m * g.rank + r;
+            f32x4 part[kMaxSplits];
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                part[s] = s < g.splits ? *reinterpret_cast<const f32x4 *>(from + s * g.mm.M * g.rank) : f32x4{0.f, 0.f, 0.f, 0.f};
+            v = part[0];
+#pragma unroll
+            for (int s = 1; s < kMaxSplits; ++s) v += part[s];
+        }
+        *reinterpret_cast<f32x4 *>(lds + row * UP + 4 * (p % (kChunk / 4))) = v;
+    }
+    __syncthreads();
 }
 
 // Three bf16 numbers whose sum is v: two cut off (exactly, whatever v is) and the rest, which has 8 bits.
@@ -125,67 +182,75 @@ __device__ __forceinline__ void split3(float v, uint32_t &a, uint32_t &b, uint32
 }
 
 // Adds the adapters' part to a wave's sums by the matrix unit: each 16-row group's adapters one after another,
-// mostly one. col: the wave's first column.
+// mostly one. col: the wave's first column. For the whole workgroup.
 template <class T>
-__device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, int64_t col, f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
+__device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, int64_t col, float *lds,
+                                             f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
     const int lane = threadIdx.x & 63, wm = wave_m<T>(), row = lane & 15, kg = lane >> 4;
+    for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
+        stage_u<T::BM, T::NW * 64>(g, m0, r0, lds);
+        const int r = r0 + 8 * kg;
 #pragma unroll
-    for (int i = 0; i < T::SUB_M; ++i) {
-        const int64_t m = m0 + T::row(wm, i) + row;
-        const int id = adapter_of(g, m);
-        for (uint64_t left = __ballot(id >= 0); left;) {
-            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-            left &= ~__ballot(id == e);
-            const uint16_t *b = g.b + (int64_t)e * g.mm.N * g.rank;
-            f32x4 sum[T::SUB_N];
+        for (int i = 0; i < T::SUB_M; ++i) {
+            const int within = T::row(wm, i) + row;
+            const int id = adapter_of(g, m0 + within);
+            const float *u = lds + within * UP + 8 * kg;
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(u), hi = *reinterpret_cast<const f32x4 *>(u + 4);
+            u32x4 xf[3];
 #pragma unroll
-            for (int j = 0; j < T::SUB_N; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int r0 = 0; r0 < g.rank; r0 += 32) {
-                const int r = r0 + 8 * kg;
-                f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-                if (id == e && r < g.rank) {
-                    lo = *reinterpret_cast<const f32x4 *>(g.u + m * g.rank + r);
-                    hi = *reinterpret_cast<const f32x4 *>(g.u + m * g.rank + r + 4);
-                }
-                u32x4 wf[T::SUB_N], xf[3];
+            for (int p = 0; p < 4; ++p) {
+                uint32_t s[2][3];
 #pragma unroll
-                for (int j = 0; j < T::SUB_N; ++j) {
-                    const int64_t n = col + 16 * j + row;
-                    wf[j] = u32x4{0, 0, 0, 0};
-                    if (n < g.mm.N && r < g.rank) wf[j] = *reinterpret_cast<const u32x4 *>(b + n * g.rank + r);
-                }
+                for (int q = 0; q < 2; ++q)
+                    split3(p < 2 ? lo[2 * p + q] : hi[2 * p - 4 + q], s[q][0], s[q][1], s[q][2]);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t s[2][3];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        split3(p < 2 ? lo[2 * p + q] : hi[2 * p - 4 + q], s[q][0], s[q][1], s[q][2]);
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) xf[t][p] = s[0][t] >> 16 | s[1][t];
-                }
-#pragma unroll
-                for (int t = 0; t < 3; ++t)
-#pragma unroll
-                    for (int j = 0; j < T::SUB_N; ++j) sum[j] = mfma_bf16(wf[j], xf[t], sum[j]);
+                for (int t = 0; t < 3; ++t) xf[t][p] = s[0][t] >> 16 | s[1][t];
             }
+            // AT adapters at a time, all their loads on their way together (a decode batch's 16 rows may have 16)
+            for (uint64_t left = __ballot(id >= 0); left;) {
+                constexpr int AT = T::SUB_M * T::SUB_N > 16 ? 2 : 4;   // (as the registers allow)
+                int e[AT];
+                u32x4 wf[AT][T::SUB_N];
 #pragma unroll
-            for (int j = 0; j < T::SUB_N; ++j)
+                for (int a = 0; a < AT; ++a) {
+                    e[a] = -2;
+                    if (!left) continue;
+                    e[a] = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+                    left &= ~__ballot(id == e[a]);
+                    const uint16_t *b = g.b + (int64_t)e[a] * g.mm.N * g.rank;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][j][q] += id == e ? sum[j][q] : 0.0f;
+                    for (int j = 0; j < T::SUB_N; ++j) {
+                        const int64_t n = col + 16 * j + row;
+                        wf[a][j] = u32x4{0, 0, 0, 0};
+                        if (n < g.mm.N && r < g.rank) wf[a][j] = *reinterpret_cast<const u32x4 *>(b + n * g.rank + r);
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < AT; ++a) {
+                    if (e[a] == -2) continue;
+#pragma unroll
+                    for (int j = 0; j < T::SUB_N; ++j) {
+                        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) sum = mfma_bf16(wf[a][j], xf[t], sum);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[i][j][q] += id == e[a] ? sum[q] : 0.0f;
+                    }
+                }
+            }
         }
     }
 }
 
-// The same for one 16 x 16 block whose rows may all have different adapters: each lane takes its row's
-// adapter by itself, in fp32. n: the first of the lane's 4 columns.
-__device__ __forceinline__ f32x4 own_adapter(const AdapterArgs &g, int64_t m, int64_t n) {
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    const int id = adapter_of(g, m);
-    if (id < 0 || n >= g.mm.N) return sum;
-    const float *u = g.u + m * g.rank;
-    const uint16_t *b = g.b + ((int64_t)id * g.mm.N + n) * g.rank;
+// The same where rows may all have different adapters: each lane takes its row's adapter by itself, in fp32, for
+// 4 columns from n on. u: of the row, `ranks` of them from r0 on.
+__device__ __forceinline__ void own_adapter(const AdapterArgs &g, int id, int64_t n, const float *u, int r0, f32x4 &sum) {
+    if (id < 0 || n >= g.mm.N) return;
+    const uint16_t *b = g.b + ((int64_t)id * g.mm.N + n) * g.rank + r0;
     const int64_t last = g.mm.N - 1 - n;
-    for (int r = 0; r < g.rank; r += 8) {
+    const int ranks = g.rank - r0 < kChunk ? g.rank - r0 : kChunk;
+#pragma unroll 2
+    for (int r = 0; r < ranks; r += 8) {
         const f32x4 lo = *reinterpret_cast<const f32x4 *>(u + r), hi = *reinterpret_cast<const f32x4 *>(u + r + 4);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {   // (columns past N repeat the last one: they are not stored)
@@ -197,40 +262,56 @@ __device__ __forceinline__ f32x4 own_adapter(const AdapterArgs &g, int64_t m, in
             }
         }
     }
-    return sum;
 }
 
 __device__ __forceinline__ f32x4 bias_of(const AdapterArgs &g, int64_t n) {
     return g.bias && n < g.mm.N ? load4<0>(g.bias, n, g.mm.N - n) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// ADD: no W, base is added
-template <int BM, int BN, int NW, int NSTAGE, int ADD, int OUT_BF16>
+// ADD: no W, base is added. SHARED: rows by the matrix unit, whose neighbours mostly have one adapter, after the
+// product; else each lane for itself, while the product's first copies are on their way.
+template <int BM, int BN, int NW, int NSTAGE, int SHARED, int ADD, int OUT_BF16>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void adapter_kernel(AdapterArgs g) {
     using T = Tile<BM, BN, NW, 2, NSTAGE>;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    constexpr int U_BYTES = 4 * UP * BM, STAGES = T::STAGE * NSTAGE;
+    // (u over the stages where it is read after the product)
+    __shared__ __attribute__((aligned(16))) uint8_t smem[SHARED ? (U_BYTES > STAGES ? U_BYTES : STAGES) : STAGES + U_BYTES];
+    float *const lds = reinterpret_cast<float *>(smem + (SHARED ? 0 : STAGES));
     int64_t m0, n0;
     find_tile<T, BN>(g.mm, m0, n0);
+    const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
+    const int64_t col = n0 + wn * T::WN, M = g.mm.M, N = g.mm.N;
     f32x4 acc[T::SUB_M][T::SUB_N];
+    auto own = [&]() {
+        if constexpr (!SHARED) {
+            for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
+                stage_u<BM, NW * 64>(g, m0, r0, lds);
+#pragma unroll
+                for (int i = 0; i < T::SUB_M; ++i) {
+                    const int within = T::row(wm, i) + (lane & 15), id = adapter_of(g, m0 + within);
+#pragma unroll
+                    for (int j = 0; j < T::SUB_N; ++j)
+                        own_adapter(g, id, col + 16 * j + 4 * (lane >> 4), lds + within * UP, r0, acc[i][j]);
+                }
+            }
+        }
+    };
     if constexpr (ADD) {
 #pragma unroll
         for (int i = 0; i < T::SUB_M; ++i)
 #pragma unroll
             for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        own();
     } else {
-        multiply<T, 0, 0, 0, OUT_BF16>(g.mm, m0, n0, smem, acc);
+        multiply<T, 0, 0, 0, OUT_BF16>(g.mm, m0, n0, smem, acc, own);
     }
-    const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
-    const int64_t col = n0 + wn * T::WN, M = g.mm.M, N = g.mm.N;
-    constexpr bool SHARED = T::SUB_M * T::SUB_N > 4;
-    if constexpr (SHARED) add_adapters<T>(g, m0, col, acc);
+    if constexpr (SHARED) add_adapters<T>(g, m0, col, lds, acc);
     f32x4 bias[T::SUB_N];
 #pragma unroll
     for (int j = 0; j < T::SUB_N; ++j) bias[j] = bias_of(g, col + 16 * j + 4 * (lane >> 4));
     store_tile<T, OUT_BF16, T::SUB_N>(g.y, N, m0, M, n0, N, smem, [&](int i, int j) {
         const int64_t m = m0 + T::row(wm, i) + (lane & 15), n = col + 16 * j + 4 * (lane >> 4);
         f32x4 v = acc[i][j] + bias[j];
-        if constexpr (!SHARED) v += own_adapter(g, m, n);
         if constexpr (ADD) {
             if (m < M && n < N) v += load4<OUT_BF16>(g.base, m * N + n, N - n);
         }
@@ -238,79 +319,130 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
     });
 }
 
+// At most 16 rows
 template <int OUT_BF16>
 __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs g) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kFewStage * kFewStages];
-    __shared__ f32x4 part[2][64];
+    constexpr int RX = 1;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<RX>::BYTES];
+    __shared__ __attribute__((aligned(16))) float u[Few<RX>::ROWS * UP];
     const int64_t n0 = (int64_t)blockIdx.x * kFewN;
-    const f32x4 acc = few<0, OUT_BF16>(g.mm, n0, smem, part);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t m = lane & 15, n = n0 + 16 * wave + 4 * (lane >> 4), N = g.mm.N;
-    if (wave >= 2 || m >= g.mm.M || n >= N) return;
-    store4<OUT_BF16>(g.y, m * N + n, acc + bias_of(g, n) + own_adapter(g, m, n), N - n);
+    const int64_t n = n0 + 16 * (wave & 1) + 4 * (lane >> 4), N = g.mm.N;
+    f32x4 own[RX], acc[RX];
+#pragma unroll
+    for (int i = 0; i < RX; ++i) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    few<RX, 0, OUT_BF16>(g.mm, n0, smem, acc, [&]() {
+        for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
+            stage_u<Few<RX>::ROWS, 256>(g, 0, r0, u);
+            if (wave < 2) {
+#pragma unroll
+                for (int i = 0; i < RX; ++i) {
+                    const int m = 16 * i + (lane & 15);
+                    own_adapter(g, adapter_of(g, m), n, u + m * UP, r0, own[i]);
+                }
+            }
+        }
+    });
+    if (wave >= 2) return;
+    const f32x4 bias = bias_of(g, n);
+#pragma unroll
+    for (int i = 0; i < RX; ++i) {
+        const int64_t m = 16 * i + (lane & 15);
+        if (m < g.mm.M && n < N) store4<OUT_BF16>(g.y, m * N + n, acc[i] + own[i] + bias, N - n);
+    }
 }
 
 template <int BM, int BN, int NW, int NSTAGE>
 hipError_t launch_tile(AdapterArgs a, bool out_bf16, hipStream_t stream) {
+    constexpr int SHARED = BM >= 128;
     if (!lay_out(a.mm, BM, BN, NW * 64)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(NW * 64);
-    if (a.base) {
-        if (out_bf16) adapter_kernel<BM, BN, NW, NSTAGE, 1, 1><<<grid, block, 0, stream>>>(a);
-        else adapter_kernel<BM, BN, NW, NSTAGE, 1, 0><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (out_bf16) adapter_kernel<BM, BN, NW, NSTAGE, 0, 1><<<grid, block, 0, stream>>>(a);
-        else adapter_kernel<BM, BN, NW, NSTAGE, 0, 0><<<grid, block, 0, stream>>>(a);
-    }
+    if (out_bf16) adapter_kernel<BM, BN, NW, NSTAGE, SHARED, 0, 1><<<grid, block, 0, stream>>>(a);
+    else adapter_kernel<BM, BN, NW, NSTAGE, SHARED, 0, 0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
+}
+// (one stage: LDS holds u and the outputs only)
+template <int SHARED>
+hipError_t launch_add(AdapterArgs a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a.mm, 64, 64, 256)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(256);
+    if (out_bf16) adapter_kernel<64, 64, 4, 1, SHARED, 1, 1><<<grid, block, 0, stream>>>(a);
+    else adapter_kernel<64, 64, 4, 1, SHARED, 1, 0><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_few(const AdapterArgs &a, bool out_bf16, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.mm.N + kFewN - 1) / kFewN)), block(256);
+    if (out_bf16) adapter_few_kernel<1><<<grid, block, 0, stream>>>(a);
+    else adapter_few_kernel<0><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// Whether the rows are taken one by one in the first product: A is then read for each of them (from the caches),
+// which at 32 ranks of 512 rows takes as long as the tiles take with a different adapter in every row.
+bool by_rows(int64_t M, int64_t rank) { return M <= 512 && M * rank <= 16384; }
+
+// The parts of K: enough for two workgroups a CU, each with some steps to go
+int splits_of(int64_t M, int64_t K, int64_t rank) {
+    const int64_t steps = (K + KSTEP - 1) / KSTEP;
+    const int64_t wgs = by_rows(M, rank) ? M : (M + ShrinkTile::BM - 1) / ShrinkTile::BM * ((rank + ShrinkTile::BN - 1) / ShrinkTile::BN);
+    const int64_t least = by_rows(M, rank) ? 16 : 8, most = steps / least < kMaxSplits ? steps / least : kMaxSplits;
+    int64_t n = 512 / (wgs < 1 ? 1 : wgs);
+    n = n < most ? n : most;
+    return n < 1 ? 1 : (int)n;
 }
 
 hipError_t launch_shrink(const AdapterArgs &a, hipStream_t stream) {
     const int64_t M = a.mm.M;
-    if (M <= 256) {
-        const dim3 grid((unsigned)((M + 15) / 16), M < 16 ? (unsigned)M : 16);
-        adapter_shrink_kernel<1, 1, 16><<<grid, dim3(1024), 0, stream>>>(a);
-    } else if (a.rank <= 16) {
-        adapter_shrink_kernel<2, 1, 8><<<dim3((unsigned)((M + 31) / 32), 2), dim3(512), 0, stream>>>(a);
+    if (by_rows(M, a.rank)) {
+        const dim3 grid((unsigned)M, a.splits);
+        if (a.rank <= 16) adapter_row_kernel<1><<<grid, dim3(256), 0, stream>>>(a);
+        else adapter_row_kernel<4><<<grid, dim3(256), 0, stream>>>(a);
     } else {
-        adapter_shrink_kernel<2, 4, 8><<<dim3((unsigned)((M + 31) / 32), 2), dim3(512), 0, stream>>>(a);
+        const int64_t tiles = (M + ShrinkTile::BM - 1) / ShrinkTile::BM;
+        const int blocks = (a.rank + ShrinkTile::BN - 1) / ShrinkTile::BN;
+        // (a decode batch's rows differ, a prefill batch's are runs)
+        const dim3 grid((unsigned)tiles, a.splits * blocks, M <= 512 ? 8 : 2);
+        adapter_shrink_kernel<<<grid, dim3(256), 0, stream>>>(a);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank) { return (size_t)(M * rank * 4); }
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t K, int64_t rank) {
+    return (size_t)(splits_of(M, K, rank) * M * rank * 4);
+}
 
 hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a,
                                  const uint16_t *b, const float *scales, const int32_t *ids, const void *base, void *y,
                                  bool out_bf16, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank,
                                  void *workspace, hipStream_t stream) {
     AdapterArgs g{{x, w, M, N, K, K, K, 0, 0, 1}, bias, a, b, scales, ids, static_cast<float *>(workspace), w ? nullptr : base, y,
-                  (int)adapters, (int)rank};
+                  (int)adapters, (int)rank, splits_of(M, K, rank)};
     if (adapters > 0)
         if (hipError_t e = launch_shrink(g, stream)) return e;
-    if (!w) return M <= 256 ? launch_tile<32, 64, 4, 6>(g, out_bf16, stream) : launch_tile<128, 128, 4, 4>(g, out_bf16, stream);
-    if (M <= kFewRows) {
-        const dim3 grid((unsigned)((N + kFewN - 1) / kFewN)), block(256);
-        if (out_bf16) adapter_few_kernel<1><<<grid, block, 0, stream>>>(g);
-        else adapter_few_kernel<0><<<grid, block, 0, stream>>>(g);
-        return hipGetLastError();
-    }
+    if (!w && base) return M <= 64 ? launch_add<0>(g, out_bf16, stream) : launch_add<1>(g, out_bf16, stream);
+    // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
+    if (M <= Few<1>::ROWS) return launch_few(g, out_bf16, stream);
     auto time = [&](int bm, int bn, double first, double more, double end) {
         const double tiles = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn), rounds = std::ceil(tiles / 256.0);
         return (double)((K + KSTEP - 1) / KSTEP) * (first + more * (rounds - 1.0)) + end * rounds;
     };
-    const double t[5] = {time(32, 64, 0.155, 0.125, 1.1), time(64, 64, 0.21, 0.18, 1.4), time(128, 128, 0.45, 0.53, 5.0),
-                         time(128, 256, 0.75, 0.83, 5.7), time(256, 256, 1.3, 1.5, 8.0)};
+    const double t[7] = {time(32, 64, 0.155, 0.125, 1.1), time(64, 64, 0.21, 0.18, 1.4), time(128, 128, 0.45, 0.53, 5.0),
+                         time(128, 256, 0.75, 0.83, 5.7), time(256, 256, 1.3, 1.5, 8.0),
+                         time(32, 32, 0.105, 0.085, 1.0), time(64, 32, 0.145, 0.12, 1.1)};
     int best = 0;
-    for (int i = 1; i < 5; ++i)
+    for (int i = 1; i < 7; ++i)
         if (t[i] < t[best]) best = i;
     switch (best) {
     case 0: return launch_tile<32, 64, 4, 6>(g, out_bf16, stream);
     case 1: return launch_tile<64, 64, 4, 5>(g, out_bf16, stream);
     case 2: return launch_tile<128, 128, 4, 4>(g, out_bf16, stream);
     case 3: return launch_tile<128, 256, 8, 3>(g, out_bf16, stream);
-    default: return launch_tile<256, 256, 8, 2>(g, out_bf16, stream);
+    case 4: return launch_tile<256, 256, 8, 2>(g, out_bf16, stream);
+    case 5: return launch_tile<32, 32, 4, 8>(g, out_bf16, stream);
+    default: return launch_tile<64, 32, 4, 8>(g, out_bf16, stream);
     }
 }
 

@@ -546,8 +546,8 @@ int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t 
                                                      static_cast<hipStream_t>(stream)));
 }
 
-size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank) {
-    return adapter_ok(M, 0, 0, 0, rank) ? fp8q::adapter_linear_workspace_bytes(M, rank) : 0;
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t K, int64_t rank) {
+    return adapter_ok(M, 0, K, 0, rank) ? fp8q::adapter_linear_workspace_bytes(M, K, rank) : 0;
 }
 
 int adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a, const uint16_t *b,
@@ -561,7 +561,7 @@ int adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, cons
     if (misaligned(x, 16) || misaligned(w, 16) || misaligned(a, 16) || misaligned(b, 16) || misaligned(bias, 4) ||
         misaligned(scales, 4) || misaligned(ids, 4) || misaligned(base, 4) || misaligned(y, 4) || misaligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
-    if (adapters > 0 && fp8q::adapter_linear_workspace_bytes(M, rank) > (workspace ? workspace_bytes : 0))
+    if (adapters > 0 && fp8q::adapter_linear_workspace_bytes(M, K, rank) > (workspace ? workspace_bytes : 0))
         return FP8Q_ERR_WORKSPACE;
     if (int e = check_device()) return e;
     return finish(fp8q::launch_adapter_linear(x, w, bias, a, b, scales, ids, base, y, y_dtype == FP8Q_OUT_BF16, M, N, K,

@@ -536,7 +536,7 @@ PyObject *adapter(PyObject *const *a) {
     const Tensor *bias = bias_of(a[6], N, x);
     if (base && reinterpret_cast<uintptr_t>(base->data_ptr()) % 4) raise(PyExc_ValueError, "y must be 4-byte aligned");
     const Tensor y = output(a[9], shape, base ? base->scalar_type() : type_of_code(a[8]), 4, x);
-    const size_t bytes = L ? adapter_linear_workspace_bytes(M, r) : 0;
+    const size_t bytes = L ? adapter_linear_workspace_bytes(M, K, r) : 0;
     const Tensor ws = bytes ? like(x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
     const On on(x);
     check("adapter_linear",

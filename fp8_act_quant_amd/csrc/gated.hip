@@ -50,7 +50,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
     int64_t m0, n0;
     find_tile<T, BN / 2>(g.mm, m0, n0);
     f32x4 acc[T::SUB_M][T::SUB_N];
-    multiply<T, 0, 0, 1, MODE>(g.mm, m0, n0, smem, acc);
+    multiply<T, 0, 0, 1, MODE>(g.mm, m0, n0, smem, acc, []() {});
     const int64_t M = g.mm.M, F = g.mm.N;
     auto gate = [&](int i, int j) { return acc[i][j]; };
     auto up = [&](int i, int j) { return acc[i][j + HALF]; };
@@ -86,36 +86,43 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
     }
 }
 
-// At most 16 rows
-template <int MODE>
+// At most 16 RX rows
+template <int RX, int MODE>
 __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kFewStage * kFewStages];
-    __shared__ f32x4 part[2][64];
-    __shared__ f32x4 ups[64];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<RX>::BYTES];
+    f32x4 *const ups = reinterpret_cast<f32x4 *>(smem);
     const int64_t n0 = (int64_t)blockIdx.x * (kFewN / 2);
-    const f32x4 acc = few<1, MODE>(g.mm, n0, smem, part);
+    f32x4 acc[RX];
+    few<RX, 1, MODE>(g.mm, n0, smem, acc, []() {});
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (wave == 1) ups[lane] = acc;
-    __syncthreads();
-    const int64_t m = lane & 15, n = n0 + 4 * (lane >> 4), F = g.mm.N;
-    if (wave || m >= g.mm.M || n >= F) return;
-    const f32x4 up = ups[lane];
-    f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
+    if (wave == 1) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const Activation act = activate(acc[r], g.gelu);
-        a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
-        b[r] = dh[r] * act.value;
+        for (int i = 0; i < RX; ++i) ups[64 * i + lane] = acc[i];
     }
-    if constexpr (MODE == 2) {
-        store4<1>(g.gu, m * 2 * F + n, a, F - n);
-        store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
-    } else {
-        store4<MODE>(g.h, m * F + n, a, F - n);
-        if (g.gu) {
-            store4<1>(g.gu, m * 2 * F + n, acc, F - n);
-            store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int i = 0; i < RX; ++i) {
+        const int64_t m = 16 * i + (lane & 15), n = n0 + 4 * (lane >> 4), F = g.mm.N;
+        if (m >= g.mm.M || n >= F) continue;
+        const f32x4 up = ups[64 * i + lane];
+        f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const Activation act = activate(acc[i][r], g.gelu);
+            a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
+            b[r] = dh[r] * act.value;
+        }
+        if constexpr (MODE == 2) {
+            store4<1>(g.gu, m * 2 * F + n, a, F - n);
+            store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
+        } else {
+            store4<MODE>(g.h, m * F + n, a, F - n);
+            if (g.gu) {
+                store4<1>(g.gu, m * 2 * F + n, acc[i], F - n);
+                store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
+            }
         }
     }
 }
@@ -153,7 +160,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
     int64_t m0, n0;
     find_tile<T, BN>(g.mm, m0, n0);
     f32x4 acc[T::SUB_M][T::SUB_N];
-    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc);
+    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc, []() {});
     store_tile<T, OUT_BF16, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, [&](int i, int j) { return acc[i][j]; });
 }
 
@@ -179,15 +186,21 @@ int best_tile(const double *t, int n) {
     return best;
 }
 
+template <int RX>
+hipError_t launch_gated_few(const GatedArgs &a, int mode, hipStream_t stream) {
+    const dim3 grid((unsigned)((a.mm.N + kFewN / 2 - 1) / (kFewN / 2))), block(256);
+    if (mode == 0) gated_few_kernel<RX, 0><<<grid, block, 0, stream>>>(a);
+    else if (mode == 1) gated_few_kernel<RX, 1><<<grid, block, 0, stream>>>(a);
+    else gated_few_kernel<RX, 2><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
     const int64_t M = a.mm.M, F = a.mm.N, K = a.mm.K;
-    if (M <= kFewRows) {
-        const dim3 grid((unsigned)((F + kFewN / 2 - 1) / (kFewN / 2))), block(256);
-        if (mode == 0) gated_few_kernel<0><<<grid, block, 0, stream>>>(a);
-        else if (mode == 1) gated_few_kernel<1><<<grid, block, 0, stream>>>(a);
-        else gated_few_kernel<2><<<grid, block, 0, stream>>>(a);
-        return hipGetLastError();
-    }
+    // few rows against the tiles, us: 24 x 3584 x 7168 20.7 / 27.6, 24 x 768 x 7168 13.9 / 17.2, 48 x 3584 x 7168 (four
+    // blocks of rows) 30.0 / 26.1
+    if (M <= 16) return launch_gated_few<1>(a, mode, stream);
+    if (M <= 32) return launch_gated_few<2>(a, mode, stream);
     const double t[5] = {tile_time(M, 2 * F, K, 32, 64, 0.155, 0.125, 1.1), tile_time(M, 2 * F, K, 64, 64, 0.21, 0.18, 1.4),
                          tile_time(M, 2 * F, K, 128, 128, 0.45, 0.53, 5.0),
                          tile_time(M, 2 * F, K, 128, 256, 0.75, 0.83, 5.7),

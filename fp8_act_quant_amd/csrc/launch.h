@@ -132,7 +132,7 @@ hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, c
 // Linear layers with an adapter per token (adapter.hip): K and rank multiples of 8, rank <= kMaxRank; w, or base
 // of y's type; the workspace holds adapter_linear_workspace_bytes.
 constexpr int64_t kMaxRank = 256;
-size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank);
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t K, int64_t rank);
 hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, const uint16_t *a,
                                  const uint16_t *b, const float *scales, const int32_t *ids, const void *base, void *y,
                                  bool out_bf16, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank,

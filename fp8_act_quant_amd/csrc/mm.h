@@ -282,9 +282,9 @@ struct Operands {
 // retire in order, and the count left open at the end of each load slot (IPW) covers exactly what the
 // load slots before the data's use have queued since; the barrier then makes it visible. Steps past the
 // last copy zeros, which keeps the counts the same.
-template <class T, int XT, int WT, int GATED, int TAG>
+template <class T, int XT, int WT, int GATED, int TAG, class F>
 __device__ __forceinline__ void turns(const MmArgs &g, int64_t m0, int64_t n0, uint8_t *smem,
-                                      f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
+                                      f32x4 (&acc)[T::SUB_M][T::SUB_N], const F &begin) {
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, PH = SUB_M / 4;
     static_assert(T::NW == 8 && T::WAVES_M == 2 && (PH == 1 || PH == 2) && T::NSTAGE == 4 - PH, "schedule");
     constexpr int X0 = T::X_INSTR / 2;   // two phases: copies of the first 128 rows
@@ -308,6 +308,8 @@ __device__ __forceinline__ void turns(const MmArgs &g, int64_t m0, int64_t n0, u
         copies.issue(smem, 0);
         copies.issue(smem + T::STAGE, 1);
     }
+    begin();
+    __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<T::IPW>();
     lds_barrier();
     if (wave >= 4) lds_barrier();   // one slot behind
@@ -367,9 +369,9 @@ __device__ __forceinline__ void turns(const MmArgs &g, int64_t m0, int64_t n0, u
 // row group's preceded by its share of the LDS reads and copies. A stage is free once its step is in
 // registers everywhere (lgkmcnt, then the barrier), and takes the copies of step ks + NSTAGE; steps past the
 // last copy zeros, so that the count left open always covers NSTAGE - 2 steps.
-template <class T, int XT, int WT, int GATED, int TAG>
+template <class T, int XT, int WT, int GATED, int TAG, class F>
 __device__ __forceinline__ void deep(const MmArgs &g, int64_t m0, int64_t n0, uint8_t *smem,
-                                     f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
+                                     f32x4 (&acc)[T::SUB_M][T::SUB_N], const F &begin) {
     constexpr int SUB_M = T::SUB_M, SUB_N = T::SUB_N, READS = 2 * (SUB_M + SUB_N), GROUPS = 2 * SUB_M;
     static_assert(T::NW == 4 && T::WAVES_M == 2 && T::NSTAGE >= 3, "schedule");
     const int lane = threadIdx.x & 63;
@@ -384,6 +386,8 @@ __device__ __forceinline__ void deep(const MmArgs &g, int64_t m0, int64_t n0, ui
         for (int j = 0; j < SUB_N; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < T::NSTAGE; ++s) copies.issue(smem + s * T::STAGE, s);
+    begin();
+    __builtin_amdgcn_sched_barrier(0);
     wait_vmcnt<T::IPW *(T::NSTAGE - 1)>();
     lds_barrier();
     u32x4 wf0[SUB_N][2], xf0[SUB_M][2], wf1[SUB_N][2], xf1[SUB_M][2];
@@ -427,11 +431,12 @@ __device__ __forceinline__ void deep(const MmArgs &g, int64_t m0, int64_t n0, ui
     __syncthreads();
 }
 
-template <class T, int XT, int WT, int GATED, int TAG>
+// `begin` is called once the first copies are on their way; it may put something into acc, or load
+template <class T, int XT, int WT, int GATED, int TAG, class F>
 __device__ __forceinline__ void multiply(const MmArgs &g, int64_t m0, int64_t n0, uint8_t *smem,
-                                         f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
-    if constexpr (T::NW == 8) turns<T, XT, WT, GATED, TAG>(g, m0, n0, smem, acc);
-    else deep<T, XT, WT, GATED, TAG>(g, m0, n0, smem, acc);
+                                         f32x4 (&acc)[T::SUB_M][T::SUB_N], const F &begin) {
+    if constexpr (T::NW == 8) turns<T, XT, WT, GATED, TAG>(g, m0, n0, smem, acc, begin);
+    else deep<T, XT, WT, GATED, TAG>(g, m0, n0, smem, acc, begin);
 }
 template <class T>
 __device__ __forceinline__ int wave_m() {
@@ -444,17 +449,23 @@ __device__ __forceinline__ int wave_n() {
     return T::NW == 8 ? wave & 3 : wave >> 1;
 }
 
-// At most 16 rows (a decode step): every byte of W meets all of them once, so the read of W is what counts. A
+// At most 16 RX rows (a decode step): every byte of W meets all of them once, so the read of W is what counts. A
 // workgroup of 4 waves takes 32 rows of W (GATED: 16 gate rows and their up rows), which come through LDS
-// with the rows of X, four steps of 64 k to a stage. Waves 0 and 1 take 16 rows of W each and the first half
-// of every step, waves 2 and 3 the other half; the halves are added in LDS. On return waves 0 and 1 have
-// their sums: acc[r] of lane l is W row n0 + 16 * wave + 4 * (l / 16) + r (GATED: wave 0 the gate's, wave 1
-// the up's of f = n0 + ...) for X row l % 16.
-constexpr int kFewRows = 16, kFewSubs = 4, kFewStages = 3, kFewN = 32;
-constexpr int kFewStage = kFewSubs * (kFewN + kFewRows) * KB;
-template <int GATED, int TAG>
-__device__ __forceinline__ f32x4 few(const MmArgs &g, int64_t n0, uint8_t *smem, f32x4 (*part)[64]) {
-    constexpr int SUBS = kFewSubs, W_SUB = kFewN * KB, X_SUB = kFewRows * KB, IPW = SUBS + 2;
+// with the rows of X, four steps of 64 k to a stage (a stage of one step costs a barrier and a wait for LDS as
+// long as its copies). Waves 0 and 1 take 16 rows of W each and the first half of every step, waves 2 and 3 the
+// other half; the halves are added in LDS (which is free again on return). On return waves 0 and 1 have their sums: acc[i][r] of lane l is W row
+// n0 + 16 * wave + 4 * (l / 16) + r (GATED: wave 0 the gate's, wave 1 the up's of f = n0 + ...) for X row
+// 16 i + l % 16.
+constexpr int kFewSubs = 4, kFewStages = 3, kFewN = 32;
+template <int RX>
+struct Few {
+    static constexpr int ROWS = 16 * RX, W_SUB = kFewN * KB, X_SUB = ROWS * KB, STAGE = kFewSubs * (W_SUB + X_SUB);
+    static constexpr int BYTES = STAGE * kFewStages;
+};
+template <int RX, int GATED, int TAG, class F>
+__device__ __forceinline__ void few(const MmArgs &g, int64_t n0, uint8_t *smem, f32x4 (&acc)[RX], const F &begin) {
+    constexpr int SUBS = kFewSubs, W_SUB = Few<RX>::W_SUB, X_SUB = Few<RX>::X_SUB, STAGE = Few<RX>::STAGE;
+    constexpr int IPW = SUBS + 2 * RX;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4, sub = lane >> 3;
@@ -464,7 +475,7 @@ __device__ __forceinline__ f32x4 few(const MmArgs &g, int64_t n0, uint8_t *smem,
     const rsrc_t rx = make_rsrc(g.x, 2 * ((g.M - 1) * g.ldx + g.K));
     const int chunk_byte = swz_chunk(sub, lane & 7) << 4, Kb = (int)(2 * g.K);
     const uint32_t w_off = (uint32_t)((8 * (GATED ? wave & 1 : wave) + sub) * g.ldw * 2) + chunk_byte;
-    const uint32_t x_off = (uint32_t)(sub * g.ldx * 2) + chunk_byte, x_off8 = (uint32_t)((8 + sub) * g.ldx * 2) + chunk_byte;
+    const uint32_t x_off = (uint32_t)(sub * g.ldx * 2) + chunk_byte, x_step = (uint32_t)(16 * g.ldx);   // 8 rows
     auto copy = [&](uint8_t *stage, int ks) {
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
@@ -473,19 +484,22 @@ __device__ __forceinline__ f32x4 few(const MmArgs &g, int64_t n0, uint8_t *smem,
                                                      koff + chunk_byte >= Kb ? kNowhere : w_off, koff, 0, 0);
         }
         const int koff = __builtin_amdgcn_readfirstlane((ks * SUBS + wave) * KB);   // X: a step a wave
-        const bool past = koff + chunk_byte >= Kb;
-        lds_void *to = (lds_void *)(stage + SUBS * W_SUB + wave * X_SUB);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, past ? kNowhere : x_off, koff, 0, 0);
-        to = (lds_void *)(stage + SUBS * W_SUB + wave * X_SUB + 1024);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, past ? kNowhere : x_off8, koff, 0, 0);
+        const uint32_t at = koff + chunk_byte >= Kb ? kNowhere : x_off;
+#pragma unroll
+        for (int t = 0; t < 2 * RX; ++t)   // (kNowhere and rows past the last lie past the range: t x_step does not wrap)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(stage + SUBS * W_SUB + wave * X_SUB + 1024 * t), 16,
+                                                     at == kNowhere ? kNowhere : at + t * x_step, koff, 0, 0);
     };
 #pragma unroll
-    for (int s = 0; s < kFewStages - 1; ++s) copy(smem + s * kFewStage, s);
+    for (int s = 0; s < kFewStages - 1; ++s) copy(smem + s * STAGE, s);
+    begin();
+    __builtin_amdgcn_sched_barrier(0);
     const int cg = wave & 1, half = wave >> 1;
     const int at = row * KB + (swz_chunk(row, 4 * half + kg) << 4);
     const int nks = (int)((g.K + SUBS * KSTEP - 1) / (SUBS * KSTEP));
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    uint8_t *stage = smem, *last = smem + (kFewStages - 1) * kFewStage;   // `last`: of the step before
+#pragma unroll
+    for (int i = 0; i < RX; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint8_t *stage = smem, *last = smem + (kFewStages - 1) * STAGE;   // `last`: of the step before
     for (int ks = 0; ks < nks; ++ks) {
         __builtin_amdgcn_sched_barrier(0);
         wait_lgkm0();                             // the step before's reads
@@ -495,16 +509,28 @@ __device__ __forceinline__ f32x4 few(const MmArgs &g, int64_t n0, uint8_t *smem,
 #pragma unroll
         for (int s = 0; s < SUBS; ++s) {
             const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + s * W_SUB + 16 * cg * KB + at);
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(stage + SUBS * W_SUB + s * X_SUB + at);
-            acc = mfma_bf16(w, x, acc);
+#pragma unroll
+            for (int i = 0; i < RX; ++i) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(stage + SUBS * W_SUB + s * X_SUB + 16 * i * KB + at);
+                acc[i] = mfma_bf16(w, x, acc[i]);
+            }
         }
         last = stage;
-        stage = stage + kFewStage == smem + kFewStages * kFewStage ? smem : stage + kFewStage;
+        stage = stage + STAGE == smem + kFewStages * STAGE ? smem : stage + STAGE;
     }
     wait_vmcnt<0>();
-    if (half == 1) part[cg][lane] = acc;
     __syncthreads();
-    return half == 0 ? acc + part[cg][lane] : acc;
+    f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + cg * RX * 64 + lane;
+    if (half == 1) {
+#pragma unroll
+        for (int i = 0; i < RX; ++i) part[64 * i] = acc[i];
+    }
+    __syncthreads();
+    if (half == 0) {
+#pragma unroll
+        for (int i = 0; i < RX; ++i) acc[i] += part[64 * i];
+    }
+    __syncthreads();
 }
 
 // Four consecutive elements of a row with `left` of them from here on, as they are in memory

@@ -454,7 +454,7 @@ int adapter_linear(const uint16_t *x, const uint16_t *w, const float *bias, cons
                    const float *scales, const int32_t *ids, const void *base, void *y, int y_dtype, int64_t M,
                    int64_t N, int64_t K, int64_t adapters, int64_t rank, void *workspace, size_t workspace_bytes,
                    void *stream);
-size_t adapter_linear_workspace_bytes(int64_t M, int64_t rank);
+size_t adapter_linear_workspace_bytes(int64_t M, int64_t K, int64_t rank);
 
 /* Workspace size in bytes that lets fp8_block_gemm use its split-K schedule for this
  * shape and y_dtype (including the mode bits); 0 if that call does not use one or the

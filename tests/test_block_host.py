@@ -108,8 +108,10 @@ def test_adapter_validation(L):
     for bad in (dict(x=FAKE + 8), dict(w=FAKE + 8), dict(a=FAKE + 8), dict(b=FAKE + 8), dict(bias=FAKE + 2),
                 dict(scales=FAKE + 2), dict(ids=FAKE + 2), dict(w=None, base=FAKE + 2), dict(y=FAKE + 2), dict(ws=FAKE + 8)):
         assert call(**bad) == L.FP8Q_ERR_ALIGN, bad
-    need = lib.adapter_linear_workspace_bytes(4, 16)
-    assert need == 4 * 16 * 4 and lib.adapter_linear_workspace_bytes(4, 12) == lib.adapter_linear_workspace_bytes(-1, 8) == 0
+    need = lib.adapter_linear_workspace_bytes(4, 64, 16)
+    assert need >= 4 * 16 * 4
+    for bad in ((4, 64, 12), (-1, 64, 8), (4, 60, 8)):
+        assert lib.adapter_linear_workspace_bytes(*bad) == 0
     assert call(size=need - 1) == call(ws=None) == L.FP8Q_ERR_WORKSPACE
     assert call(M=0, x=None, ids=None, y=None) == call(N=0, w=None, y=None) == L.FP8Q_OK
 
