@@ -75,7 +75,7 @@ SIGNATURES = {
     "residual_norm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "gated_linear": (_INT, [_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _P]),
     "gated_linear_backward": (_INT, [_P, _P, _P, _P, _INT, _P, _INT, _P, _INT, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
-    "gated_linear_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "gated_linear_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "adapter_linear": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t,
                               _P]),
     "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),

@@ -525,8 +525,8 @@ int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uin
                                             static_cast<hipStream_t>(stream)));
 }
 
-size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F) {
-    return gated_ok(M, F, 0) ? (size_t)(M * F * 4) : 0;
+size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+    return gated_ok(M, F, K) ? fp8q::gated_linear_backward_workspace_bytes(M, F, K) : 0;
 }
 
 int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
@@ -539,7 +539,7 @@ int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t 
     if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(gu, 16) || misaligned(dx, 4) ||
         misaligned(dw, 4) || misaligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
-    if (gated_linear_backward_workspace_bytes(M, F) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    if (fp8q::gated_linear_backward_workspace_bytes(M, F, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
     if (int e = check_device()) return e;
     return finish(fp8q::launch_gated_linear_backward(dh, x, w, gu, act == FP8Q_ACT_GELU, dx, dx_dtype == FP8Q_OUT_BF16, dw,
                                                      dw_dtype == FP8Q_OUT_BF16, M, F, K, workspace,

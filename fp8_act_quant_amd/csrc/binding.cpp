@@ -504,7 +504,7 @@ PyObject *gated_backward(PyObject *const *a) {
     const Tensor *gu = nullptr;
     if (a[3] != Py_None) shaped(*(gu = &need(a[3], "gu", ScalarType::BFloat16, 16, &g.x)), "gu", g.shape(2 * g.F));
     const Tensor dx = like(g.x, g.x.sizes(), type_of_code(a[5])), dw = like(g.x, g.w.sizes(), type_of_code(a[6]));
-    const size_t bytes = gated_linear_backward_workspace_bytes(g.M, g.F);
+    const size_t bytes = gated_linear_backward_workspace_bytes(g.M, g.F, g.K);
     const Tensor ws = bytes ? like(g.x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
     const On on(g.x);
     check("gated_linear_backward",

@@ -122,7 +122,8 @@ hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const v
                                          hipStream_t stream);
 
 // Gated projections (gated.hip): x [M, K], w [2 F, K], K and F multiples of 8 (K < 2^23, F < 2^22), the
-// gradient's workspace [M, 2 F] bf16.
+// gradient's workspace holds gated_linear_backward_workspace_bytes.
+size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
 hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
                                int64_t M, int64_t F, int64_t K, hipStream_t stream);
 hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,

@@ -46,6 +46,23 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void *p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)n, 0x00020000);
 }
 
+// The same resource as four words, and a copy of 16 bytes a lane from it to LDS (from `to` on, a wave's 1 KB) of which
+// the compiler does not know: with one that it knows of, it waits for all copies under way before every transposing
+// LDS read (4096 x 7168 x 4096 by 128 x 128 tiles 600 us instead of 240). The waits here are written out anyway, and
+// those that the compiler adds for loads of its own only get longer.
+__device__ __forceinline__ u32x4 rsrc_words(const void *p, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes > (int64_t)kNowhere ? kNowhere : bytes < 0 ? 0u : (uint32_t)bytes,
+                 0x00020000u};
+}
+__device__ __forceinline__ void copy16(const u32x4 &rsrc, uint8_t *to, uint32_t off, uint32_t soff) {
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(rsrc), "s"(soff)
+                 : "memory");   // (M0: nothing else in a kernel with such copies uses it)
+}
+
 __device__ __forceinline__ int swz_chunk(int row, int chunk) { return chunk ^ (row & 7); }
 
 template <int N>
@@ -94,18 +111,21 @@ struct MmArgs {
 
 // Workgroup b's tile. Workgroups are dealt round-robin to the 8 XCDs; each XCD takes a contiguous run of
 // the tile numbers, which go down `group` tile rows per tile column, so that the tiles that an XCD holds
-// at once share panels in its L2. NT: columns of Y in a tile.
+// at once share panels in its L2. NT: columns of Y in a tile. parts: the tiles that many times over; returns which.
 template <class T, int NT>
-__device__ __forceinline__ void find_tile(const MmArgs &g, int64_t &m0, int64_t &n0) {
-    const int tiles = g.tiles_m * g.tiles_n;
+__device__ __forceinline__ int find_tile(const MmArgs &g, int64_t &m0, int64_t &n0, int parts = 1) {
+    const int tiles = g.tiles_m * g.tiles_n * parts;
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
     const int q = tiles >> 3, rem = tiles & 7;
-    const int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
+    int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
+    const int part = tl / (g.tiles_m * g.tiles_n);
+    tl -= part * (g.tiles_m * g.tiles_n);
     const int band = tl / (g.group * g.tiles_n);
     const int in_band = tl - band * g.group * g.tiles_n;
     const int band_rows = min(g.group, g.tiles_m - band * g.group);
     m0 = (int64_t)(band * g.group + in_band % band_rows) * T::BM;
     n0 = (int64_t)(in_band / band_rows) * NT;
+    return part;
 }
 
 // The tiles of a launch, and down how many tile rows to walk (so that the some 32 tiles of an XCD read the
@@ -138,6 +158,7 @@ __device__ __forceinline__ int exchange(int row) {
 template <class T, int XT, int WT, int GATED, int TAG>
 struct Copies {
     rsrc_t rx, rw, rw1;               // K-contiguous (GATED: rw1 the up rows)
+    u32x4 rxw;                        // rx where an operand is K-strided
     const uint16_t *px, *pw;          // K-strided: column m0, n0 of k-row 0
     int64_t left_x, left_w;           // their bytes from there to the operand's end
     uint32_t off[T::IPW];
@@ -167,6 +188,7 @@ struct Copies {
         } else {
             const int64_t rows = g.M - m0 < T::BM ? g.M - m0 : T::BM;
             rx = make_rsrc(g.x + m0 * ldx, 2 * ((rows - 1) * ldx + g.K));
+            rxw = rsrc_words(g.x + m0 * ldx, 2 * ((rows - 1) * ldx + g.K));
         }
         if constexpr (WT) {
             pw = g.w + n0;
@@ -196,27 +218,26 @@ struct Copies {
     __device__ __forceinline__ void issue(uint8_t *base, int ks, int first = 0, int count = T::IPW) const {
         const int koff = __builtin_amdgcn_readfirstlane(ks * KB);
         const bool past = koff + chunk_byte >= Kb;
-        rsrc_t sx, sw;
-        if constexpr (XT) sx = make_rsrc(px + ks * (KSTEP * ldx), left_x - ks * (KSTEP * 2 * ldx));
-        if constexpr (WT) sw = make_rsrc(pw + ks * (KSTEP * ldw), left_w - ks * (KSTEP * 2 * ldw));
+        u32x4 sx, sw;
+        if constexpr (XT) sx = rsrc_words(px + ks * (KSTEP * ldx), left_x - ks * (KSTEP * 2 * ldx));
+        if constexpr (WT) sw = rsrc_words(pw + ks * (KSTEP * ldw), left_w - ks * (KSTEP * 2 * ldw));
 #pragma unroll
         for (int t = 0; t < T::IPW; ++t) {
             if (t < first || t >= first + count) continue;
-            lds_void *to = (lds_void *)(base + (t < T::X_INSTR ? 0 : T::X_BYTES) + 1024 * instr(t));
+            uint8_t *to = base + (t < T::X_INSTR ? 0 : T::X_BYTES) + 1024 * instr(t);
             if (t < T::X_INSTR) {
-                if constexpr (XT) __builtin_amdgcn_raw_ptr_buffer_load_lds(sx, to, 16, off[t], 0, 0, 0);
-                else __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, past ? kNowhere : off[t], koff, 0, 0);
+                if constexpr (XT) copy16(sx, to, off[t], 0);
+                else if constexpr (WT) copy16(rxw, to, past ? kNowhere : off[t], koff);
+                else __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)to, 16, past ? kNowhere : off[t], koff, 0, 0);
             } else {
-                if constexpr (WT) {
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(sw, to, 16, off[t], 0, 0, 0);
-                } else if (GATED && up(t)) {
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw1, to, 16, past ? kNowhere : off[t], koff, 0, 0);
-                } else {
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, past ? kNowhere : off[t], koff, 0, 0);
-                }
+                if constexpr (WT) copy16(sw, to, off[t], 0);
+                else if (GATED && up(t))
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw1, (lds_void *)to, 16, past ? kNowhere : off[t], koff, 0, 0);
+                else __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)to, 16, past ? kNowhere : off[t], koff, 0, 0);
             }
         }
     }
+    static_assert(WT || !XT, "X alone is never K-strided");
 };
 
 // This wave's operands from a stage: half h (32 k) of its 16-row group i of X, or 16-column block j of W

@@ -433,7 +433,7 @@ int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uin
 int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
                           int dx_dtype, void *dw, int dw_dtype, int64_t M, int64_t F, int64_t K, void *workspace,
                           size_t workspace_bytes, void *stream);
-size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F);
+size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /* adapter_linear -- y[m] = x[m] w^T + bias + scales[e] (x[m] a[e]^T) b[e]^T, e = ids[m]: a linear layer
  * whose rows each have a low-rank adapter of their own (requests of many adapters in a batch).

@@ -87,8 +87,10 @@ def test_gated_validation(L):
     for bad in (dict(dh=FAKE + 8), dict(x=FAKE + 8), dict(w=FAKE + 8), dict(gu=FAKE + 8), dict(dx=FAKE + 2),
                 dict(dw=FAKE + 2), dict(ws=FAKE + 8)):
         assert back(**bad) == L.FP8Q_ERR_ALIGN, bad
-    need = lib.gated_linear_backward_workspace_bytes(4, 16)
-    assert need == 4 * 2 * 16 * 2 and lib.gated_linear_backward_workspace_bytes(4, 12) == 0
+    need = lib.gated_linear_backward_workspace_bytes(4, 16, 64)
+    assert need >= 4 * 2 * 16 * 2
+    for bad in ((4, 12, 64), (4, 16, 60), (-1, 16, 64)):
+        assert lib.gated_linear_backward_workspace_bytes(*bad) == 0
     assert back(size=need - 1) == back(ws=None) == L.FP8Q_ERR_WORKSPACE
     assert back(dx=None, dw=None) == back(K=0) == L.FP8Q_OK
 

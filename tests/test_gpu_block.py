@@ -324,6 +324,48 @@ def test_gated_large_projections(act):
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations(act):
+    """Every bf16 number from -90 to 90 as the gate's projection, the other one 1: the activation itself in fp32,
+    and its slope. Below fp32's normal range results may be 0."""
+    bits = torch.arange(0, 1 << 16, dtype=torch.int32, device="cuda").to(torch.int16)
+    a = bits.view(torch.bfloat16)
+    a = a[(a.abs() <= 90) & (a.abs() >= 1e-30) | (a == 0)]
+    x = torch.zeros((a.numel(), 8), device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = a, 1.0
+    w = torch.zeros((16, 8), device="cuda").bfloat16()
+    w[:8, 0] = w[8:, 1] = 1.0
+    h, gu = fq.gated_linear(x, w, act=act, keep=True, out_dtype=torch.float32)
+    assert torch.equal(gu[:, 0], a) and (gu[:, 8:] == 1).all()
+    value, slope = act64(a.double(), act)
+    tiny = 100 * 2.0 ** -126
+    assert ((h[:, 0].double() - value).abs() <= ACT * U * value.abs() + tiny).all()
+    # dg = slope, du = act of one row at a time come back as dx = [dg du] w
+    one = torch.zeros((a.numel(), 8), device="cuda").bfloat16()
+    one[:, 3] = 1.0
+    dx, _ = fq.gated_linear_backward(one, x, w, gu, act=act, dx_dtype=torch.float32)
+    again, _ = fq.gated_linear_backward(one, x, w, None, act=act, dx_dtype=torch.float32)
+    assert torch.equal(dx, again)
+    mag = torch.sigmoid(a.double()) if act == "silu" else 0.5 * torch.erfc(-a.double() / math.sqrt(2))
+    mag = mag + (slope - mag).abs()
+    assert ((dx[:, 0].double() - slope).abs() <= half(torch.bfloat16) * slope.abs() + ACT * U * mag * 2 + tiny).all()
+    assert ((dx[:, 1].double() - value).abs() <= half(torch.bfloat16) * value.abs() * (1 + ACT * U) + ACT * U * value.abs() + tiny).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_specials(act):
+    """+inf is itself, NaN stays NaN in its row."""
+    x = torch.zeros((3, 8), device="cuda").bfloat16()
+    x[0, 0], x[1, 0], x[2, 0] = float("inf"), float("nan"), 2.0
+    w = torch.zeros((16, 8), device="cuda").bfloat16()
+    w[:8, 0], w[8:, 1] = 1.0, 1.0
+    x[:, 1] = 1.0
+    h, gu = fq.gated_linear(x[:, :].clone(), w, act=act, keep=True)
+    # (inf * 0 in the up projection: w's zeros meet x's infinities)
+    dx, dw = fq.gated_linear_backward(torch.ones((1, 8), device="cuda").bfloat16(), x[2:].clone(), w, gu[2:].clone(), act=act)
+    assert torch.isnan(h[1]).all() and torch.isfinite(h[2]).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
 def test_gated_empty():
     def e(*shape):
         return torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
