@@ -268,24 +268,23 @@ __device__ __forceinline__ f32x4 bias_of(const AdapterArgs &g, int64_t n) {
     return g.bias && n < g.mm.N ? load4<0>(g.bias, n, g.mm.N - n) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// ADD: no W, base is added. SHARED: rows by the matrix unit, whose neighbours mostly have one adapter, after the
+// A tile. ADD: no W, base is added. SHARED: rows by the matrix unit, whose neighbours mostly have one adapter, after the
 // product; else each lane for itself, while the product's first copies are on their way.
-template <int BM, int BN, int NW, int NSTAGE, int SHARED, int ADD, int OUT_BF16>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void adapter_kernel(AdapterArgs g) {
-    using T = Tile<BM, BN, NW, 2, NSTAGE>;
-    constexpr int U_BYTES = 4 * UP * BM, STAGES = T::STAGE * NSTAGE;
-    // (u over the stages where it is read after the product)
-    __shared__ __attribute__((aligned(16))) uint8_t smem[SHARED ? (U_BYTES > STAGES ? U_BYTES : STAGES) : STAGES + U_BYTES];
-    float *const lds = reinterpret_cast<float *>(smem + (SHARED ? 0 : STAGES));
-    int64_t m0, n0;
-    find_tile<T, BN>(g.mm, m0, n0);
+template <class T, int SHARED>
+constexpr int tile_bytes() {   // (u over the stages where it is read after the product)
+    constexpr int U = 4 * UP * T::BM, STAGES = T::STAGE * T::NSTAGE;
+    return SHARED ? (U > STAGES ? U : STAGES) : STAGES + U;
+}
+template <class T, int SHARED, int ADD, int OUT_BF16>
+__device__ __forceinline__ void adapter_tile(const AdapterArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
+    float *const lds = reinterpret_cast<float *>(smem + (SHARED ? 0 : T::STAGE * T::NSTAGE));
     const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
     const int64_t col = n0 + wn * T::WN, M = g.mm.M, N = g.mm.N;
     f32x4 acc[T::SUB_M][T::SUB_N];
     auto own = [&]() {
         if constexpr (!SHARED) {
             for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
-                stage_u<BM, NW * 64>(g, m0, r0, lds);
+                stage_u<T::BM, T::NW * 64>(g, m0, r0, lds);
 #pragma unroll
                 for (int i = 0; i < T::SUB_M; ++i) {
                     const int within = T::row(wm, i) + (lane & 15), id = adapter_of(g, m0 + within);
@@ -317,6 +316,32 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
         }
         return v;
     });
+}
+
+template <int BM, int BN, int NW, int NSTAGE, int SHARED, int ADD, int OUT_BF16>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void adapter_kernel(AdapterArgs g) {
+    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[tile_bytes<T, SHARED>()];
+    int64_t m0, n0;
+    find_tile<T, BN>(g.mm, m0, n0);
+    adapter_tile<T, SHARED, ADD, OUT_BF16>(g, m0, n0, smem);
+}
+
+template <int OUT_BF16>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void adapter_large_kernel(AdapterArgs g) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[tile_bytes<HalfTile, 1>()];
+    static_assert(tile_bytes<HalfTile, 1>() >= tile_bytes<WholeTile, 1>(), "LDS of both");
+    bool second;
+    int tile, half;
+    if (!find_share(g.mm.tiles_m * g.mm.tiles_n, 0, second, tile, half)) return;
+    int64_t m0, n0;
+    place_tile(g.mm, tile, 256, 256, m0, n0);
+    if (half < 0) {
+        adapter_tile<WholeTile, 1, 0, OUT_BF16>(g, m0, n0, smem);
+    } else {
+        m0 += 128 * half;
+        if (m0 < g.mm.M) adapter_tile<HalfTile, 1, 0, OUT_BF16>(g, m0, n0, smem);
+    }
 }
 
 // At most 16 rows
@@ -359,6 +384,13 @@ hipError_t launch_tile(AdapterArgs a, bool out_bf16, hipStream_t stream) {
     const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(NW * 64);
     if (out_bf16) adapter_kernel<BM, BN, NW, NSTAGE, SHARED, 0, 1><<<grid, block, 0, stream>>>(a);
     else adapter_kernel<BM, BN, NW, NSTAGE, SHARED, 0, 0><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+hipError_t launch_large(AdapterArgs a, bool out_bf16, hipStream_t stream) {
+    if (!lay_out(a.mm, 256, 256, 2 * 512)) return hipErrorInvalidValue;
+    const dim3 grid(share_grid(a.mm.tiles_m * a.mm.tiles_n, 0)), block(512);
+    if (out_bf16) adapter_large_kernel<1><<<grid, block, 0, stream>>>(a);
+    else adapter_large_kernel<0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 // (one stage: LDS holds u and the outputs only)
@@ -440,7 +472,7 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
     case 1: return launch_tile<64, 64, 4, 5>(g, out_bf16, stream);
     case 2: return launch_tile<128, 128, 4, 4>(g, out_bf16, stream);
     case 3: return launch_tile<128, 256, 8, 3>(g, out_bf16, stream);
-    case 4: return launch_tile<256, 256, 8, 2>(g, out_bf16, stream);
+    case 4: return launch_large(g, out_bf16, stream);
     case 5: return launch_tile<32, 32, 4, 8>(g, out_bf16, stream);
     default: return launch_tile<64, 32, 4, 8>(g, out_bf16, stream);
     }

@@ -13,7 +13,6 @@
 // pass over memory) or by the same product again with another epilogue, then takes two products whose
 // operands are transposed by their LDS reads.
 #include <cmath>
-#include <cstdlib>
 
 #include <fp8q.h>
 
@@ -80,13 +79,9 @@ __device__ __forceinline__ Activation activate(float a, int gelu) {
 }
 
 // MODE 0, 1: h in fp32, bf16; 2: dg and du
-template <int BM, int BN, int NW, int NSTAGE, int MODE>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_kernel(GatedArgs g) {
-    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+template <class T, int MODE>
+__device__ __forceinline__ void gated_tile(const GatedArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
     constexpr int HALF = T::SUB_N / 2;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
-    int64_t m0, n0;
-    find_tile<T, BN / 2>(g.mm, m0, n0);
     f32x4 acc[T::SUB_M][T::SUB_N];
     multiply<T, 0, 0, 1, MODE>(g.mm, m0, n0, smem, acc, []() {});
     const int64_t M = g.mm.M, F = g.mm.N;
@@ -122,6 +117,33 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
     if (g.gu) {
         store_tile<T, 1, HALF>(g.gu, 2 * F, m0, M, n0, F, smem, gate);
         store_tile<T, 1, HALF>(g.gu + F, 2 * F, m0, M, n0, F, smem, up);
+    }
+}
+
+template <int BM, int BN, int NW, int NSTAGE, int MODE>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_kernel(GatedArgs g) {
+    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    int64_t m0, n0;
+    find_tile<T, BN / 2>(g.mm, m0, n0);
+    gated_tile<T, MODE>(g, m0, n0, smem);
+}
+
+constexpr int kShareBytes = HalfTile::STAGE * HalfTile::NSTAGE;
+static_assert(kShareBytes >= WholeTile::STAGE * WholeTile::NSTAGE, "LDS of both");
+template <int MODE>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gated_large_kernel(GatedArgs g) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kShareBytes];
+    bool second;
+    int tile, half;
+    if (!find_share(g.mm.tiles_m * g.mm.tiles_n, 0, second, tile, half)) return;
+    int64_t m0, n0;
+    place_tile(g.mm, tile, 256, 128, m0, n0);
+    if (half < 0) {
+        gated_tile<WholeTile, MODE>(g, m0, n0, smem);
+    } else {
+        m0 += 128 * half;
+        if (m0 < g.mm.M) gated_tile<HalfTile, MODE>(g, m0, n0, smem);
     }
 }
 
@@ -194,6 +216,40 @@ struct ProductArgs {
     void *y;
     int splits;
 };
+template <class T, int XT, int OUT_BF16>
+__device__ __forceinline__ void grad_tile(const ProductArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
+    f32x4 acc[T::SUB_M][T::SUB_N];
+    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc, []() {});
+    store_tile<T, OUT_BF16, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, [&](int i, int j) { return acc[i][j]; });
+}
+
+// Both products' largest tiles in one launch (either may have none)
+template <int DX_BF16, int DW_BF16>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gated_grads_kernel(ProductArgs dw, ProductArgs dx) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kShareBytes];
+    bool second;
+    int tile, half;
+    if (!find_share(dw.mm.tiles_m * dw.mm.tiles_n, dx.mm.tiles_m * dx.mm.tiles_n, second, tile, half)) return;
+    int64_t m0, n0;
+    if (second) {
+        place_tile(dx.mm, tile, 256, 256, m0, n0);
+        if (half < 0) {
+            grad_tile<WholeTile, 0, DX_BF16>(dx, m0, n0, smem);
+        } else {
+            m0 += 128 * half;
+            if (m0 < dx.mm.M) grad_tile<HalfTile, 0, DX_BF16>(dx, m0, n0, smem);
+        }
+    } else {
+        place_tile(dw.mm, tile, 256, 256, m0, n0);
+        if (half < 0) {
+            grad_tile<WholeTile, 1, DW_BF16>(dw, m0, n0, smem);
+        } else {
+            m0 += 128 * half;
+            if (m0 < dw.mm.M) grad_tile<HalfTile, 1, DW_BF16>(dw, m0, n0, smem);
+        }
+    }
+}
+
 template <int BM, int BN, int NW, int NSTAGE, int XT, int OUT_BF16>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_grad_kernel(ProductArgs g) {
     using T = Tile<BM, BN, NW, 2, NSTAGE>;
@@ -208,9 +264,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
         g.mm.K = (k1 < g.mm.K ? k1 : g.mm.K) - k0;
         g.y = static_cast<float *>(g.y) + part * g.mm.M * g.mm.N;
     }
-    f32x4 acc[T::SUB_M][T::SUB_N];
-    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc, []() {});
-    store_tile<T, OUT_BF16, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, [&](int i, int j) { return acc[i][j]; });
+    grad_tile<T, XT, OUT_BF16>(g, m0, n0, smem);
 }
 
 // The parts' sums added in order, 8 elements a thread (their number is a multiple of 8)
@@ -255,6 +309,15 @@ int best_tile(const double *t, int n) {
     return best;
 }
 
+hipError_t launch_gated_large(GatedArgs a, int mode, hipStream_t stream) {
+    if (!lay_out(a.mm, 256, 128, 2 * 512)) return hipErrorInvalidValue;
+    const dim3 grid(share_grid(a.mm.tiles_m * a.mm.tiles_n, 0)), block(512);
+    if (mode == 0) gated_large_kernel<0><<<grid, block, 0, stream>>>(a);
+    else if (mode == 1) gated_large_kernel<1><<<grid, block, 0, stream>>>(a);
+    else gated_large_kernel<2><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <int RX>
 hipError_t launch_gated_few(const GatedArgs &a, int mode, hipStream_t stream) {
     const dim3 grid((unsigned)((a.mm.N + kFewN / 2 - 1) / (kFewN / 2))), block(256);
@@ -279,7 +342,7 @@ hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
     case 1: return launch_gated_tile<64, 64, 4, 5>(a, mode, stream);
     case 2: return launch_gated_tile<128, 128, 4, 4>(a, mode, stream);
     case 3: return launch_gated_tile<128, 256, 8, 3>(a, mode, stream);
-    default: return launch_gated_tile<256, 256, 8, 2>(a, mode, stream);
+    default: return launch_gated_large(a, mode, stream);
     }
 }
 
@@ -292,38 +355,37 @@ hipError_t launch_product_tile(ProductArgs a, bool out_bf16, hipStream_t stream)
     return hipGetLastError();
 }
 
-// A product's tile and the parts of its K, by their time: parts cost the writing and reading of their sums (at some
-// 4 TB/s) and a launch.
+// A product's tile and the parts of its K, by their time: rounds of 256 tiles, each an epilogue and K's steps; parts cost
+// the writing and reading of their sums (mostly from the caches) and a launch. The constants are fitted to times (us) at
+// 4096, 2048, 1021, 256 and 64 tokens of 7168 and 1536 channels and 512 to 4096 hidden ones, with 1 to 8 parts; K-strided X
+// (dW) takes a tenth longer. The largest tiles' last round may be half a one.
 struct Plan {
-    int tile, splits;
+    int tile, splits;   // tile: 0 .. 3
 };
-constexpr int kMaxParts = 8;
+constexpr int kMaxParts = 8, kLargest = 3;
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
     static const struct {
         int bm, bn;
         double first, more, end;
-    } tiles[4] = {{64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7}, {256, 256, 1.3, 1.5, 8.0}};
-    Plan best = {3, 1};
+    } tiles[4] = {{64, 64, 0.21, 0.19, 0.8}, {128, 128, 0.43, 0.46, 3.5}, {128, 256, 0.78, 0.82, 5.7}, {256, 256, 1.25, 1.35, 8.0}};
+    Plan best = {kLargest, 1};
     if (M == 0 || N == 0) return best;
     double least = HUGE_VAL;
     const int64_t steps = (K + KSTEP - 1) / KSTEP;
     for (int t = 0; t < 4; ++t)
         for (int s = 1; s <= kMaxParts && (s == 1 || steps / s >= 4); ++s) {
             const double n = (double)((M + tiles[t].bm - 1) / tiles[t].bm) * (double)((N + tiles[t].bn - 1) / tiles[t].bn) * s;
-            if (n > 1e6 && t < 3) continue;
+            if (n > 1e6 && t < kLargest) continue;   // (a grid holds 2^32 threads)
             const double rounds = std::ceil(n / 256.0), per = (double)((steps + s - 1) / s);
             const double us = per * (tiles[t].first + tiles[t].more * (rounds - 1.0)) + tiles[t].end * rounds +
-                              (s > 1 ? (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 4e6 + 4.0 : 0.0);
+                              (s > 1 ? (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 8e6 + 3.0 : 0.0);
             if (us < least) least = us, best = {t, s};
         }
     return best;
 }
 
 template <int XT>
-hipError_t launch_product(ProductArgs a, bool out_bf16, float *parts, hipStream_t stream) {
-    Plan p = plan_of(a.mm.M, a.mm.N, a.mm.K);
-    if (const char *e = getenv("GT")) p.tile = atoi(e);
-    if (const char *e = getenv("GS")) p.splits = atoi(e);
+hipError_t launch_product(ProductArgs a, Plan p, bool out_bf16, float *parts, hipStream_t stream) {
     void *const y = a.y;
     const bool bf16 = out_bf16 && p.splits == 1;
     a.splits = p.splits;
@@ -340,6 +402,16 @@ hipError_t launch_product(ProductArgs a, bool out_bf16, float *parts, hipStream_
     const dim3 grid((unsigned)(need < 4096 ? need : 4096)), block(256);
     if (out_bf16) gated_sum_kernel<1><<<grid, block, 0, stream>>>(parts, y, n, p.splits);
     else gated_sum_kernel<0><<<grid, block, 0, stream>>>(parts, y, n, p.splits);
+    return hipGetLastError();
+}
+
+hipError_t launch_grads(ProductArgs dw, ProductArgs dx, bool dw_bf16, bool dx_bf16, hipStream_t stream) {
+    if (!lay_out(dw.mm, 256, 256, 4 * 512) || !lay_out(dx.mm, 256, 256, 4 * 512)) return hipErrorInvalidValue;
+    const dim3 grid(share_grid(dw.mm.tiles_m * dw.mm.tiles_n, dx.mm.tiles_m * dx.mm.tiles_n)), block(512);
+    if (dx_bf16 && dw_bf16) gated_grads_kernel<1, 1><<<grid, block, 0, stream>>>(dw, dx);
+    else if (dx_bf16) gated_grads_kernel<1, 0><<<grid, block, 0, stream>>>(dw, dx);
+    else if (dw_bf16) gated_grads_kernel<0, 1><<<grid, block, 0, stream>>>(dw, dx);
+    else gated_grads_kernel<0, 0><<<grid, block, 0, stream>>>(dw, dx);
     return hipGetLastError();
 }
 
@@ -371,10 +443,15 @@ hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, c
             return e;
         }
     }
-    if (dx && M > 0 && K > 0)
-        if (hipError_t e = launch_product<0>({{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, 1}, dx_bf16, parts, stream)) return e;
-    if (dw && F > 0 && K > 0)
-        if (hipError_t e = launch_product<1>({{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, 1}, dw_bf16, parts, stream)) return e;
+    const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, 1}, pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, 1};
+    const Plan lx = plan_of(M, K, 2 * F), lw = plan_of(2 * F, K, M);
+    const bool has_x = dx && M > 0 && K > 0, has_w = dw && F > 0 && K > 0;
+    if (has_x && has_w && lx.tile == kLargest && lw.tile == kLargest && lx.splits == 1 && lw.splits == 1)
+        return launch_grads(pw, px, dw_bf16, dx_bf16, stream);
+    if (has_x)
+        if (hipError_t e = launch_product<0>(px, lx, dx_bf16, parts, stream)) return e;
+    if (has_w)
+        if (hipError_t e = launch_product<1>(pw, lw, dw_bf16, parts, stream)) return e;
     return hipSuccess;
 }
 

@@ -109,6 +109,15 @@ struct MmArgs {
     int tiles_m, tiles_n, group;
 };
 
+// The m and n of tile number `tile`
+__device__ __forceinline__ void place_tile(const MmArgs &g, int tile, int bm, int bn, int64_t &m0, int64_t &n0) {
+    const int band = tile / (g.group * g.tiles_n);
+    const int in_band = tile - band * g.group * g.tiles_n;
+    const int band_rows = min(g.group, g.tiles_m - band * g.group);
+    m0 = (int64_t)(band * g.group + in_band % band_rows) * bm;
+    n0 = (int64_t)(in_band / band_rows) * bn;
+}
+
 // Workgroup b's tile. Workgroups are dealt round-robin to the 8 XCDs; each XCD takes a contiguous run of
 // the tile numbers, which go down `group` tile rows per tile column, so that the tiles that an XCD holds
 // at once share panels in its L2. NT: columns of Y in a tile. parts: the tiles that many times over; returns which.
@@ -120,13 +129,41 @@ __device__ __forceinline__ int find_tile(const MmArgs &g, int64_t &m0, int64_t &
     int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
     const int part = tl / (g.tiles_m * g.tiles_n);
     tl -= part * (g.tiles_m * g.tiles_n);
-    const int band = tl / (g.group * g.tiles_n);
-    const int in_band = tl - band * g.group * g.tiles_n;
-    const int band_rows = min(g.group, g.tiles_m - band * g.group);
-    m0 = (int64_t)(band * g.group + in_band % band_rows) * T::BM;
-    n0 = (int64_t)(in_band / band_rows) * NT;
+    place_tile(g, tl, T::BM, NT, m0, n0);
     return part;
 }
+
+// The largest tiles, of one product or of two independent ones of n_a and n_b tiles, one a CU: each XCD takes a
+// contiguous run of a's and one of b's. Where they are more than its 32 CUs take at once and the last round has
+// at most 16, that round's tiles are cut into halves of 128 rows for twice the CUs (896 tiles of 256 x 256: 3.5 rounds
+// instead of 4, a 12th of the time). Returns false where a workgroup has none; half: -1 (whole), 0 or 1.
+__host__ __device__ __forceinline__ int run_of(int n, int xcd) { return (int)((int64_t)n * xcd / 8); }
+__host__ __device__ __forceinline__ int whole_of(int total) {
+    const int last = total & 31;
+    return total > 32 && last <= 16 ? total - last : total;
+}
+__device__ __forceinline__ bool find_share(int n_a, int n_b, bool &second, int &tile, int &half) {
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int a0 = run_of(n_a, xcd), b0 = run_of(n_b, xcd), a = run_of(n_a, xcd + 1) - a0, total = a + run_of(n_b, xcd + 1) - b0;
+    const int whole = whole_of(total);
+    int at = slot;
+    half = -1;
+    if (slot >= whole) at = whole + (slot - whole) / 2, half = (slot - whole) & 1;
+    second = at >= a;
+    tile = second ? b0 + at - a : a0 + at;
+    return at < total;
+}
+inline unsigned share_grid(int n_a, int n_b) {
+    int most = 0;
+    for (int xcd = 0; xcd < 8; ++xcd) {
+        const int total = run_of(n_a, xcd + 1) - run_of(n_a, xcd) + run_of(n_b, xcd + 1) - run_of(n_b, xcd);
+        const int slots = 2 * total - whole_of(total);
+        most = slots > most ? slots : most;
+    }
+    return 8 * (unsigned)most;
+}
+using WholeTile = Tile<256, 256, 8, 2, 2>;
+using HalfTile = Tile<128, 256, 8, 2, 3>;
 
 // The tiles of a launch, and down how many tile rows to walk (so that the some 32 tiles of an XCD read the
 // fewest rows of both operands). False: more than a grid holds.
