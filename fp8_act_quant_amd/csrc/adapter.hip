@@ -145,11 +145,11 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterArgs g) {
 
 // 32 ranks of the u of ROWS rows into LDS (fp32, pitch UP), the parts of K added in order; zeros past the rank
 // and where a row has no adapter. Read by each lane for itself from memory they took longer than all
-// else that an adapter costs (1021 x 1533, 8 parts: 27 us, now 7). Between two barriers.
+// else that an adapter costs (1021 x 1533, 8 parts: 27 us, now 7). For the whole workgroup; what reads it comes after
+// a barrier.
 constexpr int kChunk = 32, UP = kChunk + 4;
 template <int ROWS, int THREADS>
 __device__ __forceinline__ void stage_u(const AdapterArgs &g, int64_t m0, int r0, float *lds) {
-    __syncthreads();
     for (int p = threadIdx.x; p < ROWS * (kChunk / 4); p += THREADS) {
         const int row = p / (kChunk / 4), r = r0 + 4 * (p % (kChunk / 4));
         const int64_t m = m0 + row;
@@ -166,7 +166,6 @@ __device__ __forceinline__ void stage_u(const AdapterArgs &g, int64_t m0, int r0
         }
         *reinterpret_cast<f32x4 *>(lds + row * UP + 4 * (p % (kChunk / 4))) = v;
     }
-    __syncthreads();
 }
 
 // Three bf16 numbers whose sum is v: two cut off (exactly, whatever v is) and the rest, which has 8 bits.
@@ -188,7 +187,9 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, i
                                              f32x4 (&acc)[T::SUB_M][T::SUB_N]) {
     const int lane = threadIdx.x & 63, wm = wave_m<T>(), row = lane & 15, kg = lane >> 4;
     for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
+        __syncthreads();
         stage_u<T::BM, T::NW * 64>(g, m0, r0, lds);
+        __syncthreads();
         const int r = r0 + 8 * kg;
 #pragma unroll
         for (int i = 0; i < T::SUB_M; ++i) {
@@ -243,26 +244,81 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, i
 }
 
 // The same where rows may all have different adapters: each lane takes its row's adapter by itself, in fp32, for
-// 4 columns from n on. u: of the row, `ranks` of them from r0 on.
-__device__ __forceinline__ void own_adapter(const AdapterArgs &g, int id, int64_t n, const float *u, int r0, f32x4 &sum) {
-    if (id < 0 || n >= g.mm.N) return;
-    const uint16_t *b = g.b + ((int64_t)id * g.mm.N + n) * g.rank + r0;
-    const int64_t last = g.mm.N - 1 - n;
-    const int ranks = g.rank - r0 < kChunk ? g.rank - r0 : kChunk;
-#pragma unroll 2
-    for (int r = 0; r < ranks; r += 8) {
-        const f32x4 lo = *reinterpret_cast<const f32x4 *>(u + r), hi = *reinterpret_cast<const f32x4 *>(u + r + 4);
+// the 4 columns of each of its blocks. begin() asks for the first 16 ranks of B and puts the first ranks of u into
+// LDS; end() comes after the product, during which those loads arrive (waited for at once, they and the ids before
+// them took 8 us of a 48 x 7168 x 7168 product's 30).
+template <int SM, int SN, int ROWS, int THREADS>
+struct OwnAdapters {
+    int id[SM];
+    u32x4 first[SM][SN][4][2];
+
+    // B's ranks r .. r + 7 for columns n .. n + 3; columns past N repeat the last one (they are not stored)
+    __device__ __forceinline__ void read(const AdapterArgs &g, int e, int64_t n, int r, u32x4 (&v)[4]) const {
+        const uint16_t *b = g.b + ((int64_t)e * g.mm.N + n) * g.rank + r;
+        const int64_t last = g.mm.N - 1 - n;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // (columns past N repeat the last one: they are not stored)
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(b + (q < last ? q : last) * g.rank + r);
+        for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const u32x4 *>(b + (q < last ? q : last) * g.rank);
+    }
+    __device__ __forceinline__ static void add(const float *u, const u32x4 (&v)[4], f32x4 &sum) {
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(u), hi = *reinterpret_cast<const f32x4 *>(u + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                sum[q] = __builtin_fmaf(p < 2 ? lo[2 * p] : hi[2 * p - 4], bf16lo_to_f32(v[p]), sum[q]);
-                sum[q] = __builtin_fmaf(p < 2 ? lo[2 * p + 1] : hi[2 * p - 3], bf16hi_to_f32(v[p]), sum[q]);
+                sum[q] = __builtin_fmaf(p < 2 ? lo[2 * p] : hi[2 * p - 4], bf16lo_to_f32(v[q][p]), sum[q]);
+                sum[q] = __builtin_fmaf(p < 2 ? lo[2 * p + 1] : hi[2 * p - 3], bf16hi_to_f32(v[q][p]), sum[q]);
             }
+    }
+    // within: the lane's row of group i, i = 0 .. SM - 1, counted from m0; col: the first of its columns in block j
+    template <class W, class C>
+    __device__ __forceinline__ void begin(const AdapterArgs &g, int64_t m0, float *lds, const W &within, const C &col) {
+#pragma unroll
+        for (int i = 0; i < SM; ++i) id[i] = adapter_of(g, m0 + within(i));
+        stage_u<ROWS, THREADS>(g, m0, 0, lds);
+#pragma unroll
+        for (int i = 0; i < SM; ++i)
+#pragma unroll
+            for (int j = 0; j < SN; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (id[i] >= 0 && col(j) < g.mm.N && 8 * h < g.rank) {
+                        u32x4 v[4];
+                        read(g, id[i], col(j), 8 * h, v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) first[i][j][q][h] = v[q];
+                    }
+    }
+    template <class W, class C>
+    __device__ __forceinline__ void end(const AdapterArgs &g, int64_t m0, float *lds, const W &within, const C &col,
+                                        f32x4 (&acc)[SM][SN]) const {
+        for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
+            if (r0) {
+                __syncthreads();
+                stage_u<ROWS, THREADS>(g, m0, r0, lds);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < SM; ++i)
+#pragma unroll
+                for (int j = 0; j < SN; ++j) {
+                    if (id[i] < 0 || col(j) >= g.mm.N) continue;
+                    const float *u = lds + within(i) * UP;
+#pragma unroll
+                    for (int r = 0; r < kChunk; r += 8) {
+                        if (r0 + r >= g.rank) continue;
+                        u32x4 v[4];
+                        if (r0 == 0 && r < 16) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q] = first[i][j][q][r / 8];
+                        } else {
+                            read(g, id[i], col(j), r0 + r, v);
+                        }
+                        add(u + r, v, acc[i][j]);
+                    }
+                }
         }
     }
-}
+};
 
 __device__ __forceinline__ f32x4 bias_of(const AdapterArgs &g, int64_t n) {
     return g.bias && n < g.mm.N ? load4<0>(g.bias, n, g.mm.N - n) : f32x4{0.f, 0.f, 0.f, 0.f};
@@ -281,30 +337,23 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs &g, int64_t m0, i
     const int lane = threadIdx.x & 63, wm = wave_m<T>(), wn = wave_n<T>();
     const int64_t col = n0 + wn * T::WN, M = g.mm.M, N = g.mm.N;
     f32x4 acc[T::SUB_M][T::SUB_N];
-    auto own = [&]() {
-        if constexpr (!SHARED) {
-            for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
-                stage_u<T::BM, T::NW * 64>(g, m0, r0, lds);
-#pragma unroll
-                for (int i = 0; i < T::SUB_M; ++i) {
-                    const int within = T::row(wm, i) + (lane & 15), id = adapter_of(g, m0 + within);
-#pragma unroll
-                    for (int j = 0; j < T::SUB_N; ++j)
-                        own_adapter(g, id, col + 16 * j + 4 * (lane >> 4), lds + within * UP, r0, acc[i][j]);
-                }
-            }
-        }
+    auto within = [&](int i) { return T::row(wm, i) + (lane & 15); };
+    auto first = [&](int j) { return col + 16 * j + 4 * (lane >> 4); };
+    OwnAdapters<SHARED ? 1 : T::SUB_M, SHARED ? 1 : T::SUB_N, T::BM, T::NW * 64> own;
+    auto begin = [&]() {
+        if constexpr (!SHARED) own.begin(g, m0, lds, within, first);
     };
     if constexpr (ADD) {
 #pragma unroll
         for (int i = 0; i < T::SUB_M; ++i)
 #pragma unroll
             for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        own();
+        begin();
     } else {
-        multiply<T, 0, 0, 0, OUT_BF16>(g.mm, m0, n0, smem, acc, own);
+        multiply<T, 0, 0, 0, OUT_BF16>(g.mm, m0, n0, smem, acc, begin);
     }
     if constexpr (SHARED) add_adapters<T>(g, m0, col, lds, acc);
+    else own.end(g, m0, lds, within, first, acc);
     f32x4 bias[T::SUB_N];
 #pragma unroll
     for (int j = 0; j < T::SUB_N; ++j) bias[j] = bias_of(g, col + 16 * j + 4 * (lane >> 4));
@@ -353,28 +402,15 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs g) {
     const int64_t n0 = (int64_t)blockIdx.x * kFewN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = n0 + 16 * (wave & 1) + 4 * (lane >> 4), N = g.mm.N;
-    f32x4 own[RX], acc[RX];
-#pragma unroll
-    for (int i = 0; i < RX; ++i) own[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    few<RX, 0, OUT_BF16>(g.mm, n0, smem, acc, [&]() {
-        for (int r0 = 0; r0 < g.rank; r0 += kChunk) {
-            stage_u<Few<RX>::ROWS, 256>(g, 0, r0, u);
-            if (wave < 2) {
-#pragma unroll
-                for (int i = 0; i < RX; ++i) {
-                    const int m = 16 * i + (lane & 15);
-                    own_adapter(g, adapter_of(g, m), n, u + m * UP, r0, own[i]);
-                }
-            }
-        }
-    });
-    if (wave >= 2) return;
-    const f32x4 bias = bias_of(g, n);
-#pragma unroll
-    for (int i = 0; i < RX; ++i) {
-        const int64_t m = 16 * i + (lane & 15);
-        if (m < g.mm.M && n < N) store4<OUT_BF16>(g.y, m * N + n, acc[i] + own[i] + bias, N - n);
-    }
+    auto within = [&](int) { return lane & 15; };
+    auto first = [&](int) { return n; };
+    OwnAdapters<1, 1, Few<RX>::ROWS, 256> own;
+    f32x4 sum[RX], acc[1][1];
+    few<RX, 0, OUT_BF16>(g.mm, n0, smem, sum, [&]() { own.begin(g, 0, u, within, first); });
+    acc[0][0] = sum[0];
+    own.end(g, 0, u, within, first, acc);
+    const int64_t m = lane & 15;
+    if (wave < 2 && m < g.mm.M && n < N) store4<OUT_BF16>(g.y, m * N + n, acc[0][0] + bias_of(g, n), N - n);
 }
 
 template <int BM, int BN, int NW, int NSTAGE>
@@ -457,16 +493,18 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
     if (!w && base) return M <= 64 ? launch_add<0>(g, out_bf16, stream) : launch_add<1>(g, out_bf16, stream);
     // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
     if (M <= Few<1>::ROWS) return launch_few(g, out_bf16, stream);
-    auto time = [&](int bm, int bn, double first, double more, double end) {
-        const double tiles = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn), rounds = std::ceil(tiles / 256.0);
-        return (double)((K + KSTEP - 1) / KSTEP) * (first + more * (rounds - 1.0)) + end * rounds;
-    };
-    const double t[7] = {time(32, 64, 0.155, 0.125, 1.1), time(64, 64, 0.21, 0.18, 1.4), time(128, 128, 0.45, 0.53, 5.0),
-                         time(128, 256, 0.75, 0.83, 5.7), time(256, 256, 1.3, 1.5, 8.0),
-                         time(32, 32, 0.105, 0.085, 1.0), time(64, 32, 0.145, 0.12, 1.1)};
-    int best = 0;
-    for (int i = 1; i < 7; ++i)
-        if (t[i] < t[best]) best = i;
+    static const struct {
+        int bm, bn;
+        double first, more, end;
+    } tiles[7] = {{32, 64, 0.155, 0.125, 1.1}, {64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7},
+                  {256, 256, 1.3, 1.5, 8.0}, {32, 32, 0.105, 0.085, 1.0}, {64, 32, 0.145, 0.12, 1.1}};
+    int best = 4;
+    double least = HUGE_VAL;
+    for (int t = 0; t < 7; ++t) {
+        const double us = tile_time(M, N, (K + KSTEP - 1) / KSTEP, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more, tiles[t].end,
+                                    t == 4);
+        if (us < least) least = us, best = t;
+    }
     switch (best) {
     case 0: return launch_tile<32, 64, 4, 6>(g, out_bf16, stream);
     case 1: return launch_tile<64, 64, 4, 5>(g, out_bf16, stream);

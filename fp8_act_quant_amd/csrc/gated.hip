@@ -297,18 +297,6 @@ hipError_t launch_gated_tile(GatedArgs a, int mode, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The tile by its time: rounds of 256 tiles (one a CU), each an epilogue and K's steps.
-double tile_time(int64_t M, int64_t N, int64_t K, int bm, int bn, double first, double more, double end) {
-    const double tiles = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn), rounds = std::ceil(tiles / 256.0);
-    return (double)((K + KSTEP - 1) / KSTEP) * (first + more * (rounds - 1.0)) + end * rounds;
-}
-int best_tile(const double *t, int n) {
-    int best = 0;
-    for (int i = 1; i < n; ++i)
-        if (t[i] < t[best]) best = i;
-    return best;
-}
-
 hipError_t launch_gated_large(GatedArgs a, int mode, hipStream_t stream) {
     if (!lay_out(a.mm, 256, 128, 2 * 512)) return hipErrorInvalidValue;
     const dim3 grid(share_grid(a.mm.tiles_m * a.mm.tiles_n, 0)), block(512);
@@ -333,11 +321,19 @@ hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
     // blocks of rows) 30.0 / 26.1
     if (M <= 16) return launch_gated_few<1>(a, mode, stream);
     if (M <= 32) return launch_gated_few<2>(a, mode, stream);
-    const double t[5] = {tile_time(M, 2 * F, K, 32, 64, 0.155, 0.125, 1.1), tile_time(M, 2 * F, K, 64, 64, 0.21, 0.18, 1.4),
-                         tile_time(M, 2 * F, K, 128, 128, 0.45, 0.53, 5.0),
-                         tile_time(M, 2 * F, K, 128, 256, 0.75, 0.83, 5.7),
-                         tile_time(M, 2 * F, K, 256, 256, 1.3, 1.5, 8.0)};
-    switch (best_tile(t, 5)) {
+    static const struct {
+        int bm, bn;
+        double first, more, end;
+    } tiles[5] = {{32, 64, 0.155, 0.125, 1.1}, {64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7},
+                  {256, 256, 1.3, 1.5, 8.0}};
+    int best = 4;
+    double least = HUGE_VAL;
+    for (int t = 0; t < 5; ++t) {
+        const double us = tile_time(M, 2 * F, (K + KSTEP - 1) / KSTEP, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more,
+                                    tiles[t].end, t == 4);
+        if (us < least) least = us, best = t;
+    }
+    switch (best) {
     case 0: return launch_gated_tile<32, 64, 4, 6>(a, mode, stream);
     case 1: return launch_gated_tile<64, 64, 4, 5>(a, mode, stream);
     case 2: return launch_gated_tile<128, 128, 4, 4>(a, mode, stream);
@@ -374,10 +370,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
     const int64_t steps = (K + KSTEP - 1) / KSTEP;
     for (int t = 0; t < 4; ++t)
         for (int s = 1; s <= kMaxParts && (s == 1 || steps / s >= 4); ++s) {
-            const double n = (double)((M + tiles[t].bm - 1) / tiles[t].bm) * (double)((N + tiles[t].bn - 1) / tiles[t].bn) * s;
-            if (n > 1e6 && t < kLargest) continue;   // (a grid holds 2^32 threads)
-            const double rounds = std::ceil(n / 256.0), per = (double)((steps + s - 1) / s);
-            const double us = per * (tiles[t].first + tiles[t].more * (rounds - 1.0)) + tiles[t].end * rounds +
+            // (a part's tiles follow one another's as if they were rows below)
+            const int64_t rows = (M + tiles[t].bm - 1) / tiles[t].bm * tiles[t].bm * s;
+            const double us = tile_time(rows, N, (steps + s - 1) / s, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more,
+                                        tiles[t].end, false) +
                               (s > 1 ? (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 8e6 + 3.0 : 0.0);
             if (us < least) least = us, best = {t, s};
         }

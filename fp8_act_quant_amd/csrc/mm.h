@@ -162,6 +162,15 @@ inline unsigned share_grid(int n_a, int n_b) {
     }
     return 8 * (unsigned)most;
 }
+// A product's time (us) by its tiles: rounds of 256 of them (one a CU), each an epilogue and K's steps, of which a later
+// round's may hide behind the round before. halves: the last round may be half a one.
+inline double tile_time(int64_t M, int64_t N, int64_t steps, int bm, int bn, double first, double more, double end, bool halves) {
+    const double n = (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn);
+    if (n > 4e6) return halves ? 1e30 : 1e31;   // (a grid holds 2^32 threads; the largest tiles have the fewest)
+    const int64_t whole = (int64_t)n / 256, last = (int64_t)n % 256;
+    const double rounds = (double)whole + (last == 0 ? 0.0 : halves && whole > 0 && last <= 128 ? 0.6 : 1.0);
+    return (double)steps * (first + more * (rounds - 1.0)) + end * rounds;
+}
 using WholeTile = Tile<256, 256, 8, 2, 2>;
 using HalfTile = Tile<128, 256, 8, 2, 3>;
 
