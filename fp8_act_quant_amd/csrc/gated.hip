@@ -209,53 +209,30 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const uint16_t *dh, co
     }
 }
 
-// dx (XT 0) and dW (XT 1): W's operand is K-strided in both. K in `splits` parts, each a set of tiles of its own,
-// whose sums go to y + part * M * N and are added by a second kernel.
+// The gradient's products, dW = d^T x and dx = d W, in one launch: W's operand is K-strided in both, X's in dW's (XT).
+// K in `splits` parts, each a set of tiles of its own, whose sums go to y + part * M * N and are added by a
+// second kernel.
 struct ProductArgs {
     MmArgs mm;
     void *y;
-    int splits;
+    int bf16, splits;   // splits 0: not wanted
 };
-template <class T, int XT, int OUT_BF16>
+__host__ __device__ __forceinline__ int tiles_of(const ProductArgs &g) { return g.mm.tiles_m * g.mm.tiles_n * g.splits; }
+
+template <class T, int XT, int TAG>
 __device__ __forceinline__ void grad_tile(const ProductArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
     f32x4 acc[T::SUB_M][T::SUB_N];
-    multiply<T, XT, 1, 0, 4 + 2 * XT + OUT_BF16>(g.mm, m0, n0, smem, acc, []() {});
-    store_tile<T, OUT_BF16, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, [&](int i, int j) { return acc[i][j]; });
+    multiply<T, XT, 1, 0, TAG>(g.mm, m0, n0, smem, acc, []() {});
+    auto value = [&](int i, int j) { return acc[i][j]; };
+    if (g.bf16) store_tile<T, 1, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, value);
+    else store_tile<T, 0, T::SUB_N>(g.y, g.mm.N, m0, g.mm.M, n0, g.mm.N, smem, value);
 }
 
-// Both products' largest tiles in one launch (either may have none)
-template <int DX_BF16, int DW_BF16>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gated_grads_kernel(ProductArgs dw, ProductArgs dx) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[kShareBytes];
-    bool second;
-    int tile, half;
-    if (!find_share(dw.mm.tiles_m * dw.mm.tiles_n, dx.mm.tiles_m * dx.mm.tiles_n, second, tile, half)) return;
+template <class T, int XT, int TAG>
+__device__ __forceinline__ void grad_part(ProductArgs g, int tile, uint8_t *smem) {
+    const int n = g.mm.tiles_m * g.mm.tiles_n, part = tile / n;
     int64_t m0, n0;
-    if (second) {
-        place_tile(dx.mm, tile, 256, 256, m0, n0);
-        if (half < 0) {
-            grad_tile<WholeTile, 0, DX_BF16>(dx, m0, n0, smem);
-        } else {
-            m0 += 128 * half;
-            if (m0 < dx.mm.M) grad_tile<HalfTile, 0, DX_BF16>(dx, m0, n0, smem);
-        }
-    } else {
-        place_tile(dw.mm, tile, 256, 256, m0, n0);
-        if (half < 0) {
-            grad_tile<WholeTile, 1, DW_BF16>(dw, m0, n0, smem);
-        } else {
-            m0 += 128 * half;
-            if (m0 < dw.mm.M) grad_tile<HalfTile, 1, DW_BF16>(dw, m0, n0, smem);
-        }
-    }
-}
-
-template <int BM, int BN, int NW, int NSTAGE, int XT, int OUT_BF16>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_grad_kernel(ProductArgs g) {
-    using T = Tile<BM, BN, NW, 2, NSTAGE>;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
-    int64_t m0, n0;
-    const int part = find_tile<T, BN>(g.mm, m0, n0, g.splits);
+    place_tile(g.mm, tile - part * n, T::BM, T::BN, m0, n0);
     if (g.splits > 1) {
         const int64_t steps = (g.mm.K + KSTEP - 1) / KSTEP;
         const int64_t k0 = part * steps / g.splits * KSTEP, k1 = (part + 1) * steps / g.splits * KSTEP;
@@ -263,21 +240,71 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8
         g.mm.w += k0 * g.mm.ldw;
         g.mm.K = (k1 < g.mm.K ? k1 : g.mm.K) - k0;
         g.y = static_cast<float *>(g.y) + part * g.mm.M * g.mm.N;
+        g.bf16 = 0;
     }
-    grad_tile<T, XT, OUT_BF16>(g, m0, n0, smem);
+    grad_tile<T, XT, TAG>(g, m0, n0, smem);
 }
 
-// The parts' sums added in order, 8 elements a thread (their number is a multiple of 8)
-template <int OUT_BF16>
-__global__ __launch_bounds__(256) void gated_sum_kernel(const float *parts, void *y, int64_t n, int splits) {
+// Each XCD takes a contiguous run of dW's tiles, then one of dx's
+template <int BM, int BN, int NW, int NSTAGE>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW == 8 ? 2 : 1, 2))) void gated_grads_kernel(ProductArgs dw, ProductArgs dx) {
+    using T = Tile<BM, BN, NW, 2, NSTAGE>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[T::STAGE * NSTAGE];
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    const int w0 = run_of(tiles_of(dw), xcd), w = run_of(tiles_of(dw), xcd + 1) - w0;
+    const int x0 = run_of(tiles_of(dx), xcd), x = run_of(tiles_of(dx), xcd + 1) - x0;
+    if (slot < w) grad_part<T, 1, 4>(dw, w0 + slot, smem);
+    else if (slot < w + x) grad_part<T, 0, 4>(dx, x0 + slot - w, smem);
+}
+
+// The largest tiles, K whole
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gated_grads_large_kernel(ProductArgs dw, ProductArgs dx) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kShareBytes];
+    bool second;
+    int tile, half;
+    if (!find_share(tiles_of(dw), tiles_of(dx), second, tile, half)) return;
+    int64_t m0, n0;
+    if (second) {
+        place_tile(dx.mm, tile, 256, 256, m0, n0);
+        if (half < 0) {
+            grad_tile<WholeTile, 0, 5>(dx, m0, n0, smem);
+        } else {
+            m0 += 128 * half;
+            if (m0 < dx.mm.M) grad_tile<HalfTile, 0, 5>(dx, m0, n0, smem);
+        }
+    } else {
+        place_tile(dw.mm, tile, 256, 256, m0, n0);
+        if (half < 0) {
+            grad_tile<WholeTile, 1, 5>(dw, m0, n0, smem);
+        } else {
+            m0 += 128 * half;
+            if (m0 < dw.mm.M) grad_tile<HalfTile, 1, 5>(dw, m0, n0, smem);
+        }
+    }
+}
+
+// The parts' sums added in order, 8 elements a thread (their number is a multiple of 8), of either product that has
+// parts; y: where they go
+struct SumArgs {
+    const float *parts[2];
+    void *y[2];
+    int64_t n[2];   // 0: no parts
+    int bf16[2], splits[2];
+};
+__global__ __launch_bounds__(256) void gated_sum_kernel(SumArgs g) {
     const int64_t step = (int64_t)gridDim.x * 256 * 8;
-    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < n; at += step) {
+    for (int64_t p = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; p < g.n[0] + g.n[1]; p += step) {
+        const int which = p >= g.n[0];
+        const int64_t at = which ? p - g.n[0] : p, n = which ? g.n[1] : g.n[0];
+        const float *from = (which ? g.parts[1] : g.parts[0]) + at;
+        const int splits = which ? g.splits[1] : g.splits[0];
+        void *const y = which ? g.y[1] : g.y[0];
         f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
         for (int s = 0; s < splits; ++s) {
-            a += *reinterpret_cast<const f32x4 *>(parts + s * n + at);
-            b += *reinterpret_cast<const f32x4 *>(parts + s * n + at + 4);
+            a += *reinterpret_cast<const f32x4 *>(from + s * n);
+            b += *reinterpret_cast<const f32x4 *>(from + s * n + 4);
         }
-        if constexpr (OUT_BF16) {
+        if (which ? g.bf16[1] : g.bf16[0]) {
             *reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(y) + at) = u32x4{
                 pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
         } else {
@@ -342,72 +369,92 @@ hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
     }
 }
 
-template <int BM, int BN, int NW, int NSTAGE, int XT>
-hipError_t launch_product_tile(ProductArgs a, bool out_bf16, hipStream_t stream) {
-    if (!lay_out(a.mm, BM, BN, NW * 64)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n * a.splits)), block(NW * 64);
-    if (out_bf16) gated_grad_kernel<BM, BN, NW, NSTAGE, XT, 1><<<grid, block, 0, stream>>>(a);
-    else gated_grad_kernel<BM, BN, NW, NSTAGE, XT, 0><<<grid, block, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
-// A product's tile and the parts of its K, by their time: rounds of 256 tiles, each an epilogue and K's steps; parts cost
-// the writing and reading of their sums (mostly from the caches) and a launch. The constants are fitted to times (us) at
-// 4096, 2048, 1021, 256 and 64 tokens of 7168 and 1536 channels and 512 to 4096 hidden ones, with 1 to 8 parts; K-strided X
-// (dW) takes a tenth longer. The largest tiles' last round may be half a one.
+// The gradient's tiles and the parts of its products' K, by their time (us): up to 256 tiles run at once, one a CU, each
+// K's steps and an epilogue; more of them take turns. Parts cost the writing and reading of their sums (mostly from the
+// caches) and a launch. The constants are fitted to times at 4096, 2048, 1021, 256 and 64 tokens of 7168 and 1536 channels
+// and 512 to 4096 hidden ones, with 1 to 8 parts; K-strided X (dW) takes a tenth longer. Both products in one launch, by
+// one kind of tile, or each by its own: 1021 tokens, 1536 -> 4096 78 / 70 us, 1000 x 1096 -> 1000 26 / 33.
 struct Plan {
-    int tile, splits;   // tile: 0 .. 3
+    int tile, parts_w, parts_x;   // tile: 0 .. kLargest; the parts of a product that is not in it 0
+    double us;
 };
 constexpr int kMaxParts = 8, kLargest = 3;
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
+Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
     static const struct {
         int bm, bn;
         double first, more, end;
     } tiles[4] = {{64, 64, 0.21, 0.19, 0.8}, {128, 128, 0.43, 0.46, 3.5}, {128, 256, 0.78, 0.82, 5.7}, {256, 256, 1.25, 1.35, 8.0}};
-    Plan best = {kLargest, 1};
-    if (M == 0 || N == 0) return best;
-    double least = HUGE_VAL;
-    const int64_t steps = (K + KSTEP - 1) / KSTEP;
-    for (int t = 0; t < 4; ++t)
-        for (int s = 1; s <= kMaxParts && (s == 1 || steps / s >= 4); ++s) {
-            // (a part's tiles follow one another's as if they were rows below)
-            const int64_t rows = (M + tiles[t].bm - 1) / tiles[t].bm * tiles[t].bm * s;
-            const double us = tile_time(rows, N, (steps + s - 1) / s, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more,
-                                        tiles[t].end, false) +
-                              (s > 1 ? (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 8e6 + 3.0 : 0.0);
-            if (us < least) least = us, best = {t, s};
-        }
+    Plan best = {kLargest, has_w, has_x, HUGE_VAL};
+    const int64_t steps_w = (M + KSTEP - 1) / KSTEP, steps_x = (2 * F + KSTEP - 1) / KSTEP;
+    auto sums = [](int s, int64_t n) { return s > 1 ? (2.0 * s + 1.0) * (double)n * 4.0 / 8e6 : 0.0; };
+    for (int t = 0; t <= kLargest; ++t) {
+        auto count = [&](int64_t m, int64_t n) {
+            return (double)((m + tiles[t].bm - 1) / tiles[t].bm) * (double)((n + tiles[t].bn - 1) / tiles[t].bn);
+        };
+        auto most = [&](bool has, int64_t steps) {
+            return !has ? 0 : t == kLargest || steps < 8 ? 1 : steps / 4 < kMaxParts ? (int)(steps / 4) : kMaxParts;
+        };
+        for (int sw = has_w; sw <= most(has_w, steps_w); ++sw)
+            for (int sx = has_x; sx <= most(has_x, steps_x); ++sx) {
+                const double nw = count(2 * F, K) * sw, nx = count(M, K) * sx, n = nw + nx;
+                if (n > 1e6 && t < kLargest) continue;   // (a grid holds 2^32 threads)
+                const double pw = sw ? 1.1 * (double)((steps_w + sw - 1) / sw) : 0.0, px = sx ? (double)((steps_x + sx - 1) / sx) : 0.0;
+                const double longest = pw > px ? pw : px;
+                const double run = n <= 256.0 ? longest * tiles[t].first + tiles[t].end
+                                              : tiles[t].more * ((nw * pw + nx * px) / 256.0 + 0.5 * longest) + tiles[t].end * (n / 256.0 + 0.5);
+                const double us = run + (sw > 1 || sx > 1 ? 3.0 : 0.0) + sums(sw, 2 * F * K) + sums(sx, M * K);
+                if (us < best.us) best = {t, sw, sx, us};
+            }
+    }
     return best;
 }
+struct Plans {
+    bool joint;
+    Plan both, w, x;
+};
+Plans plans_of(int64_t M, int64_t F, int64_t K) {
+    Plans p{true, plan_of(M, F, K, true, true), plan_of(M, F, K, true, false), plan_of(M, F, K, false, true)};
+    p.joint = p.both.us <= p.w.us + p.x.us + 2.0;
+    return p;
+}
 
-template <int XT>
-hipError_t launch_product(ProductArgs a, Plan p, bool out_bf16, float *parts, hipStream_t stream) {
-    void *const y = a.y;
-    const bool bf16 = out_bf16 && p.splits == 1;
-    a.splits = p.splits;
-    if (p.splits > 1) a.y = parts;
-    hipError_t e = hipSuccess;
-    switch (p.tile) {
-    case 0: e = launch_product_tile<64, 64, 4, 5, XT>(a, bf16, stream); break;
-    case 1: e = launch_product_tile<128, 128, 4, 4, XT>(a, bf16, stream); break;
-    case 2: e = launch_product_tile<128, 256, 8, 3, XT>(a, bf16, stream); break;
-    default: e = launch_product_tile<256, 256, 8, 2, XT>(a, bf16, stream); break;
-    }
-    if (e || p.splits == 1) return e;
-    const int64_t n = a.mm.M * a.mm.N, need = (n / 8 + 255) / 256;
-    const dim3 grid((unsigned)(need < 4096 ? need : 4096)), block(256);
-    if (out_bf16) gated_sum_kernel<1><<<grid, block, 0, stream>>>(parts, y, n, p.splits);
-    else gated_sum_kernel<0><<<grid, block, 0, stream>>>(parts, y, n, p.splits);
+template <int BM, int BN, int NW, int NSTAGE>
+hipError_t launch_grads_tile(const ProductArgs &dw, const ProductArgs &dx, hipStream_t stream) {
+    const unsigned grid = share_grid(tiles_of(dw), tiles_of(dx));   // (of the largest tiles' halves, or more than enough)
+    gated_grads_kernel<BM, BN, NW, NSTAGE><<<dim3(grid), dim3(NW * 64), 0, stream>>>(dw, dx);
     return hipGetLastError();
 }
 
-hipError_t launch_grads(ProductArgs dw, ProductArgs dx, bool dw_bf16, bool dx_bf16, hipStream_t stream) {
-    if (!lay_out(dw.mm, 256, 256, 4 * 512) || !lay_out(dx.mm, 256, 256, 4 * 512)) return hipErrorInvalidValue;
-    const dim3 grid(share_grid(dw.mm.tiles_m * dw.mm.tiles_n, dx.mm.tiles_m * dx.mm.tiles_n)), block(512);
-    if (dx_bf16 && dw_bf16) gated_grads_kernel<1, 1><<<grid, block, 0, stream>>>(dw, dx);
-    else if (dx_bf16) gated_grads_kernel<1, 0><<<grid, block, 0, stream>>>(dw, dx);
-    else if (dw_bf16) gated_grads_kernel<0, 1><<<grid, block, 0, stream>>>(dw, dx);
-    else gated_grads_kernel<0, 0><<<grid, block, 0, stream>>>(dw, dx);
+hipError_t launch_grads(ProductArgs dw, ProductArgs dx, const Plan &plan, float *parts, hipStream_t stream) {
+    static const int bm[] = {64, 128, 128, 256}, bn[] = {64, 128, 256, 256}, threads[] = {256, 256, 512, 512};
+    if (dw.splits) dw.splits = plan.parts_w;
+    if (dx.splits) dx.splits = plan.parts_x;
+    // (twice the tiles, of two products, in the largest ones' halves)
+    if (!lay_out(dw.mm, bm[plan.tile], bn[plan.tile], threads[plan.tile] * 4 * kMaxParts) ||
+        !lay_out(dx.mm, bm[plan.tile], bn[plan.tile], threads[plan.tile] * 4 * kMaxParts))
+        return hipErrorInvalidValue;
+    SumArgs sum{};
+    ProductArgs *const each[2] = {&dx, &dw};
+    for (int i = 0; i < 2; ++i) {
+        ProductArgs &p = *each[i];
+        if (p.splits <= 1) continue;
+        const int64_t n = p.mm.M * p.mm.N;
+        sum.parts[i] = parts, sum.y[i] = p.y, sum.n[i] = n, sum.bf16[i] = p.bf16, sum.splits[i] = p.splits;
+        p.y = parts;
+        parts += p.splits * n;
+    }
+    hipError_t e = hipSuccess;
+    switch (plan.tile) {
+    case 0: e = launch_grads_tile<64, 64, 4, 5>(dw, dx, stream); break;
+    case 1: e = launch_grads_tile<128, 128, 4, 4>(dw, dx, stream); break;
+    case 2: e = launch_grads_tile<128, 256, 8, 3>(dw, dx, stream); break;
+    default:
+        gated_grads_large_kernel<<<dim3(share_grid(tiles_of(dw), tiles_of(dx))), dim3(512), 0, stream>>>(dw, dx);
+        e = hipGetLastError();
+    }
+    if (e || sum.n[0] + sum.n[1] == 0) return e;
+    const int64_t need = ((sum.n[0] + sum.n[1]) / 8 + 255) / 256;
+    gated_sum_kernel<<<dim3((unsigned)(need < 4096 ? need : 4096)), dim3(256), 0, stream>>>(sum);
     return hipGetLastError();
 }
 
@@ -418,11 +465,11 @@ hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bo
     return launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, h, gu, nullptr, gelu}, h_bf16, stream);
 }
 
-// dg and du, then the sums of the product that has more of them
+// dg and du, then the parts' sums
 size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-    const int64_t sx = plan_of(M, K, 2 * F).splits, sw = plan_of(2 * F, K, M).splits;
-    const int64_t px = sx > 1 ? sx * M * K * 4 : 0, pw = sw > 1 ? sw * 2 * F * K * 4 : 0;
-    return (size_t)(M * F * 4 + (px > pw ? px : pw));
+    const Plans p = plans_of(M, F, K);
+    const int64_t x = p.joint ? p.both.parts_x : p.x.parts_x, w = p.joint ? p.both.parts_w : p.w.parts_w;
+    return (size_t)(M * F * 4 + (x > 1 ? x * M * K * 4 : 0) + (w > 1 ? w * 2 * F * K * 4 : 0));
 }
 
 hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,
@@ -439,15 +486,16 @@ hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, c
             return e;
         }
     }
-    const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, 1}, pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, 1};
-    const Plan lx = plan_of(M, K, 2 * F), lw = plan_of(2 * F, K, M);
-    const bool has_x = dx && M > 0 && K > 0, has_w = dw && F > 0 && K > 0;
-    if (has_x && has_w && lx.tile == kLargest && lw.tile == kLargest && lx.splits == 1 && lw.splits == 1)
-        return launch_grads(pw, px, dw_bf16, dx_bf16, stream);
-    if (has_x)
-        if (hipError_t e = launch_product<0>(px, lx, dx_bf16, parts, stream)) return e;
-    if (has_w)
-        if (hipError_t e = launch_product<1>(pw, lw, dw_bf16, parts, stream)) return e;
+    const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, dx_bf16, dx && M > 0 && K > 0};
+    const ProductArgs pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, dw_bf16, dw && F > 0 && K > 0};
+    const Plans plans = plans_of(M, F, K);
+    if (plans.joint) return px.splits || pw.splits ? launch_grads(pw, px, plans.both, parts, stream) : hipSuccess;
+    // (one after the other: their parts' sums may share their place)
+    ProductArgs none{};
+    if (pw.splits)
+        if (hipError_t e = launch_grads(pw, none, plans.w, parts, stream)) return e;
+    if (px.splits)
+        if (hipError_t e = launch_grads(none, px, plans.x, parts, stream)) return e;
     return hipSuccess;
 }
 

@@ -120,17 +120,13 @@ __device__ __forceinline__ void place_tile(const MmArgs &g, int tile, int bm, in
 
 // Workgroup b's tile. Workgroups are dealt round-robin to the 8 XCDs; each XCD takes a contiguous run of
 // the tile numbers, which go down `group` tile rows per tile column, so that the tiles that an XCD holds
-// at once share panels in its L2. NT: columns of Y in a tile. parts: the tiles that many times over; returns which.
+// at once share panels in its L2. NT: columns of Y in a tile.
 template <class T, int NT>
-__device__ __forceinline__ int find_tile(const MmArgs &g, int64_t &m0, int64_t &n0, int parts = 1) {
-    const int tiles = g.tiles_m * g.tiles_n * parts;
+__device__ __forceinline__ void find_tile(const MmArgs &g, int64_t &m0, int64_t &n0) {
+    const int tiles = g.tiles_m * g.tiles_n;
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
     const int q = tiles >> 3, rem = tiles & 7;
-    int tl = xcd * q + (xcd < rem ? xcd : rem) + slot;
-    const int part = tl / (g.tiles_m * g.tiles_n);
-    tl -= part * (g.tiles_m * g.tiles_n);
-    place_tile(g, tl, T::BM, NT, m0, n0);
-    return part;
+    place_tile(g, xcd * q + (xcd < rem ? xcd : rem) + slot, T::BM, NT, m0, n0);
 }
 
 // The largest tiles, of one product or of two independent ones of n_a and n_b tiles, one a CU: each XCD takes a
@@ -178,6 +174,8 @@ using HalfTile = Tile<128, 256, 8, 2, 3>;
 // fewest rows of both operands). False: more than a grid holds.
 inline bool lay_out(MmArgs &a, int bm, int bn, int threads) {
     const int64_t tm = (a.M + bm - 1) / bm, tn = (a.N + bn - 1) / bn;
+    a.tiles_m = a.tiles_n = 0;
+    if (tm == 0 || tn == 0) return true;
     if (tm > 0x7FFFFFFF || tn > 0x7FFFFFFF || tm > 0xFFFFFFFFll / threads / tn) return false;
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
