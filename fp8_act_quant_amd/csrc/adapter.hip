@@ -394,23 +394,22 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // At most 16 rows
-template <int OUT_BF16>
+template <int NB, int OUT_BF16>
 __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs g) {
-    constexpr int RX = 1;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<RX>::BYTES];
-    __shared__ __attribute__((aligned(16))) float u[Few<RX>::ROWS * UP];
-    const int64_t n0 = (int64_t)blockIdx.x * kFewN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = n0 + 16 * (wave & 1) + 4 * (lane >> 4), N = g.mm.N;
-    auto within = [&](int) { return lane & 15; };
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<1, NB>::BYTES];
+    __shared__ __attribute__((aligned(16))) float u[16 * UP];
+    const int64_t n0 = (int64_t)blockIdx.x * NB, N = g.mm.N;
+    // four columns of a row a thread, 4 NB threads in all
+    const int row = (threadIdx.x / (NB / 4)) & 15, at = 4 * (threadIdx.x % (NB / 4));
+    const bool mine = threadIdx.x < 4 * NB;
+    const int64_t n = mine ? n0 + at : N;
+    auto within = [&](int) { return row; };
     auto first = [&](int) { return n; };
-    OwnAdapters<1, 1, Few<RX>::ROWS, 256> own;
-    f32x4 sum[RX], acc[1][1];
-    few<RX, 0, OUT_BF16>(g.mm, n0, smem, sum, [&]() { own.begin(g, 0, u, within, first); });
-    acc[0][0] = sum[0];
+    OwnAdapters<1, 1, 16, 256> own;
+    const float *const sums = few<1, NB, 0, OUT_BF16>(g.mm, n0, smem, [&]() { own.begin(g, 0, u, within, first); });
+    f32x4 acc[1][1] = {{*reinterpret_cast<const f32x4 *>(sums + row * NB + at)}};
     own.end(g, 0, u, within, first, acc);
-    const int64_t m = lane & 15;
-    if (wave < 2 && m < g.mm.M && n < N) store4<OUT_BF16>(g.y, m * N + n, acc[0][0] + bias_of(g, n), N - n);
+    if (mine && row < g.mm.M && n < N) store4<OUT_BF16>(g.y, row * N + n, acc[0][0] + bias_of(g, n), N - n);
 }
 
 template <int BM, int BN, int NW, int NSTAGE>
@@ -439,10 +438,11 @@ hipError_t launch_add(AdapterArgs a, bool out_bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int NB>
 hipError_t launch_few(const AdapterArgs &a, bool out_bf16, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.mm.N + kFewN - 1) / kFewN)), block(256);
-    if (out_bf16) adapter_few_kernel<1><<<grid, block, 0, stream>>>(a);
-    else adapter_few_kernel<0><<<grid, block, 0, stream>>>(a);
+    const dim3 grid((unsigned)((a.mm.N + NB - 1) / NB)), block(256);
+    if (out_bf16) adapter_few_kernel<NB, 1><<<grid, block, 0, stream>>>(a);
+    else adapter_few_kernel<NB, 0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -492,7 +492,7 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
         if (hipError_t e = launch_shrink(g, stream)) return e;
     if (!w && base) return M <= 64 ? launch_add<0>(g, out_bf16, stream) : launch_add<1>(g, out_bf16, stream);
     // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
-    if (M <= Few<1>::ROWS) return launch_few(g, out_bf16, stream);
+    if (M <= 16) return N <= 4096 ? launch_few<16>(g, out_bf16, stream) : launch_few<32>(g, out_bf16, stream);
     static const struct {
         int bm, bn;
         double first, more, end;

@@ -148,42 +148,34 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // At most 16 RX rows
-template <int RX, int MODE>
+template <int RX, int NB, int MODE>
 __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<RX>::BYTES];
-    f32x4 *const ups = reinterpret_cast<f32x4 *>(smem);
-    const int64_t n0 = (int64_t)blockIdx.x * (kFewN / 2);
-    f32x4 acc[RX];
-    few<RX, 1, MODE>(g.mm, n0, smem, acc, []() {});
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (wave == 1) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Few<RX, NB>::BYTES];
+    constexpr int COLS = NB / 2;
+    const int64_t n0 = (int64_t)blockIdx.x * COLS, F = g.mm.N;
+    const float *const sums = few<RX, NB, 1, MODE>(g.mm, n0, smem, []() {});
+    const int p = threadIdx.x, row = p / (COLS / 4), at = 4 * (p % (COLS / 4));
+    static_assert(16 * RX * COLS / 4 <= 256, "four columns a thread");
+    const int64_t m = row, n = n0 + at;
+    if (row >= 16 * RX || m >= g.mm.M || n >= F) return;
+    const f32x4 gate = *reinterpret_cast<const f32x4 *>(sums + row * NB + at);
+    const f32x4 up = *reinterpret_cast<const f32x4 *>(sums + row * NB + COLS + at);
+    f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
 #pragma unroll
-        for (int i = 0; i < RX; ++i) ups[64 * i + lane] = acc[i];
+    for (int r = 0; r < 4; ++r) {
+        const Activation act = activate(gate[r], g.gelu);
+        a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
+        b[r] = dh[r] * act.value;
     }
-    __syncthreads();
-    if (wave) return;
-#pragma unroll
-    for (int i = 0; i < RX; ++i) {
-        const int64_t m = 16 * i + (lane & 15), n = n0 + 4 * (lane >> 4), F = g.mm.N;
-        if (m >= g.mm.M || n >= F) continue;
-        const f32x4 up = ups[64 * i + lane];
-        f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const Activation act = activate(acc[i][r], g.gelu);
-            a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
-            b[r] = dh[r] * act.value;
-        }
-        if constexpr (MODE == 2) {
-            store4<1>(g.gu, m * 2 * F + n, a, F - n);
-            store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
-        } else {
-            store4<MODE>(g.h, m * F + n, a, F - n);
-            if (g.gu) {
-                store4<1>(g.gu, m * 2 * F + n, acc[i], F - n);
-                store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
-            }
+    if constexpr (MODE == 2) {
+        store4<1>(g.gu, m * 2 * F + n, a, F - n);
+        store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
+    } else {
+        store4<MODE>(g.h, m * F + n, a, F - n);
+        if (g.gu) {
+            store4<1>(g.gu, m * 2 * F + n, gate, F - n);
+            store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
         }
     }
 }
@@ -333,12 +325,12 @@ hipError_t launch_gated_large(GatedArgs a, int mode, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int RX>
+template <int RX, int NB>
 hipError_t launch_gated_few(const GatedArgs &a, int mode, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.mm.N + kFewN / 2 - 1) / (kFewN / 2))), block(256);
-    if (mode == 0) gated_few_kernel<RX, 0><<<grid, block, 0, stream>>>(a);
-    else if (mode == 1) gated_few_kernel<RX, 1><<<grid, block, 0, stream>>>(a);
-    else gated_few_kernel<RX, 2><<<grid, block, 0, stream>>>(a);
+    const dim3 grid((unsigned)((a.mm.N + NB / 2 - 1) / (NB / 2))), block(256);
+    if (mode == 0) gated_few_kernel<RX, NB, 0><<<grid, block, 0, stream>>>(a);
+    else if (mode == 1) gated_few_kernel<RX, NB, 1><<<grid, block, 0, stream>>>(a);
+    else gated_few_kernel<RX, NB, 2><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -346,8 +338,8 @@ hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
     const int64_t M = a.mm.M, F = a.mm.N, K = a.mm.K;
     // few rows against the tiles, us: 24 x 3584 x 7168 20.7 / 27.6, 24 x 768 x 7168 13.9 / 17.2, 48 x 3584 x 7168 (four
     // blocks of rows) 30.0 / 26.1
-    if (M <= 16) return launch_gated_few<1>(a, mode, stream);
-    if (M <= 32) return launch_gated_few<2>(a, mode, stream);
+    if (M <= 16) return F <= 2048 ? launch_gated_few<1, 16>(a, mode, stream) : launch_gated_few<1, 32>(a, mode, stream);
+    if (M <= 32) return launch_gated_few<2, 32>(a, mode, stream);
     static const struct {
         int bm, bn;
         double first, more, end;

@@ -515,87 +515,110 @@ __device__ __forceinline__ int wave_n() {
 }
 
 // At most 16 RX rows (a decode step): every byte of W meets all of them once, so the read of W is what counts. A
-// workgroup of 4 waves takes 32 rows of W (GATED: 16 gate rows and their up rows), which come through LDS
-// with the rows of X, four steps of 64 k to a stage (a stage of one step costs a barrier and a wait for LDS as
-// long as its copies). Waves 0 and 1 take 16 rows of W each and the first half of every step, waves 2 and 3 the
-// other half; the halves are added in LDS (which is free again on return). On return waves 0 and 1 have their sums: acc[i][r] of lane l is W row
-// n0 + 16 * wave + 4 * (l / 16) + r (GATED: wave 0 the gate's, wave 1 the up's of f = n0 + ...) for X row
-// 16 i + l % 16.
-constexpr int kFewSubs = 4, kFewStages = 3, kFewN = 32;
-template <int RX>
+// workgroup of 4 waves takes NB = 32 or 16 rows of W (GATED: half of them gate rows and half their up rows), which
+// come through LDS with the rows of X, four steps of 64 k to a stage (a stage of one step costs a barrier and a wait for
+// LDS as long as its copies). NB = 32: waves 0 and 1 take 16 rows of W each and the first half of every step, waves 2
+// and 3 the other half. NB = 16, which gives the GPU twice the workgroups where W is small: each wave a step. The
+// waves' sums are added in LDS: returns [row * NB + n] for row < 16 RX, the sums of X row `row` and the workgroup's row
+// n of W (GATED: the gate rows first), for all to read. us with 32 / 16 rows: 1 x 7168 x 4096 11.0 / 10.5,
+// 1 x 7168 x 1536 10.0 / 7.4.
+template <int RX, int NB>
 struct Few {
-    static constexpr int ROWS = 16 * RX, W_SUB = kFewN * KB, X_SUB = ROWS * KB, STAGE = kFewSubs * (W_SUB + X_SUB);
-    static constexpr int BYTES = STAGE * kFewStages;
+    static constexpr int ROWS = 16 * RX, SUBS = 4, STAGES = NB == 32 ? 3 : 5;
+    static constexpr int W_SUB = NB * KB, X_SUB = ROWS * KB, STAGE = SUBS * (W_SUB + X_SUB), BYTES = STAGE * STAGES;
+    static_assert(NB == 32 || NB == 16, "rows of W");
 };
-template <int RX, int GATED, int TAG, class F>
-__device__ __forceinline__ void few(const MmArgs &g, int64_t n0, uint8_t *smem, f32x4 (&acc)[RX], const F &begin) {
-    constexpr int SUBS = kFewSubs, W_SUB = Few<RX>::W_SUB, X_SUB = Few<RX>::X_SUB, STAGE = Few<RX>::STAGE;
-    constexpr int IPW = SUBS + 2 * RX;
+template <int RX, int NB, int GATED, int TAG, class F>
+__device__ __forceinline__ const float *few(const MmArgs &g, int64_t n0, uint8_t *smem, const F &begin) {
+    using P = Few<RX, NB>;
+    constexpr int SUBS = P::SUBS, W_SUB = P::W_SUB, X_SUB = P::X_SUB, STAGE = P::STAGE, STAGES = P::STAGES;
+    constexpr int W_EACH = NB / 8, IPW = W_EACH + 2 * RX;   // copies of a stage a wave: of W's 8-row pieces, of X's
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4, sub = lane >> 3;
-    const int64_t most = GATED ? kFewN / 2 : kFewN, rows = g.N - n0 < most ? g.N - n0 : most;
-    // (of GATED the waves 0 and 1 copy gate rows, 2 and 3 their up rows)
-    const rsrc_t rw = make_rsrc(g.w + (n0 + (GATED && wave >= 2 ? g.N : 0)) * g.ldw, 2 * ((rows - 1) * g.ldw + g.K));
+    const int64_t most = GATED ? NB / 2 : NB, rows = g.N - n0 < most ? g.N - n0 : most;
+    // W: a wave copies one 8-row piece of every step (NB = 32), or both of one (NB = 16)
+    auto resource = [&](bool up) { return make_rsrc(g.w + (n0 + (up ? g.N : 0)) * g.ldw, 2 * ((rows - 1) * g.ldw + g.K)); };
+    const rsrc_t rw = resource(GATED && NB == 32 && wave >= 2), rw1 = resource(GATED && NB == 16);
     const rsrc_t rx = make_rsrc(g.x, 2 * ((g.M - 1) * g.ldx + g.K));
     const int chunk_byte = swz_chunk(sub, lane & 7) << 4, Kb = (int)(2 * g.K);
-    const uint32_t w_off = (uint32_t)((8 * (GATED ? wave & 1 : wave) + sub) * g.ldw * 2) + chunk_byte;
-    const uint32_t x_off = (uint32_t)(sub * g.ldx * 2) + chunk_byte, x_step = (uint32_t)(16 * g.ldx);   // 8 rows
+    const int piece = NB == 32 ? (GATED ? wave & 1 : wave) : 0;
+    const uint32_t w_off = (uint32_t)((8 * piece + sub) * g.ldw * 2) + chunk_byte;
+    const uint32_t x_off = (uint32_t)(sub * g.ldx * 2) + chunk_byte, w_step = (uint32_t)(16 * g.ldw), x_step = (uint32_t)(16 * g.ldx);
     auto copy = [&](uint8_t *stage, int ks) {
+        const int mine = __builtin_amdgcn_readfirstlane((ks * SUBS + wave) * KB);   // this wave's step
+        const bool past = mine + chunk_byte >= Kb;
+        if constexpr (NB == 32) {
 #pragma unroll
-        for (int s = 0; s < SUBS; ++s) {
-            const int koff = __builtin_amdgcn_readfirstlane((ks * SUBS + s) * KB);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(stage + s * W_SUB + 1024 * wave), 16,
-                                                     koff + chunk_byte >= Kb ? kNowhere : w_off, koff, 0, 0);
+            for (int s = 0; s < SUBS; ++s) {
+                const int koff = __builtin_amdgcn_readfirstlane((ks * SUBS + s) * KB);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(stage + s * W_SUB + 1024 * wave), 16,
+                                                         koff + chunk_byte >= Kb ? kNowhere : w_off, koff, 0, 0);
+            }
+        } else {
+            lds_void *to = (lds_void *)(stage + wave * W_SUB), *to1 = (lds_void *)(stage + wave * W_SUB + 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, past ? kNowhere : w_off, mine, 0, 0);
+            if constexpr (GATED) __builtin_amdgcn_raw_ptr_buffer_load_lds(rw1, to1, 16, past ? kNowhere : w_off, mine, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to1, 16, past ? kNowhere : w_off + w_step, mine, 0, 0);
         }
-        const int koff = __builtin_amdgcn_readfirstlane((ks * SUBS + wave) * KB);   // X: a step a wave
-        const uint32_t at = koff + chunk_byte >= Kb ? kNowhere : x_off;
 #pragma unroll
-        for (int t = 0; t < 2 * RX; ++t)   // (kNowhere and rows past the last lie past the range: t x_step does not wrap)
+        for (int t = 0; t < 2 * RX; ++t)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(stage + SUBS * W_SUB + wave * X_SUB + 1024 * t), 16,
-                                                     at == kNowhere ? kNowhere : at + t * x_step, koff, 0, 0);
+                                                     past ? kNowhere : x_off + t * x_step, mine, 0, 0);
     };
 #pragma unroll
-    for (int s = 0; s < kFewStages - 1; ++s) copy(smem + s * STAGE, s);
+    for (int s = 0; s < STAGES - 1; ++s) copy(smem + s * STAGE, s);
     begin();
     __builtin_amdgcn_sched_barrier(0);
     const int cg = wave & 1, half = wave >> 1;
-    const int at = row * KB + (swz_chunk(row, 4 * half + kg) << 4);
+    const int lo = row * KB + (swz_chunk(row, kg) << 4), hi = row * KB + (swz_chunk(row, 4 + kg) << 4);
     const int nks = (int)((g.K + SUBS * KSTEP - 1) / (SUBS * KSTEP));
+    f32x4 acc[RX];
 #pragma unroll
     for (int i = 0; i < RX; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    uint8_t *stage = smem, *last = smem + (kFewStages - 1) * STAGE;   // `last`: of the step before
+    uint8_t *stage = smem, *last = smem + (STAGES - 1) * STAGE;   // `last`: of the step before
     for (int ks = 0; ks < nks; ++ks) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_lgkm0();                             // the step before's reads
-        wait_vmcnt<IPW *(kFewStages - 2)>();      // this step has landed
+        wait_lgkm0();                         // the step before's reads
+        wait_vmcnt<IPW *(STAGES - 2)>();      // this step has landed
         lds_barrier();
-        copy(last, ks + kFewStages - 1);
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + s * W_SUB + 16 * cg * KB + at);
+        copy(last, ks + STAGES - 1);
+        auto multiply = [&](int s, int at, int w_base) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + s * W_SUB + w_base + at);
 #pragma unroll
             for (int i = 0; i < RX; ++i) {
                 const u32x4 x = *reinterpret_cast<const u32x4 *>(stage + SUBS * W_SUB + s * X_SUB + 16 * i * KB + at);
                 acc[i] = mfma_bf16(w, x, acc[i]);
             }
+        };
+        if constexpr (NB == 32) {
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s) multiply(s, half ? hi : lo, 16 * cg * KB);
+        } else {
+            multiply(wave, lo, 0);
+            multiply(wave, hi, 0);
         }
         last = stage;
-        stage = stage + STAGE == smem + kFewStages * STAGE ? smem : stage + STAGE;
+        stage = stage + STAGE == smem + STAGES * STAGE ? smem : stage + STAGE;
     }
     wait_vmcnt<0>();
     __syncthreads();
-    f32x4 *const part = reinterpret_cast<f32x4 *>(smem) + cg * RX * 64 + lane;
-    if (half == 1) {
+    // Each wave's sums, as rows of X; then all of a sum's added
+    constexpr int PARTS = NB == 32 ? 2 : 4, SIZE = P::ROWS * NB;
+    static_assert(PARTS * SIZE * 4 <= P::BYTES, "LDS of the sums");
+    float *const sums = reinterpret_cast<float *>(smem);
+    float *const part = sums + (NB == 32 ? half : wave) * SIZE + (NB == 32 ? 16 * cg : 0) + 4 * kg;
 #pragma unroll
-        for (int i = 0; i < RX; ++i) part[64 * i] = acc[i];
+    for (int i = 0; i < RX; ++i) *reinterpret_cast<f32x4 *>(part + (16 * i + row) * NB) = acc[i];
+    __syncthreads();
+    for (int p = threadIdx.x; p < SIZE / 4; p += 256) {
+        f32x4 v = reinterpret_cast<const f32x4 *>(sums)[p];
+#pragma unroll
+        for (int q = 1; q < PARTS; ++q) v += reinterpret_cast<const f32x4 *>(sums + q * SIZE)[p];
+        reinterpret_cast<f32x4 *>(sums)[p] = v;
     }
     __syncthreads();
-    if (half == 0) {
-#pragma unroll
-        for (int i = 0; i < RX; ++i) acc[i] += part[64 * i];
-    }
-    __syncthreads();
+    return sums;
 }
 
 // Four consecutive elements of a row with `left` of them from here on, as they are in memory
