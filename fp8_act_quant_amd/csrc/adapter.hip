@@ -43,64 +43,50 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs &g, int64_t m) {
 
 // u in two ways. K is cut into `splits` parts, whose sums are kept apart (u[part]) and added where u is used.
 //
-// Few rows, which may all have different adapters: a workgroup takes one row and one part of K, its 4 waves a
-// quarter of that each, A straight from memory into the matrix unit's registers (16 RB ranks at a time), whose
-// other operand is the row 16 times. Bound by latency and the reads of A.
-template <int RB>
+// Few rows, which may all have different adapters: a workgroup takes 16 ranks of one row and one part of K, its 4 waves
+// a quarter of that each, A straight from memory into the matrix unit's registers, whose other operand is the row 16
+// times. Bound by latency and the reads of A (250 rows of 7168 at rank 64: 34 us, 6.7 TB/s from the caches). All of a row's
+// 64 ranks in one workgroup took 13.3 us at 30 rows of 3000, now 4.1.
 __global__ __launch_bounds__(256) void adapter_row_kernel(AdapterArgs g) {
-    constexpr int U = RB == 1 ? 4 : 2;   // steps of 64 k on their way
-    __shared__ f32x4 part[4][RB][4];
+    constexpr int U = 4;   // steps of 64 k on their way
+    __shared__ f32x4 part[4][4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
     const int64_t m = blockIdx.x, K = g.mm.K;
-    const int e = adapter_of(g, m);
+    const int e = adapter_of(g, m), r0 = 16 * blockIdx.z, r = r0 + row;
     if (e < 0) return;
     const rsrc_t rx = make_rsrc(g.mm.x + m * K, 2 * K), ra = make_rsrc(g.a + (int64_t)e * g.rank * K, 2 * g.rank * K);
     const int steps = (int)((K + KSTEP - 1) / KSTEP), parts = 4 * g.splits, p = 4 * blockIdx.y + wave;
     const int s0 = (int)((int64_t)p * steps / parts), s1 = (int)((int64_t)(p + 1) * steps / parts);
     const uint32_t pitch = (uint32_t)(2 * K);
-    for (int r0 = 0; r0 < g.rank; r0 += 16 * RB) {
-        f32x4 acc[RB];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int s = s0; s < s1; s += U) {
+        u32x4 xf[U][2], af[U][2];
 #pragma unroll
-        for (int j = 0; j < RB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int s = s0; s < s1; s += U) {
-            u32x4 xf[U][2], af[U][2][RB];
+        for (int v = 0; v < U; ++v)
 #pragma unroll
-            for (int v = 0; v < U; ++v)
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = (uint32_t)((s + v) * KB + 64 * h + 16 * kg);
+                const bool in = s + v < s1 && k < pitch;
+                xf[v][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? k : kNowhere, 0, 0));
+                af[v][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                    ra, in && r < g.rank ? r * pitch + k : kNowhere, 0, 0));
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t k = (uint32_t)((s + v) * KB + 64 * h + 16 * kg);
-                    const bool in = s + v < s1 && k < pitch;
-                    xf[v][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? k : kNowhere, 0, 0));
+        for (int v = 0; v < U; ++v)
 #pragma unroll
-                    for (int j = 0; j < RB; ++j) {
-                        const int r = r0 + 16 * j + row;
-                        af[v][h][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                            ra, in && r < g.rank ? r * pitch + k : kNowhere, 0, 0));
-                    }
-                }
+            for (int h = 0; h < 2; ++h) acc = mfma_bf16(af[v][h], xf[v][h], acc);
+    }
+    if (row == 0) part[wave][kg] = acc;
+    __syncthreads();
+    const int at = r0 + 4 * (int)threadIdx.x;
+    if (threadIdx.x < 4 && at < g.rank) {
+        f32x4 sum = part[0][threadIdx.x];
 #pragma unroll
-            for (int v = 0; v < U; ++v)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < RB; ++j) acc[j] = mfma_bf16(af[v][h][j], xf[v][h], acc[j]);
-        }
-        __syncthreads();
-        if (row == 0) {
-#pragma unroll
-            for (int j = 0; j < RB; ++j) part[wave][j][kg] = acc[j];
-        }
-        __syncthreads();
-        const int r = r0 + 4 * (int)threadIdx.x;
-        if (threadIdx.x < 4 * RB && r < g.rank) {
-            f32x4 sum = part[0][threadIdx.x / 4][threadIdx.x % 4];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) sum += part[w][threadIdx.x / 4][threadIdx.x % 4];
-            const float scale = g.scales ? g.scales[e] : 1.0f;
-            *reinterpret_cast<f32x4 *>(g.u + ((int64_t)blockIdx.y * g.mm.M + m) * g.rank + r) = sum * scale;
-        }
+        for (int w = 1; w < 4; ++w) sum += part[w][threadIdx.x];
+        const float scale = g.scales ? g.scales[e] : 1.0f;
+        *reinterpret_cast<f32x4 *>(g.u + ((int64_t)blockIdx.y * g.mm.M + m) * g.rank + at) = sum * scale;
     }
 }
 
@@ -209,7 +195,7 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, i
             }
             // AT adapters at a time, all their loads on their way together (a decode batch's 16 rows may have 16)
             for (uint64_t left = __ballot(id >= 0); left;) {
-                constexpr int AT = T::SUB_M * T::SUB_N > 16 ? 2 : 4;   // (as the registers allow)
+                constexpr int AT = T::SUB_M * T::SUB_N > 16 || T::NSTAGE == 1 ? 2 : 4;   // (as the registers allow)
                 int e[AT];
                 u32x4 wf[AT][T::SUB_N];
 #pragma unroll
@@ -347,7 +333,10 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs &g, int64_t m0, i
 #pragma unroll
         for (int i = 0; i < T::SUB_M; ++i)
 #pragma unroll
-            for (int j = 0; j < T::SUB_N; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < T::SUB_N; ++j) {
+                const int64_t m = m0 + within(i), n = first(j);
+                acc[i][j] = m < M && n < N ? load4<OUT_BF16>(g.base, m * N + n, N - n) : f32x4{0.f, 0.f, 0.f, 0.f};
+            }
         begin();
     } else {
         multiply<T, 0, 0, 0, OUT_BF16>(g.mm, m0, n0, smem, acc, begin);
@@ -358,12 +347,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs &g, int64_t m0, i
 #pragma unroll
     for (int j = 0; j < T::SUB_N; ++j) bias[j] = bias_of(g, col + 16 * j + 4 * (lane >> 4));
     store_tile<T, OUT_BF16, T::SUB_N>(g.y, N, m0, M, n0, N, smem, [&](int i, int j) {
-        const int64_t m = m0 + T::row(wm, i) + (lane & 15), n = col + 16 * j + 4 * (lane >> 4);
-        f32x4 v = acc[i][j] + bias[j];
-        if constexpr (ADD) {
-            if (m < M && n < N) v += load4<OUT_BF16>(g.base, m * N + n, N - n);
-        }
-        return v;
+        return acc[i][j] + bias[j];
     });
 }
 
@@ -412,9 +396,12 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs g) {
     if (mine && row < g.mm.M && n < N) store4<OUT_BF16>(g.y, row * N + n, acc[0][0] + bias_of(g, n), N - n);
 }
 
-template <int BM, int BN, int NW, int NSTAGE>
+// SHARED from 65 rows on, us at rank 64: 90 rows an adapter, 250 x 7168 x 7168 82 / 107, 500 x 3000 x 3000 41 / 61;
+// one row an adapter 107 / 124 and 71 / 93, 500 x 1000 x 1000 at rank 16 15 / 14.
+template <int BM, int BN, int NW, int NSTAGE, int SHARED = BM >= 128>
 hipError_t launch_tile(AdapterArgs a, bool out_bf16, hipStream_t stream) {
-    constexpr int SHARED = BM >= 128;
+    if constexpr (!SHARED)
+        if (a.mm.M > 64) return launch_tile<BM, BN, NW, NSTAGE, 1>(a, out_bf16, stream);
     if (!lay_out(a.mm, BM, BN, NW * 64)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(NW * 64);
     if (out_bf16) adapter_kernel<BM, BN, NW, NSTAGE, SHARED, 0, 1><<<grid, block, 0, stream>>>(a);
@@ -428,13 +415,13 @@ hipError_t launch_large(AdapterArgs a, bool out_bf16, hipStream_t stream) {
     else adapter_large_kernel<0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
-// (one stage: LDS holds u and the outputs only)
-template <int SHARED>
+// (stages only for the room: LDS holds u and the outputs)
+template <int BM, int BN, int SHARED>
 hipError_t launch_add(AdapterArgs a, bool out_bf16, hipStream_t stream) {
-    if (!lay_out(a.mm, 64, 64, 256)) return hipErrorInvalidValue;
+    if (!lay_out(a.mm, BM, BN, 256)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(a.mm.tiles_m * a.mm.tiles_n)), block(256);
-    if (out_bf16) adapter_kernel<64, 64, 4, 1, SHARED, 1, 1><<<grid, block, 0, stream>>>(a);
-    else adapter_kernel<64, 64, 4, 1, SHARED, 1, 0><<<grid, block, 0, stream>>>(a);
+    if (out_bf16) adapter_kernel<BM, BN, 4, BM == 32 ? 2 : 1, SHARED, 1, 1><<<grid, block, 0, stream>>>(a);
+    else adapter_kernel<BM, BN, 4, BM == 32 ? 2 : 1, SHARED, 1, 0><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -453,7 +440,7 @@ bool by_rows(int64_t M, int64_t rank) { return M <= 512 && M * rank <= 16384; }
 // The parts of K: enough for two workgroups a CU, each with some steps to go
 int splits_of(int64_t M, int64_t K, int64_t rank) {
     const int64_t steps = (K + KSTEP - 1) / KSTEP;
-    const int64_t wgs = by_rows(M, rank) ? M : (M + ShrinkTile::BM - 1) / ShrinkTile::BM * ((rank + ShrinkTile::BN - 1) / ShrinkTile::BN);
+    const int64_t wgs = by_rows(M, rank) ? M * ((rank + 15) / 16) : (M + ShrinkTile::BM - 1) / ShrinkTile::BM * ((rank + ShrinkTile::BN - 1) / ShrinkTile::BN);
     const int64_t least = by_rows(M, rank) ? 16 : 8, most = steps / least < kMaxSplits ? steps / least : kMaxSplits;
     int64_t n = 512 / (wgs < 1 ? 1 : wgs);
     n = n < most ? n : most;
@@ -463,9 +450,7 @@ int splits_of(int64_t M, int64_t K, int64_t rank) {
 hipError_t launch_shrink(const AdapterArgs &a, hipStream_t stream) {
     const int64_t M = a.mm.M;
     if (by_rows(M, a.rank)) {
-        const dim3 grid((unsigned)M, a.splits);
-        if (a.rank <= 16) adapter_row_kernel<1><<<grid, dim3(256), 0, stream>>>(a);
-        else adapter_row_kernel<4><<<grid, dim3(256), 0, stream>>>(a);
+        adapter_row_kernel<<<dim3((unsigned)M, a.splits, (a.rank + 15) / 16), dim3(256), 0, stream>>>(a);
     } else {
         const int64_t tiles = (M + ShrinkTile::BM - 1) / ShrinkTile::BM;
         const int blocks = (a.rank + ShrinkTile::BN - 1) / ShrinkTile::BN;
@@ -490,7 +475,14 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
                   (int)adapters, (int)rank, splits_of(M, K, rank)};
     if (adapters > 0)
         if (hipError_t e = launch_shrink(g, stream)) return e;
-    if (!w && base) return M <= 64 ? launch_add<0>(g, out_bf16, stream) : launch_add<1>(g, out_bf16, stream);
+    if (!w && base) {
+        // (a wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
+        // 23 / 27, 1500 x 3000 24 / 28; where it leaves CUs idle, or neighbours differ: 1500 x 1000 17 / 11, 500 x 7168 55 / 57,
+        // 500 x 3000 56 / 27)
+        if (M <= 64) return launch_add<32, 32, 0>(g, out_bf16, stream);
+        return ((M + 63) / 64) * ((N + 255) / 256) < 256 ? launch_add<64, 64, 1>(g, out_bf16, stream)
+                                                          : launch_add<64, 256, 1>(g, out_bf16, stream);
+    }
     // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
     if (M <= 16) return N <= 4096 ? launch_few<16>(g, out_bf16, stream) : launch_few<32>(g, out_bf16, stream);
     static const struct {
