@@ -476,10 +476,12 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
     if (adapters > 0)
         if (hipError_t e = launch_shrink(g, stream)) return e;
     if (!w && base) {
-        // (a wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
-        // 23 / 27, 1500 x 3000 24 / 28; where it leaves CUs idle, or neighbours differ: 1500 x 1000 17 / 11, 500 x 7168 55 / 57,
-        // 500 x 3000 56 / 27)
-        if (M <= 64) return launch_add<32, 32, 0>(g, out_bf16, stream);
+        // Each lane for itself while that is little to read, us against the matrix unit with every row's adapter another
+        // and with 90 rows an adapter: 500 x 1000 at rank 16 5.5 / 10.5 and 4.4 / 6.4, 250 x 1000 at 64 9.1 / 20 and
+        // 6.2 / 9.5; 250 x 3000 at 64 20 / 20 and 11 / 9, 500 x 7168 at 64 74 / 53 and 35 / 19.
+        if (M <= 64 || M * N * rank <= 1 << 24) return launch_add<32, 32, 0>(g, out_bf16, stream);
+        // A wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
+        // 23 / 27, 1500 x 3000 24 / 28; but where it leaves CUs idle: 1500 x 1000 17 / 11, 500 x 7168 55 / 57, 500 x 3000 56 / 27.
         return ((M + 63) / 64) * ((N + 255) / 256) < 256 ? launch_add<64, 64, 1>(g, out_bf16, stream)
                                                           : launch_add<64, 256, 1>(g, out_bf16, stream);
     }
