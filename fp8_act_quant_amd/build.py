@@ -7,6 +7,8 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +25,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # every fp32 rounding is written out explicitly (fmaf where a fused op is wanted)
     "-ffp-contract=off",
     # keep the compiler from forming packed-fp32 VALU ops
@@ -42,16 +43,25 @@ def hipcc() -> str:
     return p
 
 
-def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *srcs]
+def _run(cmd, what, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libfp8q.so")
+        raise RuntimeError(what)
+
+
+def build(verbose: bool = False) -> str:
+    """Each source by a compiler of its own, side by side, then the library from them."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as objects, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(objects, s + ".o") for s in SOURCES]
+        jobs = [pool.submit(_run, [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", o],
+                            f"hipcc failed building {s}", verbose) for s, o in zip(SOURCES, objs)]
+        for j in jobs:
+            j.result()
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], "hipcc failed linking libfp8q.so", verbose)
     os.replace(tmp, LIB)
     build_binding(verbose)
     return LIB
@@ -74,12 +84,7 @@ def build_binding(verbose: bool = False) -> str:
            "-I", INCLUDE, os.path.join(CSRC, "binding.cpp"), "-o", tmp,
            "-L", os.path.join(top, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
            "-L", PKG, "-l:libfp8q.so", "-Wl,-rpath,$ORIGIN"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("g++ failed building _native.so")
+    _run(cmd, "g++ failed building _native.so", verbose)
     os.replace(tmp, BINDING)
     return BINDING
 
