@@ -91,7 +91,8 @@ __global__ __launch_bounds__(256) void adapter_row_kernel(AdapterArgs g) {
 }
 
 // Many rows: tiles of 32 rows x 64 ranks (mm.h), for each of the rows' adapters, of which workgroup
-// blockIdx.z takes those numbered blockIdx.z, blockIdx.z + gridDim.z, ...: mostly there is one.
+// blockIdx.z takes those numbered blockIdx.z, blockIdx.z + gridDim.z, ...: mostly there is one. Bound by the copies of x
+// and A into LDS, some 65 KB/us a CU (8192 x 7168 at rank 64 31-44 us for 117 MB of x, 1021 rows at 24 7.6).
 using ShrinkTile = Tile<32, 64, 4, 2, 6>;
 __global__ __launch_bounds__(256) void adapter_shrink_kernel(AdapterArgs g) {
     using T = ShrinkTile;
@@ -311,7 +312,10 @@ __device__ __forceinline__ f32x4 bias_of(const AdapterArgs &g, int64_t n) {
 }
 
 // A tile. ADD: no W, base is added. SHARED: rows by the matrix unit, whose neighbours mostly have one adapter, after the
-// product; else each lane for itself, while the product's first copies are on their way.
+// product; else each lane for itself, while the product's first copies are on their way. At rank 64 on the device:
+// 8192 x 7168 x 7168 652 us, the matrix unit busy 0.65 (5000 rows 91% of the rate without adapters); added alone, 5000 x
+// 7168 94 us (28 are the outputs' bytes at a copy's rate, the rest waits for u, ids and B in turn). A decode batch of 48 x
+// 7168 x 7168 at rank 16 30 us, 3.8 TB/s: each workgroup copies all of x into its LDS at a CU's 65 KB/us.
 template <class T, int SHARED>
 constexpr int tile_bytes() {   // (u over the stages where it is read after the product)
     constexpr int U = 4 * UP * T::BM, STAGES = T::STAGE * T::NSTAGE;

@@ -592,7 +592,7 @@ const char *fp8q_strerror(int status) {
     switch (status) {
     case FP8Q_OK: return "ok";
     case FP8Q_ERR_NULL: return "a required pointer is NULL";
-    case FP8Q_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 128 (8-bit integers: 16), or too large)";
+    case FP8Q_ERR_SHAPE: return "invalid shape (negative size, K not a multiple of 128 (8-bit integers: 16; the dense block: sizes of 8), or too large)";
     case FP8Q_ERR_ALIGN: return "pointer alignment below what the entry point requires";
     case FP8Q_ERR_DTYPE: return "unknown element type or flag";
     case FP8Q_ERR_UNSUPPORTED: return "no gfx950 device is current";
@@ -605,6 +605,6 @@ const char *fp8q_strerror(int status) {
     }
 }
 
-int fp8q_version(void) { return (1 << 16) | 6; }
+int fp8q_version(void) { return (1 << 16) | 7; }
 
 }  // extern "C"

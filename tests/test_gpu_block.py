@@ -354,7 +354,7 @@ def test_activations(act):
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activation_specials(act):
-    """+inf is itself, NaN stays NaN in its row."""
+    """+inf is itself, NaN stays NaN in its row, and neither reaches another row."""
     x = torch.zeros((3, 8), device="cuda").bfloat16()
     x[0, 0], x[1, 0], x[2, 0] = float("inf"), float("nan"), 2.0
     w = torch.zeros((16, 8), device="cuda").bfloat16()
@@ -364,6 +364,9 @@ def test_activation_specials(act):
     # (inf * 0 in the up projection: w's zeros meet x's infinities)
     dx, dw = fq.gated_linear_backward(torch.ones((1, 8), device="cuda").bfloat16(), x[2:].clone(), w, gu[2:].clone(), act=act)
     assert torch.isnan(h[1]).all() and torch.isfinite(h[2]).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    w[8:, 0] = 1.0   # both projections infinite
+    h = fq.gated_linear(x, w, act=act)
+    assert (h[0] == float("inf")).all() and torch.isnan(h[1]).all() and torch.isfinite(h[2]).all()
 
 
 def test_gated_empty():
