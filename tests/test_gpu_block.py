@@ -492,6 +492,24 @@ def test_adapter_rows_are_their_own():
         assert torch.equal(y[1:], z[1:])
 
 
+@pytest.mark.parametrize("M,N", [(40, 200), (130, 200), (513, 1536), (1030, 7168)])
+def test_adapters_added_are_their_own(M, N):
+    """The same beside another projection; rows without an adapter, and calls without any, keep their bits."""
+    s = adapter_inputs(M, N, 136, 6, 64, "mixed", M)
+    base = randn(rng(M), M, N)
+    args = [s[k] for k in ("x", "a", "b", "ids", "scales")]
+    y = fq.adapter_add(base, *args)
+    a, b, scales = (s[k].clone() for k in ("a", "b", "scales"))
+    a[2], b[3], scales[4] = float("nan"), float("inf"), float("nan")
+    z = fq.adapter_add(base, s["x"], a, b, s["ids"], scales)
+    touched = (s["ids"] >= 2) & (s["ids"] <= 4)
+    assert torch.equal(y[~touched], z[~touched])
+    assert not torch.isfinite(z[touched]).all(dim=-1).any()
+    no = (s["ids"] < 0) | (s["ids"] >= 6)
+    assert no.any() and torch.equal(y[no], base[no])
+    assert torch.equal(fq.adapter_add(base, s["x"], a[:0], b[:0], s["ids"], scales[:0]), base)
+
+
 def test_adapter_sums_keep_fp32():
     """x a^T of 24 bits: with W zero and b one, fp32 output holds it to the last bit but one."""
     g = rng(3)
