@@ -19,7 +19,7 @@
 // enters the second norm before its rounding. Outputs round once. The order of every sum is fixed.
 // 16384 x 7168 bf16 177 us, 5.3 TB/s (a copy of 1 GB: 5.15); the gradient of 4096 x 7168 94 us, 3.7 TB/s, of
 // 16384 x 2048 82 us, 4.9 TB/s. One row of 7168 takes 4 us on the device, most of it two dependent sums. Rows above 8192
-// outgrow the gradient's registers and are read again from the caches (2048 x 16384 520 us, 0.8 TB/s).
+// outgrow the gradient's registers: their statistics and the rest are two kernels.
 #include <fp8q.h>
 
 #include "device_common.h"
@@ -277,27 +277,22 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormA
 }
 
 // The same in LDS, for the gradient, whose sums over the rows take the registers: 16 bytes of each of a
-// wave's lanes side by side, which meets no bank conflict. Without HOLD (rows too long) read again.
-template <int NT, int NV, bool HOLD>
+// wave's lanes side by side, which meets no bank conflict.
+template <int NT, int NV>
 struct SharedChannels {
     f32x4 *at;
-    const float *v;
-    int tid, H;
-    static constexpr int SIZE = HOLD ? 2 * NT * NV : 1;
-    __device__ __forceinline__ SharedChannels(f32x4 *lds, const float *v_, int tid_, int H_) : at(lds), v(v_), tid(tid_), H(H_) {
-        if constexpr (HOLD) {   // (a workgroup's waves write the same where each has a row)
+    int tid;
+    static constexpr int SIZE = 2 * NT * NV;
+    __device__ __forceinline__ SharedChannels(f32x4 *lds, const float *v, int tid_, int H) : at(lds), tid(tid_) {
+        // (a workgroup's waves write the same where each has a row)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const Raw<0> r = Channels<NT, NV, false>(v, tid, H).read(i);
+        for (int i = 0; i < NV; ++i) {
+            const Raw<0> r = Channels<NT, NV, false>(v, tid, H).read(i);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) at[(2 * i + h) * NT + tid] = __builtin_bit_cast(f32x4, r.v[h]);
-            }
+            for (int h = 0; h < 2; ++h) at[(2 * i + h) * NT + tid] = __builtin_bit_cast(f32x4, r.v[h]);
         }
     }
-    __device__ __forceinline__ f32x4 operator()(int i, int h) const {   // half h of piece i
-        if constexpr (HOLD) return at[(2 * i + h) * NT + tid];
-        else return __builtin_bit_cast(f32x4, Channels<NT, NV, false>(v, tid, H).read(i).v[h]);
-    }
+    __device__ __forceinline__ f32x4 operator()(int i, int h) const { return at[(2 * i + h) * NT + tid]; }   // half h of piece i
 };
 
 // keeps the compiler from holding what it has computed from v: that is computed again from v instead
@@ -307,15 +302,46 @@ __device__ __forceinline__ void forget(Raw<BF16> &v) {
     for (int h = 0; h < (BF16 ? 1 : 2); ++h) asm volatile("" : "+v"(v.v[h]));
 }
 
+// What the gradient takes from row m, piece tid + i NT of it; what is not there counts as zeros
+template <int BF16, int NT, int GATES>
+struct GradInputs {
+    struct Piece {
+        Raw<BF16> t, dz, dt, y, gate;
+    };
+    const NormArgs &g;
+    int tid;
+    bool need_y;
+    __device__ __forceinline__ GradInputs(const NormArgs &g_, int tid_)
+        : g(g_), tid(tid_), need_y(g_.y && (g_.post || g_.sums[2] || GATES)) {}
+    __device__ __forceinline__ Piece read(int64_t m, int i) const {
+        Piece p;
+#pragma unroll
+        for (int h = 0; h < (BF16 ? 1 : 2); ++h)
+            p.t.v[h] = p.dz.v[h] = p.dt.v[h] = p.y.v[h] = p.gate.v[h] = u32x4{0, 0, 0, 0};
+        if (g.weight) {
+            p.t = load8<BF16>(g.x, m, tid + i * NT, g.H);
+            p.dz = load8<BF16>(g.dz, m, tid + i * NT, g.H);
+        }
+        if (g.dt) p.dt = load8<BF16>(g.dt, m, tid + i * NT, g.H);
+        if (need_y) p.y = load8<BF16>(g.y, m, tid + i * NT, g.H);
+        if constexpr (GATES) p.gate = load8<BF16>(g.gates, m, tid + i * NT, g.H);
+        return p;
+    }
+    __device__ __forceinline__ Piece settled(Piece p, int i) const {
+        const int at = tid + i * NT;
+        p.t = settle(p.t, at, g.H), p.dz = settle(p.dz, at, g.H), p.dt = settle(p.dt, at, g.H), p.y = settle(p.y, at, g.H);
+        if constexpr (GATES) p.gate = settle(p.gate, at, g.H);
+        return p;
+    }
+};
+
 // The gradient. The sums over the rows leave as one partial row per workgroup, which a second kernel
 // adds up (with one workgroup they are the sums).
 template <int BF16, int NT, int NV, int GATES>
 __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(NormArgs g) {
     constexpr int ROWS = rows_of<NT>();
-    // a row's inputs stay in registers (where they fit), the next row's are on their way; else they are read
-    // again for each use, from the caches
-    constexpr bool KEEP = NT * NV <= 1024, AHEAD = KEEP && (NV == 1 || BF16);
-    typedef SharedChannels<NT, NV, KEEP> Vector;
+    constexpr bool AHEAD = NV == 1 || BF16;   // the next row's inputs are on their way (where registers hold them)
+    typedef SharedChannels<NT, NV> Vector;
     __shared__ f32x4 channels[3][Vector::SIZE];
     __shared__ float part[2][3][NT / 64];
     __shared__ float across[ROWS > 1 ? 3 * NT * NV * 8 : 1];
@@ -325,35 +351,12 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
     const float inv = 1.0f / (float)H;
     int turn = 0;
 
-    struct Inputs {
-        Raw<BF16> t, dz, dt, y, gate;
-    };
-    Inputs next[AHEAD ? NV : 1];
-    const bool need_y = g.y && (g.post || g.sums[2] || GATES);
-    auto read = [&](int64_t m, int i) {
-        Inputs p;
-#pragma unroll
-        for (int h = 0; h < (BF16 ? 1 : 2); ++h)   // what is not there counts as zeros
-            p.t.v[h] = p.dz.v[h] = p.dt.v[h] = p.y.v[h] = p.gate.v[h] = u32x4{0, 0, 0, 0};
-        if (g.weight) {
-            p.t = load8<BF16>(g.x, m, tid + i * NT, H);
-            p.dz = load8<BF16>(g.dz, m, tid + i * NT, H);
-        }
-        if (g.dt) p.dt = load8<BF16>(g.dt, m, tid + i * NT, H);
-        if (need_y) p.y = load8<BF16>(g.y, m, tid + i * NT, H);
-        if constexpr (GATES) p.gate = load8<BF16>(g.gates, m, tid + i * NT, H);
-        return p;
-    };
-    auto settled = [&](Inputs p, int i) {
-        const int at = tid + i * NT;
-        p.t = settle(p.t, at, H), p.dz = settle(p.dz, at, H), p.dt = settle(p.dt, at, H), p.y = settle(p.y, at, H);
-        if constexpr (GATES) p.gate = settle(p.gate, at, H);
-        return p;
-    };
+    const GradInputs<BF16, NT, GATES> of(g, tid);
+    typename GradInputs<BF16, NT, GATES>::Piece next[AHEAD ? NV : 1];
     if constexpr (AHEAD) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (row < g.T) next[i] = read(row, i);
+            if (row < g.T) next[i] = of.read(row, i);
     }
     const Vector weight(channels[0], g.weight, tid, H), post(channels[1], g.post, tid, H), gate(channels[2], g.gate, tid, H);
     float sum[3][NV][8];
@@ -365,30 +368,22 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
             for (int e = 0; e < 8; ++e) sum[a][i][e] = 0.0f;
 
     for (; row < g.T; row += step) {
-        Inputs in[KEEP ? NV : 1];
-        if constexpr (KEEP) {
+        typename GradInputs<BF16, NT, GATES>::Piece in[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                in[i] = settled(AHEAD ? next[AHEAD ? i : 0] : read(row, i), i);
-            }
-        }
+        for (int i = 0; i < NV; ++i) in[i] = of.settled(AHEAD ? next[AHEAD ? i : 0] : of.read(row, i), i);
         if constexpr (AHEAD) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (row + step < g.T) next[i] = read(row + step, i);
+                if (row + step < g.T) next[i] = of.read(row + step, i);
         }
         auto inputs = [&](int i) {
-            if constexpr (KEEP) {
-                if constexpr (BF16) forget(in[i].t), forget(in[i].dz), forget(in[i].y);
-                return in[i];
-            } else {
-                return settled(read(row, i), i);
-            }
+            if constexpr (BF16) forget(in[i].t), forget(in[i].dz), forget(in[i].y);
+            return in[i];
         };
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Inputs p = inputs(i);
+            const auto p = inputs(i);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const f32x4 w = weight(i, h);
@@ -406,13 +401,13 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
         const float r = g.weight ? 1.0f / __builtin_sqrtf(s[0] * inv + g.eps) : 0.0f, mean = s[1] * inv * r;
         const float q = g.post ? 1.0f / __builtin_sqrtf(s[2] * inv + g.eps) : 1.0f;
         // the gradient with respect to t
-        auto slope = [&](const Inputs &p, int e, float w) {
+        auto slope = [&](const auto &p, int e, float w) {
             return __builtin_fmaf(r, __builtin_fmaf(-(p.t.at(e) * r), mean, p.dz.at(e) * w), p.dt.at(e));
         };
-        float d[KEEP ? NV : 1][8], dot[1] = {0.0f};
+        float d[NV][8], dot[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Inputs p = inputs(i);
+            const auto p = inputs(i);
             float out[8], dg[8], dn[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -429,7 +424,7 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
                     sum[1][i][e] = __builtin_fmaf(dn[e], yh, sum[1][i][e]);
                     dn[e] *= b[f];
                     dot[0] = __builtin_fmaf(dn[e], yh, dot[0]);
-                    if constexpr (KEEP) d[i][e] = dn[e];
+                    d[i][e] = dn[e];
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -444,19 +439,14 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Inputs p = inputs(i);
+            const auto p = inputs(i);
             float out[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                f32x4 w, b, c;
-                if constexpr (!KEEP) w = weight(i, h), b = post(i, h), c = gate(i, h);
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
                     const int e = 4 * h + f;
-                    float dn;
-                    if constexpr (KEEP) dn = d[i][e];
-                    else dn = slope(p, e, w[f]) * (GATES ? p.gate.at(e) : c[f]) * b[f];
-                    out[e] = g.post ? q * __builtin_fmaf(-(p.y.at(e) * q), m, dn) : dn;
+                    out[e] = g.post ? q * __builtin_fmaf(-(p.y.at(e) * q), m, d[i][e]) : d[i][e];
                 }
             }
             store8<BF16>(g.z, row, tid + i * NT, H, out);
@@ -492,6 +482,133 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
     }
 }
 
+// Rows above 8192, whose inputs do not fit the registers beside the sums over the rows: r, mean, q and m of each row
+// first (see residual_norm_grad_kernel), a workgroup to a row, then everything else by strips of 2048 channels, the inputs
+// read a second time (bf16 2048 x 16384: 63 us for the reads of the first, 4.1 TB/s, 78 us for the second, 5.1). With both in
+// one kernel, inputs and vectors read again from the caches for each use, that gradient took 520 us, now 157; with the
+// vectors of the first read from the caches for each row 189.
+template <int BF16, int GATES>
+__global__ __launch_bounds__(512) void norm_grad_rows_kernel(NormArgs g, f32x4 *rows) {
+    constexpr int NT = 512, NV = 4;
+    typedef SharedChannels<NT, NV> Vector;
+    typedef typename GradInputs<BF16, NT, GATES>::Piece Piece;
+    __shared__ f32x4 channels[2][Vector::SIZE];
+    __shared__ float part[2][3][NT / 64];
+    const int tid = threadIdx.x;
+    const GradInputs<BF16, NT, GATES> of(g, tid);
+    const float inv = 1.0f / (float)g.H;
+    int64_t row = blockIdx.x;
+    int turn = 0;
+    Piece next[BF16 ? NV : 1];   // the next row's (where registers hold them)
+    if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) next[i] = of.read(row, i);   // (there are no more workgroups than rows)
+    }
+    const Vector weight(channels[0], g.weight, tid, g.H), post(channels[1], g.post, tid, g.H);   // (post: times the gate)
+    if (g.gate) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Raw<0> c = Channels<NT, NV, false>(g.gate, tid, g.H).read(i);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) post.at[(2 * i + h) * NT + tid] *= __builtin_bit_cast(f32x4, c.v[h]);
+        }
+    }
+    for (; row < g.T; row += gridDim.x) {
+        Piece in[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) in[i] = BF16 ? next[BF16 ? i : 0] : of.read(row, i);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) in[i] = of.settled(in[i], i);
+        if constexpr (BF16) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (row + gridDim.x < g.T) next[i] = of.read(row + gridDim.x, i);
+        }
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 w = weight(i, h);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int e = 4 * h + f;
+                    const float t = in[i].t.at(e), y = in[i].y.at(e);
+                    s[0] = __builtin_fmaf(t, t, s[0]);
+                    s[1] = __builtin_fmaf(in[i].dz.at(e) * w[f], t, s[1]);
+                    s[2] = __builtin_fmaf(y, y, s[2]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);   // a piece at a time, which takes fewer registers
+        }
+        row_sums<NT>(s, part, turn);
+        const float r = g.weight ? 1.0f / __builtin_sqrtf(s[0] * inv + g.eps) : 0.0f, mean = s[1] * inv * r;
+        const float q = g.post ? 1.0f / __builtin_sqrtf(s[2] * inv + g.eps) : 1.0f;
+        float dot[1] = {0.0f};
+        if (g.post) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if constexpr (BF16) forget(in[i].t), forget(in[i].dz), forget(in[i].y);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 w = weight(i, h), b = post(i, h);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const int e = 4 * h + f;
+                        const float v = __builtin_fmaf(r, __builtin_fmaf(-(in[i].t.at(e) * r), mean, in[i].dz.at(e) * w[f]), in[i].dt.at(e));
+                        dot[0] = __builtin_fmaf(GATES ? v * in[i].gate.at(e) * b[f] : v * b[f], in[i].y.at(e) * q, dot[0]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            row_sums<NT>(dot, part, turn);
+        }
+        if (tid == 0) rows[row] = f32x4{r, mean, q, dot[0] * inv};
+    }
+}
+
+template <int BF16, int GATES>
+__global__ __launch_bounds__(256) void norm_grad_strips_kernel(NormArgs g, const f32x4 *rows) {
+    constexpr int NT = 256;
+    const int tid = blockIdx.x * NT + threadIdx.x;   // this thread's piece of every row
+    const GradInputs<BF16, NT, GATES> of(g, tid);
+    typedef Channels<NT, 1, true> Vector;
+    const Vector weight(g.weight, tid, g.H), post(g.post, tid, g.H), gate(g.gate, tid, g.H);
+    const Raw<0> w = weight(0), b = post(0), c = gate(0);
+    float sum[3][8];
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[a][e] = 0.0f;
+    int64_t row = blockIdx.y;
+    typename GradInputs<BF16, NT, GATES>::Piece next = of.read(row, 0);   // (there are no more workgroups than rows)
+    for (; row < g.T; row += gridDim.y) {
+        const auto p = of.settled(next, 0);
+        if (row + gridDim.y < g.T) next = of.read(row + gridDim.y, 0);
+        const f32x4 of_row = rows[row];
+        const float r = of_row[0], mean = of_row[1], q = of_row[2], m = of_row[3];
+        float out[8], dg[8], dy[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float yh = p.y.at(e) * q;
+            const float v = __builtin_fmaf(r, __builtin_fmaf(-(p.t.at(e) * r), mean, p.dz.at(e) * w.at(e)), p.dt.at(e));
+            sum[0][e] = __builtin_fmaf(p.dz.at(e), p.t.at(e) * r, sum[0][e]);
+            out[e] = g.scale * v;
+            dg[e] = v * (yh * b.at(e));
+            if constexpr (!GATES) sum[2][e] += dg[e];
+            const float dn = v * (GATES ? p.gate.at(e) : c.at(e));
+            sum[1][e] = __builtin_fmaf(dn, yh, sum[1][e]);
+            dy[e] = g.post ? q * __builtin_fmaf(-yh, m, dn * b.at(e)) : dn;
+        }
+        store8<BF16>(g.t, row, tid, g.H, out);
+        if constexpr (GATES) store8<BF16>(g.dgates, row, tid, g.H, dg);
+        if (g.y) store8<BF16>(g.z, row, tid, g.H, dy);
+    }
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+        if (g.sums[a]) store8<0>(g.sums[a] + blockIdx.y * g.pitch, 0, tid, g.H, sum[a]);
+}
+
 // The partial rows added up: 64 channels a workgroup, 16 threads to a channel (256 partials of 3 x 7168 5 us, from the
 // caches)
 __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *partials, int64_t n, int H, float *o0, float *o1,
@@ -515,18 +632,18 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float *partials, 
     }
 }
 
-// calls f.run<NT, NV>() for rows of H elements; those above 4096 by MID threads, above 8192 by LONG
-template <int MID, int LONG, class F>
+// calls f.run<NT, NV>() for rows of H elements, those above 4096 by MID threads, or f.run_long() above 8192
+template <int MID, class F>
 void for_length(int H, const F &f) {
     if (H <= 512) f.template run<64, 1>();
     else if (H <= 1024) f.template run<128, 1>();
     else if (H <= 2048) f.template run<256, 1>();
     else if (H <= 4096) f.template run<512, 1>();
     else if (H <= 8192) f.template run<MID, 8192 / 8 / MID>();
-    else f.template run<LONG, 16384 / 8 / LONG>();
+    else f.run_long();
 }
 
-constexpr int64_t kCUs = 256;
+constexpr int64_t kCUs = 256, kStripRows = 128;
 
 template <int BF16>
 struct Forward {
@@ -540,18 +657,29 @@ struct Forward {
         if (a.gates) residual_norm_kernel<BF16, NT, NV, 1><<<grid, dim3(THREADS), 0, stream>>>(a);
         else residual_norm_kernel<BF16, NT, NV, 0><<<grid, dim3(THREADS), 0, stream>>>(a);
     }
+    void run_long() const { run<1024, 2>(); }
 };
 
 template <int BF16>
 struct Backward {
     const NormArgs &a;
     int64_t workgroups;
+    f32x4 *rows;
     hipStream_t stream;
     template <int NT, int NV>
     void run() const {
         const dim3 grid((unsigned)workgroups), block(NT * rows_of<NT>());
         if (a.gates) residual_norm_grad_kernel<BF16, NT, NV, 1><<<grid, block, 0, stream>>>(a);
         else residual_norm_grad_kernel<BF16, NT, NV, 0><<<grid, block, 0, stream>>>(a);
+    }
+    template <int GATES>
+    void strips() const {
+        norm_grad_rows_kernel<BF16, GATES><<<dim3((unsigned)(a.T < kCUs ? a.T : kCUs)), dim3(512), 0, stream>>>(a, rows);
+        norm_grad_strips_kernel<BF16, GATES><<<dim3((a.H + 2047) / 2048, (unsigned)workgroups), dim3(256), 0, stream>>>(a, rows);
+    }
+    void run_long() const {
+        if (a.gates) strips<1>();
+        else strips<0>();
     }
 };
 
@@ -560,7 +688,7 @@ struct Backward {
 // 4096 x 1024 33 / 24 / 21, 16384 x 512 30 / 26 / 29, 1024 x 1091 15 / 16 / 22.
 int64_t grad_workgroups(int64_t T, int64_t H) {
     const int64_t need = H <= 512 ? (T + 3) / 4 : T;
-    const int64_t most = H > 2048 ? kCUs : H > 512 && H <= 1024 && T >= 4096 ? 4 * kCUs : T >= 1536 ? 2 * kCUs : kCUs;
+    const int64_t most = H > 8192 ? kStripRows : H > 2048 ? kCUs : H > 512 && H <= 1024 && T >= 4096 ? 4 * kCUs : T >= 1536 ? 2 * kCUs : kCUs;
     return need < most ? need : most;
 }
 
@@ -572,14 +700,14 @@ hipError_t launch_residual_norm(const void *x, const void *y, bool bf16, const f
     NormArgs a{};
     a.x = x, a.y = y, a.weight = weight, a.post = post, a.gate = gate, a.gates = gates, a.scale = scale, a.eps = eps;
     a.t = t, a.z = z, a.T = T, a.H = (int)H;
-    if (bf16) for_length<1024, 1024>((int)H, Forward<1>{a, stream});
-    else for_length<1024, 1024>((int)H, Forward<0>{a, stream});
+    if (bf16) for_length<1024>((int)H, Forward<1>{a, stream});
+    else for_length<1024>((int)H, Forward<0>{a, stream});
     return hipGetLastError();
 }
 
 size_t residual_norm_grad_workspace_bytes(int64_t T, int64_t H) {
     const int64_t n = grad_workgroups(T, H);
-    return n > 1 ? (size_t)(n * 3 * H * 4) : 0;
+    return (size_t)((n > 1 ? n * 3 * H * 4 : 0) + (H > 8192 ? 16 * T : 0));
 }
 
 hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const void *t, const void *y, bool bf16,
@@ -591,12 +719,13 @@ hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const v
     a.x = t, a.y = y, a.dt = dt, a.dz = dz, a.weight = weight, a.post = post, a.gate = gate, a.gates = gates;
     a.scale = scale, a.eps = eps, a.t = dx, a.z = dy, a.dgates = dgates, a.T = T, a.H = (int)H;
     const int64_t n = grad_workgroups(T, H);
-    float *const out[3] = {dweight, dpost, dgate}, *const partials = static_cast<float *>(workspace);
+    f32x4 *const rows = static_cast<f32x4 *>(workspace);   // (of long rows only)
+    float *const out[3] = {dweight, dpost, dgate}, *const partials = reinterpret_cast<float *>(rows + (H > 8192 ? T : 0));
     for (int i = 0; i < 3; ++i) a.sums[i] = out[i] ? (n > 1 ? partials + i * H : out[i]) : nullptr;
     a.pitch = 3 * H;
     if (n > 0) {
-        if (bf16) for_length<512, 512>((int)H, Backward<1>{a, n, stream});
-        else for_length<512, 512>((int)H, Backward<0>{a, n, stream});
+        if (bf16) for_length<512>((int)H, Backward<1>{a, n, rows, stream});
+        else for_length<512>((int)H, Backward<0>{a, n, rows, stream});
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (n == 1 || !(dweight || dpost || dgate)) return hipSuccess;

@@ -169,6 +169,28 @@ def test_residual_norm_backward(T, H, dtype):
     near(dweight, ref["dweight"][0], (ROW + rows) * U * ref["dweight"][1], "dweight")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 9000), (129, 10240), (600, 9001)])
+def test_gradient_of_long_rows(T, H, dtype):
+    test_residual_norm_backward(T, H, dtype)
+
+
+def test_gradient_of_long_rows_is_its_own():
+    """A NaN in one row stays in its row and in the sums; the same call gives the same bits."""
+    g = rng(7)
+    T, H = 300, 8200
+    t, y, dz = (randn(g, T, H) for _ in range(3))
+    w, post = torch.rand(H, device="cuda"), torch.rand(H, device="cuda")
+    one, two = (fq.residual_norm_backward(None, dz, t, y, w, post=post) for _ in range(2))
+    assert all(torch.equal(a, b) for a, b in zip(one[:4], two[:4]))
+    bad = y.clone()
+    bad[77] = float("nan")
+    dx, dy, dw, dp, _ = fq.residual_norm_backward(None, dz, t, bad, w, post=post)
+    keep = torch.arange(T, device="cuda") != 77
+    assert torch.equal(dx, one[0]) and torch.equal(dw, one[2]) and torch.equal(dy[keep], one[1][keep])
+    assert torch.isnan(dy[77]).all() and torch.isnan(dp).all()
+
+
 def test_norm_gradient_by_differences():
     """The formulas above, against differences of the forward formula in 64 bits."""
     g = rng(5)
