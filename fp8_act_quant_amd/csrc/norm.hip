@@ -484,9 +484,9 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_grad_kernel(
 
 // Rows above 8192, whose inputs do not fit the registers beside the sums over the rows: r, mean, q and m of each row
 // first (see residual_norm_grad_kernel), a workgroup to a row, then everything else by strips of 2048 channels, the inputs
-// read a second time (bf16 2048 x 16384: 63 us for the reads of the first, 4.1 TB/s, 78 us for the second, 5.1). With both in
-// one kernel, inputs and vectors read again from the caches for each use, that gradient took 520 us, now 157; with the
-// vectors of the first read from the caches for each row 189.
+// read a second time (bf16 2048 x 16384: 65 us for the reads of the first, 4.1 TB/s, 78 us for the second, 5.1). With both in
+// one kernel, inputs and vectors read again from the caches for each use, that gradient took 520 us, now 145; with the
+// vectors of the first read from the caches for each row 32 us more.
 template <int BF16, int GATES>
 __global__ __launch_bounds__(512) void norm_grad_rows_kernel(NormArgs g, f32x4 *rows) {
     constexpr int NT = 512, NV = 4;
@@ -643,7 +643,7 @@ void for_length(int H, const F &f) {
     else f.run_long();
 }
 
-constexpr int64_t kCUs = 256, kStripRows = 128;
+constexpr int64_t kCUs = 256;
 
 template <int BF16>
 struct Forward {
@@ -685,10 +685,13 @@ struct Backward {
 
 // Workgroups of the gradient, each of which leaves a partial row: as many as run at once, where that is worth
 // their partials. us with 256 / 512 / 1024 of them, bf16: 4096 x 7168 94 / 103 / 129, 4096 x 2048 34 / 28 / 32,
-// 4096 x 1024 33 / 24 / 21, 16384 x 512 30 / 26 / 29, 1024 x 1091 15 / 16 / 22.
+// 4096 x 1024 33 / 24 / 21, 16384 x 512 30 / 26 / 29, 1024 x 1091 15 / 16 / 22. Of strips of long rows three workgroups a
+// CU run at once; us with 96 / 128 / 256 to a strip: bf16 2048 x 16384 (8 strips) 145 / 157 / 154, fp32 2048 x 12288 (6)
+// 233 / 215 / 216.
 int64_t grad_workgroups(int64_t T, int64_t H) {
     const int64_t need = H <= 512 ? (T + 3) / 4 : T;
-    const int64_t most = H > 8192 ? kStripRows : H > 2048 ? kCUs : H > 512 && H <= 1024 && T >= 4096 ? 4 * kCUs : T >= 1536 ? 2 * kCUs : kCUs;
+    const int64_t most = H > 8192 ? 3 * kCUs / ((H + 2047) / 2048) : H > 2048 ? kCUs
+                         : H > 512 && H <= 1024 && T >= 4096 ? 4 * kCUs : T >= 1536 ? 2 * kCUs : kCUs;
     return need < most ? need : most;
 }
 
