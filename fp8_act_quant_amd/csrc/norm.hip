@@ -13,8 +13,8 @@
 //
 // Bound by memory: four rows of H elements a token, six for the gradient. So a row is read once, into
 // registers, NT threads to a row and NV pieces of 8 elements a thread, and a workgroup walks many rows:
-// the per-channel vectors stay in registers too (read again for every row they would be more bytes
-// than the rows themselves), the next row's loads are on their way while a row is reduced, and the
+// the per-channel vectors stay in registers too, up to 8192 channels (read again for every row they would be
+// more bytes than the rows themselves, if from the caches), the next row's loads are on their way while a row is reduced, and the
 // gradient's sums over the rows are carried in registers. Squares, sums and every step are fp32; t
 // enters the second norm before its rounding. Outputs round once. The order of every sum is fixed.
 // 16384 x 7168 bf16 177 us, 5.3 TB/s (a copy of 1 GB: 5.15); the gradient of 4096 x 7168 94 us, 3.7 TB/s, of
@@ -197,7 +197,9 @@ constexpr int rows_of() { return NT == 64 ? 4 : 1; }
 template <int BF16, int NT, int NV, int GATES>
 __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormArgs g) {
     constexpr int ROWS = rows_of<NT>();
-    constexpr bool AHEAD = NV <= 2;   // the next row's loads a row ahead, the channels in registers
+    // The channels in registers; of rows above 8192, whose next row's loads already fill those, read again for each row.
+    // us, read / held: bf16 4096 x 12288 with a gate per element 100 / 117, fp32 289 / 309; without 93 / 93, 229 / 229
+    constexpr bool HELD = NV == 1;
     __shared__ float part[2][3][NT / 64];
     const int tid = threadIdx.x % NT, H = g.H;
     const int64_t step = (int64_t)gridDim.x * ROWS;
@@ -214,10 +216,9 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormA
             if constexpr (GATES) gt[i] = load8<BF16>(g.gates, m, tid + i * NT, H);
         }
     };
-    if (AHEAD && row < g.T) load(row);
-    const Channels<NT, NV, AHEAD> weight(g.weight, tid, H), post(g.post, tid, H), gate(g.gate, tid, H);
+    if (row < g.T) load(row);
+    const Channels<NT, NV, HELD> weight(g.weight, tid, H), post(g.post, tid, H), gate(g.gate, tid, H);
     for (; row < g.T; row += step) {
-        if constexpr (!AHEAD) load(row);
         float t[NV][8], n[NV][8];
         Raw<BF16> gates[NV];
 #pragma unroll
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(NT * rows_of<NT>()) void residual_norm_kernel(NormA
                 n[i][e] = g.y ? ys.at(e) : 0.0f;
             }
         }
-        if (AHEAD && row + step < g.T) load(row + step);
+        if (row + step < g.T) load(row + step);
         if (g.y) {
             float q = 1.0f;
             if (g.post) {
