@@ -14,8 +14,8 @@
 // Bound by memory: four rows of H elements a token, six for the gradient. So a row is read once, into
 // registers, NT threads to a row and NV pieces of 8 elements a thread, and a workgroup walks many rows:
 // the per-channel vectors stay in registers too, up to 8192 channels (read again for every row they would be
-// more bytes than the rows themselves, if from the caches), the next row's loads are on their way while a row is reduced, and the
-// gradient's sums over the rows are carried in registers. Squares, sums and every step are fp32; t
+// more bytes than the rows themselves, if from the caches), the next row's loads are on their way while a row is
+// reduced, and the gradient's sums over the rows are carried in registers. Squares, sums and every step are fp32; t
 // enters the second norm before its rounding. Outputs round once. The order of every sum is fixed.
 // 16384 x 7168 bf16 177 us, 5.3 TB/s (a copy of 1 GB: 5.15); the gradient of 4096 x 7168 94 us, 3.7 TB/s, of
 // 16384 x 2048 82 us, 4.9 TB/s. One row of 7168 takes 4 us on the device, most of it two dependent sums. Rows above 8192
