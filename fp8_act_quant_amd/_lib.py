@@ -36,6 +36,11 @@ FP8Q_NORM_GATES = 1
 FP8Q_ACT_SILU = 0
 FP8Q_ACT_GELU = 1
 
+FP8Q_PLAN_GATED = 0
+FP8Q_PLAN_GATED_BACKWARD = 1
+FP8Q_PLAN_ADAPTER = 2
+FP8Q_PLAN_ADAPTER_ADD = 3
+
 # name -> (restype, argtypes); the exports of include/fp8q.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -81,6 +86,7 @@ SIGNATURES = {
     "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "fp8q_gemm_force_config": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "fp8q_gemm_config_name": (ctypes.c_char_p, [ctypes.c_int]),
+    "fp8q_dense_plan": (_INT, [_INT, _I64, _I64, _I64, _I64, _P]),
     "fp8q_gemm_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, _P, _P]),
     "fp8q_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8q_version": (ctypes.c_int, []),

@@ -413,7 +413,7 @@ hipError_t launch_tile(AdapterArgs a, bool out_bf16, hipStream_t stream) {
     return hipGetLastError();
 }
 hipError_t launch_large(AdapterArgs a, bool out_bf16, hipStream_t stream) {
-    if (!lay_out(a.mm, 256, 256, 2 * 512)) return hipErrorInvalidValue;
+    if (!lay_out(a.mm, 256, 256, 512, kShareMore)) return hipErrorInvalidValue;
     const dim3 grid(share_grid(a.mm.tiles_m * a.mm.tiles_n, 0)), block(512);
     if (out_bf16) adapter_large_kernel<1><<<grid, block, 0, stream>>>(a);
     else adapter_large_kernel<0><<<grid, block, 0, stream>>>(a);
@@ -465,6 +465,36 @@ hipError_t launch_shrink(const AdapterArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// The second launch: few rows, a tile (with W), or a tile that only adds
+struct AdapterTile {
+    int bm, bn;
+    double first, more, end;
+};
+constexpr AdapterTile kTiles[7] = {{32, 64, 0.155, 0.125, 1.1}, {64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7},
+                                   {256, 256, 1.3, 1.5, 8.0}, {32, 32, 0.105, 0.085, 1.0}, {64, 32, 0.145, 0.12, 1.1}};
+enum { kFew16 = 7, kFew32, kAddOwn, kAddNarrow, kAddWide };
+int adapter_choice(int64_t M, int64_t N, int64_t K) {
+    // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
+    if (M <= 16) return N <= 4096 ? kFew16 : kFew32;
+    int best = 4;
+    double least = HUGE_VAL;
+    for (int t = 0; t < 7; ++t) {
+        const AdapterTile &tile = kTiles[t];
+        const double us = tile_time(M, N, (K + KSTEP - 1) / KSTEP, tile.bm, tile.bn, tile.first, tile.more, tile.end, t == 4);
+        if (us < least) least = us, best = t;
+    }
+    return best;
+}
+int added_choice(int64_t M, int64_t N, int64_t rank) {
+    // Each lane for itself while that is little to read, us against the matrix unit with every row's adapter another
+    // and with 90 rows an adapter: 500 x 1000 at rank 16 5.5 / 10.5 and 4.4 / 6.4, 250 x 1000 at 64 9.1 / 20 and
+    // 6.2 / 9.5; 250 x 3000 at 64 20 / 20 and 11 / 9, 500 x 7168 at 64 74 / 53 and 35 / 19.
+    if (M <= 64 || M * N * rank <= 1 << 24) return kAddOwn;
+    // A wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
+    // 23 / 27, 1500 x 3000 24 / 28; but where it leaves CUs idle: 1500 x 1000 17 / 11, 500 x 7168 55 / 57, 500 x 3000 56 / 27.
+    return ((M + 63) / 64) * ((N + 255) / 256) < 256 ? kAddNarrow : kAddWide;
+}
+
 }  // namespace
 
 size_t adapter_linear_workspace_bytes(int64_t M, int64_t K, int64_t rank) {
@@ -479,31 +509,12 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
                   (int)adapters, (int)rank, splits_of(M, K, rank)};
     if (adapters > 0)
         if (hipError_t e = launch_shrink(g, stream)) return e;
-    if (!w && base) {
-        // Each lane for itself while that is little to read, us against the matrix unit with every row's adapter another
-        // and with 90 rows an adapter: 500 x 1000 at rank 16 5.5 / 10.5 and 4.4 / 6.4, 250 x 1000 at 64 9.1 / 20 and
-        // 6.2 / 9.5; 250 x 3000 at 64 20 / 20 and 11 / 9, 500 x 7168 at 64 74 / 53 and 35 / 19.
-        if (M <= 64 || M * N * rank <= 1 << 24) return launch_add<32, 32, 0>(g, out_bf16, stream);
-        // A wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
-        // 23 / 27, 1500 x 3000 24 / 28; but where it leaves CUs idle: 1500 x 1000 17 / 11, 500 x 7168 55 / 57, 500 x 3000 56 / 27.
-        return ((M + 63) / 64) * ((N + 255) / 256) < 256 ? launch_add<64, 64, 1>(g, out_bf16, stream)
-                                                          : launch_add<64, 256, 1>(g, out_bf16, stream);
-    }
-    // (24 rows against the tiles, us: x 7168 x 7168 21.7 / 21.0, x 7168 x 2048 9.4 / 7.4)
-    if (M <= 16) return N <= 4096 ? launch_few<16>(g, out_bf16, stream) : launch_few<32>(g, out_bf16, stream);
-    static const struct {
-        int bm, bn;
-        double first, more, end;
-    } tiles[7] = {{32, 64, 0.155, 0.125, 1.1}, {64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7},
-                  {256, 256, 1.3, 1.5, 8.0}, {32, 32, 0.105, 0.085, 1.0}, {64, 32, 0.145, 0.12, 1.1}};
-    int best = 4;
-    double least = HUGE_VAL;
-    for (int t = 0; t < 7; ++t) {
-        const double us = tile_time(M, N, (K + KSTEP - 1) / KSTEP, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more, tiles[t].end,
-                                    t == 4);
-        if (us < least) least = us, best = t;
-    }
-    switch (best) {
+    switch (!w && base ? added_choice(M, N, rank) : adapter_choice(M, N, K)) {
+    case kAddOwn: return launch_add<32, 32, 0>(g, out_bf16, stream);
+    case kAddNarrow: return launch_add<64, 64, 1>(g, out_bf16, stream);
+    case kAddWide: return launch_add<64, 256, 1>(g, out_bf16, stream);
+    case kFew16: return launch_few<16>(g, out_bf16, stream);
+    case kFew32: return launch_few<32>(g, out_bf16, stream);
     case 0: return launch_tile<32, 64, 4, 6>(g, out_bf16, stream);
     case 1: return launch_tile<64, 64, 4, 5>(g, out_bf16, stream);
     case 2: return launch_tile<128, 128, 4, 4>(g, out_bf16, stream);
@@ -512,6 +523,23 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
     case 5: return launch_tile<32, 32, 4, 8>(g, out_bf16, stream);
     default: return launch_tile<64, 32, 4, 8>(g, out_bf16, stream);
     }
+}
+
+void adapter_report(int64_t M, int64_t N, int64_t K, int64_t rank, bool add, LaunchReport *r) {
+    const int choice = add ? added_choice(M, N, rank) : adapter_choice(M, N, K);
+    const bool few = choice == kFew16 || choice == kFew32;
+    const int bm = few ? 16 : choice == kAddOwn ? 32 : choice >= kAddNarrow ? 64 : kTiles[choice].bm;
+    const int bn = choice == kFew16 ? 16 : few || choice == kAddOwn ? 32 : choice == kAddNarrow ? 64 : choice == kAddWide ? 256 : kTiles[choice].bn;
+    const int threads = choice == 3 || choice == 4 ? 512 : 256;
+    const int shared = few || choice == kAddOwn ? 0 : choice >= kAddNarrow || bm >= 128 || M > 64;
+    MmArgs mm{nullptr, nullptr, M, N, K, K, K, 0, 0, 1};
+    const bool fits = lay_out(mm, bm, bn, threads, choice == 4 ? kShareMore : 0);
+    const int64_t tiles = (int64_t)mm.tiles_m * mm.tiles_n;
+    r[0] = {bm, bn, 1, shared, !fits ? -1 : choice == 4 ? share_grid((int)tiles, 0) : tiles, threads};
+    const bool rows = by_rows(M, rank);
+    const int64_t blocks = (rank + ShrinkTile::BN - 1) / ShrinkTile::BN, splits = splits_of(M, K, rank);
+    r[1] = rows ? LaunchReport{1, 16, splits, 1, M * splits * ((rank + 15) / 16), 256}
+                : LaunchReport{ShrinkTile::BM, ShrinkTile::BN, splits, 0, (M + ShrinkTile::BM - 1) / ShrinkTile::BM * splits * blocks, 256};
 }
 
 }  // namespace fp8q

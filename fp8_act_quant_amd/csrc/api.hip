@@ -526,7 +526,9 @@ int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uin
 }
 
 size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-    return gated_ok(M, F, K) ? fp8q::gated_linear_backward_workspace_bytes(M, F, K) : 0;
+    if (!gated_ok(M, F, K)) return 0;
+    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K);
+    return plans.fits ? fp8q::gated_linear_backward_workspace_bytes(plans, M, F, K) : 0;
 }
 
 int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
@@ -539,10 +541,12 @@ int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t 
     if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(gu, 16) || misaligned(dx, 4) ||
         misaligned(dw, 4) || misaligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
-    if (fp8q::gated_linear_backward_workspace_bytes(M, F, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
+    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K);
+    if (!plans.fits) return FP8Q_ERR_SHAPE;
+    if (fp8q::gated_linear_backward_workspace_bytes(plans, M, F, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
     if (int e = check_device()) return e;
     return finish(fp8q::launch_gated_linear_backward(dh, x, w, gu, act == FP8Q_ACT_GELU, dx, dx_dtype == FP8Q_OUT_BF16, dw,
-                                                     dw_dtype == FP8Q_OUT_BF16, M, F, K, workspace,
+                                                     dw_dtype == FP8Q_OUT_BF16, M, F, K, plans, workspace,
                                                      static_cast<hipStream_t>(stream)));
 }
 
@@ -588,6 +592,22 @@ int fp8q_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dtype, int *config, in
     return FP8Q_OK;
 }
 
+int fp8q_dense_plan(int call, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t *plan) {
+    if (call < FP8Q_PLAN_GATED || call > FP8Q_PLAN_ADAPTER_ADD) return FP8Q_ERR_DTYPE;
+    const bool adapters = call >= FP8Q_PLAN_ADAPTER;
+    if (M <= 0 || N <= 0 || (adapters ? !adapter_ok(M, N, K, 1, rank) : !gated_ok(M, N, K))) return FP8Q_ERR_SHAPE;
+    if (!plan) return FP8Q_ERR_NULL;
+    fp8q::LaunchReport r[2] = {};
+    if (call == FP8Q_PLAN_GATED) fp8q::gated_report(M, N, K, r);
+    else if (call == FP8Q_PLAN_GATED_BACKWARD) fp8q::gated_gradient_report(M, N, K, r);
+    else fp8q::adapter_report(M, N, K, rank, call == FP8Q_PLAN_ADAPTER_ADD, r);
+    for (int i = 0; i < 2; ++i) {
+        const int64_t row[6] = {r[i].rows, r[i].columns, r[i].parts, r[i].shared, r[i].workgroups, r[i].threads};
+        for (int j = 0; j < 6; ++j) plan[6 * i + j] = row[j];
+    }
+    return FP8Q_OK;
+}
+
 const char *fp8q_strerror(int status) {
     switch (status) {
     case FP8Q_OK: return "ok";
@@ -605,6 +625,6 @@ const char *fp8q_strerror(int status) {
     }
 }
 
-int fp8q_version(void) { return (1 << 16) | 7; }
+int fp8q_version(void) { return (1 << 16) | 8; }
 
 }  // extern "C"

@@ -322,7 +322,7 @@ hipError_t launch_gated_tile(GatedArgs a, int mode, hipStream_t stream) {
 }
 
 hipError_t launch_gated_large(GatedArgs a, int mode, hipStream_t stream) {
-    if (!lay_out(a.mm, 256, 128, 2 * 512)) return hipErrorInvalidValue;
+    if (!lay_out(a.mm, 256, 128, 512, kShareMore)) return hipErrorInvalidValue;
     const dim3 grid(share_grid(a.mm.tiles_m * a.mm.tiles_n, 0)), block(512);
     if (mode == 0) gated_large_kernel<0><<<grid, block, 0, stream>>>(a);
     else if (mode == 1) gated_large_kernel<1><<<grid, block, 0, stream>>>(a);
@@ -339,25 +339,34 @@ hipError_t launch_gated_few(const GatedArgs &a, int mode, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
-    const int64_t M = a.mm.M, F = a.mm.N, K = a.mm.K;
+// The projections' tiles: few rows (of X) or a tile, and their number
+struct GatedTile {
+    int bm, bn, threads;
+    double first, more, end;
+};
+constexpr GatedTile kGatedTiles[5] = {{32, 64, 256, 0.155, 0.125, 1.1}, {64, 64, 256, 0.21, 0.18, 1.4}, {128, 128, 256, 0.45, 0.53, 5.0},
+                                      {128, 256, 512, 0.75, 0.83, 5.7}, {256, 256, 512, 1.3, 1.5, 8.0}};
+enum { kFew16 = 5, kFew32, kFew32Twice };   // 16 rows against 16 or 32 rows of W, 32 rows against 32
+int gated_choice(int64_t M, int64_t F, int64_t K) {
     // few rows against the tiles, us: 24 x 3584 x 7168 20.7 / 27.6, 24 x 768 x 7168 13.9 / 17.2, 48 x 3584 x 7168 (four
     // blocks of rows) 30.0 / 26.1
-    if (M <= 16) return F <= 2048 ? launch_gated_few<1, 16>(a, mode, stream) : launch_gated_few<1, 32>(a, mode, stream);
-    if (M <= 32) return launch_gated_few<2, 32>(a, mode, stream);
-    static const struct {
-        int bm, bn;
-        double first, more, end;
-    } tiles[5] = {{32, 64, 0.155, 0.125, 1.1}, {64, 64, 0.21, 0.18, 1.4}, {128, 128, 0.45, 0.53, 5.0}, {128, 256, 0.75, 0.83, 5.7},
-                  {256, 256, 1.3, 1.5, 8.0}};
+    if (M <= 16) return F <= 2048 ? kFew16 : kFew32;
+    if (M <= 32) return kFew32Twice;
     int best = 4;
     double least = HUGE_VAL;
     for (int t = 0; t < 5; ++t) {
-        const double us = tile_time(M, 2 * F, (K + KSTEP - 1) / KSTEP, tiles[t].bm, tiles[t].bn, tiles[t].first, tiles[t].more,
-                                    tiles[t].end, t == 4);
+        const GatedTile &tile = kGatedTiles[t];
+        const double us = tile_time(M, 2 * F, (K + KSTEP - 1) / KSTEP, tile.bm, tile.bn, tile.first, tile.more, tile.end, t == 4);
         if (us < least) least = us, best = t;
     }
-    switch (best) {
+    return best;
+}
+
+hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
+    switch (gated_choice(a.mm.M, a.mm.N, a.mm.K)) {
+    case kFew16: return launch_gated_few<1, 16>(a, mode, stream);
+    case kFew32: return launch_gated_few<1, 32>(a, mode, stream);
+    case kFew32Twice: return launch_gated_few<2, 32>(a, mode, stream);
     case 0: return launch_gated_tile<32, 64, 4, 6>(a, mode, stream);
     case 1: return launch_gated_tile<64, 64, 4, 5>(a, mode, stream);
     case 2: return launch_gated_tile<128, 128, 4, 4>(a, mode, stream);
@@ -371,22 +380,23 @@ hipError_t launch_gated(const GatedArgs &a, int mode, hipStream_t stream) {
 // caches) and a launch. The constants are fitted to times at 4096, 2048, 1021, 256 and 64 tokens of 7168 and 1536 channels
 // and 512 to 4096 hidden ones, with 1 to 8 parts; K-strided X (dW) takes a tenth longer. Both products in one launch, by
 // one kind of tile, or each by its own: 1021 tokens, 1536 -> 4096 78 / 70 us, 1000 x 1096 -> 1000 26 / 33.
-struct Plan {
-    int tile, parts_w, parts_x;   // tile: 0 .. kLargest; the parts of a product that is not in it 0
-    double us;
-};
 constexpr int kMaxParts = 8, kLargest = 3;
+struct GradTile {
+    int bm, bn, threads;
+    double first, more, end;
+};
+constexpr GradTile kGradTiles[kLargest + 1] = {{64, 64, 256, 0.21, 0.19, 0.8}, {128, 128, 256, 0.43, 0.46, 3.5},
+                                               {128, 256, 512, 0.78, 0.82, 5.7}, {256, 256, 512, 1.25, 1.35, 8.0}};
+using Plan = GatedGradPlan;
+// (only plans whose workgroups a grid holds; with none us stays infinite)
 Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
-    static const struct {
-        int bm, bn;
-        double first, more, end;
-    } tiles[4] = {{64, 64, 0.21, 0.19, 0.8}, {128, 128, 0.43, 0.46, 3.5}, {128, 256, 0.78, 0.82, 5.7}, {256, 256, 1.25, 1.35, 8.0}};
     Plan best = {kLargest, has_w, has_x, HUGE_VAL};
     const int64_t steps_w = (M + KSTEP - 1) / KSTEP, steps_x = (2 * F + KSTEP - 1) / KSTEP;
     auto sums = [](int s, int64_t n) { return s > 1 ? (2.0 * s + 1.0) * (double)n * 4.0 / 8e6 : 0.0; };
     for (int t = 0; t <= kLargest; ++t) {
+        const GradTile &tile = kGradTiles[t];
         auto count = [&](int64_t m, int64_t n) {
-            return (double)((m + tiles[t].bm - 1) / tiles[t].bm) * (double)((n + tiles[t].bn - 1) / tiles[t].bn);
+            return (double)((m + tile.bm - 1) / tile.bm) * (double)((n + tile.bn - 1) / tile.bn);
         };
         auto most = [&](bool has, int64_t steps) {
             return !has ? 0 : t == kLargest || steps < 8 ? 1 : steps / 4 < kMaxParts ? (int)(steps / 4) : kMaxParts;
@@ -394,25 +404,16 @@ Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
         for (int sw = has_w; sw <= most(has_w, steps_w); ++sw)
             for (int sx = has_x; sx <= most(has_x, steps_x); ++sx) {
                 const double nw = count(2 * F, K) * sw, nx = count(M, K) * sx, n = nw + nx;
-                if (n > 1e6 && t < kLargest) continue;   // (a grid holds 2^32 threads)
+                if (n > (double)(grid_limit(tile.threads) - kShareMore)) continue;
                 const double pw = sw ? 1.1 * (double)((steps_w + sw - 1) / sw) : 0.0, px = sx ? (double)((steps_x + sx - 1) / sx) : 0.0;
                 const double longest = pw > px ? pw : px;
-                const double run = n <= 256.0 ? longest * tiles[t].first + tiles[t].end
-                                              : tiles[t].more * ((nw * pw + nx * px) / 256.0 + 0.5 * longest) + tiles[t].end * (n / 256.0 + 0.5);
+                const double run = n <= 256.0 ? longest * tile.first + tile.end
+                                              : tile.more * ((nw * pw + nx * px) / 256.0 + 0.5 * longest) + tile.end * (n / 256.0 + 0.5);
                 const double us = run + (sw > 1 || sx > 1 ? 3.0 : 0.0) + sums(sw, 2 * F * K) + sums(sx, M * K);
                 if (us < best.us) best = {t, sw, sx, us};
             }
     }
     return best;
-}
-struct Plans {
-    bool joint;
-    Plan both, w, x;
-};
-Plans plans_of(int64_t M, int64_t F, int64_t K) {
-    Plans p{true, plan_of(M, F, K, true, true), plan_of(M, F, K, true, false), plan_of(M, F, K, false, true)};
-    p.joint = p.both.us <= p.w.us + p.x.us + 2.0;
-    return p;
 }
 
 template <int BM, int BN, int NW, int NSTAGE>
@@ -423,12 +424,10 @@ hipError_t launch_grads_tile(const ProductArgs &dw, const ProductArgs &dx, hipSt
 }
 
 hipError_t launch_grads(ProductArgs dw, ProductArgs dx, const Plan &plan, float *parts, hipStream_t stream) {
-    static const int bm[] = {64, 128, 128, 256}, bn[] = {64, 128, 256, 256}, threads[] = {256, 256, 512, 512};
+    const GradTile &tile = kGradTiles[plan.tile];
     if (dw.splits) dw.splits = plan.parts_w;
     if (dx.splits) dx.splits = plan.parts_x;
-    // (twice the tiles, of two products, in the largest ones' halves)
-    if (!lay_out(dw.mm, bm[plan.tile], bn[plan.tile], threads[plan.tile] * 4 * kMaxParts) ||
-        !lay_out(dx.mm, bm[plan.tile], bn[plan.tile], threads[plan.tile] * 4 * kMaxParts))
+    if (!lay_out(dw.mm, tile.bm, tile.bn, tile.threads) || !lay_out(dx.mm, tile.bm, tile.bn, tile.threads))   // (plan_of saw to it)
         return hipErrorInvalidValue;
     SumArgs sum{};
     ProductArgs *const each[2] = {&dx, &dw};
@@ -462,16 +461,47 @@ hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bo
     return launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, h, gu, nullptr, gelu}, h_bf16, stream);
 }
 
+GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K) {
+    GatedGradPlans p{true, true, plan_of(M, F, K, true, true), plan_of(M, F, K, true, false), plan_of(M, F, K, false, true)};
+    p.joint = p.both.us <= p.w.us + p.x.us + 2.0 && p.both.us < HUGE_VAL;
+    p.fits = p.joint || (p.w.us < HUGE_VAL && p.x.us < HUGE_VAL);
+    return p;
+}
+
 // dg and du, then the parts' sums
-size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-    const Plans p = plans_of(M, F, K);
+size_t gated_linear_backward_workspace_bytes(const GatedGradPlans &p, int64_t M, int64_t F, int64_t K) {
     const int64_t x = p.joint ? p.both.parts_x : p.x.parts_x, w = p.joint ? p.both.parts_w : p.w.parts_w;
     return (size_t)(M * F * 4 + (x > 1 ? x * M * K * 4 : 0) + (w > 1 ? w * 2 * F * K * 4 : 0));
 }
 
+void gated_report(int64_t M, int64_t F, int64_t K, LaunchReport *r) {
+    const int choice = gated_choice(M, F, K);
+    if (choice >= kFew16) {
+        const int nb = choice == kFew16 ? 16 : 32;
+        *r = {choice == kFew32Twice ? 32 : 16, nb, 1, 0, (F + nb / 2 - 1) / (nb / 2), 256};
+        return;
+    }
+    const GatedTile &tile = kGatedTiles[choice];
+    MmArgs mm{nullptr, nullptr, M, F, K, K, K, 0, 0, 1};
+    const bool fits = lay_out(mm, tile.bm, tile.bn / 2, tile.threads, choice == 4 ? kShareMore : 0);
+    const int64_t tiles = (int64_t)mm.tiles_m * mm.tiles_n;
+    *r = {tile.bm, tile.bn, 1, 0, !fits ? -1 : choice == 4 ? share_grid((int)tiles, 0) : tiles, tile.threads};
+}
+
+void gated_gradient_report(int64_t M, int64_t F, int64_t K, LaunchReport *r) {
+    const GatedGradPlans p = gated_gradient_plans(M, F, K);
+    const Plan &w = p.joint ? p.both : p.w, &x = p.joint ? p.both : p.x;
+    MmArgs mw{nullptr, nullptr, 2 * F, K, M, 2 * F, K, 0, 0, 1}, mx{nullptr, nullptr, M, K, 2 * F, 2 * F, K, 0, 0, 1};
+    const GradTile &tw = kGradTiles[w.tile], &tx = kGradTiles[x.tile];
+    const bool fits = p.fits && lay_out(mw, tw.bm, tw.bn, tw.threads) && lay_out(mx, tx.bm, tx.bn, tx.threads);
+    const int nw = fits ? mw.tiles_m * mw.tiles_n * w.parts_w : 0, nx = fits ? mx.tiles_m * mx.tiles_n * x.parts_x : 0;
+    r[0] = {tw.bm, tw.bn, w.parts_w, p.joint, fits ? (int64_t)share_grid(nw, p.joint ? nx : 0) : -1, tw.threads};
+    r[1] = {tx.bm, tx.bn, x.parts_x, p.joint, fits ? (int64_t)share_grid(p.joint ? nw : 0, nx) : -1, tx.threads};
+}
+
 hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,
                                         bool gelu, void *dx, bool dx_bf16, void *dw, bool dw_bf16, int64_t M, int64_t F,
-                                        int64_t K, void *workspace, hipStream_t stream) {
+                                        int64_t K, const GatedGradPlans &plans, void *workspace, hipStream_t stream) {
     uint16_t *const d = static_cast<uint16_t *>(workspace);   // [M, 2 F]
     float *const parts = reinterpret_cast<float *>(d + M * 2 * F);
     if (M > 0 && F > 0) {
@@ -485,7 +515,6 @@ hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, c
     }
     const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, dx_bf16, dx && M > 0 && K > 0};
     const ProductArgs pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, dw_bf16, dw && F > 0 && K > 0};
-    const Plans plans = plans_of(M, F, K);
     if (plans.joint) return px.splits || pw.splits ? launch_grads(pw, px, plans.both, parts, stream) : hipSuccess;
     // (one after the other: their parts' sums may share their place)
     ProductArgs none{};

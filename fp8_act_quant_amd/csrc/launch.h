@@ -123,12 +123,21 @@ hipError_t launch_residual_norm_backward(const void *dt, const void *dz, const v
 
 // Gated projections (gated.hip): x [M, K], w [2 F, K], K and F multiples of 8 (K < 2^23, F < 2^22), the
 // gradient's workspace holds gated_linear_backward_workspace_bytes.
-size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
+struct GatedGradPlan {
+    int tile, parts_w, parts_x;   // tile: a kind of tile; the parts of each product's K, 0 where the plan is not for it
+    double us;
+};
+struct GatedGradPlans {
+    bool joint, fits;             // both products in one launch; whether the launches fit a grid
+    GatedGradPlan both, w, x;
+};
+GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K);
+size_t gated_linear_backward_workspace_bytes(const GatedGradPlans &plans, int64_t M, int64_t F, int64_t K);
 hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
                                int64_t M, int64_t F, int64_t K, hipStream_t stream);
 hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu,
                                         bool gelu, void *dx, bool dx_bf16, void *dw, bool dw_bf16, int64_t M, int64_t F,
-                                        int64_t K, void *workspace, hipStream_t stream);
+                                        int64_t K, const GatedGradPlans &plans, void *workspace, hipStream_t stream);
 
 // Linear layers with an adapter per token (adapter.hip): K and rank multiples of 8, rank <= kMaxRank; w, or base
 // of y's type; the workspace holds adapter_linear_workspace_bytes.
@@ -138,5 +147,14 @@ hipError_t launch_adapter_linear(const uint16_t *x, const uint16_t *w, const flo
                                  const uint16_t *b, const float *scales, const int32_t *ids, const void *base, void *y,
                                  bool out_bf16, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank,
                                  void *workspace, hipStream_t stream);
+
+// What a call of the dense block's products launches: the rows and columns of a workgroup's tile, parts of K, whether
+// its way is the shared one (see fp8q_dense_plan), workgroups (-1: more than a grid holds) and their threads
+struct LaunchReport {
+    int64_t rows, columns, parts, shared, workgroups, threads;
+};
+void gated_report(int64_t M, int64_t F, int64_t K, LaunchReport *r);                                    // one launch
+void gated_gradient_report(int64_t M, int64_t F, int64_t K, LaunchReport *r);                           // two
+void adapter_report(int64_t M, int64_t N, int64_t K, int64_t rank, bool add, LaunchReport *r);          // two
 
 }  // namespace fp8q

@@ -170,13 +170,19 @@ inline double tile_time(int64_t M, int64_t N, int64_t steps, int bm, int bn, dou
 using WholeTile = Tile<256, 256, 8, 2, 2>;
 using HalfTile = Tile<128, 256, 8, 2, 3>;
 
+// The most workgroups of `threads` threads in a grid, which holds 2^32 - 1 threads
+constexpr int64_t grid_limit(int threads) { return 0xFFFFFFFFll / threads; }
+// Workgroups of share_grid beyond the tiles: 16 halves an XCD, and XCDs of one or two tiles fewer than another
+constexpr int64_t kShareMore = 8 * 18;
+
 // The tiles of a launch, and down how many tile rows to walk (so that the some 32 tiles of an XCD read the
-// fewest rows of both operands). False: more than a grid holds.
-inline bool lay_out(MmArgs &a, int bm, int bn, int threads) {
+// fewest rows of both operands). False: more than a grid holds, `more` workgroups beside the tiles.
+inline bool lay_out(MmArgs &a, int bm, int bn, int threads, int64_t more = 0) {
     const int64_t tm = (a.M + bm - 1) / bm, tn = (a.N + bn - 1) / bn;
     a.tiles_m = a.tiles_n = 0;
     if (tm == 0 || tn == 0) return true;
-    if (tm > 0x7FFFFFFF || tn > 0x7FFFFFFF || tm > 0xFFFFFFFFll / threads / tn) return false;
+    const int64_t most = grid_limit(threads) - more;
+    if (tm > most || tn > most || tm > most / tn) return false;
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
     int64_t best = -1;

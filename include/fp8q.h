@@ -485,6 +485,22 @@ int fp8q_gemm_force_config(int config, int splits);
 const char *fp8q_gemm_config_name(int config);
 int fp8q_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dtype, int *config, int *splits);
 
+/* The launches that the dense block's products would use for a shape, for tuning and tests (host only).
+ * fp8q_dense_plan(call, M, N, K, rank, plan) writes plan[2][6]: of each launch the rows and columns of a
+ * workgroup's tile, the parts of K, a mark, the workgroups (-1: more than a grid holds) and the threads of one.
+ *   FP8Q_PLAN_GATED: gated_linear (N = F), whose tiles' columns are rows of w; one launch.
+ *   FP8Q_PLAN_GATED_BACKWARD: the products of gated_linear_backward, dw then dx; mark: both are one launch, whose
+ *      workgroups stand in both rows.
+ *   FP8Q_PLAN_ADAPTER, FP8Q_PLAN_ADAPTER_ADD: adapter_linear with w, with base; mark: rows share their adapter's
+ *      products. Then x a^T; mark: a row at a time.
+ * rank is read for the adapters only. Returns FP8Q_OK, or FP8Q_ERR_DTYPE (call) / FP8Q_ERR_SHAPE (M and N positive, the
+ * other limits as the call's) / FP8Q_ERR_NULL without writing. */
+#define FP8Q_PLAN_GATED 0
+#define FP8Q_PLAN_GATED_BACKWARD 1
+#define FP8Q_PLAN_ADAPTER 2
+#define FP8Q_PLAN_ADAPTER_ADD 3
+int fp8q_dense_plan(int call, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t *plan);
+
 /* Static string describing a status code (never NULL). */
 const char *fp8q_strerror(int status);
 

@@ -1,0 +1,73 @@
+"""Which kernels the dense block's products choose (host only): every choice within the documented sizes, as far as
+their operands fit a GPU's memory, is one that a grid holds."""
+import ctypes
+import itertools
+
+import pytest
+
+from fp8_act_quant_amd import _lib as L
+
+MEMORY = 288 << 30
+GRID = 2 ** 32 - 1           # threads
+
+
+def plan(call, M, N, K, rank=8):
+    out = (ctypes.c_int64 * 12)()
+    assert L.lib.fp8q_dense_plan(call, M, N, K, rank, out) == L.FP8Q_OK
+    return tuple(out[:6]), tuple(out[6:])
+
+
+def tiles(M, N, launch):
+    return -(-M // launch[0]) * -(-N // launch[1])
+
+
+def sizes(least, most, step=8):
+    """Numbers over a whole range, on both sides of its powers of two."""
+    n = least
+    while n < most:
+        yield from (v for v in (n - step, n, n + step) if least <= v <= most)
+        n *= 2
+    yield most
+
+
+def test_gated_plans_fit_a_grid():
+    seen = 0
+    for M, F, K in itertools.product(sizes(1, 1 << 26, 1), sizes(8, (1 << 22) - 8), sizes(8, (1 << 23) - 8)):
+        held = 2 * M * K + 4 * F * K + 2 * M * F
+        if held > MEMORY:
+            continue
+        r, _ = plan(L.FP8Q_PLAN_GATED, M, F, K)
+        wanted = -(-M // r[0]) * -(-F // (r[1] // 2))
+        assert wanted <= r[4] <= wanted + 144 and r[4] * r[5] <= GRID, (M, F, K, r)
+        if held + 2 * M * K + 4 * F * K + 4 * M * F > MEMORY:      # dx, dw and dg, du beside them
+            continue
+        seen += 1
+        w, x = plan(L.FP8Q_PLAN_GATED_BACKWARD, M, F, K)
+        n = [tiles(2 * F, K, w) * w[2], tiles(M, K, x) * x[2]]
+        assert w[3] == x[3] and (not w[3] or w[4:] == x[4:])
+        for mine, r in zip(n if not w[3] else [sum(n)], (w, x)):
+            assert mine <= r[4] <= 2 * mine + 144 and r[4] * r[5] <= GRID, (M, F, K, r)
+        # and the call itself has nothing against the size
+        assert L.lib.gated_linear_backward_workspace_bytes(M, F, K) >= 4 * M * F
+        assert L.lib.gated_linear_backward(65536, 65536, 65536, None, 0, 65536, 1, 65536, 1, M, F, K, None, 0,
+                                           None) == L.FP8Q_ERR_WORKSPACE
+    assert seen > 5000
+
+
+def test_gradients_past_a_grid_are_refused():
+    """dw alone would be 2^29 tiles."""
+    F = K = (1 << 22) - 8
+    assert L.lib.gated_linear_backward_workspace_bytes(8, F, K) == 0
+    assert L.lib.gated_linear_backward(65536, 65536, 65536, None, 0, 65536, 1, 65536, 1, 8, F, K, 65536, 1 << 60,
+                                       None) == L.FP8Q_ERR_SHAPE
+    assert plan(L.FP8Q_PLAN_GATED_BACKWARD, 8, F, K)[0][4] == -1
+
+
+def test_plan_arguments():
+    out = (ctypes.c_int64 * 12)()
+    for args, status in (((4, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE), ((-1, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE),
+                         ((0, 0, 8, 8, 8, out), L.FP8Q_ERR_SHAPE), ((0, 8, 12, 8, 8, out), L.FP8Q_ERR_SHAPE),
+                         ((1, 8, 8, 12, 8, out), L.FP8Q_ERR_SHAPE), ((2, 8, 0, 8, 8, out), L.FP8Q_ERR_SHAPE),
+                         ((3, 8, 8, 8, 12, out), L.FP8Q_ERR_SHAPE), ((0, 8, 8, 8, 8, None), L.FP8Q_ERR_NULL)):
+        assert L.lib.fp8q_dense_plan(*args) == status, args
+    assert list(out) == [0] * 12
