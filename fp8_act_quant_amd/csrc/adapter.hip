@@ -489,7 +489,7 @@ int added_choice(int64_t M, int64_t N, int64_t rank) {
     // Each lane for itself while that is little to read, us against the matrix unit with every row's adapter another
     // and with 90 rows an adapter: 500 x 1000 at rank 16 5.5 / 10.5 and 4.4 / 6.4, 250 x 1000 at 64 9.1 / 20 and
     // 6.2 / 9.5; 250 x 3000 at 64 20 / 20 and 11 / 9, 500 x 7168 at 64 74 / 53 and 35 / 19.
-    if (M <= 64 || M * N * rank <= 1 << 24) return kAddOwn;
+    if ((M <= 64 || M * N * rank <= 1 << 24) && (M + 31) / 32 * ((N + 31) / 32) <= grid_limit(256)) return kAddOwn;
     // A wide tile reads u's parts less often, us against 64 columns at rank 64: 5000 x 7168 94 / 150, 5000 x 1000
     // 23 / 27, 1500 x 3000 24 / 28; but where it leaves CUs idle: 1500 x 1000 17 / 11, 500 x 7168 55 / 57, 500 x 3000 56 / 27.
     return ((M + 63) / 64) * ((N + 255) / 256) < 256 ? kAddNarrow : kAddWide;

@@ -63,6 +63,23 @@ def test_gradients_past_a_grid_are_refused():
     assert plan(L.FP8Q_PLAN_GATED_BACKWARD, 8, F, K)[0][4] == -1
 
 
+def test_adapter_plans_fit_a_grid():
+    """y, x and W or base within memory, and u, of adapters of the least and the most ranks."""
+    seen = 0
+    for M, N, K in itertools.product(sizes(1, 1 << 26, 1), sizes(1, 1 << 28, 1), sizes(8, (1 << 23) - 8)):
+        if 2 * M * K + 2 * M * N + 2 * N * K > MEMORY:
+            continue
+        for rank in (8, 256):
+            if 4 * M * rank + 2 * rank * (K + N) > MEMORY:
+                continue
+            seen += 1
+            for call in (L.FP8Q_PLAN_ADAPTER, L.FP8Q_PLAN_ADAPTER_ADD):
+                r, u = plan(call, M, N, K, rank)
+                assert tiles(M, N, r) <= r[4] <= tiles(M, N, r) + 144 and r[4] * r[5] <= GRID, (call, M, N, K, rank, r)
+                assert 0 < u[4] * u[5] <= GRID and u[1] * u[2] >= 16, (M, N, K, rank, u)
+    assert seen > 5000
+
+
 def test_plan_arguments():
     out = (ctypes.c_int64 * 12)()
     for args, status in (((4, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE), ((-1, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE),

@@ -60,7 +60,7 @@ def slopes64(dh, gu, off, act, lost):
 
 
 def product_of(d, off, w, terms):
-    """d w, a sum of `terms`, and how far its fp32 form may be off where d is off by `off`."""
+    """d w, w [terms, N], and how far its fp32 form may be off where d is off by `off`."""
     w = w.double()
     return d @ w, off @ w.abs() + 2 * (terms / 32 + 32) * U * ((d.abs() + off) @ w.abs())
 
@@ -87,3 +87,25 @@ def test_gradient_of_very_many_rows():
         xs = x[lo:lo + (1 << 22)].double()
         ref += (dh[lo:lo + (1 << 22), F - 1].double() * act64(xs @ w[F - 1].double(), "silu")[0]) @ xs
     assert float((dw[2 * F - 1].double() - ref).norm() / ref.norm()) < half(torch.bfloat16)
+
+
+def test_adapters_of_the_most_channels():
+    """2^28 channels of an output that adapters are added to, for more than 32 rows: 2^24 of the smallest tiles."""
+    M, N, K, r = 33, 1 << 28, 8, 8
+    g = rng(2)
+    x, a = randn(g, M, K), randn(g, 2, r, K, std=0.5)
+    b = torch.empty((2, N, r), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    ids = (torch.arange(M, device="cuda") % 3 - 1).to(torch.int32)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    at = torch.tensor([0, 31, 32, 1 << 27, N - 33, N - 1], device="cuda")
+    base = y[:, at].double()
+    got = fq.adapter_add(y, x, a, b, ids, out=y)[:, at]
+    ref, off = base.clone(), 2 * U * base.abs()
+    for e in range(2):
+        rows = (ids == e).nonzero()[:, 0]
+        u, off_u = product64(x[rows], a[e])
+        add, lost = product_of(u, off_u, b[e, at].t(), r)
+        ref[rows] += add
+        off[rows] += lost
+    near(got, ref, off + 4 * U * ref.abs())
+    assert torch.equal(got[ids < 0].double(), base[ids < 0])
