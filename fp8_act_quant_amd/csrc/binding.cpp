@@ -4,8 +4,8 @@
 //
 // Native because these calls are small: a decode step's kernel takes 3 us, and checks, allocations
 // and ctypes in Python took 6 us a call around the 3 us that the launch itself takes; here they
-// take about 1 us. Names, defaults and documentation are in moe.py, int8.py and
-// block.py.
+// take about 1 us (gated_linear_backward 2 to 4: the choice of its tiles, for the workspace and for the
+// launch, is 0.1 to 1.4 us each). Names, defaults and documentation are in moe.py, int8.py and block.py.
 #include <Python.h>
 
 #include <ATen/Context.h>

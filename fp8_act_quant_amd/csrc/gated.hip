@@ -391,25 +391,36 @@ using Plan = GatedGradPlan;
 // (only plans whose workgroups a grid holds; with none us stays infinite)
 Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
     Plan best = {kLargest, has_w, has_x, HUGE_VAL};
-    const int64_t steps_w = (M + KSTEP - 1) / KSTEP, steps_x = (2 * F + KSTEP - 1) / KSTEP;
-    auto sums = [](int s, int64_t n) { return s > 1 ? (2.0 * s + 1.0) * (double)n * 4.0 / 8e6 : 0.0; };
+    // What does not depend on the other product's parts: K's steps of a part, and what its sums cost
+    struct Parts {
+        int least, most;
+        double steps[kMaxParts + 1], sums[kMaxParts + 1];
+        Parts(bool has, int64_t k_steps, double longer, int64_t outputs) : least(has), most(0) {
+            steps[0] = sums[0] = 0.0;
+            if (!has) return;
+            most = k_steps < 8 ? 1 : k_steps / 4 < kMaxParts ? (int)(k_steps / 4) : kMaxParts;
+            for (int s = 1; s <= most; ++s) {
+                steps[s] = longer * (double)((k_steps + s - 1) / s);
+                sums[s] = s > 1 ? (2.0 * s + 1.0) * (double)outputs * 4.0 / 8e6 : 0.0;
+            }
+        }
+    };
+    const Parts pw(has_w, (M + KSTEP - 1) / KSTEP, 1.1, 2 * F * K), px(has_x, (2 * F + KSTEP - 1) / KSTEP, 1.0, M * K);
     for (int t = 0; t <= kLargest; ++t) {
         const GradTile &tile = kGradTiles[t];
         auto count = [&](int64_t m, int64_t n) {
             return (double)((m + tile.bm - 1) / tile.bm) * (double)((n + tile.bn - 1) / tile.bn);
         };
-        auto most = [&](bool has, int64_t steps) {
-            return !has ? 0 : t == kLargest || steps < 8 ? 1 : steps / 4 < kMaxParts ? (int)(steps / 4) : kMaxParts;
-        };
-        for (int sw = has_w; sw <= most(has_w, steps_w); ++sw)
-            for (int sx = has_x; sx <= most(has_x, steps_x); ++sx) {
-                const double nw = count(2 * F, K) * sw, nx = count(M, K) * sx, n = nw + nx;
-                if (n > (double)(grid_limit(tile.threads) - kShareMore)) continue;
-                const double pw = sw ? 1.1 * (double)((steps_w + sw - 1) / sw) : 0.0, px = sx ? (double)((steps_x + sx - 1) / sx) : 0.0;
-                const double longest = pw > px ? pw : px;
+        const double tiles_w = has_w ? count(2 * F, K) : 0.0, tiles_x = has_x ? count(M, K) : 0.0;
+        const double limit = (double)(grid_limit(tile.threads) - kShareMore);
+        for (int sw = pw.least; sw <= (t == kLargest ? pw.least : pw.most); ++sw)
+            for (int sx = px.least; sx <= (t == kLargest ? px.least : px.most); ++sx) {
+                const double nw = tiles_w * sw, nx = tiles_x * sx, n = nw + nx;
+                if (n > limit) continue;
+                const double longest = pw.steps[sw] > px.steps[sx] ? pw.steps[sw] : px.steps[sx];
                 const double run = n <= 256.0 ? longest * tile.first + tile.end
-                                              : tile.more * ((nw * pw + nx * px) / 256.0 + 0.5 * longest) + tile.end * (n / 256.0 + 0.5);
-                const double us = run + (sw > 1 || sx > 1 ? 3.0 : 0.0) + sums(sw, 2 * F * K) + sums(sx, M * K);
+                                              : tile.more * ((nw * pw.steps[sw] + nx * px.steps[sx]) * (1.0 / 256.0) + 0.5 * longest) + tile.end * (n * (1.0 / 256.0) + 0.5);
+                const double us = run + (sw > 1 || sx > 1 ? 3.0 : 0.0) + pw.sums[sw] + px.sums[sx];
                 if (us < best.us) best = {t, sw, sx, us};
             }
     }
