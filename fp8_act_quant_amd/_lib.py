@@ -35,11 +35,13 @@ FP8Q_MOE_KEEP_SCORES = 4
 FP8Q_NORM_GATES = 1
 FP8Q_ACT_SILU = 0
 FP8Q_ACT_GELU = 1
+FP8Q_GATED_WIDE = 256
 
 FP8Q_PLAN_GATED = 0
 FP8Q_PLAN_GATED_BACKWARD = 1
 FP8Q_PLAN_ADAPTER = 2
 FP8Q_PLAN_ADAPTER_ADD = 3
+FP8Q_PLAN_GATED_BACKWARD_WIDE = 4
 
 # name -> (restype, argtypes); the exports of include/fp8q.h
 _P = ctypes.c_void_p
@@ -81,6 +83,7 @@ SIGNATURES = {
     "gated_linear": (_INT, [_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _P]),
     "gated_linear_backward": (_INT, [_P, _P, _P, _P, _INT, _P, _INT, _P, _INT, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "gated_linear_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "gated_linear_backward_wide_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "adapter_linear": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t,
                               _P]),
     "adapter_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from ._binding import native, out_code
-from ._lib import FP8Q_ACT_GELU, FP8Q_ACT_SILU
+from ._lib import FP8Q_ACT_GELU, FP8Q_ACT_SILU, FP8Q_GATED_WIDE
 
 _ACTS = {"silu": FP8Q_ACT_SILU, "gelu": FP8Q_ACT_GELU}
 
@@ -71,11 +71,13 @@ def gated_linear(x: torch.Tensor, w: torch.Tensor, act: str = "silu", keep: bool
 
 
 def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w: torch.Tensor, gu: torch.Tensor | None = None,
-                          act: str = "silu", dx_dtype=torch.bfloat16, dw_dtype=torch.float32):
+                          act: str = "silu", dx_dtype=torch.bfloat16, dw_dtype=torch.float32, wide: bool = False):
     """Gradients of gated_linear: ``(dx, dw)`` of x's and w's shapes from dh bfloat16 [..., F]. gu as the
     call with keep returned it; without it the projections are computed again. The projections'
-    gradient is rounded to bfloat16 on its way into both (also where they are float32)."""
-    return native.gated_backward(dh, x, w, gu, _act(act), out_code(dx_dtype), out_code(dw_dtype))
+    gradient is rounded to bfloat16 on its way into both (also where they are float32), or with
+    wide goes into them with 16 bits, as two bfloat16 numbers, which takes 1.3 to 2.7 times as long."""
+    return native.gated_backward(dh, x, w, gu, _act(act) | (FP8Q_GATED_WIDE if wide else 0), out_code(dx_dtype),
+                                 out_code(dw_dtype))
 
 
 def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,

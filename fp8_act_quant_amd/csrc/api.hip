@@ -109,6 +109,12 @@ bool gated_ok(int64_t M, int64_t F, int64_t K) {
            2 * F <= kMaxDenseK && M <= kMaxDenseRows;
 }
 
+size_t gated_gradient_bytes(int64_t M, int64_t F, int64_t K, bool wide) {
+    if (!gated_ok(M, F, K)) return 0;
+    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K, wide);
+    return plans.fits ? fp8q::gated_linear_backward_workspace_bytes(plans, M, F, K) : 0;
+}
+
 bool adapter_ok(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank) {
     return M >= 0 && N >= 0 && K >= 0 && K % kDenseStep == 0 && K <= kMaxDenseK && M <= kMaxDenseRows &&
            N <= kMaxDenseN && adapters >= 0 && adapters <= INT32_MAX && rank >= kDenseStep && rank % kDenseStep == 0 &&
@@ -526,14 +532,18 @@ int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uin
 }
 
 size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-    if (!gated_ok(M, F, K)) return 0;
-    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K);
-    return plans.fits ? fp8q::gated_linear_backward_workspace_bytes(plans, M, F, K) : 0;
+    return gated_gradient_bytes(M, F, K, false);
+}
+
+size_t gated_linear_backward_wide_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+    return gated_gradient_bytes(M, F, K, true);
 }
 
 int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
                           int dx_dtype, void *dw, int dw_dtype, int64_t M, int64_t F, int64_t K, void *workspace,
                           size_t workspace_bytes, void *stream) {
+    const bool wide = act >= 0 && (act & FP8Q_GATED_WIDE);
+    if (wide) act -= FP8Q_GATED_WIDE;
     if (!is_type(dx_dtype) || !is_type(dw_dtype) || (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU)) return FP8Q_ERR_DTYPE;
     if (!gated_ok(M, F, K)) return FP8Q_ERR_SHAPE;
     if (K == 0 || (!dx && !dw)) return FP8Q_OK;
@@ -541,7 +551,7 @@ int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t 
     if (misaligned(dh, 16) || misaligned(x, 16) || misaligned(w, 16) || misaligned(gu, 16) || misaligned(dx, 4) ||
         misaligned(dw, 4) || misaligned(workspace, 16))
         return FP8Q_ERR_ALIGN;
-    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K);
+    const fp8q::GatedGradPlans plans = fp8q::gated_gradient_plans(M, F, K, wide);
     if (!plans.fits) return FP8Q_ERR_SHAPE;
     if (fp8q::gated_linear_backward_workspace_bytes(plans, M, F, K) > (workspace ? workspace_bytes : 0)) return FP8Q_ERR_WORKSPACE;
     if (int e = check_device()) return e;
@@ -593,14 +603,14 @@ int fp8q_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dtype, int *config, in
 }
 
 int fp8q_dense_plan(int call, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t *plan) {
-    if (call < FP8Q_PLAN_GATED || call > FP8Q_PLAN_ADAPTER_ADD) return FP8Q_ERR_DTYPE;
-    const bool adapters = call >= FP8Q_PLAN_ADAPTER;
+    if (call < FP8Q_PLAN_GATED || call > FP8Q_PLAN_GATED_BACKWARD_WIDE) return FP8Q_ERR_DTYPE;
+    const bool adapters = call == FP8Q_PLAN_ADAPTER || call == FP8Q_PLAN_ADAPTER_ADD;
     if (M <= 0 || N <= 0 || (adapters ? !adapter_ok(M, N, K, 1, rank) : !gated_ok(M, N, K))) return FP8Q_ERR_SHAPE;
     if (!plan) return FP8Q_ERR_NULL;
     fp8q::LaunchReport r[2] = {};
     if (call == FP8Q_PLAN_GATED) fp8q::gated_report(M, N, K, r);
-    else if (call == FP8Q_PLAN_GATED_BACKWARD) fp8q::gated_gradient_report(M, N, K, r);
-    else fp8q::adapter_report(M, N, K, rank, call == FP8Q_PLAN_ADAPTER_ADD, r);
+    else if (adapters) fp8q::adapter_report(M, N, K, rank, call == FP8Q_PLAN_ADAPTER_ADD, r);
+    else fp8q::gated_gradient_report(M, N, K, call == FP8Q_PLAN_GATED_BACKWARD_WIDE, r);
     for (int i = 0; i < 2; ++i) {
         const int64_t row[6] = {r[i].rows, r[i].columns, r[i].parts, r[i].shared, r[i].workgroups, r[i].threads};
         for (int j = 0; j < 6; ++j) plan[6 * i + j] = row[j];

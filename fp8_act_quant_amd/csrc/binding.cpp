@@ -496,7 +496,7 @@ PyObject *gated(PyObject *const *a) {
     return keep ? pack({h, gu}) : wrap(h);
 }
 
-// (dh, x, w, gu or None, act, dx dtype code, dw dtype code)
+// (dh, x, w, gu or None, act and flags, dx dtype code, dw dtype code)
 PyObject *gated_backward(PyObject *const *a) {
     const Gated g(a[1], a[2]);
     const Tensor &dh = need(a[0], "dh", ScalarType::BFloat16, 16, &g.x);
@@ -504,12 +504,14 @@ PyObject *gated_backward(PyObject *const *a) {
     const Tensor *gu = nullptr;
     if (a[3] != Py_None) shaped(*(gu = &need(a[3], "gu", ScalarType::BFloat16, 16, &g.x)), "gu", g.shape(2 * g.F));
     const Tensor dx = like(g.x, g.x.sizes(), type_of_code(a[5])), dw = like(g.x, g.w.sizes(), type_of_code(a[6]));
-    const size_t bytes = gated_linear_backward_workspace_bytes(g.M, g.F, g.K);
+    const int act = (int)integer(a[4], "act");
+    const size_t bytes = act & FP8Q_GATED_WIDE ? gated_linear_backward_wide_workspace_bytes(g.M, g.F, g.K)
+                                               : gated_linear_backward_workspace_bytes(g.M, g.F, g.K);
     const Tensor ws = bytes ? like(g.x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
     const On on(g.x);
     check("gated_linear_backward",
           gated_linear_backward(ptr<uint16_t>(dh), ptr<uint16_t>(g.x), ptr<uint16_t>(g.w),
-                                static_cast<const uint16_t *>(data(gu)), (int)integer(a[4], "act"), dx.data_ptr(),
+                                static_cast<const uint16_t *>(data(gu)), act, dx.data_ptr(),
                                 code_of(dx), dw.data_ptr(), code_of(dw), g.M, g.F, g.K, out_of(ws), bytes, on.stream()));
     return pack({dx, dw});
 }

@@ -6,7 +6,10 @@
 //
 // act is SiLU, a / (1 + e^-a), or GELU, a * Phi(a) with Phi by erfc (which keeps its relative precision
 // where Phi is small). Products are bf16 with fp32 sums (mm.h); activation and product are fp32 on the
-// sums, rounded once. The gradient's products take dg and du rounded to bf16, the matrix unit's type.
+// sums, rounded once. The gradient's products take dg and du rounded to bf16, the matrix unit's type, or where the
+// caller asks for more (`wide`) as two bf16 numbers, the rounded one and what it lost (16 bits in all), each with
+// products of its own. Error of a bf16 output against 64 bits 2.3e-3 rms rounded, 1.7e-3 (the output's own rounding) wide;
+// 4096 x 7168 -> 2048 397 / 1060 us, 1021 x 1536 -> 4096 102 / 213, 16 x 128 -> 128 7.5 / 10.
 //
 // The projections' columns are dealt so that a lane holds g and u of the same element: nothing of them
 // goes through memory unless the caller keeps them. The gradient forms dg and du from kept projections (a
@@ -30,6 +33,7 @@ struct GatedArgs {
     void *h;              // [M, F]
     uint16_t *gu;         // [M, 2 F] or null; the gradient: dg and du
     const uint16_t *dh;   // the gradient: [M, F]
+    uint16_t *rest;       // the gradient: what dg and du lose in gu, [M, 2 F], or null
     int gelu;
 };
 
@@ -82,6 +86,13 @@ __device__ __forceinline__ Activation activate(float a, int gelu) {
     return {a * p, p * __builtin_fmaf(a, 1.0f - p, 1.0f)};
 }
 
+// What v loses when it is rounded to bf16 (nothing where that is not finite: infinities stay the first number's)
+__device__ __forceinline__ float rest_of(float v) {
+    const float r = bf16lo_to_f32(pack_bf16x2(v, 0.0f));
+    return __builtin_fabsf(r) < __builtin_inff() ? v - r : 0.0f;
+}
+__device__ __forceinline__ f32x4 rest_of(const f32x4 &v) { return f32x4{rest_of(v[0]), rest_of(v[1]), rest_of(v[2]), rest_of(v[3])}; }
+
 // MODE 0, 1: h in fp32, bf16; 2: dg and du
 template <class T, int MODE>
 __device__ __forceinline__ void gated_tile(const GatedArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
@@ -121,6 +132,12 @@ __device__ __forceinline__ void gated_tile(const GatedArgs &g, int64_t m0, int64
     if (g.gu) {
         store_tile<T, 1, HALF>(g.gu, 2 * F, m0, M, n0, F, smem, gate);
         store_tile<T, 1, HALF>(g.gu + F, 2 * F, m0, M, n0, F, smem, up);
+    }
+    if constexpr (MODE == 2) {
+        if (g.rest) {
+            store_tile<T, 1, HALF>(g.rest, 2 * F, m0, M, n0, F, smem, [&](int i, int j) { return rest_of(acc[i][j]); });
+            store_tile<T, 1, HALF>(g.rest + F, 2 * F, m0, M, n0, F, smem, [&](int i, int j) { return rest_of(acc[i][j + HALF]); });
+        }
     }
 }
 
@@ -175,6 +192,10 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
     if constexpr (MODE == 2) {
         store4<1>(g.gu, m * 2 * F + n, a, F - n);
         store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
+        if (g.rest) {
+            store4<1>(g.rest, m * 2 * F + n, rest_of(a), F - n);
+            store4<1>(g.rest, (m * 2 + 1) * F + n, rest_of(b), F - n);
+        }
     } else {
         store4<MODE>(g.h, m * F + n, a, F - n);
         if (g.gu) {
@@ -186,35 +207,48 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
 
 // dg and du from kept projections, 8 elements a thread (F is a multiple of 8): bound by memory (4096 x 2048 15.5 us,
 // 5.4 TB/s, some of it from the caches)
-__global__ __launch_bounds__(256) void gated_slope_kernel(const uint16_t *dh, const uint16_t *gu, uint16_t *d, int64_t n,
-                                                          int64_t F, int gelu) {
+template <bool WIDE>
+__global__ __launch_bounds__(256) void gated_slope_kernel(const uint16_t *dh, const uint16_t *gu, uint16_t *d, uint16_t *rest,
+                                                          int64_t n, int64_t F, int gelu) {
     const int64_t step = (int64_t)gridDim.x * 256, per = F / 8;
     for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < n; p += step) {
         const int64_t m = p / per, at = m * 2 * F + 8 * (p - m * per);
         const u32x4 vh = *reinterpret_cast<const u32x4 *>(dh + 8 * p), vg = *reinterpret_cast<const u32x4 *>(gu + at),
                     vu = *reinterpret_cast<const u32x4 *>(gu + at + F);
-        u32x4 a, b;
+        u32x4 a, b, ra, rb;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const Activation lo = activate(bf16lo_to_f32(vg[i]), gelu), hi = activate(bf16hi_to_f32(vg[i]), gelu);
             const float hl = bf16lo_to_f32(vh[i]), hh = bf16hi_to_f32(vh[i]);
-            a[i] = pack_bf16x2(hl * bf16lo_to_f32(vu[i]) * lo.slope, hh * bf16hi_to_f32(vu[i]) * hi.slope);
-            b[i] = pack_bf16x2(hl * lo.value, hh * hi.value);
+            const float gl = hl * bf16lo_to_f32(vu[i]) * lo.slope, gh = hh * bf16hi_to_f32(vu[i]) * hi.slope;
+            const float ul = hl * lo.value, uh = hh * hi.value;
+            a[i] = pack_bf16x2(gl, gh);
+            b[i] = pack_bf16x2(ul, uh);
+            if constexpr (WIDE) {
+                ra[i] = pack_bf16x2(rest_of(gl), rest_of(gh));
+                rb[i] = pack_bf16x2(rest_of(ul), rest_of(uh));
+            }
         }
         *reinterpret_cast<u32x4 *>(d + at) = a;
         *reinterpret_cast<u32x4 *>(d + at + F) = b;
+        if constexpr (WIDE) {
+            *reinterpret_cast<u32x4 *>(rest + at) = ra;
+            *reinterpret_cast<u32x4 *>(rest + at + F) = rb;
+        }
     }
 }
 
 // The gradient's products, dW = d^T x and dx = d W, in one launch: W's operand is K-strided in both, X's in dW's (XT).
 // K in `splits` parts, each a set of tiles of its own, whose sums go to y + part * M * N and are added by a
-// second kernel.
+// second kernel. With two pieces the parts of d's rests, `rest` elements behind d, follow those of d.
 struct ProductArgs {
     MmArgs mm;
     void *y;
     int bf16, splits;   // splits 0: not wanted
+    int pieces;
+    int64_t rest;
 };
-__host__ __device__ __forceinline__ int tiles_of(const ProductArgs &g) { return g.mm.tiles_m * g.mm.tiles_n * g.splits; }
+__host__ __device__ __forceinline__ int tiles_of(const ProductArgs &g) { return g.mm.tiles_m * g.mm.tiles_n * g.splits * g.pieces; }
 
 template <class T, int XT, int TAG>
 __device__ __forceinline__ void grad_tile(const ProductArgs &g, int64_t m0, int64_t n0, uint8_t *smem) {
@@ -230,10 +264,11 @@ __device__ __forceinline__ void grad_part(ProductArgs g, int tile, uint8_t *smem
     const int n = g.mm.tiles_m * g.mm.tiles_n, part = tile / n;
     int64_t m0, n0;
     place_tile(g.mm, tile - part * n, T::BM, T::BN, m0, n0);
-    if (g.splits > 1) {
+    if (g.splits * g.pieces > 1) {
         const int64_t steps = (g.mm.K + KSTEP - 1) / KSTEP;
-        const int64_t k0 = part * steps / g.splits * KSTEP, k1 = (part + 1) * steps / g.splits * KSTEP;
-        g.mm.x += XT ? k0 * g.mm.ldx : k0;
+        const int piece = part / g.splits, of = part - piece * g.splits;
+        const int64_t k0 = of * steps / g.splits * KSTEP, k1 = (of + 1) * steps / g.splits * KSTEP;
+        g.mm.x += (XT ? k0 * g.mm.ldx : k0) + piece * g.rest;
         g.mm.w += k0 * g.mm.ldw;
         g.mm.K = (k1 < g.mm.K ? k1 : g.mm.K) - k0;
         g.y = static_cast<float *>(g.y) + part * g.mm.M * g.mm.N;
@@ -281,12 +316,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // The parts' sums added in order, 8 elements a thread (their number is a multiple of 8), of either product that has
-// parts; y: where they go
+// parts; y: where they go. Of two pieces, the second's sums (half the parts) are added where the first's are finite: an
+// infinite weight times a rest of 0, or of the other sign, would make NaN of an infinity.
 struct SumArgs {
     const float *parts[2];
     void *y[2];
     int64_t n[2];   // 0: no parts
     int bf16[2], splits[2];
+    int pieces;
 };
 __global__ __launch_bounds__(256) void gated_sum_kernel(SumArgs g) {
     const int64_t step = (int64_t)gridDim.x * 256 * 8;
@@ -300,6 +337,18 @@ __global__ __launch_bounds__(256) void gated_sum_kernel(SumArgs g) {
         for (int s = 0; s < splits; ++s) {
             a += *reinterpret_cast<const f32x4 *>(from + s * n);
             b += *reinterpret_cast<const f32x4 *>(from + s * n + 4);
+        }
+        if (g.pieces > 1) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f}, d = c;
+            for (int s = splits; s < 2 * splits; ++s) {
+                c += *reinterpret_cast<const f32x4 *>(from + s * n);
+                d += *reinterpret_cast<const f32x4 *>(from + s * n + 4);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                a[r] = __builtin_fabsf(a[r]) < __builtin_inff() ? a[r] + c[r] : a[r];
+                b[r] = __builtin_fabsf(b[r]) < __builtin_inff() ? b[r] + d[r] : b[r];
+            }
         }
         if (which ? g.bf16[1] : g.bf16[0]) {
             *reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(y) + at) = u32x4{
@@ -389,29 +438,29 @@ constexpr GradTile kGradTiles[kLargest + 1] = {{64, 64, 256, 0.21, 0.19, 0.8}, {
                                                {128, 256, 512, 0.78, 0.82, 5.7}, {256, 256, 512, 1.25, 1.35, 8.0}};
 using Plan = GatedGradPlan;
 // (only plans whose workgroups a grid holds; with none us stays infinite)
-Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
+Plan plan_of(int64_t M, int64_t F, int64_t K, int pieces, bool has_w, bool has_x) {
     Plan best = {kLargest, has_w, has_x, HUGE_VAL};
     // What does not depend on the other product's parts: K's steps of a part, and what its sums cost
     struct Parts {
         int least, most;
         double steps[kMaxParts + 1], sums[kMaxParts + 1];
-        Parts(bool has, int64_t k_steps, double longer, int64_t outputs) : least(has), most(0) {
+        Parts(bool has, int64_t k_steps, double longer, int64_t outputs, int pieces) : least(has), most(0) {
             steps[0] = sums[0] = 0.0;
             if (!has) return;
             most = k_steps < 8 ? 1 : k_steps / 4 < kMaxParts ? (int)(k_steps / 4) : kMaxParts;
             for (int s = 1; s <= most; ++s) {
                 steps[s] = longer * (double)((k_steps + s - 1) / s);
-                sums[s] = s > 1 ? (2.0 * s + 1.0) * (double)outputs * 4.0 / 8e6 : 0.0;
+                sums[s] = s * pieces > 1 ? (2.0 * s * pieces + 1.0) * (double)outputs * 4.0 / 8e6 : 0.0;
             }
         }
     };
-    const Parts pw(has_w, (M + KSTEP - 1) / KSTEP, 1.1, 2 * F * K), px(has_x, (2 * F + KSTEP - 1) / KSTEP, 1.0, M * K);
-    for (int t = 0; t <= kLargest; ++t) {
+    const Parts pw(has_w, (M + KSTEP - 1) / KSTEP, 1.1, 2 * F * K, pieces), px(has_x, (2 * F + KSTEP - 1) / KSTEP, 1.0, M * K, pieces);
+    for (int t = 0; t <= (pieces > 1 ? kLargest - 1 : kLargest); ++t) {   // (the largest have no parts)
         const GradTile &tile = kGradTiles[t];
         auto count = [&](int64_t m, int64_t n) {
             return (double)((m + tile.bm - 1) / tile.bm) * (double)((n + tile.bn - 1) / tile.bn);
         };
-        const double tiles_w = has_w ? count(2 * F, K) : 0.0, tiles_x = has_x ? count(M, K) : 0.0;
+        const double tiles_w = has_w ? pieces * count(2 * F, K) : 0.0, tiles_x = has_x ? pieces * count(M, K) : 0.0;
         const double limit = (double)(grid_limit(tile.threads) - kShareMore);
         for (int sw = pw.least; sw <= (t == kLargest ? pw.least : pw.most); ++sw)
             for (int sx = px.least; sx <= (t == kLargest ? px.least : px.most); ++sx) {
@@ -420,7 +469,7 @@ Plan plan_of(int64_t M, int64_t F, int64_t K, bool has_w, bool has_x) {
                 const double longest = pw.steps[sw] > px.steps[sx] ? pw.steps[sw] : px.steps[sx];
                 const double run = n <= 256.0 ? longest * tile.first + tile.end
                                               : tile.more * ((nw * pw.steps[sw] + nx * px.steps[sx]) * (1.0 / 256.0) + 0.5 * longest) + tile.end * (n * (1.0 / 256.0) + 0.5);
-                const double us = run + (sw > 1 || sx > 1 ? 3.0 : 0.0) + pw.sums[sw] + px.sums[sx];
+                const double us = run + (sw > 1 || sx > 1 || pieces > 1 ? 3.0 : 0.0) + pw.sums[sw] + px.sums[sx];
                 if (us < best.us) best = {t, sw, sx, us};
             }
     }
@@ -444,11 +493,12 @@ hipError_t launch_grads(ProductArgs dw, ProductArgs dx, const Plan &plan, float 
     ProductArgs *const each[2] = {&dx, &dw};
     for (int i = 0; i < 2; ++i) {
         ProductArgs &p = *each[i];
-        if (p.splits <= 1) continue;
+        if (p.splits * p.pieces <= 1) continue;
         const int64_t n = p.mm.M * p.mm.N;
         sum.parts[i] = parts, sum.y[i] = p.y, sum.n[i] = n, sum.bf16[i] = p.bf16, sum.splits[i] = p.splits;
+        sum.pieces = p.pieces;
         p.y = parts;
-        parts += p.splits * n;
+        parts += p.splits * p.pieces * n;
     }
     hipError_t e = hipSuccess;
     switch (plan.tile) {
@@ -469,20 +519,22 @@ hipError_t launch_grads(ProductArgs dw, ProductArgs dx, const Plan &plan, float 
 
 hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
                                int64_t M, int64_t F, int64_t K, hipStream_t stream) {
-    return launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, h, gu, nullptr, gelu}, h_bf16, stream);
+    return launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, h, gu, nullptr, nullptr, gelu}, h_bf16, stream);
 }
 
-GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K) {
-    GatedGradPlans p{true, true, plan_of(M, F, K, true, true), plan_of(M, F, K, true, false), plan_of(M, F, K, false, true)};
+GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K, bool wide) {
+    const int pieces = wide ? 2 : 1;
+    GatedGradPlans p{true, true, pieces, plan_of(M, F, K, pieces, true, true), plan_of(M, F, K, pieces, true, false),
+                     plan_of(M, F, K, pieces, false, true)};
     p.joint = p.both.us <= p.w.us + p.x.us + 2.0 && p.both.us < HUGE_VAL;
     p.fits = p.joint || (p.w.us < HUGE_VAL && p.x.us < HUGE_VAL);
     return p;
 }
 
-// dg and du, then the parts' sums
+// dg and du, and their rests, then the parts' sums
 size_t gated_linear_backward_workspace_bytes(const GatedGradPlans &p, int64_t M, int64_t F, int64_t K) {
-    const int64_t x = p.joint ? p.both.parts_x : p.x.parts_x, w = p.joint ? p.both.parts_w : p.w.parts_w;
-    return (size_t)(M * F * 4 + (x > 1 ? x * M * K * 4 : 0) + (w > 1 ? w * 2 * F * K * 4 : 0));
+    const int64_t x = p.pieces * (p.joint ? p.both.parts_x : p.x.parts_x), w = p.pieces * (p.joint ? p.both.parts_w : p.w.parts_w);
+    return (size_t)(p.pieces * M * F * 4 + (x > 1 ? x * M * K * 4 : 0) + (w > 1 ? w * 2 * F * K * 4 : 0));
 }
 
 void gated_report(int64_t M, int64_t F, int64_t K, LaunchReport *r) {
@@ -499,13 +551,13 @@ void gated_report(int64_t M, int64_t F, int64_t K, LaunchReport *r) {
     *r = {tile.bm, tile.bn, 1, 0, !fits ? -1 : choice == 4 ? share_grid((int)tiles, 0) : tiles, tile.threads};
 }
 
-void gated_gradient_report(int64_t M, int64_t F, int64_t K, LaunchReport *r) {
-    const GatedGradPlans p = gated_gradient_plans(M, F, K);
+void gated_gradient_report(int64_t M, int64_t F, int64_t K, bool wide, LaunchReport *r) {
+    const GatedGradPlans p = gated_gradient_plans(M, F, K, wide);
     const Plan &w = p.joint ? p.both : p.w, &x = p.joint ? p.both : p.x;
     MmArgs mw{nullptr, nullptr, 2 * F, K, M, 2 * F, K, 0, 0, 1}, mx{nullptr, nullptr, M, K, 2 * F, 2 * F, K, 0, 0, 1};
     const GradTile &tw = kGradTiles[w.tile], &tx = kGradTiles[x.tile];
     const bool fits = p.fits && lay_out(mw, tw.bm, tw.bn, tw.threads) && lay_out(mx, tx.bm, tx.bn, tx.threads);
-    const int nw = fits ? mw.tiles_m * mw.tiles_n * w.parts_w : 0, nx = fits ? mx.tiles_m * mx.tiles_n * x.parts_x : 0;
+    const int nw = fits ? mw.tiles_m * mw.tiles_n * w.parts_w * p.pieces : 0, nx = fits ? mx.tiles_m * mx.tiles_n * x.parts_x * p.pieces : 0;
     r[0] = {tw.bm, tw.bn, w.parts_w, p.joint, fits ? (int64_t)share_grid(nw, p.joint ? nx : 0) : -1, tw.threads};
     r[1] = {tx.bm, tx.bn, x.parts_x, p.joint, fits ? (int64_t)share_grid(p.joint ? nw : 0, nx) : -1, tx.threads};
 }
@@ -514,18 +566,22 @@ hipError_t launch_gated_linear_backward(const uint16_t *dh, const uint16_t *x, c
                                         bool gelu, void *dx, bool dx_bf16, void *dw, bool dw_bf16, int64_t M, int64_t F,
                                         int64_t K, const GatedGradPlans &plans, void *workspace, hipStream_t stream) {
     uint16_t *const d = static_cast<uint16_t *>(workspace);   // [M, 2 F]
-    float *const parts = reinterpret_cast<float *>(d + M * 2 * F);
+    const int64_t size = M * 2 * F;
+    uint16_t *const rest = plans.pieces > 1 ? d + size : nullptr;
+    float *const parts = reinterpret_cast<float *>(d + plans.pieces * size);
     if (M > 0 && F > 0) {
         if (gu) {
             const int64_t n = M * F / 8, need = (n + 255) / 256;
-            gated_slope_kernel<<<dim3((unsigned)(need < 8192 ? need : 8192)), dim3(256), 0, stream>>>(dh, gu, d, n, F, gelu);
+            const dim3 grid((unsigned)(need < 8192 ? need : 8192));
+            if (rest) gated_slope_kernel<true><<<grid, dim3(256), 0, stream>>>(dh, gu, d, rest, n, F, gelu);
+            else gated_slope_kernel<false><<<grid, dim3(256), 0, stream>>>(dh, gu, d, nullptr, n, F, gelu);
             if (hipError_t e = hipGetLastError()) return e;
-        } else if (hipError_t e = launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, nullptr, d, dh, gelu}, 2, stream)) {
+        } else if (hipError_t e = launch_gated({{x, w, M, F, K, K, K, 0, 0, 1}, nullptr, d, dh, rest, gelu}, 2, stream)) {
             return e;
         }
     }
-    const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, dx_bf16, dx && M > 0 && K > 0};
-    const ProductArgs pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, dw_bf16, dw && F > 0 && K > 0};
+    const ProductArgs px{{d, w, M, K, 2 * F, 2 * F, K, 0, 0, 1}, dx, dx_bf16, dx && M > 0 && K > 0, plans.pieces, size};
+    const ProductArgs pw{{d, x, 2 * F, K, M, 2 * F, K, 0, 0, 1}, dw, dw_bf16, dw && F > 0 && K > 0, plans.pieces, size};
     if (plans.joint) return px.splits || pw.splits ? launch_grads(pw, px, plans.both, parts, stream) : hipSuccess;
     // (one after the other: their parts' sums may share their place)
     ProductArgs none{};

@@ -129,9 +129,10 @@ struct GatedGradPlan {
 };
 struct GatedGradPlans {
     bool joint, fits;             // both products in one launch; whether the launches fit a grid
+    int pieces;                   // bf16 numbers that stand for one of the projections' gradient (wide: 2)
     GatedGradPlan both, w, x;
 };
-GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K);
+GatedGradPlans gated_gradient_plans(int64_t M, int64_t F, int64_t K, bool wide);
 size_t gated_linear_backward_workspace_bytes(const GatedGradPlans &plans, int64_t M, int64_t F, int64_t K);
 hipError_t launch_gated_linear(const uint16_t *x, const uint16_t *w, void *h, bool h_bf16, uint16_t *gu, bool gelu,
                                int64_t M, int64_t F, int64_t K, hipStream_t stream);
@@ -154,7 +155,7 @@ struct LaunchReport {
     int64_t rows, columns, parts, shared, workgroups, threads;
 };
 void gated_report(int64_t M, int64_t F, int64_t K, LaunchReport *r);                                    // one launch
-void gated_gradient_report(int64_t M, int64_t F, int64_t K, LaunchReport *r);                           // two
+void gated_gradient_report(int64_t M, int64_t F, int64_t K, bool wide, LaunchReport *r);                // two
 void adapter_report(int64_t M, int64_t N, int64_t K, int64_t rank, bool add, LaunchReport *r);          // two
 
 }  // namespace fp8q

@@ -411,6 +411,8 @@ size_t residual_norm_backward_workspace_bytes(int64_t T, int64_t H);
 /* Activations of gated_linear. */
 #define FP8Q_ACT_SILU 0        /* a / (1 + exp(-a))                                              */
 #define FP8Q_ACT_GELU 1        /* a * Phi(a), Phi the normal distribution (not its tanh form)    */
+/* Flag of gated_linear_backward, or'ed to its act. */
+#define FP8Q_GATED_WIDE 256    /* the projections' gradient enters the products with 16 bits     */
 
 /* gated_linear -- h = act(x Wg^T) * (x Wu^T), w = [Wg; Wu]: both projections of a feed-forward
  * block, the activation and the product in one kernel.
@@ -426,14 +428,17 @@ int gated_linear(const uint16_t *x, const uint16_t *w, void *h, int h_dtype, uin
  * dw_dtype (either may be NULL: not wanted).
  *   gu as gated_linear wrote it, or NULL: the projections are computed again. The gradient of
  *   the projections is rounded to bf16 (the matrix unit's type) on its way into dx and dw, whose
- *   sums are fp32. dh, x, w, gu 16-byte aligned, dx and dw 4-byte.
- *   workspace: gated_linear_backward_workspace_bytes bytes of any contents, 16-byte aligned (NULL
+ *   sums are fp32; with FP8Q_GATED_WIDE or'ed to act it goes into them as two bf16 numbers, 16 bits in all, which
+ *   takes 1.3 to 2.7 times as long. dh, x, w, gu 16-byte aligned, dx and dw 4-byte.
+ *   workspace: gated_linear_backward_workspace_bytes (with FP8Q_GATED_WIDE
+ *   gated_linear_backward_wide_workspace_bytes) bytes of any contents, 16-byte aligned (NULL
  *   where that is 0); a smaller one is refused with FP8Q_ERR_WORKSPACE. Calls that may run at
  *   the same time must not share it. M = 0 still writes dw (zeros). */
 int gated_linear_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *w, const uint16_t *gu, int act, void *dx,
                           int dx_dtype, void *dw, int dw_dtype, int64_t M, int64_t F, int64_t K, void *workspace,
                           size_t workspace_bytes, void *stream);
 size_t gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
+size_t gated_linear_backward_wide_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /* adapter_linear -- y[m] = x[m] w^T + bias + scales[e] (x[m] a[e]^T) b[e]^T, e = ids[m]: a linear layer
  * whose rows each have a low-rank adapter of their own (requests of many adapters in a batch).
@@ -489,7 +494,7 @@ int fp8q_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dtype, int *config, in
  * fp8q_dense_plan(call, M, N, K, rank, plan) writes plan[2][6]: of each launch the rows and columns of a
  * workgroup's tile, the parts of K, a mark, the workgroups (-1: more than a grid holds) and the threads of one.
  *   FP8Q_PLAN_GATED: gated_linear (N = F), whose tiles' columns are rows of w; one launch.
- *   FP8Q_PLAN_GATED_BACKWARD: the products of gated_linear_backward, dw then dx; mark: both are one launch, whose
+ *   FP8Q_PLAN_GATED_BACKWARD, ..._WIDE: the products of gated_linear_backward, dw then dx; mark: both are one launch, whose
  *      workgroups stand in both rows.
  *   FP8Q_PLAN_ADAPTER, FP8Q_PLAN_ADAPTER_ADD: adapter_linear with w, with base; mark: rows share their adapter's
  *      products. Then x a^T; mark: a row at a time.
@@ -499,6 +504,7 @@ int fp8q_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dtype, int *config, in
 #define FP8Q_PLAN_GATED_BACKWARD 1
 #define FP8Q_PLAN_ADAPTER 2
 #define FP8Q_PLAN_ADAPTER_ADD 3
+#define FP8Q_PLAN_GATED_BACKWARD_WIDE 4
 int fp8q_dense_plan(int call, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t *plan);
 
 /* Static string describing a status code (never NULL). */

@@ -42,15 +42,19 @@ def test_gated_plans_fit_a_grid():
         if held + 2 * M * K + 4 * F * K + 4 * M * F > MEMORY:      # dx, dw and dg, du beside them
             continue
         seen += 1
-        w, x = plan(L.FP8Q_PLAN_GATED_BACKWARD, M, F, K)
-        n = [tiles(2 * F, K, w) * w[2], tiles(M, K, x) * x[2]]
-        assert w[3] == x[3] and (not w[3] or w[4:] == x[4:])
-        for mine, r in zip(n if not w[3] else [sum(n)], (w, x)):
-            assert mine <= r[4] <= 2 * mine + 144 and r[4] * r[5] <= GRID, (M, F, K, r)
-        # and the call itself has nothing against the size
-        assert L.lib.gated_linear_backward_workspace_bytes(M, F, K) >= 4 * M * F
-        assert L.lib.gated_linear_backward(65536, 65536, 65536, None, 0, 65536, 1, 65536, 1, M, F, K, None, 0,
-                                           None) == L.FP8Q_ERR_WORKSPACE
+        for call, pieces, need in ((L.FP8Q_PLAN_GATED_BACKWARD, 1, L.lib.gated_linear_backward_workspace_bytes(M, F, K)),
+                                   (L.FP8Q_PLAN_GATED_BACKWARD_WIDE, 2, L.lib.gated_linear_backward_wide_workspace_bytes(M, F, K))):
+            if pieces == 2 and held + 10 * M * K + 20 * F * K + 8 * M * F > MEMORY:   # (and both pieces' sums)
+                continue
+            w, x = plan(call, M, F, K)
+            n = [pieces * tiles(2 * F, K, w) * w[2], pieces * tiles(M, K, x) * x[2]]
+            assert w[3] == x[3] and (not w[3] or w[4:] == x[4:])
+            for mine, r in zip(n if not w[3] else [sum(n)], (w, x)):
+                assert mine <= r[4] <= 2 * mine + 144 and r[4] * r[5] <= GRID, (call, M, F, K, r)
+            # and the call itself has nothing against the size
+            assert need >= 4 * M * F * pieces
+            assert L.lib.gated_linear_backward(65536, 65536, 65536, None, L.FP8Q_GATED_WIDE * (pieces - 1), 65536, 1, 65536,
+                                               1, M, F, K, 65536, need - 1, None) == L.FP8Q_ERR_WORKSPACE
     assert seen > 5000
 
 
@@ -80,9 +84,19 @@ def test_adapter_plans_fit_a_grid():
     assert seen > 5000
 
 
+def test_wide_flag_is_the_gradients():
+    def back(act):
+        return L.lib.gated_linear_backward(65536, 65536, 65536, None, act, 65536, 1, 65536, 1, 4, 16, 64, None, 0, None)
+    assert back(L.FP8Q_GATED_WIDE) == back(L.FP8Q_GATED_WIDE | L.FP8Q_ACT_GELU) == L.FP8Q_ERR_WORKSPACE
+    for act in (L.FP8Q_GATED_WIDE | 2, L.FP8Q_GATED_WIDE * 2, L.FP8Q_GATED_WIDE * 3, -L.FP8Q_GATED_WIDE, -1):
+        assert back(act) == L.FP8Q_ERR_DTYPE, act
+    assert L.lib.gated_linear(65536, 65536, 65536, 1, None, L.FP8Q_GATED_WIDE, 4, 16, 64, None) == L.FP8Q_ERR_DTYPE
+    assert L.lib.gated_linear_backward_wide_workspace_bytes(4, 12, 64) == 0
+
+
 def test_plan_arguments():
     out = (ctypes.c_int64 * 12)()
-    for args, status in (((4, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE), ((-1, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE),
+    for args, status in (((5, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE), ((-1, 8, 8, 8, 8, out), L.FP8Q_ERR_DTYPE),
                          ((0, 0, 8, 8, 8, out), L.FP8Q_ERR_SHAPE), ((0, 8, 12, 8, 8, out), L.FP8Q_ERR_SHAPE),
                          ((1, 8, 8, 12, 8, out), L.FP8Q_ERR_SHAPE), ((2, 8, 0, 8, 8, out), L.FP8Q_ERR_SHAPE),
                          ((3, 8, 8, 8, 12, out), L.FP8Q_ERR_SHAPE), ((0, 8, 8, 8, 8, None), L.FP8Q_ERR_NULL)):

@@ -109,3 +109,72 @@ def test_adapters_of_the_most_channels():
         off[rows] += lost
     near(got, ref, off + 4 * U * ref.abs())
     assert torch.equal(got[ids < 0].double(), base[ids < 0])
+
+
+@pytest.mark.parametrize("M,F,K", [(1, 8, 8), (1, 2048, 1536), (17, 72, 520), (31, 2056, 264), (64, 200, 64), (333, 1000, 1096),
+                                   (1021, 512, 1544), (1500, 2048, 1032), (2050, 96, 4104)])
+def test_wide_gradient(M, F, K):
+    """With `wide` the projections' gradient keeps 16 bits: two roundings to bf16, the second of what the first lost."""
+    g = rng(M + F + K)
+    x, w, dh = randn(g, M, K), randn(g, 2 * F, K, std=1.5 * K ** -0.5), randn(g, M, F)
+    gu = fq.gated_linear(x, w, keep=True)[1]
+    for act, kept in (("silu", True), ("gelu", False), ("gelu", True), ("silu", False)):
+        at = (gu.double(), torch.zeros_like(gu, dtype=torch.float64)) if kept else product64(x, w)
+        d, off = slopes64(dh, *at, act, half(torch.bfloat16) ** 2)
+        want = product_of(d, off, w, 2 * F), product_of(d.t(), off.t(), x, M)
+        args = (dh, x, w, gu if kept else None, act)
+        got = fq.gated_linear_backward(*args, dx_dtype=torch.float32, wide=True)
+        # (two sums, of the first and of the second numbers, whose magnitudes are 1 + 2^-8 of one's)
+        for y, (ref, slack) in zip(got, want):
+            near(y, ref, slack * (1 + 2 * half(torch.bfloat16)), (act, kept))
+        rough = fq.gated_linear_backward(*args, dx_dtype=torch.float32)
+        if M * F > 4096:
+            for y, z, (ref, _) in zip(got, rough, want):
+                assert float((z.double() - ref).norm()) > 20 * float((y.double() - ref).norm()), (act, kept)
+        short = fq.gated_linear_backward(*args, dw_dtype=torch.bfloat16, wide=True)
+        assert all(torch.equal(y.bfloat16(), z) for y, z in zip(got, short))
+
+
+def test_wide_gradient_of_infinite_weights():
+    """An infinite weight makes the gradient infinite, also where nothing was lost in the first rounding."""
+    M, F, K = 40, 16, 24
+    x, w = torch.zeros((M, K), device="cuda").bfloat16(), torch.zeros((2 * F, K), device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    w[:F, 0], w[F:, 1] = 1.0, 1.0
+    dh = torch.ones((M, F), device="cuda").bfloat16()
+    gu = torch.ones((M, 2 * F), device="cuda").bfloat16()
+    w[F + 3, 7] = float("inf")        # du = act(1) > 0 meets it; its rest may be of either sign
+    w[F + 4, 8] = float("inf")
+    gu[:, 4] = 0.0                    # act(0) = 0 meets it: NaN, as 0 * inf is
+    for act in ("silu", "gelu"):
+        dx, _ = fq.gated_linear_backward(dh, x, w, gu, act, dx_dtype=torch.float32, wide=True)
+        assert (dx[:, 7] == float("inf")).all() and torch.isnan(dx[:, 8]).all()
+        assert torch.isfinite(dx[:, [0, 1, 2, 6, 9]]).all()
+
+
+def test_wide_gradient_empty_captured_and_on_a_stream():
+    def e(*shape):
+        return torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    dx, dw = fq.gated_linear_backward(e(0, 16), e(0, 64), e(32, 64), wide=True)
+    assert dx.shape == (0, 64) and dw.shape == (32, 64) and (dw == 0).all()
+    dx, dw = fq.gated_linear_backward(e(5, 0), e(5, 64), e(0, 64), wide=True)
+    assert (dx == 0).all() and dw.shape == (0, 64)
+    g = rng(8)
+    M, F, K = 300, 264, 520
+    x, w, dh = randn(g, M, K), randn(g, 2 * F, K, std=K ** -0.5), randn(g, M, F)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        fq.gated_linear_backward(dh, x, w, wide=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fq.gated_linear_backward(dh, x, w, wide=True)
+    for k in range(3):
+        x.copy_(randn(g, M, K))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in out]
+        with torch.cuda.stream(side):
+            eager = fq.gated_linear_backward(dh, x, w, wide=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), k
