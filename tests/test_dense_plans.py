@@ -1,10 +1,13 @@
 """Which kernels the dense block's products choose (host only): every choice within the documented sizes, as far as
-their operands fit a GPU's memory, is one that a grid holds."""
+their operands fit a GPU's memory, is one that a grid holds, and every kind of choice is one that a GPU test runs."""
 import ctypes
 import itertools
+import math
+import random
 
-import pytest
-
+import test_gpu_block
+import test_gpu_dense_limits
+import test_gpu_dense_shapes
 from fp8_act_quant_amd import _lib as L
 
 MEMORY = 288 << 30
@@ -102,3 +105,39 @@ def test_plan_arguments():
                          ((3, 8, 8, 8, 12, out), L.FP8Q_ERR_SHAPE), ((0, 8, 8, 8, 8, None), L.FP8Q_ERR_NULL)):
         assert L.lib.fp8q_dense_plan(*args) == status, args
     assert list(out) == [0] * 12
+
+
+def kinds(call, M, N, K, rank=8):
+    """What kinds of launches a call makes: tiles, marks, and whether K is in parts."""
+    a, b = plan(call, M, N, K, rank)
+    if call == L.FP8Q_PLAN_GATED:
+        return {(call, *a[:2])}
+    if call in (L.FP8Q_PLAN_ADAPTER, L.FP8Q_PLAN_ADAPTER_ADD):
+        return {(call, *a[:2], a[3]), ("u", *b[:2], b[3], b[2] > 1)}
+    if a[3]:
+        return {(call, "joint", *a[:2], a[2] > 1, b[2] > 1)}
+    return {(call, "dw", *a[:2], a[2] > 1), (call, "dx", *b[:2], b[2] > 1)}
+
+
+def test_every_kind_of_launch_is_tested():
+    """Sizes drawn over the whole range, beside the shapes that the GPU tests run."""
+    tested = set()
+    for M, F, K in test_gpu_block.GATED + test_gpu_dense_shapes.PROJECTIONS:
+        tested |= kinds(L.FP8Q_PLAN_GATED, M, F, K) | kinds(L.FP8Q_PLAN_GATED_BACKWARD, M, F, K)
+    for M, F, K in test_gpu_dense_limits.WIDE + test_gpu_dense_shapes.PROJECTIONS:
+        tested |= kinds(L.FP8Q_PLAN_GATED_BACKWARD_WIDE, M, F, K)
+    for M, N, K, _, r, *_ in test_gpu_block.ADAPTERS + test_gpu_dense_shapes.ADAPTERS:
+        tested |= kinds(L.FP8Q_PLAN_ADAPTER, M, N, K, r) | kinds(L.FP8Q_PLAN_ADAPTER_ADD, M, N, K, r)
+    rng = random.Random(1)
+
+    def log(least, most):
+        return int(round(math.exp(rng.uniform(math.log(least), math.log(most + 0.49)))))
+    met = set()
+    for _ in range(20000):
+        M, N, K, r = log(1, 16384), 8 * log(1, 2304), 8 * log(1, 896), 8 * log(1, 32)
+        for call in (L.FP8Q_PLAN_GATED, L.FP8Q_PLAN_GATED_BACKWARD, L.FP8Q_PLAN_GATED_BACKWARD_WIDE):
+            met |= kinds(call, M, N, K)
+        N = log(1, 18432)
+        for call in (L.FP8Q_PLAN_ADAPTER, L.FP8Q_PLAN_ADAPTER_ADD):
+            met |= kinds(call, M, N, K, r)
+    assert len(met) > 70 and not met - tested, met - tested

@@ -111,8 +111,11 @@ def test_adapters_of_the_most_channels():
     assert torch.equal(got[ids < 0].double(), base[ids < 0])
 
 
-@pytest.mark.parametrize("M,F,K", [(1, 8, 8), (1, 2048, 1536), (17, 72, 520), (31, 2056, 264), (64, 200, 64), (333, 1000, 1096),
-                                   (1021, 512, 1544), (1500, 2048, 1032), (2050, 96, 4104)])
+WIDE = [(1, 8, 8), (1, 2048, 1536), (17, 72, 520), (31, 2056, 264), (64, 200, 64), (333, 1000, 1096), (1021, 512, 1544),
+        (1500, 2048, 1032), (2050, 96, 4104)]
+
+
+@pytest.mark.parametrize("M,F,K", WIDE)
 def test_wide_gradient(M, F, K):
     """With `wide` the projections' gradient keeps 16 bits: two roundings to bf16, the second of what the first lost."""
     g = rng(M + F + K)
@@ -178,3 +181,35 @@ def test_wide_gradient_empty_captured_and_on_a_stream():
             eager = fq.gated_linear_backward(dh, x, w, wide=True)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, eager)), k
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("M,F,K", [(5, 16, 64), (465, 616, 24), (759, 1168, 1600), (2909, 456, 976)])
+def test_one_gradient_alone(M, F, K, wide):
+    """The C call without dx, or without dw, whose launches are one or two: the other has the same bits, and a
+    workspace of the stated size is not written past."""
+    g = rng(M)
+    x, w, dh = randn(g, M, K), randn(g, 2 * F, K, std=K ** -0.5), randn(g, M, F)
+    want = fq.gated_linear_backward(dh, x, w, dw_dtype=torch.bfloat16, wide=wide)
+    need = (fq.lib.gated_linear_backward_wide_workspace_bytes if wide else fq.lib.gated_linear_backward_workspace_bytes)(M, F, K)
+    for k in range(2):
+        ws = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = [torch.full_like(v, 7.0) for v in want]
+        at = [v.data_ptr() if i == k else None for i, v in enumerate(got)]
+        assert fq.lib.gated_linear_backward(dh.data_ptr(), x.data_ptr(), w.data_ptr(), None, 256 if wide else 0, at[0], 1, at[1],
+                                            1, M, F, K, ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(got[k], want[k]) and (got[1 - k] == 7).all() and (ws[need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("H", [8, 515, 4100, 9001])
+def test_norm_without_the_stream(H):
+    """The C call with y and weight whose t is not wanted: z alone."""
+    g = rng(H)
+    for dtype, code in ((torch.bfloat16, 1), (torch.float32, 0)):
+        x, y = randn(g, 37, H, dtype=dtype), randn(g, 37, H, dtype=dtype)
+        w, post = torch.rand(H, device="cuda"), torch.rand(H, device="cuda")
+        want = fq.residual_norm(x, y, w, post=post, gate=w, scale=0.5)[1]
+        z = torch.empty_like(want)
+        assert fq.lib.residual_norm(x.data_ptr(), y.data_ptr(), code, w.data_ptr(), post.data_ptr(), w.data_ptr(), 0, 0.5, 1e-6,
+                                    None, z.data_ptr(), 37, H, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(z, want)
