@@ -10,7 +10,8 @@
 // all requests. Rows of one request need not be neighbours; where they are, as in a prefill batch, 16 rows
 // at a time share the products with their adapter's B.
 //
-// u keeps its 32 bits: the matrix unit takes it as three bf16 numbers whose sum it is. What an adapter
+// u keeps its 32 bits: the matrix unit takes it as three bf16 numbers whose sum it is, of which the first decides
+// where B is infinite. What an adapter
 // holds reaches no row of another one (not even as 0 * NaN): sums of rows with other ids are dropped.
 #include <cmath>
 
@@ -218,11 +219,14 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, i
                     if (e[a] == -2) continue;
 #pragma unroll
                     for (int j = 0; j < T::SUB_N; ++j) {
-                        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+                        const f32x4 first = mfma_bf16(wf[a][j], xf[0], f32x4{0.f, 0.f, 0.f, 0.f});
+                        const f32x4 sum = mfma_bf16(wf[a][j], xf[2], mfma_bf16(wf[a][j], xf[1], first));
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) sum = mfma_bf16(wf[a][j], xf[t], sum);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][j][q] += id == e[a] ? sum[q] : 0.0f;
+                        for (int q = 0; q < 4; ++q) {
+                            // (an infinite B times a lower number of 0 is NaN: then the first number's sum is u B's)
+                            const float all = sum[q] == sum[q] ? sum[q] : first[q];
+                            acc[i][j][q] += id == e[a] ? all : 0.0f;
+                        }
                     }
                 }
             }

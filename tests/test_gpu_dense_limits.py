@@ -213,3 +213,42 @@ def test_norm_without_the_stream(H):
         assert fq.lib.residual_norm(x.data_ptr(), y.data_ptr(), code, w.data_ptr(), post.data_ptr(), w.data_ptr(), 0, 0.5, 1e-6,
                                     None, z.data_ptr(), 37, H, torch.cuda.current_stream().cuda_stream) == 0
         assert torch.equal(z, want)
+
+
+@pytest.mark.parametrize("M", [3, 60, 100, 300, 2305])
+def test_adapter_infinities_by_every_way(M):
+    """A row's own adapter with an infinity in B: u B is infinite where u is not 0, however few bits u has, and NaN
+    where it is 0, whatever the way the rows are taken; infinite u too. Other columns and rows stay finite."""
+    N, K, r = {300: 1500, 2305: 7408}.get(M, 200), 64, 40
+    x = torch.zeros((M, K), device="cuda").bfloat16()
+    x[:, 0] = torch.where(torch.arange(M, device="cuda") % 2 == 0, 1.0, -2.5)     # few bits: nothing is left below bf16
+    x[:, 1] = torch.randn(M, device="cuda").abs() + 0.5
+    x[:, 2] = 1.0
+    a = torch.zeros((2, r, K), device="cuda").bfloat16()
+    a[:, 0, 0] = a[:, 33, 1] = 1.0                         # u = x0 at rank 0, x1 at rank 33, 0 elsewhere
+    a[:, 34, 1] = 1.0 + 2.0 ** -7
+    a[:, 35, 2] = float("inf")
+    b = torch.zeros((2, N, r), device="cuda").bfloat16()
+    b[:, :, 35] = 1.0
+    a[0, 35, 2] = 0.0
+    b[0, 5, 0] = b[0, 9, 33] = float("inf")
+    b[0, 6, 0] = b[0, 12, 34] = float("-inf")
+    b[0, 7, 1] = float("inf")
+    b[0, 8, 0] = float("nan")
+    b[0, 10, 0], b[0, 10, 33] = float("inf"), 2.0
+    ids = torch.where(torch.arange(M, device="cuda") % 16 == 7, 1, 0).to(torch.int32)
+    ids[2::16] = -1
+    mine, other = ids == 0, ids == 1
+    sign = torch.sign(x[:, 0].float())
+    base = torch.ones((M, N), device="cuda").bfloat16()
+    w = torch.zeros((N, K), device="cuda").bfloat16()
+    for y in (fq.adapter_linear(x, w, a, b, ids), fq.adapter_linear(x, w, a, b, ids, out_dtype=torch.float32),
+              fq.adapter_add(base, x, a, b, ids)):
+        y = y.float()
+        inf = torch.full((M,), float("inf"), device="cuda")
+        for column, want in ((5, inf * sign), (6, -inf * sign), (9, inf), (12, -inf), (10, inf * sign)):
+            assert torch.equal(y[mine, column], want[mine]), column
+        assert torch.isnan(y[mine][:, [7, 8]]).all()
+        rest = [c for c in range(N) if c not in (5, 6, 7, 8, 9, 10, 12)]
+        assert torch.isfinite(y[mine][:, rest]).all() and torch.isfinite(y[ids < 0]).all()
+        assert (y[other] == float("inf")).all()
