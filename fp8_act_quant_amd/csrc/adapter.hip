@@ -225,7 +225,7 @@ __device__ __forceinline__ void add_adapters(const AdapterArgs &g, int64_t m0, i
                         for (int q = 0; q < 4; ++q) {
                             // (an infinite B times a lower number of 0 is NaN: then the first number's sum is u B's)
                             const float all = sum[q] == sum[q] ? sum[q] : first[q];
-                            acc[i][j][q] += id == e[a] ? all : 0.0f;
+                            acc[i][j][q] = id == e[a] ? acc[i][j][q] + all : acc[i][j][q];   // (another row's -0 stays)
                         }
                     }
                 }
@@ -355,7 +355,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs &g, int64_t m0, i
 #pragma unroll
     for (int j = 0; j < T::SUB_N; ++j) bias[j] = bias_of(g, col + 16 * j + 4 * (lane >> 4));
     store_tile<T, OUT_BF16, T::SUB_N>(g.y, N, m0, M, n0, N, smem, [&](int i, int j) {
-        return acc[i][j] + bias[j];
+        return g.bias ? acc[i][j] + bias[j] : acc[i][j];   // (-0 + 0 would be 0)
     });
 }
 
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void adapter_few_kernel(AdapterArgs g) {
     const float *const sums = few<1, NB, 0, OUT_BF16>(g.mm, n0, smem, [&]() { own.begin(g, 0, u, within, first); });
     f32x4 acc[1][1] = {{*reinterpret_cast<const f32x4 *>(sums + row * NB + at)}};
     own.end(g, 0, u, within, first, acc);
-    if (mine && row < g.mm.M && n < N) store4<OUT_BF16>(g.y, row * N + n, acc[0][0] + bias_of(g, n), N - n);
+    if (mine && row < g.mm.M && n < N) store4<OUT_BF16>(g.y, row * N + n, g.bias ? acc[0][0] + bias_of(g, n) : acc[0][0], N - n);
 }
 
 // SHARED from 65 rows on, us at rank 64: 90 rows an adapter, 250 x 7168 x 7168 82 / 107, 500 x 3000 x 3000 41 / 61;

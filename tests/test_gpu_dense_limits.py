@@ -252,3 +252,29 @@ def test_adapter_infinities_by_every_way(M):
         rest = [c for c in range(N) if c not in (5, 6, 7, 8, 9, 10, 12)]
         assert torch.isfinite(y[mine][:, rest]).all() and torch.isfinite(y[ids < 0]).all()
         assert (y[other] == float("inf")).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N", [(3, 200), (60, 201), (300, 1500), (2305, 4100)])
+def test_rows_without_an_adapter_keep_every_bit(M, N, dtype):
+    """Added to another projection's output: where a row has no adapter, every bit of it stays, of negative zeros,
+    subnormal numbers and infinities too; NaN stays NaN."""
+    g = rng(M)
+    K, r = 64, 40
+    x, a, b = randn(g, M, K), randn(g, 3, r, K), randn(g, 3, N, r)
+    ids = (torch.arange(M, device="cuda") % 5 - 2).to(torch.int32)
+    y = randn(g, M, N, dtype=dtype)
+    y[:, 1::7] = -0.0
+    y[:, 2::7] = -1e-39 if dtype == torch.float32 else -2.0 ** -130
+    y[:, 3::7] = float("-inf")
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    no = ids < 0
+    before = y.clone()
+    got = fq.adapter_add(y, x, a, b, ids)
+    assert torch.equal(got[no].view(bits), before[no].view(bits)) and not torch.equal(got[~no], before[~no])
+    y[no, 4] = float("nan")
+    again = fq.adapter_add(y, x, a, b, ids, out=y)
+    assert again is y or again.data_ptr() == y.data_ptr()
+    keep = torch.arange(N, device="cuda") != 4
+    assert torch.equal(y[no][:, keep].view(bits), before[no][:, keep].view(bits)) and torch.isnan(y[no, 4]).all()
+    assert torch.equal(y[~no], got[~no])
