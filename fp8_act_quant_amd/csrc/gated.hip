@@ -41,28 +41,53 @@ struct GatedArgs {
 // place) and the roundings of their arguments put right, which a large argument would otherwise pass on
 // multiplied: some 20 to 35 operations. (expf, erfcf and the division took 100 and more, and a tile has 64 of
 // these a lane: the projections of 1021 x 1536 -> 4096 with GELU's gradient 36 us, now 33.5.)
-struct Activation {
-    float value, slope;
-};
 constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147182f;
 __device__ __forceinline__ float reciprocal(float d) {
     const float r = __builtin_amdgcn_rcpf(d);
     return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
-// e^-(v + rest), v up to 88, rest a rounding of v
-__device__ __forceinline__ float exp_minus(float v, float rest) {
+// e^-(v + rest) times 2^shift, v up to 113, rest a rounding of v; shift 0, or 64 where v is above 64: it then makes
+// the exponent smaller, which is exact
+__device__ __forceinline__ float exp_minus(float v, float rest, float shift) {
     const float t = -v * kLog2e;
     const float off = __builtin_fmaf(-v, kLog2e, -t) - __builtin_fmaf(v, kLog2eRest, rest * kLog2e);
-    const float e = __builtin_amdgcn_exp2f(t);
+    const float e = __builtin_amdgcn_exp2f(t + shift);
     return __builtin_fmaf(e * kLn2, off, e);
 }
-__device__ __forceinline__ Activation activate(float a, int gelu) {
-    float p;
-    if (gelu) {
-        // Phi(a) = erfc(-a / sqrt 2) / 2; for negative a, e^(-a^2 / 2) / 2 times erfc's other factor, a polynomial
-        // in 1 / (1 + |a| / sqrt 8) (fitted to relative errors of 3e-8); beyond 13.3 that is 0
-        const float c = __builtin_amdgcn_fmed3f(a, -13.3f, 13.3f), half = 0.5f * c, v = c * half;
-        const float e = exp_minus(v, __builtin_fmaf(c, half, -v));
+// Far below zero the exponential leaves the normal numbers before its product with a does. There it is carried with a
+// factor of 2^64, which comes off last: by SiLU in a branch of its own below -87 (done for every a, 4096 x 512 -> 4096
+// took 50.4 us instead of 45.2), by GELU for the slope alone, whose value there is no normal number.
+constexpr float kFarSilu = -87.0f, kFar = 64.0f, kBack = 0x1p-64f;
+
+// four of them; slope is left as it is without SLOPE
+template <bool SLOPE>
+__device__ __forceinline__ void silu4(const f32x4 &a, f32x4 &value, f32x4 &slope) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float p = reciprocal(1.0f + exp_minus(__builtin_amdgcn_fmed3f(a[r], kFarSilu, -kFarSilu), 0.0f, 0.0f));
+        p = a[r] == a[r] ? p : a[r];
+        value[r] = a[r] * p;
+        if constexpr (SLOPE) slope[r] = p * __builtin_fmaf(a[r], 1.0f - p, 1.0f);
+    }
+    if ((a[0] < kFarSilu) | (a[1] < kFarSilu) | (a[2] < kFarSilu) | (a[3] < kFarSilu)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            // (e^a / (1 + e^a) is e^a here; below -110 nothing is left of it)
+            const float e = a[r] < -110.0f ? 0.0f : exp_minus(-a[r], 0.0f, kFar);
+            value[r] = a[r] < kFarSilu ? a[r] * e * kBack : value[r];
+            if constexpr (SLOPE) slope[r] = a[r] < kFarSilu ? e * (1.0f + a[r]) * kBack : slope[r];
+        }
+    }
+}
+// Phi(a) = erfc(-a / sqrt 2) / 2; for negative a, e^(-a^2 / 2) / 2 times erfc's other factor, a polynomial in
+// 1 / (1 + |a| / sqrt 8) (its coefficients, as they stand here, within 7.4e-8 relative); from 14.5 on that is 0
+template <bool SLOPE>
+__device__ __forceinline__ void gelu4(const f32x4 &a, f32x4 &value, f32x4 &slope) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float c = __builtin_amdgcn_fmed3f(a[r], -15.0f, 15.0f), half = 0.5f * c, v = c * half;
+        const bool far = SLOPE && v > kFar;
+        const float e = exp_minus(v, __builtin_fmaf(c, half, -v), far ? kFar : 0.0f), back = far ? kBack : 1.0f;
         const float w = reciprocal(__builtin_fmaf(__builtin_fabsf(c), 0.353553391f, 1.0f));
         float g = -0.0540772378f;
         g = __builtin_fmaf(g, w, 0.258805364f);
@@ -74,16 +99,17 @@ __device__ __forceinline__ Activation activate(float a, int gelu) {
         g = __builtin_fmaf(g, w, 0.280724078f);
         g = __builtin_fmaf(g, w, 0.282262772f);
         g = __builtin_fmaf(g, w, -7.95229838e-6f);
-        const float q = 0.5f * e * g;
-        p = c > 0.0f ? 1.0f - q : q;
-        p = a == a ? p : a;
-        return {a * p, __builtin_fmaf(c, e * 0.398942280f, p)};
+        const float q = 0.5f * e * g * back;
+        float p = c > 0.0f ? 1.0f - q : q;
+        p = a[r] == a[r] ? p : a[r];
+        value[r] = a[r] * p;
+        if constexpr (SLOPE) slope[r] = __builtin_fmaf(c * (e * 0.398942280f), back, p);
     }
-    const float c = __builtin_amdgcn_fmed3f(a, -87.0f, 87.0f);
-    p = reciprocal(1.0f + exp_minus(c, 0.0f));
-    p = a < -87.0f ? 0.0f : p;
-    p = a == a ? p : a;
-    return {a * p, p * __builtin_fmaf(a, 1.0f - p, 1.0f)};
+}
+template <bool SLOPE>
+__device__ __forceinline__ void activate4(const f32x4 &a, int gelu, f32x4 &value, f32x4 &slope) {
+    if (gelu) gelu4<SLOPE>(a, value, slope);
+    else silu4<SLOPE>(a, value, slope);
 }
 
 // What v loses when it is rounded to bf16 (nothing where that is not finite: infinities stay the first number's)
@@ -112,21 +138,18 @@ __device__ __forceinline__ void gated_tile(const GatedArgs &g, int64_t m0, int64
                 const int64_t n = n0 + 16 * (wn * HALF + j) + 4 * (lane >> 4);
                 f32x4 dh = {0.f, 0.f, 0.f, 0.f};
                 if (m < M && n < F) dh = load4<1>(g.dh, m * F + n, F - n);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const Activation a = activate(acc[i][j][r], g.gelu);
-                    acc[i][j][r] = dh[r] * acc[i][j + HALF][r] * a.slope;
-                    acc[i][j + HALF][r] = dh[r] * a.value;
-                }
+                f32x4 value, slope;
+                activate4<true>(acc[i][j], g.gelu, value, slope);
+                acc[i][j] = dh * acc[i][j + HALF] * slope;
+                acc[i][j + HALF] = dh * value;
             }
             __builtin_amdgcn_sched_barrier(0);   // (16 rows at a time, as the registers allow)
         }
     } else {
         store_tile<T, MODE, HALF>(g.h, F, m0, M, n0, F, smem, [&](int i, int j) {
-            f32x4 v;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = activate(acc[i][j][r], g.gelu).value * acc[i][j + HALF][r];
-            return v;
+            f32x4 value, none;
+            activate4<false>(acc[i][j], g.gelu, value, none);
+            return value * acc[i][j + HALF];
         });
     }
     if (g.gu) {
@@ -181,15 +204,10 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
     if (row >= 16 * RX || m >= g.mm.M || n >= F) return;
     const f32x4 gate = *reinterpret_cast<const f32x4 *>(sums + row * NB + at);
     const f32x4 up = *reinterpret_cast<const f32x4 *>(sums + row * NB + COLS + at);
-    f32x4 a, b, dh = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (MODE == 2) dh = load4<1>(g.dh, m * F + n, F - n);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const Activation act = activate(gate[r], g.gelu);
-        a[r] = MODE == 2 ? dh[r] * up[r] * act.slope : act.value * up[r];
-        b[r] = dh[r] * act.value;
-    }
+    f32x4 value, slope;
+    activate4<MODE == 2>(gate, g.gelu, value, slope);
     if constexpr (MODE == 2) {
+        const f32x4 dh = load4<1>(g.dh, m * F + n, F - n), a = dh * up * slope, b = dh * value;
         store4<1>(g.gu, m * 2 * F + n, a, F - n);
         store4<1>(g.gu, (m * 2 + 1) * F + n, b, F - n);
         if (g.rest) {
@@ -197,7 +215,7 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedArgs g) {
             store4<1>(g.rest, (m * 2 + 1) * F + n, rest_of(b), F - n);
         }
     } else {
-        store4<MODE>(g.h, m * F + n, a, F - n);
+        store4<MODE>(g.h, m * F + n, value * up, F - n);
         if (g.gu) {
             store4<1>(g.gu, m * 2 * F + n, gate, F - n);
             store4<1>(g.gu, (m * 2 + 1) * F + n, up, F - n);
@@ -216,18 +234,17 @@ __global__ __launch_bounds__(256) void gated_slope_kernel(const uint16_t *dh, co
         const u32x4 vh = *reinterpret_cast<const u32x4 *>(dh + 8 * p), vg = *reinterpret_cast<const u32x4 *>(gu + at),
                     vu = *reinterpret_cast<const u32x4 *>(gu + at + F);
         u32x4 a, b, ra, rb;
+        auto four = [](const u32x4 &v, int i) {   // elements 2 i .. 2 i + 3
+            return f32x4{bf16lo_to_f32(v[i]), bf16hi_to_f32(v[i]), bf16lo_to_f32(v[i + 1]), bf16hi_to_f32(v[i + 1])};
+        };
+        auto put = [](u32x4 &to, int i, const f32x4 &v) { to[i] = pack_bf16x2(v[0], v[1]), to[i + 1] = pack_bf16x2(v[2], v[3]); };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Activation lo = activate(bf16lo_to_f32(vg[i]), gelu), hi = activate(bf16hi_to_f32(vg[i]), gelu);
-            const float hl = bf16lo_to_f32(vh[i]), hh = bf16hi_to_f32(vh[i]);
-            const float gl = hl * bf16lo_to_f32(vu[i]) * lo.slope, gh = hh * bf16hi_to_f32(vu[i]) * hi.slope;
-            const float ul = hl * lo.value, uh = hh * hi.value;
-            a[i] = pack_bf16x2(gl, gh);
-            b[i] = pack_bf16x2(ul, uh);
-            if constexpr (WIDE) {
-                ra[i] = pack_bf16x2(rest_of(gl), rest_of(gh));
-                rb[i] = pack_bf16x2(rest_of(ul), rest_of(uh));
-            }
+        for (int i = 0; i < 4; i += 2) {
+            f32x4 value, slope;
+            activate4<true>(four(vg, i), gelu, value, slope);
+            const f32x4 h = four(vh, i), dg = h * four(vu, i) * slope, du = h * value;
+            put(a, i, dg), put(b, i, du);
+            if constexpr (WIDE) put(ra, i, rest_of(dg)), put(rb, i, rest_of(du));
         }
         *reinterpret_cast<u32x4 *>(d + at) = a;
         *reinterpret_cast<u32x4 *>(d + at + F) = b;

@@ -278,3 +278,34 @@ def test_rows_without_an_adapter_keep_every_bit(M, N, dtype):
     keep = torch.arange(N, device="cuda") != 4
     assert torch.equal(y[no][:, keep].view(bits), before[no][:, keep].view(bits)) and torch.isnan(y[no, 4]).all()
     assert torch.equal(y[~no], got[~no])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_down_to_the_smallest_numbers(act):
+    """Every bf16 number from -200 to 200 as the gate's projection: value and slope within ACT U wherever they are
+    normal fp32 numbers, and nothing but less than the smallest of those otherwise."""
+    a = torch.arange(0, 1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    a = a[(a.abs() <= 200) & (a.abs() >= 1e-30) | (a == 0)]
+    x = torch.zeros((a.numel(), 8), device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = a, 1.0
+    w = torch.zeros((16, 8), device="cuda").bfloat16()
+    w[:8, 0] = w[8:, 1] = 1.0
+    tiny = 2.0 ** -126
+    value, slope, mag = act64(a.double(), act)
+    for rows in (slice(0, a.numel()), slice(0, 16)):      # by tiles, and few rows
+        h, gu = fq.gated_linear(x[rows].contiguous(), w, act=act, keep=True, out_dtype=torch.float32)
+        assert ((h[:, 0].double() - value[rows]).abs() <= ACT * U * value[rows].abs() + tiny).all()
+    h, gu = fq.gated_linear(x, w, act=act, keep=True, out_dtype=torch.float32)
+    far = (value.abs() > 2 * tiny) & (a < -80 if act == "silu" else a < -12.5)
+    assert far.any() and (h[far] != 0).all()
+    one = torch.zeros((a.numel(), 8), device="cuda").bfloat16()
+    one[:, 3] = 1.0
+    for kept in (gu, None):
+        dx, _ = fq.gated_linear_backward(one, x, w, kept, act=act, dx_dtype=torch.float32)
+        assert ((dx[:, 0].double() - slope).abs() <= half(torch.bfloat16) * slope.abs() + 2 * ACT * U * mag + tiny).all()
+        assert ((dx[:, 1].double() - value).abs() <= half(torch.bfloat16) * value.abs() * (1 + ACT * U) + ACT * U * value.abs() + tiny).all()
+    # beyond all of that, the limits
+    x[:, 0] = 1e30
+    x[::2, 0] = -1e30
+    h = fq.gated_linear(x, w, act=act, out_dtype=torch.float32)
+    assert (h[::2] == 0).all() and (h[1::2] == x[1::2, :1].float()).all()
