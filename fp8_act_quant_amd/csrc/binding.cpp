@@ -118,6 +118,12 @@ int64_t integer(PyObject *o, const char *name) {
     return v;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v == 1;
+}
+
 float real(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
@@ -487,7 +493,7 @@ struct Gated {
 PyObject *gated(PyObject *const *a) {
     const Gated g(a[0], a[1]);
     const int act = (int)integer(a[2], "act");
-    const bool keep = PyObject_IsTrue(a[3]) == 1;
+    const bool keep = truth(a[3]);
     const Tensor h = like(g.x, g.shape(g.F), type_of_code(a[4])),
                  gu = keep ? like(g.x, g.shape(2 * g.F), ScalarType::BFloat16) : Tensor();
     const On on(g.x);

@@ -309,3 +309,15 @@ def test_activations_down_to_the_smallest_numbers(act):
     x[::2, 0] = -1e30
     h = fq.gated_linear(x, w, act=act, out_dtype=torch.float32)
     assert (h[::2] == 0).all() and (h[1::2] == x[1::2, :1].float()).all()
+
+
+def test_keep_raises_its_own_error():
+    """keep is taken for its truth, and an object that has none raises its own error."""
+    x, w = torch.ones((2, 8), device="cuda").bfloat16(), torch.ones((16, 8), device="cuda").bfloat16()
+
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+    with pytest.raises(KeyError, match="neither"):
+        fq.gated_linear(x, w, keep=Neither())
+    assert len(fq.gated_linear(x, w, keep=1)) == 2 and torch.is_tensor(fq.gated_linear(x, w, keep=[]))
