@@ -5,7 +5,7 @@ Tolerances: half(t) is half a step of t relative to the value; U = 2^-24 is fp32
 32 products at a time, with every product and addition off by at most 2 U: a sum over K is off by at most
 2 (K / 32 + 32) U of the sum of its terms' magnitudes. The activations of the kernels are some 35 fp32
 operations on the hardware's exponential and reciprocal, each within one unit in the last place (2 U), and a
-polynomial fitted to 7e-8 (1.2 U): 16 U relative covers the few of them that carry the result's full size.
+polynomial within 5.1e-8 (0.9 U): 16 U relative covers the few of them that carry the result's full size.
 """
 import pytest
 import torch
