@@ -57,10 +57,11 @@ __device__ __forceinline__ u32x4 rsrc_words(const void *p, int64_t bytes) {
 }
 __device__ __forceinline__ void copy16(const u32x4 &rsrc, uint8_t *to, uint32_t off, uint32_t soff) {
     const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)to;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
+    uint32_t m0;   // (M0 is put back: the compiler, which takes no clobber of it, may hold a value of its own there)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
                  : "s"(lds), "v"(off), "s"(rsrc), "s"(soff)
-                 : "memory");   // (M0: nothing else in a kernel with such copies uses it)
+                 : "memory");
 }
 
 __device__ __forceinline__ int swz_chunk(int row, int chunk) { return chunk ^ (row & 7); }
