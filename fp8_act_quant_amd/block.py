@@ -89,15 +89,15 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     x bfloat16 [..., K], w bfloat16 [N, K] shared by all; a [adapters, rank, K] and b [adapters, N, rank]
     bfloat16 (K a multiple of 8, rank one up to 256, lower ranks padded with zeros); ids int32 [...]
     on the device, in any order; scales float32 [adapters]; bias float32 [N]. Returns [..., N] in
-    out_dtype (bfloat16 or float32)."""
+    out_dtype (bfloat16 or float32); out, if given, overlaps no other argument."""
     return native.adapter(x, _given(w, "w"), a, b, ids, scales, bias, None, out_code(out_dtype), out)
 
 
 def adapter_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
                 scales: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """y + scales[e] * (x a[e]^T) b[e]^T: the adapters beside another projection's output y [..., N] (float32
-    or bfloat16; of fp8_gemm, int8_linear, ...), in y's dtype. out may be y itself. Other arguments
-    as for adapter_linear."""
+    or bfloat16; of fp8_gemm, int8_linear, ...), in y's dtype. out may be y itself, and overlaps
+    neither a part of it nor b or ids. Other arguments as for adapter_linear."""
     return native.adapter(x, None, a, b, ids, scales, None, y, 0, out)
 
 

@@ -159,6 +159,12 @@ Tensor output(PyObject *out, at::IntArrayRef shape, ScalarType type, uintptr_t a
     shaped(t, "out", shape);
     return t;
 }
+// `out` written while `t` is still read: refused where they share memory
+void apart(const Tensor &out, const Tensor *t, const char *name) {
+    if (!t || !t->numel() || !out.numel()) return;
+    const char *a = static_cast<const char *>(out.data_ptr()), *b = static_cast<const char *>(t->data_ptr());
+    if (a < b + t->nbytes() && b < a + out.nbytes()) raise(PyExc_ValueError, "out must not overlap %s", name);
+}
 ScalarType type_of_code(PyObject *o) {
     return integer(o, "out_dtype") == FP8Q_OUT_BF16 ? ScalarType::BFloat16 : ScalarType::Float;
 }
@@ -544,6 +550,11 @@ PyObject *adapter(PyObject *const *a) {
     const Tensor *bias = bias_of(a[6], N, x);
     if (base && reinterpret_cast<uintptr_t>(base->data_ptr()) % 4) raise(PyExc_ValueError, "y must be 4-byte aligned");
     const Tensor y = output(a[9], shape, base ? base->scalar_type() : type_of_code(a[8]), 4, x);
+    if (a[9] != Py_None) {   // (x, a and scales are read by the first launch; beside w x is read by the second too)
+        if (w) apart(y, &x, "x"), apart(y, w, "w");
+        else if (y.data_ptr() != base->data_ptr()) apart(y, base, "y but as a whole");
+        apart(y, &lb, "b"), apart(y, &ids, "ids"), apart(y, bias, "bias");
+    }
     const size_t bytes = L ? adapter_linear_workspace_bytes(M, K, r) : 0;
     const Tensor ws = bytes ? like(x, {(int64_t)bytes}, ScalarType::Byte) : Tensor();
     const On on(x);

@@ -447,7 +447,7 @@ size_t gated_linear_backward_wide_workspace_bytes(int64_t M, int64_t F, int64_t 
  *   for 1; ids [M] int32 on the device: rows whose id is outside [0, adapters) have no adapter.
  *   y [M, N] of type y_dtype (4-byte aligned).
  *   With w NULL base [M, N] of type y_dtype takes the place of x w^T (the output of another
- *   projection: FP8, 8-bit integers); it may be y itself.
+ *   projection: FP8, 8-bit integers); it may be y itself. Otherwise y overlaps no argument.
  *   K a multiple of 8 below 2^23, rank of 8 up to 256 (adapters of lower ranks padded with zeros),
  *   adapters < 2^31, M <= 2^26, N <= 2^28. x a^T is kept in fp32 and enters the second product
  *   with all its bits; sums are fp32, rounded once. What an adapter holds (infinities, NaN) reaches

@@ -321,3 +321,25 @@ def test_keep_raises_its_own_error():
     with pytest.raises(KeyError, match="neither"):
         fq.gated_linear(x, w, keep=Neither())
     assert len(fq.gated_linear(x, w, keep=1)) == 2 and torch.is_tensor(fq.gated_linear(x, w, keep=[]))
+
+
+def test_output_over_an_argument_is_refused():
+    """y may be what it is added to; over anything else that is read while it is written there is no result."""
+    g = rng(4)
+    M, K, r = 70, 64, 8
+    x, w, a, b = randn(g, M, K), randn(g, K, K), randn(g, 2, r, K), randn(g, 2, K, r)
+    ids = torch.zeros(M, device="cuda", dtype=torch.int32)
+    buffer = torch.zeros(4 * M * K, device="cuda").bfloat16()
+    y, shifted = buffer[:M * K].view(M, K), buffer[8:8 + M * K].view(M, K)
+    for bad in (lambda: fq.adapter_linear(x, w, a, b, ids, out=x), lambda: fq.adapter_linear(y, w, a, b, ids, out=shifted),
+                lambda: fq.adapter_linear(x, y[:K], a, b, ids, out=y), lambda: fq.adapter_add(y, x, a, b, ids, out=shifted),
+                lambda: fq.adapter_add(x, x, a, y[:16].view(2, K, r), ids, out=y),
+                lambda: fq.adapter_add(x, x, a, b, y.view(-1)[:2 * M].view(torch.int32), out=y)):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+    want = fq.adapter_add(x, x, a, b, ids)
+    assert torch.equal(fq.adapter_add(x.clone(), x, a, b, ids, out=y), want)
+    assert torch.equal(fq.adapter_add(y.copy_(x), x, a, b, ids, out=y), want)
+    z = x.clone()
+    assert torch.equal(fq.adapter_add(x, z, a, b, ids, out=z), want)      # (x is read before)
+    assert fq.adapter_linear(x[:0], w, a, b, ids[:0], out=x[:0]).shape == (0, K)
