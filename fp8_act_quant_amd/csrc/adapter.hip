@@ -462,8 +462,12 @@ hipError_t launch_shrink(const AdapterArgs &a, hipStream_t stream) {
     } else {
         const int64_t tiles = (M + ShrinkTile::BM - 1) / ShrinkTile::BM;
         const int blocks = (a.rank + ShrinkTile::BN - 1) / ShrinkTile::BN;
-        // (a decode batch's rows differ, a prefill batch's are runs)
-        const dim3 grid((unsigned)tiles, a.splits * blocks, M <= 512 ? 8 : 2);
+        // Workgroups that share a tile's adapters: 8 while that fills CUs, 2 where it only adds workgroups that find none.
+        // us of both products at 7168 -> 128 with 2 / 8, in mixed order of 32 adapters and in runs of 90 rows, rank 64:
+        // 520 rows (136 workgroups with 1) 76 / 58 and 15.9 / 15.8, 760 (192) 86 / 82 and 17.1 / 17.2, 900 (232) 100 / 96 and
+        // 17.8 / 19.7, 1024 (256) 114 / 116 and 18.2 / 21.8, 8192 867 / 866 and 66 / 67; rank 128: 250 (128) 65 / 60 and 16.9 / 16.8,
+        // 500 (256) 105 / 107 and 20.9 / 24.3.
+        const dim3 grid((unsigned)tiles, a.splits * blocks, tiles * a.splits * blocks <= 192 ? 8 : 2);
         adapter_shrink_kernel<<<grid, dim3(256), 0, stream>>>(a);
     }
     return hipGetLastError();
