@@ -317,8 +317,8 @@ __device__ __forceinline__ f32x4 bias_of(const AdapterArgs &g, int64_t n) {
 
 // A tile. ADD: no W, base is added. SHARED: rows by the matrix unit, whose neighbours mostly have one adapter, after the
 // product; else each lane for itself, while the product's first copies are on their way. At rank 64 on the device:
-// 8192 x 7168 x 7168 652 us, the matrix unit busy 0.65 (5000 rows 91% of the rate without adapters); added alone, 5000 x
-// 7168 94 us (28 are the outputs' bytes at a copy's rate, the rest waits for u, ids and B in turn). A decode batch of 48 x
+// 8192 x 7168 x 7168 655 us, the matrix unit busy 0.65 (5000 rows 91% of the rate without adapters); added alone, 5000 x
+// 7168 in runs of 90 rows 111 us (28 are the outputs' bytes at a copy's rate, the rest waits for u, ids and B in turn). A decode batch of 48 x
 // 7168 x 7168 at rank 16 30 us, 3.8 TB/s: each workgroup copies all of x into its LDS at a CU's 65 KB/us.
 template <class T, int SHARED>
 constexpr int tile_bytes() {   // (u over the stages where it is read after the product)
