@@ -343,3 +343,27 @@ def test_output_over_an_argument_is_refused():
     z = x.clone()
     assert torch.equal(fq.adapter_add(x, z, a, b, ids, out=z), want)      # (x is read before)
     assert fq.adapter_linear(x[:0], w, a, b, ids[:0], out=x[:0]).shape == (0, K)
+
+
+def test_one_row_without_a_leading_dimension_and_none():
+    """x [K] is one row, with ids of no dimension; a leading dimension of 0 is no row."""
+    g = rng(6)
+    x, y, w, a, b = randn(g, 64), randn(g, 64), randn(g, 128, 64), randn(g, 2, 8, 64), randn(g, 2, 64, 8)
+    ids = torch.tensor(1, device="cuda", dtype=torch.int32)
+    v = torch.rand(64, device="cuda")
+    row = lambda t: t.view(1, -1)    # noqa: E731
+    pairs = [(fq.rms_norm(x, v), fq.rms_norm(row(x), v)),
+             (fq.residual_norm(x, y, v, gate=y), fq.residual_norm(row(x), row(y), v, gate=row(y))),
+             (fq.residual_norm(x.float(), y.float(), v, gate=v), fq.residual_norm(row(x.float()), row(y.float()), v, gate=v)),
+             (fq.residual_norm_backward(x, y, x, y, v, gate=v, post=v), fq.residual_norm_backward(row(x), row(y), row(x), row(y), v, gate=v, post=v)),
+             (fq.gated_linear(x, w), fq.gated_linear(row(x), w)),
+             (fq.gated_linear_backward(y, x, w, wide=True), fq.gated_linear_backward(row(y), row(x), w, wide=True)),
+             (fq.adapter_linear(x, w, a, torch.cat([b, b], 1), ids), fq.adapter_linear(row(x), w, a, torch.cat([b, b], 1), row(ids)[0])),
+             (fq.adapter_add(y, x, a, b, ids), fq.adapter_add(row(y), row(x), a, b, row(ids)[0]))]
+    for one, many in pairs:
+        for p, q in zip(one if isinstance(one, tuple) else (one,), many if isinstance(many, tuple) else (many,)):
+            assert p.numel() == q.numel() and torch.equal(p.view(-1), q.view(-1))
+    none = torch.empty((3, 0, 64), device="cuda").bfloat16()
+    assert fq.rms_norm(none, v).shape == fq.adapter_linear(none, w[:64], a, b, ids.expand(3, 0).contiguous()).shape == none.shape
+    dx, dw = fq.gated_linear_backward(none, none, w, wide=True)
+    assert dx.shape == none.shape and dw.shape == w.shape and (dw == 0).all()
